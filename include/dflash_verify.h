@@ -69,8 +69,10 @@ extern "C" {
 #define DFLASH_ABI_VERSION 1
 #define DFLASH_MAX_TOP_K 32
 
-/* logits storage type */
-enum { DFLASH_BF16 = 0, DFLASH_F32 = 1 };
+/* storage types: logits are DFLASH_BF16 or DFLASH_F32; the attention's tokens
+ * DFLASH_BF16 or DFLASH_F16, and its cache their type or DFLASH_E4M3 (8-bit
+ * floats with 4 exponent and 3 mantissa bits, largest value 448) */
+enum { DFLASH_BF16 = 0, DFLASH_F32 = 1, DFLASH_F16 = 2, DFLASH_E4M3 = 3 };
 
 /* return codes */
 enum {
@@ -89,6 +91,11 @@ enum {
                                             outputs are then unspecified) */
 #define DFLASH_STATUS_BAD_TEMPERATURE 8u /* temperature negative, NaN or infinite: the
                                             request is verified greedily */
+#define DFLASH_STATUS_BAD_PAGE 16u       /* a page index outside the cache: the page's keys
+                                            take no part, its slots are not written */
+#define DFLASH_STATUS_BAD_LENGTH 32u     /* a length that is negative or beyond the page
+                                            table, or token offsets that do not ascend
+                                            inside the packed tokens (clamped) */
 
 /* ABI version of the loaded library (DFLASH_ABI_VERSION). */
 int dflash_abi_version(void);
@@ -359,6 +366,121 @@ int dflash_lmhead_verify(const void* h, const void* w, int B, int gamma, int V, 
                          const int32_t* draft_tokens, const float* temperature, int top_k, float top_p,
                          uint64_t seed, void* logits, int32_t* out_tokens, int32_t* out_accept_len,
                          void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* ---- the target's attention over a paged cache ----------------------------------------
+ * The loop's target forward (the listing of "DFlash2 用投机解码给 Qwen 提速",
+ * bml.asia) runs each layer's attention for the block's tokens over
+ * everything before them. These two calls are that attention's memory side:
+ * the block's keys and values go into a paged cache, then its queries read
+ * the cache. Plain decoding is a block of one token.
+ *
+ * A cache is two arrays k and v of pages; the row of head_dim values of
+ * (page, head, slot) starts at element page * page_stride + head * head_stride
+ * + slot * slot_stride of either array, so pages may hold heads inside tokens
+ * or tokens inside heads. Position n of request b is slot n % page_size of
+ * page page_table[b * table_stride + n / page_size]. Any page size; strides
+ * and base addresses are multiples of 16 bytes; an array spans less than
+ * 64 GiB. head_dim is 64, 128 or 256. In a DFLASH_E4M3 cache a stored value
+ * stands for itself times its head's k_scale or v_scale ([device] float
+ * [kv_heads], NULL: 1).
+ *
+ * New tokens are packed: request b's are rows q_start[b] .. q_start[b + 1] - 1
+ * of the [tokens, heads, head_dim] arrays (q_start [device] int32 [batch + 1]),
+ * or, with q_start NULL, tokens / batch each. Rows that belong to no request
+ * are left alone. `strides` [host] holds element strides (multiples of 16
+ * bytes); the last dimension is contiguous. batch <= 2048.
+ *
+ * A page index outside [0, num_pages) is never followed
+ * (DFLASH_STATUS_BAD_PAGE); bad lengths and offsets are clamped
+ * (DFLASH_STATUS_BAD_LENGTH). */
+typedef struct dflash_paged_cache {
+  void* k;                   /* [device] */
+  void* v;                   /* [device] */
+  const int32_t* page_table; /* [device] [batch, max_pages] */
+  const float* k_scale;      /* [device] [kv_heads] or NULL */
+  const float* v_scale;      /* [device] [kv_heads] or NULL */
+  int64_t page_stride, head_stride, slot_stride; /* elements */
+  int64_t table_stride;      /* entries between requests */
+  int32_t num_pages, page_size, kv_heads, head_dim;
+  int32_t dtype;
+  int32_t batch, max_pages;
+} dflash_paged_cache;
+
+/* Appends new tokens: token i of request b goes to position cached_lens[b] + i
+ * ([device] int32 [batch]: tokens in the cache before the call, which is not
+ * changed). k and v [device] [tokens, kv_heads, head_dim] (dtype). The first
+ * rot_dim values of each key (and of each query of the optional q [device]
+ * [tokens, q_heads, head_dim], rotated into q_out; q_out may be q) are turned
+ * to the token's position n: pair j, values j and j + rot_dim / 2 (2j and
+ * 2j + 1 when interleaved), by the angle n w_j. phases [device] uint64
+ * [rot_dim / 2] holds w_j / (2 pi) as a 64-bit binary fraction of a turn
+ * (modulo 1), which keeps the angle exact at any position. rot_dim: a
+ * multiple of 16, 0 for no rotation. The arithmetic is fp32, rounded once to
+ * the cache's type (e4m3: over the head's scale, saturated at +-448).
+ * strides: k's token and head stride, then v's, q's, q_out's. */
+int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out,
+                     int dtype, int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens,
+                     const int32_t* q_start, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,
+                     void* stream);
+
+/* Attention of the new tokens over the cache, which already holds them:
+ * kv_lens [device] int32 [batch] counts every position, the new tokens last.
+ * Query head h reads key/value head h / (q_heads / kv_heads). out [tokens,
+ * q_heads, head_dim] = softmax(scale q k^T) v; lse (optional, [device] float
+ * [tokens, q_heads], contiguous) = log sum e^(scale q k). causal: new token i
+ * of n sees the first kv_len - n + i + 1 positions (the target's
+ * verification); otherwise every one (a drafter that attends over its whole
+ * block). Keys a row does not see take no part, whatever they hold; a row
+ * that sees none gives 0 and -inf. strides: q's token and head stride, then
+ * out's.
+ * workspace [device], 256-byte aligned, of dflash_attention_workspace_bytes();
+ * it needs no preparation, and calls that share one must be ordered. The
+ * result does not depend on how the GPU schedules the work. */
+size_t dflash_attention_workspace_bytes(int batch, int head_dim);
+int dflash_paged_attention(const dflash_paged_cache* cache, const void* q, void* out, float* lse, int dtype,
+                           int tokens, int q_heads, const int64_t* strides, const int32_t* kv_lens,
+                           const int32_t* q_start, float scale, int causal, void* workspace, size_t workspace_bytes,
+                           uint32_t* status, void* stream);
+
+/* ---- distillation of the drafter from the target's top logits ---------------------------
+ * The accept length follows the overlap of the drafter's distribution with
+ * the target's (the acceptance table of rytg.cn, section "实测数据"); a drafter is trained towards the target on the
+ * target's largest logits, which is what can be stored of a 248k vocabulary.
+ * Per row: p = softmax(teacher_logits / T) over the K entries, q =
+ * softmax(student / T) over all V logits,
+ *   loss = w sum_j p_j (log p_j - log q[id_j]),
+ *   dloss/dstudent[v] = w (q[v] - sum of p_j with id_j = v) / T.
+ * student [device] [rows, V] (dtype bf16 or fp32, rows row_stride elements
+ * apart, any alignment), teacher_ids [device] int32 [rows, K], teacher_logits
+ * [device] float [rows, K], 1 <= K <= 256, row_weight [device] float [rows] or
+ * NULL (1). Entries with id -1 take no part; other ids outside [0, V) neither
+ * (DFLASH_STATUS_BAD_TOKEN). A row without entries, or of weight 0, has loss
+ * and gradient 0 whatever its logits. A row with a NaN, or whose largest
+ * student logit or used teacher logit is infinite, gives NaN
+ * (DFLASH_STATUS_BAD_ROW). Ids may repeat.
+ *
+ * dflash_distill_loss: loss [rows] and, where row_stats ([device] float
+ * [rows, 2]) is given, each row's largest logit m and sum of e^((z - m)/T),
+ * for the backward call. */
+int dflash_distill_loss(const void* student, int64_t row_stride, int rows, int V, int dtype,
+                        const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
+                        const float* row_weight, float* loss, float* row_stats, uint32_t* status, void* stream);
+
+/* The gradient for an upstream gradient of the losses ([device] float [rows],
+ * NULL: 1): grad [rows, V] in the student's type, rows grad_stride elements
+ * apart. grad may be student itself (same stride). A row whose upstream
+ * gradient is 0 gives 0. */
+int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V, int dtype,
+                        const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
+                        const float* row_weight, const float* row_stats, const float* upstream, void* grad,
+                        int64_t grad_stride, void* stream);
+
+/* Loss and gradient (of the sum of the losses) in one call, which reads the
+ * logits once. grad may be student itself (same stride). */
+int dflash_distill_loss_grad(const void* student, int64_t row_stride, int rows, int V, int dtype,
+                             const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
+                             const float* row_weight, float* loss, void* grad, int64_t grad_stride, uint32_t* status,
+                             void* stream);
 
 #ifdef __cplusplus
 }

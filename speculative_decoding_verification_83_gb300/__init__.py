@@ -20,8 +20,9 @@ _BUILD = os.path.join(_HERE, "_build")
 LIB_PATH = os.path.join(_BUILD, "libdflash_verify.so")
 SOURCES = ["dflash_sweep.cu", "dflash_fullvocab.cu", "dflash_fvtp.cu", "dflash_candidates.cu", "dflash_lmhead.cu",
            "dflash_abi.cu",
-           "dflash_noalloc.cu"]
-HEADERS = ["dflash_device.cuh", "dflash_internal.h", "dflash_rule.cuh", "dflash_ff.cuh"]
+           "dflash_noalloc.cu", "dflash_kvappend.cu", "dflash_attention.cu", "dflash_distill.cu", "dflash_ops_abi.cu"]
+HEADERS = ["dflash_device.cuh", "dflash_internal.h", "dflash_rule.cuh", "dflash_ff.cuh", "dflash_ops.h",
+           "dflash_paged.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -115,9 +116,15 @@ EXPORTS = {
     "dflash_verify_noalloc": ("i", "pppiiiipifQpppp"),
     "dflash_lmhead_logits": ("i", "ppiiippp"),
     "dflash_lmhead_verify": ("i", "ppiiiippifQppppzpp"),
+    "dflash_kv_append": ("i", "pppppiiippppiipp"),
+    "dflash_attention_workspace_bytes": ("z", "ii"),
+    "dflash_paged_attention": ("i", "ppppiiipppfipzpp"),
+    "dflash_distill_loss": ("i", "pliiippifppppp"),
+    "dflash_distill_grad": ("i", "pliiippifppppl" "p"),
+    "dflash_distill_loss_grad": ("i", "pliiippifpppl" "pp"),
 }
 _CT = {"i": ctypes.c_int, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float,
-       "Q": ctypes.c_uint64, "s": ctypes.c_char_p, "": None}
+       "Q": ctypes.c_uint64, "l": ctypes.c_int64, "s": ctypes.c_char_p, "": None}
 
 
 def load(path: str | None = None):
@@ -609,9 +616,12 @@ def verify_host(target, draft, draft_tokens, temperature, top_k, top_p, seed, ou
     return out_tokens, out_accept_len
 
 
+from .operators import *  # noqa: E402,F401,F403
+from .operators import __all__ as _operators  # noqa: E402
+
 __all__ = [
     "build", "load", "verify", "verify_det", "verify_greedy", "shard_candidates", "gather_records",
     "verify_candidates", "verify_vocab_sharded", "candidates_words", "filter_rows", "sample_rows", "uniforms",
     "verify_host", "Workspace", "workspace_bytes", "rows_workspace_bytes", "host_staging_bytes",
-    "DFlashError", "LIB_PATH", "EXPORTS",
+    "DFlashError", "LIB_PATH", "EXPORTS", *_operators,
 ]

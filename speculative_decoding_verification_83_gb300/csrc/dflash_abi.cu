@@ -15,6 +15,7 @@
 
 #include "../../include/dflash_verify.h"
 #include "dflash_internal.h"
+#include "dflash_ops.h"
 
 using namespace dflash;
 
@@ -282,6 +283,8 @@ Params base_params(int dtype, int V) {
 }
 
 }  // namespace
+
+int dflash::context_sms(int dev) { return available_sms(dev); }
 
 void dflash::set_last_error(const char* msg) { snprintf(g_last_error, sizeof g_last_error, "%s", msg); }
 

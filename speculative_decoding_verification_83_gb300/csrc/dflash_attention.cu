@@ -1,0 +1,696 @@
+// dflash_attention.cu -- attention of a few new tokens per request over a paged
+// key/value cache: one token each in plain decoding, the block of drafts in
+// verification.
+//
+// For query row r (new token i of request b, query head h G + g of key/value
+// head h): x_j = scale q_r . k_j over the keys j the row sees (all L of the
+// request, or the first L - n + i + 1 with n new tokens and a causal mask),
+// out = sum_j e^{x_j} v_j / sum_j e^{x_j}, lse = log sum_j e^{x_j}. A row that
+// sees no key gives 0 and -inf.
+//
+// What bounds it: every key and value is read once for the n G rows that
+// share its head, 2 n G flops per byte of a 16-bit cache, so the reads of the
+// cache bound it until n G nears 100 rows. Design:
+//  * Work is a list of units (request, head, 16 query rows), each a run of
+//    64-key tiles; the list's tiles are dealt out in equal contiguous runs,
+//    one per CTA, whatever the requests' lengths. A unit that spans CTAs
+//    leaves unnormalised partial results (fp32 sum, maximum, sum of weights)
+//    in the workspace, which a second kernel joins in a fixed order: the
+//    results do not depend on timing.
+//  * In a CTA each of four warps takes its own 16 keys of every tile, with a
+//    ring of its own in shared memory filled by asynchronous 16-byte copies,
+//    which address any page size, stride and order; no barrier of the CTA is
+//    needed until the unit ends, where the warps' results are joined through
+//    shared memory. The ring runs on into the next unit.
+//  * S = Q K^T and O += P V by m16n8k16 tensor instructions with fp32
+//    accumulators; P leaves the S registers as the second product's operand.
+//    The running maximum rescales O only in steps where a maximum moved.
+//  * e4m3 caches are widened in registers, exactly, to f16. q is then scaled
+//    per row by a power of two into f16's range (exact but for values
+//    below 2^-31 of the row's largest), undone in the scores.
+// Rounding: P is rounded to the operands' type (half a step of its own
+// relative to each weight); all sums, maxima and exponents are fp32.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "dflash_paged.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kAttnThreads = kWarps * 32;
+constexpr int kWarpKeys = 16;
+constexpr int kTile = kWarps * kWarpKeys;  // keys per tile
+constexpr int kRows = 16;                  // query rows per unit
+constexpr int kMaxCtas = 640;              // CTAs whose partial results the workspace holds
+constexpr int kMinRun = 4;                 // tiles a CTA takes at least (256 keys)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -INFINITY;
+
+// ---- workspace ------------------------------------------------------------------------
+// [0] tiles per CTA, [1 .. B + 1] tiles before each request (64-bit), then per
+// CTA two slots of partial results: kRows x (maximum, sum), then kRows x D.
+__host__ __device__ inline size_t ws_header(int B) { return ((size_t)(B + 2) * 8 + 255) & ~(size_t)255; }
+__host__ __device__ inline size_t ws_ml(int B) { return ws_header(B); }
+__host__ __device__ inline size_t ws_o(int B) {
+  return ws_header(B) + (size_t)kMaxCtas * 2 * kRows * 2 * sizeof(float);
+}
+
+struct Unit {
+  int b, h, rb, L, first, n, tiles;
+  long long start;  // index of its first tile in the whole list
+};
+
+__device__ __forceinline__ int clamped_len(const AttnParams& p, int b, bool& bad) {
+  const int L = p.lens[b];
+  const long long cap = (long long)p.c.max_pages * p.c.page_size;
+  const int top = cap < 0x7fffffffLL - kTile ? (int)cap : 0x7fffffff - kTile;
+  const int c = min(max(L, 0), top);
+  bad |= c != L;
+  return c;
+}
+__device__ __forceinline__ int tiles_of(int L) { return max(1, (L + kTile - 1) / kTile); }
+
+// The unit that tile t of the list belongs to (pre: tiles before each request).
+__device__ __forceinline__ Unit locate(const AttnParams& p, const long long* pre, long long t) {
+  Unit u;
+  int lo = 0, hi = p.tk.B;  // largest b with pre[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  u.b = lo;
+  bool bad = false;
+  request_tokens(p.tk, lo, u.first, u.n, bad);
+  u.L = clamped_len(p, lo, bad);
+  u.tiles = tiles_of(u.L);
+  const int rbs = (int)(((long long)u.n * p.G + kRows - 1) / kRows);
+  const long long k = (t - pre[lo]) / u.tiles;
+  u.h = (int)(k / rbs);
+  u.rb = (int)(k - (long long)u.h * rbs);
+  u.start = pre[lo] + k * u.tiles;
+  return u;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;  // 0: the 16 bytes are zero-filled, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two e4m3 values (the low 16 bits) as two f16 values
+__device__ __forceinline__ uint32_t widen2(uint32_t v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <bool kF8, int D>
+struct Shape {
+  static constexpr int kRowBytes = kF8 ? D : 2 * D;
+  static constexpr int kHalfStage = kWarpKeys * kRowBytes;  // K or V of one warp's step
+  static constexpr int kStageBytes = 2 * kHalfStage * kWarps;
+  static constexpr int kStages = kStageBytes >= 65536 ? 3 : (98304 / kStageBytes < 8 ? 98304 / kStageBytes : 8);
+  static constexpr int kCols = 32;  // columns of O joined at a time
+  static constexpr size_t kMerge = (size_t)kWarps * kRows * (kCols + 1) * sizeof(float);
+  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kMerge + 2 * kWarps * kRows * sizeof(float);
+  static constexpr int kPerSm = kSmem > 110000 ? 1 : 2;
+};
+
+// Shared-memory place of 16-byte piece c of row r: pieces of a row are
+// exchanged so that the 8 rows of one matrix load fall in different banks.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+  return kRowBytes >= 128 ? r * kRowBytes + ((c ^ (r & 7)) << 4) : r * kRowBytes + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Whether a 32-bit word of cache values holds one that is not finite.
+template <class T, bool kF8>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  if (kF8) {  // e4m3: all ones below the sign
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (((w >> (8 * i)) & 0x7fu) == 0x7fu) return true;
+    return false;
+  }
+  constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7c00u : 0x7f80u;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+// Value d of a cache row in shared memory.
+template <class T, bool kF8, int kRowBytes>
+__device__ __forceinline__ float value_at(const unsigned char* tile, int r, int d) {
+  if (kF8) {
+    const unsigned char b = tile[piece_at<kRowBytes>(r, d >> 4) + (d & 15)];
+    return F16::unpack(widen2(b)).x;
+  }
+  return T::unpack(*reinterpret_cast<const uint16_t*>(tile + piece_at<kRowBytes>(r, d >> 3) + 2 * (d & 7))).x;
+}
+
+template <class T, bool kF8, int D>
+__global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention_kernel(const AttnParams p) {
+  using S = Shape<kF8, D>;
+  using M = typename std::conditional<kF8, F16, T>::type;  // the products' type
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* ring = smem;
+  float* merge = reinterpret_cast<float*>(smem + (size_t)S::kStages * S::kStageBytes);
+  float* merge_ml = merge + S::kMerge / sizeof(float);
+  long long* pre = reinterpret_cast<long long*>(merge_ml + 2 * kWarps * kRows);
+  __shared__ long long warp_sum[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_sync();
+
+  // ---- the list: tiles before each request
+  bool bad = false;
+  {
+    const int chunk = (p.tk.B + kAttnThreads - 1) / kAttnThreads;
+    const int lo = min(p.tk.B, tid * chunk), hi = min(p.tk.B, lo + chunk);
+    long long mine = 0;
+    for (int b = lo; b < hi; ++b) {
+      int first, n;
+      request_tokens(p.tk, b, first, n, bad);
+      const long long rbs = ((long long)n * p.G + kRows - 1) / kRows;
+      pre[b] = mine;
+      mine += rbs * p.c.kv_heads * tiles_of(clamped_len(p, b, bad));
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    for (int b = lo; b < hi; ++b) pre[b] += before;
+    if (tid == 0) pre[p.tk.B] = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+    __syncthreads();
+  }
+  if (bad && blockIdx.x == 0) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
+  const long long total = pre[p.tk.B];
+  const long long run = max((long long)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+  if (blockIdx.x == 0) {
+    long long* hdr = reinterpret_cast<long long*>(p.ws);
+    for (int b = tid; b <= p.tk.B; b += kAttnThreads) hdr[1 + b] = pre[b];
+    if (tid == 0) hdr[0] = run;
+  }
+  const long long t_begin = (long long)blockIdx.x * run, t_end = min(total, t_begin + run);
+  if (t_begin >= t_end) return;
+
+  // ---- this warp's ring: one step = this warp's 16 keys of a tile
+  const uint32_t my_ring = smem_addr(ring) + warp * 2 * S::kHalfStage;
+  __shared__ uint32_t step_mask[kWarps][8];  // per stage: the keys that exist and have a page
+
+  Unit lu = locate(p, pre, t_begin);  // the unit being loaded
+  long long lt = t_begin;
+  int l_stage = 0;
+  uint32_t next_off = 0;
+  bool next_ok = false, bad_page = false;
+  auto look_up = [&]() {  // lane l < 16: the row of key l of step lt
+    const int key = (int)(lt - lu.start) * kTile + warp * kWarpKeys + (lane & 15);
+    next_ok = key < lu.L;
+    int page = 0, slot = 0, id = 0;
+    if (next_ok) {
+      split_position(p.c, key, page, slot);
+      id = p.c.table[(long long)lu.b * p.c.table_stride + page];
+      if (id < 0 || id >= p.c.num_pages) {
+        bad_page = true;
+        next_ok = false;
+        id = 0;
+      }
+    }
+    next_off = next_ok ? row_offset(p.c, id, lu.h, slot) : 0u;
+  };
+  look_up();
+  constexpr int kPieces = S::kRowBytes / 16;        // pieces per row
+  constexpr int kLoads = kWarpKeys * kPieces / 32;  // per lane, for K and for V each
+  auto load_step = [&]() {
+    if (lt < t_end) {
+      const uint32_t ok = __ballot_sync(0xffffffffu, next_ok);
+      const uint32_t base = my_ring + l_stage * S::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = i * 32 + lane, r = at / kPieces, c = at % kPieces;
+        const uint32_t off = __shfl_sync(0xffffffffu, next_off, r);
+        const bool take = (ok >> r) & 1u;
+        const size_t o = ((size_t)off + c) * 16u;
+        const uint32_t d = base + piece_at<S::kRowBytes>(r, c);
+        cp_async16(d, p.c.k + o, take);
+        cp_async16(d + S::kHalfStage, p.c.v + o, take);
+      }
+      if (lane == 0) step_mask[warp][l_stage] = ok;
+      ++lt;
+      if (lt < t_end) {
+        if (lt >= lu.start + lu.tiles) lu = locate(p, pre, lt);
+        look_up();
+      }
+    }
+    cp_commit();
+    l_stage = l_stage + 1 == S::kStages ? 0 : l_stage + 1;
+  };
+#pragma unroll
+  for (int s = 0; s < S::kStages - 1; ++s) load_step();
+
+  const int qr = lane >> 2, qc = lane & 3;
+  // ldmatrix source rows: K, lanes 0-15 address the keys 0-7 (two 16-byte
+  // column pieces), lanes 16-31 the keys 8-15
+  int stage = 0;
+  long long t = t_begin;
+  while (t < t_end) {
+    const Unit u = locate(p, pre, t);
+    const long long u_end = min(t_end, u.start + u.tiles);
+    // ---- this thread's two query rows
+    int row_tok[2], row_head[2], vis[2];
+    float unit_scale[2];
+    bool row_ok[2];
+    uint32_t q[D / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = u.rb * kRows + qr + 8 * e;
+      const int i = r / p.G;
+      row_ok[e] = r < u.n * p.G;
+      row_tok[e] = u.first + i;
+      row_head[e] = u.h * p.G + (r - i * p.G);
+      vis[e] = !row_ok[e] ? 0 : p.causal ? min(u.L, max(0, u.L - u.n + i + 1)) : u.L;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.q + 2 * ((long long)row_tok[e] * p.q_ts + (long long)row_head[e] * p.q_hs));
+      float mult = 1.0f;
+      if (!kF8) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[ks][e] = row_ok[e] ? src[8 * ks + qc] : 0u;
+          q[ks][2 + e] = row_ok[e] ? src[8 * ks + 4 + qc] : 0u;
+        }
+      } else {
+        // an 8-bit matrix load gives a thread four neighbouring values of a
+        // key: values 4 qc .. 4 qc + 3 of 16 stand for the product's inner
+        // indexes 2 qc, 2 qc + 1, 2 qc + 8, 2 qc + 9
+        float big = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          q[ks][e] = row_ok[e] ? src[8 * ks + 2 * qc] : 0u;
+          q[ks][2 + e] = row_ok[e] ? src[8 * ks + 2 * qc + 1] : 0u;
+          const float2 f = T::unpack(q[ks][e]), g = T::unpack(q[ks][2 + e]);
+          big = fmaxf(fmaxf(fmaxf(big, fabsf(f.x)), fabsf(f.y)), fmaxf(fabsf(g.x), fabsf(g.y)));
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // the row's largest value into [2^14, 2^15): the exponent alone,
+        // limited so that both factors stay normal numbers
+        const int ex = min(max((int)(__float_as_uint(big) >> 23) - 141, -120), 120);
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        mult = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const float2 f = T::unpack(q[ks][e]), g = T::unpack(q[ks][2 + e]);
+          q[ks][e] = F16::pack(f.x * down, f.y * down);
+          q[ks][2 + e] = F16::pack(g.x * down, g.y * down);
+        }
+      }
+      unit_scale[e] = p.scale * mult;
+      if (kF8 && p.c.k_scale) unit_scale[e] *= p.c.k_scale[u.h];
+      unit_scale[e] *= kLog2e;
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
+
+    for (; t < u_end; ++t) {
+      cp_wait<S::kStages - 2>();
+      __syncwarp();
+      load_step();  // into the stage whose step every lane has finished
+      const uint32_t kb = my_ring + stage * S::kStageBytes, vb = kb + S::kHalfStage;
+      const uint32_t ok = step_mask[warp][stage] & 0xffffu;
+      // ---- S = Q K^T
+      float s[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+      if (!kF8) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t k4[4];  // keys 0-7: inner 0-7, 8-15; keys 8-15: the same
+          ldsm4(k4, kb + piece_at<S::kRowBytes>((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+          M::mma(s[0], q[ks], k4[0], k4[1]);
+          M::mma(s[1], q[ks], k4[2], k4[3]);
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks += 2) {
+          uint32_t k4[4];  // keys 0-7: values 0-15, 16-31; keys 8-15: the same
+          ldsm4(k4, kb + piece_at<S::kRowBytes>((lane & 7) + ((lane >> 4) << 3), ks + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            M::mma(s[0], q[ks + j], widen2(k4[j]), widen2(k4[j] >> 16));
+            M::mma(s[1], q[ks + j], widen2(k4[2 + j]), widen2(k4[2 + j] >> 16));
+          }
+        }
+      }
+      // ---- scale, mask, running maximum
+      const int key0 = (int)(t - u.start) * kTile + warp * kWarpKeys;
+      const bool masked = ok != 0xffffu || key0 + kWarpKeys > u.L - (p.causal ? u.n : 0);
+      float mx[2] = {kNegInf, kNegInf};
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[nb][e] * unit_scale[e >> 1];
+          if (masked) {
+            const int kk = 8 * nb + 2 * qc + (e & 1);
+            if (!((ok >> kk) & 1u) || key0 + kk >= vis[e >> 1]) x = kNegInf;
+          }
+          s[nb][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      float keep[2];
+      bool moved = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        const float m_new = fmaxf(m[e], mx[e]);
+        moved |= m_new > m[e];
+        // no key seen yet: any finite reference will do
+        const float ref = m_new == kNegInf ? 0.0f : m_new;
+        keep[e] = ex2(m[e] - ref);
+        m[e] = m_new;
+        float sum = 0.0f;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float w = ex2(s[nb][2 * e + j] - ref);
+            s[nb][2 * e + j] = w;
+            sum += w;
+          }
+        l[e] = l[e] * keep[e] + sum;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= keep[0];
+          o[i][1] *= keep[0];
+          o[i][2] *= keep[1];
+          o[i][3] *= keep[1];
+        }
+      }
+      // ---- O += P V
+      // Under a causal mask a step may hold values that only some rows see.
+      // A product with weight 0 would turn one that is not finite into NaN,
+      // so such a step (never met in sound data) is summed key by key.
+      bool unsound = false;
+      if (masked && p.causal && u.n > 1) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(
+              ring + (vb - smem_addr(ring)) + ((size_t)(i * 32 + lane) << 4));
+          unsound |= not_finite<T, kF8>(w.x) || not_finite<T, kF8>(w.y) || not_finite<T, kF8>(w.z) ||
+                     not_finite<T, kF8>(w.w);
+        }
+        unsound = __any_sync(0xffffffffu, unsound);
+      }
+      if (unsound) {
+        const unsigned char* tile = ring + (vb - smem_addr(ring));
+#pragma unroll 1
+        for (int kk = 0; kk < kWarpKeys; ++kk) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float lo = (kk >> 3) ? s[1][2 * e] : s[0][2 * e], hi = (kk >> 3) ? s[1][2 * e + 1] : s[0][2 * e + 1];
+            w[e] = __shfl_sync(0xffffffffu, (kk & 1) ? hi : lo, (lane & ~3) + ((kk & 7) >> 1));
+            if (!((ok >> kk) & 1u) || key0 + kk >= vis[e]) w[e] = -1.0f;  // not seen
+          }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (w[e >> 1] >= 0.0f || w[e >> 1] != w[e >> 1]) {
+                const int d = kF8 ? 16 * (i >> 1) + 2 * (2 * qc + (e & 1)) + (i & 1) : 8 * i + 2 * qc + (e & 1);
+                o[i][e] += w[e >> 1] * value_at<T, kF8, S::kRowBytes>(tile, kk, d);
+              }
+        }
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+        continue;
+      }
+      const uint32_t pa[4] = {M::pack(s[0][0], s[0][1]), M::pack(s[0][2], s[0][3]), M::pack(s[1][0], s[1][1]),
+                              M::pack(s[1][2], s[1][3])};
+      if (!kF8) {
+#pragma unroll
+        for (int ds = 0; ds < D / 16; ++ds) {
+          uint32_t v4[4];  // values 0-7: keys 0-7, 8-15; values 8-15: the same
+          ldsm4t(v4, vb + piece_at<S::kRowBytes>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * ds + (lane >> 4)));
+          M::mma(o[2 * ds], pa, v4[0], v4[1]);
+          M::mma(o[2 * ds + 1], pa, v4[2], v4[3]);
+        }
+      } else {
+        // a transposed load of byte pairs: even values in bytes 0 and 2, odd
+        // ones in 1 and 3, of two neighbouring keys
+#pragma unroll
+        for (int ds = 0; ds < D / 16; ds += 2) {
+          uint32_t v4[4];  // values 0-15: keys 0-7, 8-15; values 16-31: the same
+          ldsm4t(v4, vb + piece_at<S::kRowBytes>((lane & 7) + (((lane >> 3) & 1) << 3), ds + (lane >> 4)));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            M::mma(o[2 * (ds + j)], pa, widen2(__byte_perm(v4[2 * j], 0, 0x4420)),
+                   widen2(__byte_perm(v4[2 * j + 1], 0, 0x4420)));
+            M::mma(o[2 * (ds + j) + 1], pa, widen2(__byte_perm(v4[2 * j], 0, 0x4431)),
+                   widen2(__byte_perm(v4[2 * j + 1], 0, 0x4431)));
+          }
+        }
+      }
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+
+    // ---- the unit (or this CTA's run of it) ends: join the warps
+    const long long seg_begin = max(t_begin, u.start);
+    const bool whole = seg_begin == u.start && u_end == u.start + u.tiles;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (qc == 0) {
+        merge_ml[2 * (warp * kRows + qr + 8 * e)] = m[e];
+        merge_ml[2 * (warp * kRows + qr + 8 * e) + 1] = l[e];
+      }
+    }
+    __syncthreads();
+    float mine[2];  // this warp's factor for its two rows
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = kNegInf;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, merge_ml[2 * (w * kRows + qr + 8 * e)]);
+      mine[e] = m[e] == kNegInf ? 0.0f : ex2(m[e] - top);
+    }
+    // each thread then owns row jr and columns jc .. jc + 3 of each run of 32
+    const int jr = tid >> 3, jc = (tid & 7) * 4;
+    float top = kNegInf, sum = 0.0f;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, merge_ml[2 * (w * kRows + jr)]);
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = merge_ml[2 * (w * kRows + jr)], lw = merge_ml[2 * (w * kRows + jr) + 1];
+      sum += mw != kNegInf ? lw * ex2(mw - top) : lw == lw ? 0.0f : lw;  // a NaN sum stays one
+    }
+    const int jrow = u.rb * kRows + jr, ji = jrow / p.G;
+    const bool jok = jrow < u.n * p.G;
+    const long long jtok = u.first + ji, jhead = u.h * p.G + (jrow - ji * p.G);
+    const long long slot = 2LL * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
+    float* part_o = reinterpret_cast<float*>(p.ws + ws_o(p.tk.B)) + (slot * kRows + jr) * D;
+    float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
+    if ((tid & 7) == 0 && jok) {
+      if (whole) {
+        if (p.lse) p.lse[jtok * ((long long)p.G * p.c.kv_heads) + jhead] = (top + log2f(sum)) * kLn2;
+      } else {
+        float* ml = reinterpret_cast<float*>(p.ws + ws_ml(p.tk.B)) + (slot * kRows + jr) * 2;
+        ml[0] = top;
+        ml[1] = sum;
+      }
+    }
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += S::kCols) {
+      __syncthreads();
+#pragma unroll
+      for (int nb = 0; nb < S::kCols / 8; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // columns of the accumulators: two neighbours per 8, or (8-bit) the
+          // even values of 16 in one block and the odd ones in the next
+          const int col = kF8 ? 16 * (nb >> 1) + 2 * (2 * qc + (e & 1)) + (nb & 1) : 8 * nb + 2 * qc + (e & 1);
+          merge[(warp * kRows + qr + 8 * (e >> 1)) * (S::kCols + 1) + col] = o[c0 / 8 + nb][e] * mine[e >> 1];
+        }
+      __syncthreads();
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] += merge[(w * kRows + jr) * (S::kCols + 1) + jc + j];
+      if (jok) {
+        if (whole) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + 2 * (jtok * p.o_ts + jhead * p.o_hs + c0 + jc));
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(T::pack(x[0] * factor, x[1] * factor), T::pack(x[2] * factor, x[3] * factor));
+        } else {
+          *reinterpret_cast<float4*>(part_o + c0 + jc) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+    __syncthreads();  // merge_ml is written again by the next unit
+  }
+  if (bad_page) raise_status(p.status, DFLASH_STATUS_BAD_PAGE);
+  cp_wait<0>();
+}
+
+// ---- joining the partial results of units that span CTAs -------------------------------
+// One warp per query row: the segments' maxima give their factors, then the
+// segments are summed in list order.
+constexpr int kJoinWarps = 4;
+template <class T, bool kF8, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams p) {
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31;
+  const int Hq = p.G * p.c.kv_heads;
+  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= (long long)p.tk.tokens * Hq) return;
+  const int tok = (int)(row / Hq), head = (int)(row - (long long)tok * Hq);
+  const int b = request_of_token(p.tk, tok);
+  if (b < 0 || b >= p.tk.B) return;
+  int first, n;
+  bool bad = false;
+  request_tokens(p.tk, b, first, n, bad);
+  if (tok < first || tok >= first + n) return;
+  const long long* hdr = reinterpret_cast<const long long*>(p.ws);
+  const long long run = hdr[0];
+  const int tiles = tiles_of(clamped_len(p, b, bad));
+  const int h = head / p.G, r = (tok - first) * p.G + head - h * p.G;
+  const int rbs = (int)(((long long)n * p.G + kRows - 1) / kRows);
+  const long long start = hdr[1 + b] + ((long long)h * rbs + r / kRows) * tiles;
+  const int c0 = (int)(start / run), c1 = (int)((start + tiles - 1) / run);
+  if (c0 == c1) return;  // one CTA had the whole unit and wrote it
+  const float* mls = reinterpret_cast<const float*>(p.ws + ws_ml(p.tk.B));
+  const float* os = reinterpret_cast<const float*>(p.ws + ws_o(p.tk.B));
+  const int jr = r % kRows;
+  auto slot_row = [&](int c) {
+    const long long slot = 2LL * c + (max(start, (long long)c * run) == (long long)c * run ? 0 : 1);
+    return slot * kRows + jr;
+  };
+  float top = kNegInf;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, mls[slot_row(c) * 2]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  constexpr int kPer = D / 32;
+  float x[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) x[j] = 0.0f;
+  float sum = 0.0f;
+  for (int cb = c0; cb <= c1; cb += 32) {
+    const int c = cb + lane;
+    float w = 0.0f, ls = 0.0f;
+    if (c <= c1) {
+      const float2 ml = *reinterpret_cast<const float2*>(mls + slot_row(c) * 2);
+      w = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
+      ls = ml.y == ml.y ? ml.y * w : ml.y;
+    }
+    const int cnt = min(32, c1 - cb + 1);
+#pragma unroll 4
+    for (int j = 0; j < cnt; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      sum += __shfl_sync(0xffffffffu, ls, j);
+      const float* src = os + slot_row(cb + j) * D + lane * kPer;
+      float y[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) *reinterpret_cast<float2*>(y + e) = *reinterpret_cast<const float2*>(src + e);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = fmaf(y[e], wj, x[e]);
+    }
+  }
+  float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+  if (kF8 && p.c.v_scale) factor *= p.c.v_scale[h];
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + 2 * ((long long)tok * p.o_ts + (long long)head * p.o_hs)) +
+                  lane * (kPer / 2);
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) dst[e / 2] = T::pack(x[e] * factor, x[e + 1] * factor);
+  if (lane == 0 && p.lse) p.lse[row] = (top + log2f(sum)) * kLn2;
+}
+
+template <class T, bool kF8, int D>
+int launch(const AttnParams& p, int sms, void* stream) {
+  using S = Shape<kF8, D>;
+  const size_t smem = S::kSmem + (size_t)(p.tk.B + 1) * sizeof(long long);
+  static int ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(attention_kernel<T, kF8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(S::kSmem + (kOpsMaxB + 1) * sizeof(long long)));
+    if (e != cudaSuccess) return (int)e;
+    ready[dev] = 1;
+  }
+  int grid = sms * S::kPerSm;
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = smem;
+  e = cudaLaunchKernelEx(&cfg, attention_kernel<T, kF8, D>, p);
+  if (e != cudaSuccess) return (int)e;
+  const long long rows = (long long)p.tk.tokens * p.G * p.c.kv_heads;
+  cfg.gridDim = dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
+  return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, kF8, D>, p);
+}
+
+template <class T, bool kF8>
+int pick_dim(const AttnParams& p, int d, int sms, void* stream) {
+  return d == 64    ? launch<T, kF8, 64>(p, sms, stream)
+         : d == 128 ? launch<T, kF8, 128>(p, sms, stream)
+                    : launch<T, kF8, 256>(p, sms, stream);
+}
+
+}  // namespace
+
+size_t attention_workspace(int B, int head_dim) {
+  return ws_o(B) + (size_t)kMaxCtas * 2 * kRows * head_dim * sizeof(float);
+}
+
+int launch_attention(const AttnParams& p, int dtype, int cache_dtype, int head_dim, int sms, void* stream) {
+  const bool f8 = cache_dtype == DFLASH_E4M3;
+  if (dtype == DFLASH_BF16)
+    return f8 ? pick_dim<Bf16, true>(p, head_dim, sms, stream) : pick_dim<Bf16, false>(p, head_dim, sms, stream);
+  return f8 ? pick_dim<F16, true>(p, head_dim, sms, stream) : pick_dim<F16, false>(p, head_dim, sms, stream);
+}
+
+}  // namespace dflash
