@@ -74,14 +74,15 @@ struct DistillParams {
   const float* upstream;  // per row, or null (backward only)
   float inv_t;
   float* loss;
-  float* lse;  // forward: written (or null); backward: read
+  float* lse;  // [rows, 2] statistics; forward: written (or null); backward: read
   unsigned char* grad;
   long long grad_stride;
   uint32_t* status;
 };
 constexpr int kMaxTeacher = 256;
+constexpr int kMaxDistillRows = 1 << 26;  // times 16 CTAs, below 2^31
 int launch_distill_loss(const DistillParams& p, int dtype, int sms, void* stream);
-int launch_distill_grad(const DistillParams& p, int dtype, int sms, void* stream);
+int launch_distill_grad(const DistillParams& p, int dtype, void* stream);
 int launch_distill_loss_grad(const DistillParams& p, int dtype, int sms, void* stream);
 
 }  // namespace dflash

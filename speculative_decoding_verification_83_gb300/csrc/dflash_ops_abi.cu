@@ -119,7 +119,8 @@ int check_rows(const void* p, int64_t token_stride, int64_t head_stride, const c
 int check_distill(const void* student, int64_t stride, int rows, int V, int dtype, const int32_t* ids,
                   const float* teacher, int K, float temperature) {
   if (!student || !ids || !teacher) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
-  if (rows < 0) return fail(DFLASH_ERR_INVALID_ARG, "rows=%d must not be negative", rows);
+  if (rows < 0 || rows > kMaxDistillRows)
+    return fail(DFLASH_ERR_INVALID_ARG, "rows=%d outside [0, %d]", rows, kMaxDistillRows);
   if (V < 1) return fail(DFLASH_ERR_INVALID_ARG, "V=%d must be >= 1", V);
   if (K < 1 || K > kMaxTeacher) return fail(DFLASH_ERR_INVALID_ARG, "K=%d outside [1, %d]", K, kMaxTeacher);
   if (dtype != DFLASH_BF16 && dtype != DFLASH_F32)
@@ -289,9 +290,7 @@ int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V
   p.lse = const_cast<float*>(lse);
   p.grad = static_cast<unsigned char*>(grad);
   p.grad_stride = grad_stride;
-  int sms = 0;
-  if ((rc = sms_here(&sms))) return rc;
-  return launched(launch_distill_grad(p, dtype, sms, stream), "the distillation gradient");
+  return launched(launch_distill_grad(p, dtype, stream), "the distillation gradient");
 }
 
 int dflash_distill_loss_grad(const void* student, int64_t row_stride, int rows, int V, int dtype,
