@@ -15,15 +15,22 @@
 // - R is one rounded multiply-add. All sums are fp32.
 //
 // What bounds it: reading the logits and writing the gradient, once each. A row
-// is dealt out to a cluster of up to 16 CTAs. Each moves its slice into shared
-// memory by bulk copies, reduces the pieces as they land (a running reference
-// per thread), sends its (R, s) to the other CTAs through distributed shared
-// memory, and writes the gradient from the slice it still holds. Three CTAs
-// share an SM, so that one's copies and stores fill the time of another's
-// reductions and barriers. What does not fit in shared memory (rows of
-// several MB) is read again. The teacher's K entries are one warp's work while
-// the logits arrive. Per logit about 7 instructions: maxima and multiply-adds
-// work on pairs.
+// is dealt out to a cluster of a few CTAs. Each moves the first 70 KB of its
+// slice into shared memory by bulk copies, reduces the pieces as they land (a
+// running reference per thread), then the rest as it streams by; it sends its
+// (R, s) to the other CTAs through distributed shared memory and writes the
+// gradient, from shared memory and, for the rest, from L2, where the logits
+// just read still are. Three CTAs share an SM, so that one's copies and stores
+// fill the time of another's reductions and barriers: that counts for more
+// than holding whole slices. Measured at 1920 x 248320 bf16, loss and
+// gradient: clusters of 4 with 70 KB held 342 us (5.57 TB/s, 83% of a copy's
+// measured rate), of 8 with whole slices held 406 us, of 2 453 us (more CTAs
+// per row wait for their slowest, fewer read more again), of 4 with 110 KB and
+// two CTAs an SM 583 us. The loss alone holds nothing back, and fewer CTAs per
+// row are better: 158 us (6.0 TB/s) with 2, 182 us with 4. The teacher's K
+// entries are one warp's work while the logits arrive. Per logit about 8
+// instructions: maxima and multiply-adds work on pairs. The gradient alone
+// (the backward call) is a plain stream: 306 us there (6.2 TB/s).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -34,9 +41,9 @@
 namespace dflash {
 namespace {
 
-constexpr int kMaxSplit = 16;       // CTAs per row
+constexpr int kMaxSplit = 8;         // CTAs per row
 constexpr int kPieces = 4;          // bulk copies of a slice
-constexpr int kMaxHeld = 192 * 1024;  // bytes of a slice kept in shared memory
+constexpr int kMaxHeld = 70 * 1024;  // bytes of a slice kept in shared memory: three fit an SM
 constexpr float kLog2eD = 1.4426950408889634f;
 constexpr float kLn2D = 0.6931471805599453f;
 
@@ -347,7 +354,8 @@ __device__ __forceinline__ void parts_ready(bool wait) {
 // kThreads threads work on the slice; one more warp takes the teacher's
 // entries, whose two dependent loads would otherwise hold up a barrier.
 template <class T, int kThreads, bool kGrad>
-__global__ void __launch_bounds__(kThreads + 32, 1536 / (kThreads + 32)) loss_kernel(const DistillParams p, int split, int held) {
+__global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
+    loss_kernel(const DistillParams p, int split, int held) {
   constexpr int kW = kThreads / 32;
   extern __shared__ __align__(128) unsigned char slice_mem[];
   __shared__ Teacher S;
@@ -537,8 +545,6 @@ int launch_split(const DistillParams& p, int split, int held, void* stream) {
   if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
   if (!ready[dev]) {
     e = cudaFuncSetAttribute(loss_kernel<T, kThreads, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxHeld);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(loss_kernel<T, kThreads, kGrad>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return (int)e;
     ready[dev] = true;
   }
@@ -548,19 +554,19 @@ int launch_split(const DistillParams& p, int split, int held, void* stream) {
   return (int)cudaLaunchKernelEx(&cfg, loss_kernel<T, kThreads, kGrad>, p, split, held);
 }
 
-// CTAs per row: enough that three slices fit an SM's shared memory (64 KB
-// each), and, where the rows alone would leave SMs idle, up to 8 with at
-// least 8 KB each.
+// CTAs per row: slices of at most 128 KB (256 KB for the loss alone), and,
+// where the rows alone would leave SMs idle, up to 8 CTAs with at least 8 KB
+// each. Slices of up to 16 KB take 128 threads, of which 9 CTAs fit an SM.
 template <class T, bool kGrad>
 int launch_loss(const DistillParams& p, int sms, void* stream) {
   const long long bytes = (long long)p.V * T::kBytes;
   int split = 1;
-  while (split < kMaxSplit && bytes > split * 65536LL) split *= 2;
-  while (split < 8 && (long long)p.rows * split < 2LL * sms && bytes / (2 * split) >= 8192) split *= 2;
+  while (split < kMaxSplit && bytes > split * (kGrad ? 131072LL : 262144LL)) split *= 2;
+  while (split < kMaxSplit && (long long)p.rows * split < 2LL * sms && bytes / (2 * split) >= 8192) split *= 2;
   const long long slice = ((bytes + split - 1) / split + 31) / 16 * 16;
   const int held = slice < kMaxHeld ? (int)slice : kMaxHeld;
-  return held <= 16384 ? launch_split<T, 96, kGrad>(p, split, held, stream)
-                       : launch_split<T, 480, kGrad>(p, split, held, stream);
+  return slice <= 16384 ? launch_split<T, 96, kGrad>(p, split, held, stream)
+                        : launch_split<T, 352, kGrad>(p, split, held, stream);
 }
 
 template <class T>

@@ -80,7 +80,7 @@ struct DistillParams {
   uint32_t* status;
 };
 constexpr int kMaxTeacher = 256;
-constexpr int kMaxDistillRows = 1 << 26;  // times 16 CTAs, below 2^31
+constexpr int kMaxDistillRows = 1 << 27;  // times 8 CTAs, below 2^31
 int launch_distill_loss(const DistillParams& p, int dtype, int sms, void* stream);
 int launch_distill_grad(const DistillParams& p, int dtype, void* stream);
 int launch_distill_loss_grad(const DistillParams& p, int dtype, int sms, void* stream);
