@@ -12,10 +12,10 @@ the kernels behind ``include/dflash_verify.h``.
 from __future__ import annotations
 
 import ctypes
+import struct
 from fractions import Fraction
 
-from . import (DFLASH_BF16, DFLASH_F32, ERR_INVALID_ARG, DFlashError, _check, _dev, _on, _shape,
-               _status_ok, _stream_ptr, _torch, load)
+from . import DFLASH_BF16, DFLASH_F32, ERR_INVALID_ARG, DFlashError, _check, _dev, _on, _shape, _torch, load
 
 DFLASH_F16, DFLASH_E4M3 = 2, 3
 STATUS_BAD_PAGE, STATUS_BAD_LENGTH = 16, 32
@@ -33,27 +33,70 @@ class _CacheStruct(ctypes.Structure):
                 ("max_pages", ctypes.c_int32)]
 
 
-def _token_dtype(t) -> int:
+_pack4, _pack8 = struct.Struct("4q").pack, struct.Struct("8q").pack  # strides, as the library reads them
+
+
+def _raw_stream(stream, device) -> int:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return DFLASH_BF16
-    if t.dtype == torch.float16:
-        return DFLASH_F16
-    raise TypeError(f"tokens must be bfloat16 or float16, got {t.dtype}")
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _rows(t, name, heads, dim, like=None):
-    """A [tokens, heads, dim] view whose last dimension is contiguous."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+def _token_dtype(t, cache, what) -> int:
+    torch = _torch()
+    dt = t.dtype
+    if dt == torch.bfloat16:
+        code = DFLASH_BF16
+    elif dt == torch.float16:
+        code = DFLASH_F16
+    else:
+        raise TypeError(f"{what} must be bfloat16 or float16, got {dt}")
+    if cache.code != code and cache.code != DFLASH_E4M3:
+        raise TypeError(f"a {cache.dtype} cache takes no {dt} {what}")
+    return code
+
+
+def _rows(t, name, heads, dim, device, like=None):
+    """Data pointer, token stride and head stride of a [tokens, heads, dim] view
+    whose last dimension is contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have shape [tokens, {'heads' if heads is None else heads}, {dim}], "
-                         f"got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.stride(2) != 1:
+                         f"got {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    ts, hs, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device or t.shape[0] != like.shape[0]):
-        raise ValueError(f"{name} must match the tokens' dtype, device and count")
+    if like is not None and (t.dtype != like.dtype or shape[0] != like.shape[0]):
+        raise ValueError(f"{name} must match the tokens' dtype and count")
+    return t.data_ptr(), ts, hs
+
+
+def _vector(t, n, name, dtype, device):
+    """Data pointer of a contiguous [n] tensor, None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (n,):
+        raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on {device}")
+    if n > 1 and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _status_word(status, device):
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32 word")
+    if status.device != device:
+        raise ValueError(f"status is on {status.device}, the call's tensors on {device}")
+    return _dev(status, "status", _torch().int32)
 
 
 class PagedCache:
@@ -94,6 +137,7 @@ class PagedCache:
                          None if v_scale is None else v_scale.data_ptr(),
                          k.stride(0), k.stride(1), k.stride(2), page_table.stride(0), self.pages, self.page_size,
                          self.heads, self.head_dim, codes[k.dtype], self.batch, self.max_pages)
+        self.code = codes[k.dtype]
         self._struct = s
         self._ref = ctypes.byref(s)
         self._ws_bytes = load().dflash_attention_workspace_bytes(self.batch, self.head_dim)
@@ -119,14 +163,10 @@ def rope_phases(inv_freq, device=None):
 
 def _packed(cache, n_tokens, lens, lens_name, q_start):
     torch = _torch()
-    _shape(lens, (cache.batch,), lens_name)
-    _on(cache.device, **{lens_name: lens, "q_start": q_start})
-    if q_start is not None:
-        _shape(q_start, (cache.batch + 1,), "q_start")
-        return _dev(lens, lens_name, torch.int32), _dev(q_start, "q_start", torch.int32)
-    if n_tokens % cache.batch:
+    if q_start is None and n_tokens % cache.batch:
         raise ValueError(f"{n_tokens} tokens do not divide evenly over {cache.batch} requests: q_start is needed")
-    return _dev(lens, lens_name, torch.int32), None
+    return (_vector(lens, cache.batch, lens_name, torch.int32, cache.device),
+            _vector(q_start, cache.batch + 1, "q_start", torch.int32, cache.device))
 
 
 def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases=None, interleaved=False,
@@ -138,38 +178,31 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     are packed at ``q_start`` [batch + 1] int32, or tokens / batch each. Returns
     the rotated q (a new tensor, or ``q_out``, which may be ``q``), or None."""
     torch = _torch()
-    dt = _token_dtype(k)
-    if k.device != cache.device:
-        raise ValueError(f"k is on {k.device}, the cache on {cache.device}")
-    if cache.dtype != k.dtype and cache.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"a {cache.dtype} cache takes no {k.dtype} tokens")
-    n, D = k.shape[0], cache.head_dim
-    pk, pv = _rows(k, "k", cache.heads, D), _rows(v, "v", cache.heads, D, k)
+    dev, D = cache.device, cache.head_dim
+    dt = _token_dtype(k, cache, "tokens")
+    pk, kt, kh = _rows(k, "k", cache.heads, D, dev)
+    pv, vt, vh = _rows(v, "v", cache.heads, D, dev, k)
+    n = k.shape[0]
     pq = po = None
-    hq = 0
-    st = [k.stride(0), k.stride(1), v.stride(0), v.stride(1), 0, 0, 0, 0]
+    hq = qt = qh = ot = oh = 0
     if q is not None:
-        pq, hq = _rows(q, "q", None, D, k), q.shape[1]
+        pq, qt, qh = _rows(q, "q", None, D, dev, k)
+        hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n, hq, D), dtype=q.dtype, device=q.device)
-        po = _rows(q_out, "q_out", hq, D, q)
-        st[4:] = q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1)
+            q_out = torch.empty((n, hq, D), dtype=q.dtype, device=dev)
+        po, ot, oh = _rows(q_out, "q_out", hq, D, dev, q)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     lens, starts = _packed(cache, n, cached_lens, "cached_lens", q_start)
     rot = 0
     if phases is not None:
-        _on(cache.device, phases=phases)
         if phases.dim() != 1:
             raise ValueError("phases must be one-dimensional")
-        rot = 2 * phases.numel()
-        phases = _dev(phases, "phases", torch.int64)
-    _status_ok(status)
-    _on(cache.device, status=status)
-    _check(load().dflash_kv_append(cache._ref, pk, pv, pq, po, dt, n, hq, (ctypes.c_int64 * 8)(*st), lens, starts,
-                                   phases, rot, int(bool(interleaved)),
-                                   None if status is None else _dev(status, "status", torch.int32),
-                                   _stream_ptr(stream, cache.device)))
+        rot = 2 * phases.shape[0]
+        phases = _vector(phases, phases.shape[0], "phases", torch.int64, dev)
+    _check(load().dflash_kv_append(cache._ref, pk, pv, pq, po, dt, n, hq, _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens,
+                                   starts, phases, rot, 1 if interleaved else 0, _status_word(status, dev),
+                                   _raw_stream(stream, dev)))
     return q_out
 
 
@@ -190,74 +223,81 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     a uint8 tensor of ``attention_workspace_bytes``; None takes one from
     torch's allocator for the call."""
     torch = _torch()
-    dt = _token_dtype(q)
-    dev = cache.device
-    if q.device != dev:
-        raise ValueError(f"q is on {q.device}, the cache on {dev}")
-    if cache.dtype != q.dtype and cache.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"a {cache.dtype} cache takes no {q.dtype} queries")
-    D = cache.head_dim
-    pq = _rows(q, "q", None, D)
-    n, hq = q.shape[0], q.shape[1]
+    dev, D = cache.device, cache.head_dim
+    dt = _token_dtype(q, cache, "queries")
+    pq, qt, qh = _rows(q, "q", None, D, dev)
+    n, hq, _ = q.shape
     if out is None:
         out = torch.empty((n, hq, D), dtype=q.dtype, device=dev)
-    po = _rows(out, "out", hq, D, q)
-    if return_lse and lse is None:
-        lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
+    po, ot, oh = _rows(out, "out", hq, D, dev, q)
+    pl = None
     if lse is not None:
         _shape(lse, (n, hq), "lse")
         _on(dev, lse=lse)
+        pl = _dev(lse, "lse", torch.float32)
+    elif return_lse:
+        lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
+        pl = lse.data_ptr()
     lens, starts = _packed(cache, n, kv_lens, "kv_lens", q_start)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
     if workspace is None:
         if stream is None:
             workspace = torch.empty((cache._ws_bytes,), dtype=torch.uint8, device=dev)
         else:  # the allocator orders memory by the stream it is taken on
             with torch.cuda.stream(stream):
                 workspace = torch.empty((cache._ws_bytes,), dtype=torch.uint8, device=dev)
+        ws, ws_bytes = workspace.data_ptr(), cache._ws_bytes
     else:
         _on(dev, workspace=workspace)
-    _status_ok(status)
-    _on(dev, status=status)
+        ws, ws_bytes = _dev(workspace, "workspace", torch.uint8), workspace.numel()
     _check(load().dflash_paged_attention(
-        cache._ref, pq, po, None if lse is None else _dev(lse, "lse", torch.float32), dt, n, hq,
-        (ctypes.c_int64 * 4)(q.stride(0), q.stride(1), out.stride(0), out.stride(1)), lens, starts,
-        float(D ** -0.5 if scale is None else scale), int(bool(causal)),
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(),
-        None if status is None else _dev(status, "status", torch.int32), s.cuda_stream))
+        cache._ref, pq, po, pl, dt, n, hq, _pack4(qt, qh, ot, oh), lens, starts, D ** -0.5 if scale is None else scale,
+        1 if causal else 0, ws, ws_bytes, _status_word(status, dev), _raw_stream(stream, dev)))
     return (out, lse) if return_lse else out
 
 
 # ---- distillation ------------------------------------------------------------------------
-def _distill_args(student, ids, teacher, row_weight, status):
+def _distill_args(student, ids, teacher, row_weight):
     torch = _torch()
-    if student.dtype == torch.bfloat16:
-        dt = DFLASH_BF16
-    elif student.dtype == torch.float32:
-        dt = DFLASH_F32
+    dt = student.dtype
+    if dt == torch.bfloat16:
+        code = DFLASH_BF16
+    elif dt == torch.float32:
+        code = DFLASH_F32
     else:
-        raise TypeError(f"student logits must be bfloat16 or float32, got {student.dtype}")
+        raise TypeError(f"student logits must be bfloat16 or float32, got {dt}")
     if student.dim() != 2 or not student.is_cuda:
         raise ValueError("student logits must be a [rows, V] CUDA tensor")
-    if student.shape[1] > 1 and student.stride(1) != 1:
+    N, V = student.shape
+    ts, one = student.stride()
+    if V > 1 and one != 1:
         raise ValueError("student logits: rows must be contiguous")
-    N = student.shape[0]
-    if ids.dim() != 2 or ids.shape[0] != N:
-        raise ValueError(f"teacher_ids must have shape [{N}, K], got {tuple(ids.shape)}")
-    _shape(teacher, tuple(ids.shape), "teacher_logits")
-    if row_weight is not None:
-        _shape(row_weight, (N,), "row_weight")
-    _status_ok(status)
-    _on(student.device, teacher_ids=ids, teacher_logits=teacher, row_weight=row_weight, status=status)
-    return (student.data_ptr(), student.stride(0), N, student.shape[1], dt, _dev(ids, "teacher_ids", torch.int32),
-            _dev(teacher, "teacher_logits", torch.float32), ids.shape[1]), (
-        None if row_weight is None else _dev(row_weight, "row_weight", torch.float32))
+    dev, shape = student.device, ids.shape
+    if len(shape) != 2 or shape[0] != N:
+        raise ValueError(f"teacher_ids must have shape [{N}, K], got {tuple(shape)}")
+    if teacher.shape != shape:
+        raise ValueError(f"teacher_logits must have shape {tuple(shape)}, got {tuple(teacher.shape)}")
+    if ids.device != dev or teacher.device != dev:
+        raise ValueError(f"the teacher's tensors must be on the student's {dev}")
+    return (student.data_ptr(), ts, N, V, code, _dev(ids, "teacher_ids", torch.int32),
+            _dev(teacher, "teacher_logits", torch.float32), shape[1]), _vector(row_weight, N, "row_weight",
+                                                                                torch.float32, dev)
 
 
 def _no_grad_inputs(teacher, row_weight):
     for t, name in ((teacher, "teacher_logits"), (row_weight, "row_weight")):
         if t is not None and t.requires_grad:
             raise ValueError(f"{name} has no gradient here: detach it")
+
+
+def _loss(student, ids, teacher, temperature, row_weight, status, keep):
+    torch = _torch()
+    head, w = _distill_args(student, ids, teacher, row_weight)
+    dev = student.device
+    loss = torch.empty((head[2],), dtype=torch.float32, device=dev)
+    stats = torch.empty((head[2], 2), dtype=torch.float32, device=dev) if keep else None
+    _check(load().dflash_distill_loss(*head, temperature, w, loss.data_ptr(), stats.data_ptr() if keep else None,
+                                      _status_word(status, dev), _raw_stream(None, dev)))
+    return loss, stats
 
 
 _function = None
@@ -273,14 +313,7 @@ def _distill_function():
     class DistillLoss(torch.autograd.Function):
         @staticmethod
         def forward(ctx, student, ids, teacher, temperature, row_weight, status):
-            head, w = _distill_args(student, ids, teacher, row_weight, status)
-            loss = torch.empty((student.shape[0],), dtype=torch.float32, device=student.device)
-            keep = student.requires_grad
-            stats = torch.empty((student.shape[0], 2), dtype=torch.float32, device=student.device) if keep else None
-            _check(load().dflash_distill_loss(*head, temperature, w, loss.data_ptr(),
-                                              None if stats is None else stats.data_ptr(),
-                                              None if status is None else _dev(status, "status", torch.int32),
-                                              _stream_ptr(None, student.device)))
+            loss, stats = _loss(student, ids, teacher, temperature, row_weight, status, True)
             ctx.temperature = temperature
             ctx.save_for_backward(student, ids, teacher, row_weight, stats)
             return loss
@@ -289,12 +322,13 @@ def _distill_function():
         @torch.autograd.function.once_differentiable
         def backward(ctx, upstream):
             student, ids, teacher, row_weight, stats = ctx.saved_tensors
-            head, w = _distill_args(student, ids, teacher, row_weight, None)
-            upstream = upstream.contiguous().float()
-            grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+            head, w = _distill_args(student, ids, teacher, row_weight)
+            if not upstream.is_contiguous():
+                upstream = upstream.contiguous()
+            dev = student.device
+            grad = torch.empty(student.shape, dtype=student.dtype, device=dev)
             _check(load().dflash_distill_grad(*head, ctx.temperature, w, stats.data_ptr(), upstream.data_ptr(),
-                                              grad.data_ptr(), grad.stride(0),
-                                              _stream_ptr(None, student.device)))
+                                              grad.data_ptr(), head[3], _raw_stream(None, dev)))
             return grad, None, None, None, None, None
 
     _function = DistillLoss
@@ -309,6 +343,8 @@ def distill_loss(student, teacher_ids, teacher_logits, temperature: float = 1.0,
     losses [rows] fp32, differentiable in ``student``. Runs on the current
     stream."""
     _no_grad_inputs(teacher_logits, row_weight)
+    if not (student.requires_grad and _torch().is_grad_enabled()):
+        return _loss(student, teacher_ids, teacher_logits, float(temperature), row_weight, status, False)[0]
     return _distill_function().apply(student, teacher_ids, teacher_logits, float(temperature), row_weight, status)
 
 
@@ -320,20 +356,22 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
     training loops that carry the gradient on themselves, without autograd."""
     torch = _torch()
     _no_grad_inputs(teacher_logits, row_weight)
-    head, w = _distill_args(student, teacher_ids, teacher_logits, row_weight, status)
-    dev = student.device
-    loss = torch.empty((student.shape[0],), dtype=torch.float32, device=dev)
+    head, w = _distill_args(student, teacher_ids, teacher_logits, row_weight)
+    N, V, dev = head[2], head[3], student.device
+    loss = torch.empty((N,), dtype=torch.float32, device=dev)
+    gs = V
     if grad is None:
-        grad = torch.empty(student.shape, dtype=student.dtype, device=dev)
+        grad = torch.empty((N, V), dtype=student.dtype, device=dev)
     else:
-        _shape(grad, tuple(student.shape), "grad")
+        _shape(grad, (N, V), "grad")
         _on(dev, grad=grad)
-        if grad.dtype != student.dtype or (grad.shape[1] > 1 and grad.stride(1) != 1):
+        gs, one = grad.stride()
+        if grad.dtype != student.dtype or (V > 1 and one != 1):
             raise ValueError("grad must have the student's dtype and contiguous rows")
-    _check(load().dflash_distill_loss_grad(*head, float(temperature), w, loss.data_ptr(), grad.data_ptr(),
-                                           max(grad.stride(0), grad.shape[1]) if grad.shape[0] <= 1 else grad.stride(0),
-                                           None if status is None else _dev(status, "status", torch.int32),
-                                           _stream_ptr(stream, dev)))
+        if N <= 1:
+            gs = max(gs, V)
+    _check(load().dflash_distill_loss_grad(*head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
+                                           _status_word(status, dev), _raw_stream(stream, dev)))
     return loss, grad
 
 
