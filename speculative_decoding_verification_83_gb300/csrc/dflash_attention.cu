@@ -35,7 +35,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "dflash_paged.cuh"
+#include "dflash_attention.cuh"
 
 namespace dflash {
 namespace {
@@ -46,34 +46,13 @@ constexpr int kWarpKeys = 16;
 constexpr int kTile = kWarps * kWarpKeys;  // keys per tile
 constexpr int kRows = 16;                  // query rows per unit
 constexpr int kMaxCtas = 640;              // CTAs whose partial results the workspace holds
-constexpr int kMinRun = 4;                 // tiles a CTA takes at least (256 keys)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegInf = -INFINITY;
 
-// ---- workspace ------------------------------------------------------------------------
-// [0] tiles per CTA, [1 .. B + 1] tiles before each request (64-bit), then per
-// CTA two slots of partial results: kRows x (maximum, sum), then kRows x D.
-__host__ __device__ inline size_t ws_header(int B) { return ((size_t)(B + 2) * 8 + 255) & ~(size_t)255; }
-__host__ __device__ inline size_t ws_ml(int B) { return ws_header(B); }
-__host__ __device__ inline size_t ws_o(int B) {
-  return ws_header(B) + (size_t)kMaxCtas * 2 * kRows * 2 * sizeof(float);
-}
+__host__ __device__ inline AttnGeometry warp_geometry() { return {kRows, kTile, kMaxCtas}; }
 
 struct Unit {
   int b, h, rb, L, first, n, tiles;
   long long start;  // index of its first tile in the whole list
 };
-
-__device__ __forceinline__ int clamped_len(const AttnParams& p, int b, bool& bad) {
-  const int L = p.lens[b];
-  const long long cap = (long long)p.c.max_pages * p.c.page_size;
-  const int top = cap < 0x7fffffffLL - kTile ? (int)cap : 0x7fffffff - kTile;
-  const int c = min(max(L, 0), top);
-  bad |= c != L;
-  return c;
-}
-__device__ __forceinline__ int tiles_of(int L) { return max(1, (L + kTile - 1) / kTile); }
 
 // The unit that tile t of the list belongs to (pre: tiles before each request).
 __device__ __forceinline__ Unit locate(const AttnParams& p, const long long* pre, long long t) {
@@ -90,8 +69,8 @@ __device__ __forceinline__ Unit locate(const AttnParams& p, const long long* pre
   bool bad = false;
   request_tokens(p.tk, lo, u.first, u.n, bad);
   u.L = clamped_len(p, lo, bad);
-  u.tiles = tiles_of(u.L);
-  const int rbs = (int)(((long long)u.n * p.G + kRows - 1) / kRows);
+  u.tiles = tiles_of<kTile>(u.L);
+  const int rbs = row_blocks<kRows>(u.n, p.G);
   const long long k = (t - pre[lo]) / u.tiles;
   u.h = (int)(k / rbs);
   u.rb = (int)(k - (long long)u.h * rbs);
@@ -119,11 +98,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // two e4m3 values (the low 16 bits) as two f16 values
 __device__ __forceinline__ uint32_t widen2(uint32_t v) {
@@ -195,9 +169,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     for (int b = lo; b < hi; ++b) {
       int first, n;
       request_tokens(p.tk, b, first, n, bad);
-      const long long rbs = ((long long)n * p.G + kRows - 1) / kRows;
       pre[b] = mine;
-      mine += rbs * p.c.kv_heads * tiles_of(clamped_len(p, b, bad));
+      mine += (long long)row_blocks<kRows>(n, p.G) * p.c.kv_heads * tiles_of<kTile>(clamped_len(p, b, bad));
     }
     long long incl = mine;
 #pragma unroll
@@ -520,14 +493,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     const bool jok = jrow < u.n * p.G;
     const long long jtok = u.first + ji, jhead = u.h * p.G + (jrow - ji * p.G);
     const long long slot = 2LL * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
-    float* part_o = reinterpret_cast<float*>(p.ws + ws_o(p.tk.B)) + (slot * kRows + jr) * D;
+    float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry().o(p.tk.B)) + (slot * kRows + jr) * D;
     float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     if ((tid & 7) == 0 && jok) {
       if (whole) {
         if (p.lse) p.lse[jtok * ((long long)p.G * p.c.kv_heads) + jhead] = (top + log2f(sum)) * kLn2;
       } else {
-        float* ml = reinterpret_cast<float*>(p.ws + ws_ml(p.tk.B)) + (slot * kRows + jr) * 2;
+        float* ml = reinterpret_cast<float*>(p.ws + warp_geometry().ml(p.tk.B)) + (slot * kRows + jr) * 2;
         ml[0] = top;
         ml[1] = sum;
       }
@@ -570,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
 // segments are summed in list order.
 constexpr int kJoinWarps = 4;
 template <class T, bool kF8, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams p, const AttnGeometry geo) {
   grid_dependency_sync();
   const int lane = threadIdx.x & 31;
   const int Hq = p.G * p.c.kv_heads;
@@ -585,18 +558,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams 
   if (tok < first || tok >= first + n) return;
   const long long* hdr = reinterpret_cast<const long long*>(p.ws);
   const long long run = hdr[0];
-  const int tiles = tiles_of(clamped_len(p, b, bad));
+  const int tiles = max(1, (clamped_len(p, b, bad) + geo.tile - 1) / geo.tile);
   const int h = head / p.G, r = (tok - first) * p.G + head - h * p.G;
-  const int rbs = (int)(((long long)n * p.G + kRows - 1) / kRows);
-  const long long start = hdr[1 + b] + ((long long)h * rbs + r / kRows) * tiles;
+  const int rbs = (int)(((long long)n * p.G + geo.rows - 1) / geo.rows);
+  const long long start = hdr[1 + b] + ((long long)h * rbs + r / geo.rows) * tiles;
   const int c0 = (int)(start / run), c1 = (int)((start + tiles - 1) / run);
   if (c0 == c1) return;  // one CTA had the whole unit and wrote it
-  const float* mls = reinterpret_cast<const float*>(p.ws + ws_ml(p.tk.B));
-  const float* os = reinterpret_cast<const float*>(p.ws + ws_o(p.tk.B));
-  const int jr = r % kRows;
+  const float* mls = reinterpret_cast<const float*>(p.ws + geo.ml(p.tk.B));
+  const float* os = reinterpret_cast<const float*>(p.ws + geo.o(p.tk.B));
+  const int jr = r % geo.rows;
   auto slot_row = [&](int c) {
     const long long slot = 2LL * c + (max(start, (long long)c * run) == (long long)c * run ? 0 : 1);
-    return slot * kRows + jr;
+    return slot * geo.rows + jr;
   };
   float top = kNegInf;
   for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, mls[slot_row(c) * 2]);
@@ -666,11 +639,7 @@ int launch(const AttnParams& p, int sms, void* stream) {
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, attention_kernel<T, kF8, D>, p);
   if (e != cudaSuccess) return (int)e;
-  const long long rows = (long long)p.tk.tokens * p.G * p.c.kv_heads;
-  cfg.gridDim = dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.dynamicSmemBytes = 0;
-  return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, kF8, D>, p);
+  return launch_join(p, warp_geometry(), std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, kF8, D, stream);
 }
 
 template <class T, bool kF8>
@@ -680,14 +649,47 @@ int pick_dim(const AttnParams& p, int d, int sms, void* stream) {
                     : launch<T, kF8, 256>(p, sms, stream);
 }
 
-}  // namespace
-
-size_t attention_workspace(int B, int head_dim) {
-  return ws_o(B) + (size_t)kMaxCtas * 2 * kRows * head_dim * sizeof(float);
+template <class T, bool kF8, int D>
+int launch_join_dim(const AttnParams& p, const AttnGeometry& g, void* stream) {
+  const long long rows = (long long)p.tk.tokens * p.G * p.c.kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.gridDim = dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, kF8, D>, p, g);
+}
+template <class T, bool kF8>
+int launch_join_type(const AttnParams& p, const AttnGeometry& g, int d, void* stream) {
+  return d == 64    ? launch_join_dim<T, kF8, 64>(p, g, stream)
+         : d == 128 ? launch_join_dim<T, kF8, 128>(p, g, stream)
+                    : launch_join_dim<T, kF8, 256>(p, g, stream);
 }
 
+}  // namespace
+
+int launch_join(const AttnParams& p, const AttnGeometry& g, int dtype, bool f8, int head_dim, void* stream) {
+  if (dtype == DFLASH_BF16)
+    return f8 ? launch_join_type<Bf16, true>(p, g, head_dim, stream) : launch_join_type<Bf16, false>(p, g, head_dim, stream);
+  return f8 ? launch_join_type<F16, true>(p, g, head_dim, stream) : launch_join_type<F16, false>(p, g, head_dim, stream);
+}
+
+size_t attention_workspace(int B, int head_dim) {
+  const size_t a = warp_geometry().bytes(B, head_dim), b = tc_geometry(128, head_dim).bytes(B, head_dim);
+  return a > b ? a : b;
+}
+
+// Query rows that share a key/value head, per request on average: up to 16 go
+// to the warps' own products, more to the tensor-memory kernel.
 int launch_attention(const AttnParams& p, int dtype, int cache_dtype, int head_dim, int sms, void* stream) {
   const bool f8 = cache_dtype == DFLASH_E4M3;
+  const long long rows = (((long long)p.tk.tokens + p.tk.B - 1) / p.tk.B) * p.G;
+  if (!f8 && rows > 16)
+    return launch_attention_tc(p, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, dtype, head_dim, sms, stream);
   if (dtype == DFLASH_BF16)
     return f8 ? pick_dim<Bf16, true>(p, head_dim, sms, stream) : pick_dim<Bf16, false>(p, head_dim, sms, stream);
   return f8 ? pick_dim<F16, true>(p, head_dim, sms, stream) : pick_dim<F16, false>(p, head_dim, sms, stream);

@@ -1,0 +1,62 @@
+// dflash_attention.cuh -- what the two attention kernels share: the list of
+// work, the workspace of partial results, and the kernel that joins them.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "dflash_paged.cuh"
+
+namespace dflash {
+
+constexpr int kMinRun = 4;  // tiles a CTA takes at least
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A unit of work is (request, key/value head, `rows` query rows) over all of
+// the request's keys, `tile` at a time; units follow each other request by
+// request, head by head, row block by row block.
+//
+// Workspace: [0] tiles per CTA, [1 .. B + 1] tiles before each request
+// (64-bit); then for each CTA two slots of partial results, rows x (maximum,
+// sum), then rows x D.
+struct AttnGeometry {
+  int rows, tile, ctas;
+  __host__ __device__ static size_t header(int B) { return ((size_t)(B + 2) * 8 + 255) & ~(size_t)255; }
+  __host__ __device__ size_t ml(int B) const { return header(B); }
+  __host__ __device__ size_t o(int B) const { return header(B) + (size_t)ctas * 2 * rows * 2 * sizeof(float); }
+  __host__ __device__ size_t bytes(int B, int D) const { return o(B) + (size_t)ctas * 2 * rows * D * sizeof(float); }
+};
+
+__device__ __forceinline__ int clamped_len(const AttnParams& p, int b, bool& bad) {
+  const int L = p.lens[b];
+  const long long cap = (long long)p.c.max_pages * p.c.page_size;
+  const int top = cap < 0x7fffff00LL ? (int)cap : 0x7fffff00;
+  const int c = min(max(L, 0), top);
+  bad |= c != L;
+  return c;
+}
+template <int kTileKeys>
+__device__ __forceinline__ int tiles_of(int L) {
+  return max(1, (L + kTileKeys - 1) / kTileKeys);
+}
+template <int kUnitRows>
+__device__ __forceinline__ int row_blocks(int n, int G) {
+  return (int)(((long long)n * G + kUnitRows - 1) / kUnitRows);
+}
+
+// Joins the partial results of the units that span CTAs, and writes their rows.
+int launch_join(const AttnParams& p, const AttnGeometry& g, int dtype, bool f8, int head_dim, void* stream);
+
+// The tensor-memory kernel (dflash_attention_tc.cu): units of 32, 64 or 128 rows.
+AttnGeometry tc_geometry(int rows, int head_dim);
+int launch_attention_tc(const AttnParams& p, int rows, int dtype, int head_dim, int sms, void* stream);
+
+}  // namespace dflash

@@ -1,0 +1,737 @@
+// dflash_attention_tc.cu -- attention over the paged cache for blocks whose
+// query rows (new tokens x heads that share a key/value head) number more than
+// 16: the products run on the 5th-generation tensor cores, with scores,
+// weights and sums in tensor memory.
+//
+// Mathematics and work list as in dflash_attention.cu; here a unit has R = 32,
+// 64 or 128 query rows and a tile kKeys = 128 keys (64 for head_dim 256).
+// What bounds it is still the one pass over the cache: at R = 64 the products
+// take 512 of the about 2800 cycles in which a tile's 64 KB arrive, so the
+// rows that pad M to 128 cost nothing. They are put to use instead: the R rows
+// are laid out 128 / R times, and copy c takes the keys c kKeys R / 128 ... of
+// every tile as if the others were masked. Each thread of the softmax owns one
+// row of tensor memory and R / 128 of a tile's columns, so its work is the
+// same for every R, needs no exchange between lanes, and the copies' results
+// are joined once, at the end of the unit.
+//
+// Roles (one CTA per SM, persistent over its run of tiles):
+//  * warps 5-8 fill a ring of stages with 16-byte asynchronous copies, placed
+//    for the tensor cores' 128-byte swizzle; any page size, stride and order;
+//    keys that do not exist are zero-filled. The copies arrive on the stage's
+//    barrier as they land.
+//  * warp 4: one thread issues S = Q K^T (both from shared memory, into one of
+//    two score buffers) one tile ahead of O += P V (P from tensor memory, V
+//    read in place as the transposed operand).
+//  * warps 0-3: softmax. A thread reads its scores (tcgen05.ld), takes 2^(x -
+//    m), writes P back as 16-bit pairs. m is the running maximum, but moves
+//    only when a score exceeds it by 8 (weights then stay below 2^8): moving
+//    it rescales O in tensor memory, which has to wait for the product before.
+// Every wait is bounded; a CTA that gives up raises DFLASH_STATUS_TIMEOUT,
+// lets its copies land and frees its tensor memory.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "dflash_attention.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kTcCtas = 160;
+constexpr int kMmaWarp = 4;
+constexpr int kLoadWarp0 = 5, kLoadWarps = 4;
+constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
+constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the reference
+constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at once
+
+template <int D>
+struct TcShape {
+  static constexpr int kKeys = D == 256 ? 64 : 128;
+  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 3 : 2;
+  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kHalf = kKeys * D * 2;           // K or V of a stage
+  static constexpr size_t kSmem = 1024 + (size_t)kQBytes + (size_t)kStages * 2 * kHalf;
+  // tensor memory columns
+  static constexpr int kO = 0, kS = D, kP = kS + 2 * kKeys, kUsed = kP + kKeys;
+  static_assert(kUsed <= 512, "tensor memory");
+};
+
+struct TcShared {
+  uint64_t full[6], empty[6];    // per stage
+  uint64_t s_full[2], p_full[2];  // per score buffer
+  uint64_t pv_done, q_full, drained;
+  uint32_t tmem;
+  volatile int failed;
+  int unsound[kFlags];           // per unit (ordinal in the CTA): see load
+  uint32_t mask[6][4];           // per stage and load warp: its keys that exist
+  int first_b;
+  long long first_pre, sums[kTcThreads / 32];
+  float ml[2 * 128];
+};
+
+// ---- PTX wrappers (one CTA per tensor core group) ------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// D (+)= A[shared memory] B[shared memory]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// D (+)= A[tensor memory] B[shared memory]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+// waits for the loads issued so far; the values pass through, so that nothing
+// computed from them moves ahead of the wait
+__device__ __forceinline__ void wait_ld8(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// N consecutive columns of this thread's lane, 8 at a time
+__device__ __forceinline__ void ld8(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
+}
+__device__ __forceinline__ void ld32(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void st8(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&r)[N]) {
+  if constexpr (N % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) ld32(a + i, r + i);
+#pragma unroll
+    for (int i = 0; i < N; i += 32) wait_ld32(r + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) ld8(a + i, r + i);
+#pragma unroll
+    for (int i = 0; i < N; i += 8) wait_ld8(r + i);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t a, const uint32_t (&r)[N]) {
+  if constexpr (N % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) st32(a + i, r + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) st8(a + i, r + i);
+  }
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle. K-major (Q, K): rows of
+// 128 bytes, 8-row groups 1024 bytes apart (stride offset); one product's 16
+// inner values lie inside a row. MN-major (V, whose rows are the inner index):
+// 64 outer values per 128-byte row, 8 inner rows per group 1024 bytes apart
+// (stride offset), the next 64 outer values a slab further (leading offset).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)((leading & 0x3ffffu) >> 4) << 16 |
+         (uint64_t)(1024u >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+
+// A bounded wait that also gives up when another role of the CTA has.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared& S) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0u && (S.failed || global_timer_ns() - t0 > kWaitLimitNs)) {
+      S.failed = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// A position in the list of units, moved on tile by tile.
+template <int R, int kKeys>
+struct Cursor {
+  int b, h, rb, L, first, n, tiles, rbs, ordinal;
+  long long start;
+  __device__ __forceinline__ void request(const AttnParams& p) {
+    bool bad = false;
+    request_tokens(p.tk, b, first, n, bad);
+    L = clamped_len(p, b, bad);
+    tiles = tiles_of<kKeys>(L);
+    rbs = row_blocks<R>(n, p.G);
+  }
+  // the unit of tile t, request b0 being the one it falls in and pre the tiles before that
+  __device__ __forceinline__ void seek(const AttnParams& p, int b0, long long pre, long long t) {
+    b = b0;
+    request(p);
+    const long long k = (t - pre) / tiles;
+    h = (int)(k / rbs);
+    rb = (int)(k - (long long)h * rbs);
+    start = pre + k * tiles;
+    ordinal = 0;
+  }
+  __device__ __forceinline__ long long end() const { return start + tiles; }
+  __device__ __forceinline__ void next(const AttnParams& p) {
+    start += tiles;
+    ++ordinal;
+    if (++rb < rbs) return;
+    rb = 0;
+    if (++h < p.c.kv_heads) return;
+    h = 0;
+    do {
+      ++b;
+      request(p);
+    } while (rbs == 0);  // a request after the list's last tile is never asked for
+  }
+};
+
+template <class T>
+__device__ __forceinline__ bool word_not_finite(uint32_t w) {
+  constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7c00u : 0x7f80u;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+template <class T, int D, int R>
+__global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnParams p, const AttnGeometry geo) {
+  using W = TcShape<D>;
+  constexpr int kKeys = W::kKeys, kStages = W::kStages;
+  constexpr int kCopies = 128 / R, kCols = kKeys / kCopies;  // a thread's columns of a tile
+  constexpr int kChunk = kCols < 64 ? kCols : 64;            // ... in registers at a time
+  constexpr int kMine = kKeys / kLoadWarps;                  // a load warp's keys of a tile
+  constexpr uint32_t kMineMask = kMine == 32 ? 0xffffffffu : (1u << kMine) - 1u;
+  extern __shared__ unsigned char raw[];
+  __shared__ TcShared S;
+  unsigned char* mem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_mem = smem_addr(mem), ring = q_mem + W::kQBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&S.full[i], kLoadWarps * 33);  // every copying thread, and each warp's mask
+      mbar_init(&S.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 128);
+    }
+    mbar_init(&S.pv_done, 1);
+    mbar_init(&S.q_full, 128);
+    mbar_init(&S.drained, 1);
+    for (int i = 0; i < kFlags; ++i) S.unsound[i] = 0;
+    S.failed = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&S.tmem, 512);
+  grid_dependency_sync();
+
+  // ---- the list: tiles before each request, this CTA's run and its first request
+  bool bad = false;
+  long long mine = 0, before = 0, total = 0;
+  const int per = (p.tk.B + kTcThreads - 1) / kTcThreads;
+  const int b_lo = min(p.tk.B, tid * per), b_hi = min(p.tk.B, b_lo + per);
+  auto request_tiles = [&](int b) {
+    int first, n;
+    request_tokens(p.tk, b, first, n, bad);
+    return (long long)row_blocks<R>(n, p.G) * p.c.kv_heads * tiles_of<kKeys>(clamped_len(p, b, bad));
+  };
+  for (int b = b_lo; b < b_hi; ++b) mine += request_tiles(b);
+  before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) S.sums[warp] = before;
+  before -= mine;
+  __syncthreads();
+  for (int w = 0; w < kTcThreads / 32; ++w) {
+    if (w < warp) before += S.sums[w];
+    total += S.sums[w];
+  }
+  const long long run = max((long long)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+  const long long t_begin = (long long)blockIdx.x * run, t_end = min(total, t_begin + run);
+  if (blockIdx.x == 0) {
+    long long* hdr = reinterpret_cast<long long*>(p.ws);
+    long long at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      hdr[1 + b] = at;
+      at += request_tiles(b);
+    }
+    if (tid == 0) hdr[0] = run;
+    if (bad) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
+  }
+  if (t_begin < t_end && before <= t_begin && t_begin < before + mine) {
+    long long at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long n = request_tiles(b);
+      if (t_begin < at + n) {
+        S.first_b = b;
+        S.first_pre = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = S.tmem;
+
+  if (t_begin < t_end) {
+    Cursor<R, kKeys> u;
+    u.seek(p, S.first_b, S.first_pre, t_begin);
+    bool ok = true;
+
+    if (warp >= kLoadWarp0) {
+      // ---- loads: this warp's share of every tile's keys
+      constexpr int kPieces = D / 8;                 // 16-byte pieces of a row
+      constexpr int kLoads = kMine * kPieces / 32;   // per lane, for K and for V each
+      const int lw = warp - kLoadWarp0;
+      bool bad_page = false, next_ok = false;
+      uint32_t next_off = 0;
+      auto look_up = [&](long long t) {
+        const int key = (int)(t - u.start) * kKeys + lw * kMine + (lane & (kMine - 1));
+        next_ok = key < u.L;
+        int page = 0, slot = 0, id = 0;
+        if (next_ok) {
+          split_position(p.c, key, page, slot);
+          id = p.c.table[(long long)u.b * p.c.table_stride + page];
+          if (id < 0 || id >= p.c.num_pages) {
+            bad_page = true;
+            next_ok = false;
+          }
+        }
+        next_off = next_ok ? row_offset(p.c, id, u.h, slot) : 0u;
+      };
+      // Under a causal mask a tile may hold values that only some rows see, and
+      // a weight of 0 times one that is not finite would be NaN. Such a value
+      // (never met in sound data) is replaced by 0 here and added at the unit's
+      // end.
+      auto sanitise = [&](int st, int ordinal) {
+        const uint32_t vb = (uint32_t)(W::kQBytes + st * 2 * W::kHalf + W::kHalf);
+        bool found = false;
+#pragma unroll 4
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = i * 32 + lane, r = lw * kMine + at / kPieces, c = at % kPieces;
+          uint32_t* w = reinterpret_cast<uint32_t*>(mem + vb + (c >> 3) * (kKeys * 128) + r * 128 +
+                                                    (((c & 7) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (word_not_finite<T>(w[e])) {
+              found = true;
+              constexpr uint32_t m = std::is_same<T, F16>::value ? 0x7c00u : 0x7f80u;
+              uint32_t x = w[e];
+              if ((x & m) == m) x &= 0xffff0000u;
+              if (((x >> 16) & m) == m) x &= 0xffffu;
+              w[e] = x;
+            }
+        }
+        if (found) S.unsound[ordinal % kFlags] = 1;
+      };
+      look_up(t_begin);
+      int st = 0;
+      uint32_t round = 0;
+      for (long long t = t_begin; t < t_end; ++t) {
+        if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
+        const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
+        const uint32_t kb = ring + st * 2 * W::kHalf;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int at = i * 32 + lane, r = at / kPieces, c = at % kPieces;
+          const uint32_t off = __shfl_sync(0xffffffffu, next_off, r);
+          const size_t o = ((size_t)off + c) * 16u;
+          const int row = lw * kMine + r;
+          const uint32_t d = kb + (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          const int n = ((mask >> r) & 1u) ? 16 : 0;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(p.c.k + o), "r"(n) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + W::kHalf), "l"(p.c.v + o), "r"(n)
+                       : "memory");
+        }
+        if (lane == 0) {
+          S.mask[st][lw] = mask;
+          mbar_arrive(&S.full[st]);
+        }
+        if (p.causal && u.n > 1 && (t - u.start + 1) * kKeys > u.L - u.n) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          sanitise(st, u.ordinal);
+          mbar_arrive(&S.full[st]);
+        } else {
+          // arrives by itself once this thread's copies have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&S.full[st])) : "memory");
+        }
+        if (t + 1 < t_end) {
+          if (t + 1 >= u.end()) u.next(p);
+          look_up(t + 1);
+        }
+        if (++st == kStages) {
+          st = 0;
+          ++round;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (bad_page) raise_status(p.status, DFLASH_STATUS_BAD_PAGE);
+    } else if (warp == kMmaWarp) {
+      // ---- products
+      if (lane == 0) {
+        constexpr uint32_t type = std::is_same<T, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
+        constexpr uint32_t id_s = (1u << 4) | type | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
+        constexpr uint32_t id_o = (1u << 4) | type | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+        const int count = (int)(t_end - t_begin);
+        // O += P V of tile j; fresh: the unit's (or the run's) first
+        auto sum_values = [&](int j, bool fresh) {
+          const int st = j % kStages, buf = j & 1;
+          if (!tc_wait(&S.p_full[buf], (uint32_t)(j >> 1) & 1u, S)) return false;
+          fence_after();
+          const uint32_t vb = ring + st * 2 * W::kHalf + W::kHalf;
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + W::kO, tmem + W::kP + buf * (kKeys / 2) + 8 * k, operand(vb + k * 2048, kKeys * 128), id_o,
+                   !fresh || k > 0);
+          mma_commit(&S.empty[st]);
+          mma_commit(&S.pv_done);
+          return true;
+        };
+        bool fresh = true, prev_fresh = true;  // of tile j, and of the last whose P V is not issued yet
+        int units = 0, summed = 0;             // units begun, tiles whose P V is issued
+        for (int j = 0; j < count && ok; ++j) {
+          const long long t = t_begin + j;
+          if (j > 0 && t >= u.end()) {
+            u.next(p);
+            fresh = true;
+          }
+          if (fresh) {
+            // the next unit's Q comes only after the last one's sums are out
+            if (j > 0 && (ok = sum_values(j - 1, prev_fresh))) summed = j;
+            ok = ok && tc_wait(&S.q_full, (uint32_t)units & 1u, S);
+            ++units;
+          }
+          ok = ok && tc_wait(&S.full[j % kStages], (uint32_t)(j / kStages) & 1u, S);
+          if (!ok) break;
+          fence_async_smem();  // the copies, which the barrier has shown, before the asynchronous proxy reads them
+          fence_after();
+          const uint32_t kb = ring + (j % kStages) * 2 * W::kHalf;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + W::kS + (j & 1) * kKeys, operand(q_mem + (k >> 2) * 16384 + (k & 3) * 32, 16),
+                   operand(kb + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16), id_s, k > 0);
+          mma_commit(&S.s_full[j & 1]);
+          if (summed < j && (ok = sum_values(j - 1, prev_fresh))) summed = j;
+          prev_fresh = fresh;
+          fresh = false;
+        }
+        if (ok) ok = sum_values(count - 1, prev_fresh);
+        mma_commit(&S.drained);  // nothing is left in flight when the tensor memory is freed
+        mbar_wait_landed(&S.drained, 0);
+      }
+      __syncwarp();
+    } else {
+      // ---- softmax: this thread's row of tensor memory
+      const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
+      const int copy = tid / R, row = tid % R;
+      {
+        uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 8) st8(my + W::kP + i, zero);  // both buffers: the other copies' keys stay 0
+        wait_st();
+      }
+      const float c = p.scale * kLog2e;
+      float* scratch = reinterpret_cast<float*>(mem);  // Q's place, between units
+      int j = 0;
+      long long t = t_begin;
+      while (t < t_end && ok) {
+        const long long u_end = min(t_end, u.end()), u_begin = t;
+        // ---- Q, laid out kCopies times
+        const int rows_here = min(R, u.n * p.G - u.rb * R);
+        constexpr int kPieces = D / 8;
+#pragma unroll 4
+        for (int i = 0; i < kPieces; ++i) {
+          const int at = i * 128 + tid, rr = at / kPieces, cc = at % kPieces, qr = rr % R;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (qr < rows_here) {
+            const int g = u.rb * R + qr, ti = g / p.G;
+            x = *reinterpret_cast<const uint4*>(p.q + 2 * ((long long)(u.first + ti) * p.q_ts +
+                                                           (long long)(u.h * p.G + g - ti * p.G) * p.q_hs + 8 * cc));
+          }
+          *reinterpret_cast<uint4*>(mem + (cc >> 3) * 16384 + rr * 128 + (((cc & 7) ^ (rr & 7)) << 4)) = x;
+        }
+        fence_async_smem();
+        mbar_arrive(&S.q_full);
+        const int tok = (u.rb * R + row) / p.G;
+        const int vis = row >= rows_here ? 0 : p.causal ? min(u.L, max(0, u.L - u.n + tok + 1)) : u.L;
+
+        float m = kNegInf, l = 0.0f;
+        for (; t < u_end && ok; ++t, ++j) {
+          const int st = j % kStages, buf = j & 1;
+          ok = tc_wait(&S.s_full[buf], (uint32_t)(j >> 1) & 1u, S);
+          ok = ok && tc_wait(&S.full[st], (uint32_t)(j / kStages) & 1u, S);  // for the mask
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t scores = my + W::kS + buf * kKeys + copy * kCols;
+          const int key0 = (int)(t - u.start) * kKeys + copy * kCols;
+          const uint32_t all = S.mask[st][0] & S.mask[st][1] & S.mask[st][2] & S.mask[st][3];
+          const bool whole_tile = (int)(t - u.start + 1) * kKeys <= u.L - (p.causal ? u.n : 0) &&
+                                  (all & kMineMask) == kMineMask;
+          // scores of the columns from c0 on, scaled and masked
+          auto read = [&](int c0, uint32_t (&x)[kChunk]) {
+            tmem_load<kChunk>(scores + c0, x);
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+              const int k = copy * kCols + c0 + i;
+              const bool seen = whole_tile || (((S.mask[st][k / kMine] >> (k % kMine)) & 1u) && key0 + c0 + i < vis);
+              x[i] = __float_as_uint(seen ? __uint_as_float(x[i]) * c : kNegInf);
+            }
+          };
+          uint32_t x[kChunk];
+          float top = kNegInf;
+#pragma unroll
+          for (int c0 = 0; c0 < kCols; c0 += kChunk) {
+            read(c0, x);
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+          }
+          // the reference moves when the weights would pass 2^kSlack
+          const bool move = top > m + kSlack || (m == kNegInf && top > m);
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? (m == kNegInf ? 0.0f : ex2(m - top)) : 1.0f;
+            if (t > u_begin) {  // O holds sums: they are rescaled, after the product in flight
+              ok = tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              fence_after();
+              for (int d = 0; d < D; d += 32) {
+                uint32_t y[32];
+                tmem_load<32>(my + W::kO + d, y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                tmem_store<32>(my + W::kO + d, y);
+              }
+              wait_st();
+            }
+            l *= f;
+            if (move) m = top;
+          }
+          const float ref = m == kNegInf ? 0.0f : m;
+#pragma unroll
+          for (int c0 = 0; c0 < kCols; c0 += kChunk) {
+            if (kCols > kChunk) read(c0, x);  // again: not all of a row's scores fit in registers
+            uint32_t w[kChunk / 2];
+#pragma unroll
+            for (int i = 0; i < kChunk / 2; ++i) {
+              const float a = ex2(__uint_as_float(x[2 * i]) - ref), b = ex2(__uint_as_float(x[2 * i + 1]) - ref);
+              l += a + b;
+              w[i] = T::pack(a, b);
+            }
+            tmem_store<kChunk / 2>(my + W::kP + buf * (kKeys / 2) + (copy * kCols + c0) / 2, w);
+          }
+          wait_st();
+          fence_before();
+          mbar_arrive(&S.p_full[buf]);
+        }
+        if (!ok) break;
+
+        // ---- the unit (or this CTA's run of it) ends
+        ok = tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const bool whole = u_begin == u.start && u_end == u.end();
+        S.ml[2 * tid] = m;
+        S.ml[2 * tid + 1] = l;
+        const int unsound = *reinterpret_cast<volatile int*>(&S.unsound[u.ordinal % kFlags]);
+        softmax_sync();
+        float best = kNegInf;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) best = fmaxf(best, S.ml[2 * (k * R + row)]);
+        const float own = m == kNegInf ? 0.0f : ex2(m - best);
+        const long long slot = 2LL * blockIdx.x + (u_begin == t_begin ? 0 : 1);
+        auto row_sum = [&](int r, float& top) {
+          top = kNegInf;
+#pragma unroll
+          for (int k = 0; k < kCopies; ++k) top = fmaxf(top, S.ml[2 * (k * R + r)]);
+          float s = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kCopies; ++k) {
+            const float mk = S.ml[2 * (k * R + r)], lk = S.ml[2 * (k * R + r) + 1];
+            s += mk != kNegInf ? lk * ex2(mk - top) : lk == lk ? 0.0f : lk;  // a NaN sum stays one
+          }
+          return s;
+        };
+        if (tid < rows_here) {
+          float top;
+          const float sum = row_sum(tid, top);
+          if (whole) {
+            const int g = u.rb * R + tid, ti = g / p.G;
+            if (p.lse)
+              p.lse[(long long)(u.first + ti) * ((long long)p.G * p.c.kv_heads) + u.h * p.G + g - ti * p.G] =
+                  (top + log2f(sum)) * kLn2;
+          } else {
+            float* ml = reinterpret_cast<float*>(p.ws + geo.ml(p.tk.B)) + (slot * R + tid) * 2;
+            ml[0] = top;
+            ml[1] = sum;
+          }
+        }
+        for (int d0 = 0; d0 < D; d0 += 32) {
+          uint32_t y[32];
+          __syncwarp();
+          tmem_load<32>(my + W::kO + d0, y);
+          if (unsound && row < rows_here && copy == 0) {
+            // the values replaced by 0 that this row does see
+            for (int k = max(0, u.L - u.n); k < vis; ++k) {
+              if (k < (int)(u_begin - u.start) * kKeys || k >= (int)(u_end - u.start) * kKeys) continue;
+              int page, sl;
+              split_position(p.c, k, page, sl);
+              const int id = p.c.table[(long long)u.b * p.c.table_stride + page];
+              if (id < 0 || id >= p.c.num_pages) continue;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v + (size_t)row_offset(p.c, id, u.h, sl) * 16u) + d0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (word_not_finite<T>(v[i])) y[i] = __float_as_uint(__uint_as_float(y[i]) + T::unpack(v[i]).x);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            scratch[tid * 32 + (i ^ lane)] =
+                (unsound && copy == 0 && own == 0.0f) ? __uint_as_float(y[i]) : __uint_as_float(y[i]) * own;
+          softmax_sync();
+          for (int r = tid >> 3; r < rows_here; r += 16) {
+            const int c4 = (tid & 7) * 4;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < kCopies; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += scratch[(k * R + r) * 32 + ((c4 + e) ^ ((k * R + r) & 31))];
+            if (whole) {
+              float top;
+              const float sum = row_sum(r, top), f = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+              const int g = u.rb * R + r, ti = g / p.G;
+              *reinterpret_cast<uint2*>(p.out + 2 * ((long long)(u.first + ti) * p.o_ts +
+                                                     (long long)(u.h * p.G + g - ti * p.G) * p.o_hs + d0 + c4)) =
+                  make_uint2(T::pack(v[0] * f, v[1] * f), T::pack(v[2] * f, v[3] * f));
+            } else {
+              *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.ws + geo.o(p.tk.B)) + (slot * R + r) * D + d0 + c4) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            }
+          }
+          softmax_sync();  // scratch (and, after the last run, Q and S.ml) is written again
+        }
+        if (tid == 0) S.unsound[u.ordinal % kFlags] = 0;
+        fence_before();
+        if (t < t_end) u.next(p);
+      }
+    }
+    if (!ok && lane == 0) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kMmaWarp) tmem_free(tmem, 512);
+}
+
+template <class T, int D, int R>
+int launch(const AttnParams& p, int sms, void* stream) {
+  using W = TcShape<D>;
+  const AttnGeometry geo = tc_geometry(R, D);
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(attention_tc_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kSmem);
+    if (e != cudaSuccess) return (int)e;
+    ready[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.gridDim = dim3((unsigned)(sms < kTcCtas ? sms : kTcCtas));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = W::kSmem;
+  e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, D, R>, p, geo);
+  if (e != cudaSuccess) return (int)e;
+  return launch_join(p, geo, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, false, D, stream);
+}
+template <class T, int R>
+int pick_dim(const AttnParams& p, int d, int sms, void* stream) {
+  return d == 64 ? launch<T, 64, R>(p, sms, stream) : d == 128 ? launch<T, 128, R>(p, sms, stream) : launch<T, 256, R>(p, sms, stream);
+}
+template <class T>
+int pick_rows(const AttnParams& p, int rows, int d, int sms, void* stream) {
+  return rows == 32 ? pick_dim<T, 32>(p, d, sms, stream) : rows == 64 ? pick_dim<T, 64>(p, d, sms, stream) : pick_dim<T, 128>(p, d, sms, stream);
+}
+
+}  // namespace
+
+AttnGeometry tc_geometry(int rows, int head_dim) { return {rows, head_dim == 256 ? 64 : 128, kTcCtas}; }
+
+int launch_attention_tc(const AttnParams& p, int rows, int dtype, int head_dim, int sms, void* stream) {
+  return dtype == DFLASH_BF16 ? pick_rows<Bf16>(p, rows, head_dim, sms, stream)
+                              : pick_rows<F16>(p, rows, head_dim, sms, stream);
+}
+
+}  // namespace dflash

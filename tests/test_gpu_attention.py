@@ -182,6 +182,90 @@ def test_masked_values_never_count(dv, cdt, bad):
         assert not bool(g[:, first:].float().isfinite().all(-1).any())
 
 
+BLOCKS = [
+    # counts, lens, Hq, Hkv, D, page, causal, dtype: 17 to 128 rows a head and more, every
+    # head_dim, lengths around a tile's 64 and 128 keys
+    ([17], [17], 1, 1, 128, 16, True, BF),
+    ([5, 5], [127, 128], 8, 2, 128, 64, True, BF),
+    ([5, 5], [129, 640], 8, 2, 64, 5, False, HF),
+    ([8, 8], [63, 1000], 8, 2, 256, 16, True, BF),
+    ([8, 8, 8], [64, 65, 192], 16, 2, 128, 48, True, HF),
+    ([8] * 3, [2000, 8, 333], 64, 8, 128, 64, True, BF),
+    ([8] * 2, [256, 300], 8, 1, 64, 16, True, BF),
+    ([7] * 2, [300, 129], 9, 1, 256, 7, False, BF),
+    ([16] * 2, [1000, 16], 16, 2, 128, 64, True, BF),
+    ([16] * 2, [255, 257], 16, 2, 64, 32, False, HF),
+    ([16] * 2, [127, 450], 8, 1, 256, 128, True, HF),
+    ([33, 20, 1, 0], [400, 20, 300, 5], 12, 2, 128, 16, True, BF),
+    ([300], [300], 2, 1, 128, 16, True, BF),
+    ([6] * 2, [4, 3], 8, 1, 128, 16, True, BF),           # rows that see no key
+    ([8] * 90, [1 + 17 * b for b in range(90)], 8, 2, 64, 16, False, BF),
+]
+
+
+@pytest.mark.parametrize("case", BLOCKS, ids=range(len(BLOCKS)))
+@pytest.mark.parametrize("inner", [False, True])
+def test_blocks_match_the_definition(dv, case, inner):
+    counts, lens, Hq, Hkv, D, page, causal, dtype = case
+    table, caches, q, _ = make(len(lens) + D + page, counts, lens, Hq, Hkv, D, page, dtype, dtype, inner,
+                               fill=float("nan"))
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    a = check(dv, table, caches, q, None, counts, lens, page, causal, status=st)
+    b = check(dv, table, caches, q, None, counts, lens, page, causal, status=st)
+    assert int(st) == 0 and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("D,rows", [(64, 32), (64, 128), (128, 32), (128, 64), (128, 128), (256, 64)])
+def test_long_blocks_are_split(dv, D, rows):
+    """One request over every SM, its rising scores moving the reference again and again."""
+    n, lens = rows // 8, [70001]
+    table, caches, q, _ = make(D + rows, [n], lens, 16, 2, D, 64, BF, BF, False)
+    grow = torch.linspace(0.05, 3.0, lens[0], device=DEV)
+    pos = torch.arange(lens[0], device=DEV)
+    y = caches[0].transpose(1, 2)
+    at = table[0].long()[pos // 64], pos % 64
+    y[at] = (y[at].float() * grow[:, None, None]).to(BF)
+    a, la = check(dv, table, caches, q, None, [n], lens, 64, True)
+    b, lb = check(dv, table, caches, q, None, [n], lens, 64, True)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 8), (256, 16)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_masked_values_never_count_in_blocks(dv, dtype, D, G, bad):
+    """As test_masked_values_never_count, for 24 to 96 rows a head."""
+    counts, lens, page, first, n = [6, 6], [140, 70], 16, 3, 6
+    table, caches, q, _ = make(8, counts, lens, 2 * G, 2, D, page, dtype, dtype, False)
+    clean = [c.clone() for c in caches]
+    for b in range(2):
+        for i in range(first, n):
+            j = lens[b] - n + i
+            for k, c in enumerate(caches):
+                c[int(table[b, j // page]), :, j % page, k::3] = bad
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got, gl = dv.paged_attention(dv.PagedCache(caches[0], caches[1], table), q, ln, return_lse=True)
+    want, wl = dv.paged_attention(dv.PagedCache(clean[0], clean[1], table), q, ln, return_lse=True)
+    g, w = got.view(2, n, 2 * G, D), want.view(2, n, 2 * G, D)
+    assert torch.equal(g[:, :first], w[:, :first])
+    assert torch.equal(gl.view(2, n, 2 * G)[:, :first], wl.view(2, n, 2 * G)[:, :first])
+    if bad != -float("inf"):
+        assert not bool(g[:, first:].float().isfinite().all(-1).any())
+    # only values: finite scores, so a row is infinite exactly where a value it sees is
+    caches[0].copy_(clean[0])
+    got = dv.paged_attention(dv.PagedCache(caches[0], caches[1], table), q, ln).view(2, n, 2 * G, D)
+    assert torch.equal(got[:, :first], w[:, :first])
+    where = torch.zeros(D, dtype=torch.bool, device=DEV)
+    where[1::3] = True
+    assert bool((~got[:, first:].float().isfinite() == where).all())
+
+
+def test_blocks_with_extreme_scores(dv):
+    for qscale in (1e-6, 3e4):
+        table, caches, q, _ = make(3, [8, 8], [90, 300], 8, 2, 128, 16, BF, BF, False, qscale=qscale)
+        check(dv, table, caches, q, None, [8, 8], [90, 300], 16, True)
+
+
 def test_lowest_and_infinite_scores(dv):
     """Keys whose score is -inf weigh nothing; a row of them alone gives 0, -inf."""
     D, page, L = 64, 16, 40
