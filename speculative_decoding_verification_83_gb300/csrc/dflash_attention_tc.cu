@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
   constexpr int kCopies = 128 / R, kCols = kKeys / kCopies;  // a thread's columns of a tile
   constexpr int kChunk = kCols < 64 ? kCols : 64;            // ... in registers at a time
   constexpr int kMine = kKeys / kLoadWarps;                  // a load warp's keys of a tile
+  constexpr int kGroup = kChunk < kMine ? kChunk : kMine;
   constexpr uint32_t kMineMask = kMine == 32 ? 0xffffffffu : (1u << kMine) - 1u;
   extern __shared__ unsigned char raw[];
   __shared__ TcShared S;
@@ -528,14 +529,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           const uint32_t all = S.mask[st][0] & S.mask[st][1] & S.mask[st][2] & S.mask[st][3];
           const bool whole_tile = (int)(t - u.start + 1) * kKeys <= u.L - (p.causal ? u.n : 0) &&
                                   (all & kMineMask) == kMineMask;
-          // scores of the columns from c0 on, scaled and masked
+          // scores of the columns from c0 on, unscaled, -inf where masked
           auto read = [&](int c0, uint32_t (&x)[kChunk]) {
             tmem_load<kChunk>(scores + c0, x);
+            if (whole_tile) return;
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-              const int k = copy * kCols + c0 + i;
-              const bool seen = whole_tile || (((S.mask[st][k / kMine] >> (k % kMine)) & 1u) && key0 + c0 + i < vis);
-              x[i] = __float_as_uint(seen ? __uint_as_float(x[i]) * c : kNegInf);
+            for (int g = 0; g < kChunk; g += kGroup) {
+              const int k = copy * kCols + c0 + g;
+              // bit i: the key of column g + i is there and before `vis`
+              const int left = vis - (key0 + c0 + g);
+              const uint32_t before = left <= 0 ? 0u : left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+              const uint32_t seen = (S.mask[st][k / kMine] >> (k % kMine)) & before;
+#pragma unroll
+              for (int i = 0; i < kGroup; ++i)
+                if (!((seen >> i) & 1u)) x[g + i] = __float_as_uint(kNegInf);
             }
           };
           uint32_t x[kChunk];
@@ -546,11 +553,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) top = fmaxf(top, __uint_as_float(x[i]));
           }
+          top *= c;
           // the reference moves when the weights would pass 2^kSlack
           const bool move = top > m + kSlack || (m == kNegInf && top > m);
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? (m == kNegInf ? 0.0f : ex2(m - top)) : 1.0f;
-            if (t > u_begin) {  // O holds sums: they are rescaled, after the product in flight
+            if (t > u_begin) {  // O holds sums: they are rescaled, after the product in flight (the one before is
+                                // over: these scores came after it)
               ok = tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
               if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
@@ -576,7 +585,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             uint32_t w[kChunk / 2];
 #pragma unroll
             for (int i = 0; i < kChunk / 2; ++i) {
-              const float a = ex2(__uint_as_float(x[2 * i]) - ref), b = ex2(__uint_as_float(x[2 * i + 1]) - ref);
+              const float a = ex2(fmaf(__uint_as_float(x[2 * i]), c, -ref)),
+                          b = ex2(fmaf(__uint_as_float(x[2 * i + 1]), c, -ref));
               l += a + b;
               w[i] = T::pack(a, b);
             }
@@ -589,7 +599,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         if (!ok) break;
 
         // ---- the unit (or this CTA's run of it) ends
-        ok = tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
+        // A parity names a phase only if the one before the last is known to be
+        // over. The last scores show the product two tiles back done, no more:
+        // another warp may still be at its weights. So both are waited for.
+        if (j > 1) ok = tc_wait(&S.pv_done, (uint32_t)j & 1u, S);
+        ok = ok && tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
