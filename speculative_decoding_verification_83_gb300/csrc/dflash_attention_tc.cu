@@ -60,7 +60,7 @@ struct TcShape {
 struct TcShared {
   uint64_t full[6], empty[6];    // per stage
   uint64_t s_full[2], p_full[2];  // per score buffer
-  uint64_t pv_done, q_full, drained;
+  uint64_t pv_done, q_full, drained, together;
   uint32_t tmem;
   volatile int failed;
   int unsound[kFlags];           // per unit (ordinal in the CTA): see load
@@ -200,7 +200,14 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared
     }
   }
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// A barrier of the 128 softmax threads whose wait is bounded like the others
+// (a hardware barrier would hang if one warp had given up).
+__device__ __forceinline__ bool softmax_sync(uint32_t& phase, TcShared& S) {
+  mbar_arrive(&S.together);
+  const bool ok = tc_wait(&S.together, phase & 1u, S);
+  ++phase;
+  return __all_sync(0xffffffffu, ok);
+}
 
 // A position in the list of units, moved on tile by tile.
 template <int R, int kKeys>
@@ -272,6 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
     mbar_init(&S.pv_done, 1);
     mbar_init(&S.q_full, 128);
     mbar_init(&S.drained, 1);
+    mbar_init(&S.together, 128);
     for (int i = 0; i < kFlags; ++i) S.unsound[i] = 0;
     S.failed = 0;
     fence_barrier_init();
@@ -492,6 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       const float c = p.scale * kLog2e;
       float* scratch = reinterpret_cast<float*>(mem);  // Q's place, between units
       int j = 0;
+      uint32_t syncs = 0;
       long long t = t_begin;
       while (t < t_end && ok) {
         const long long u_end = min(t_end, u.end()), u_begin = t;
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         S.ml[2 * tid] = m;
         S.ml[2 * tid + 1] = l;
         const int unsound = *reinterpret_cast<volatile int*>(&S.unsound[u.ordinal % kFlags]);
-        softmax_sync();
+        if (!(ok = softmax_sync(syncs, S))) break;
         float best = kNegInf;
 #pragma unroll
         for (int k = 0; k < kCopies; ++k) best = fmaxf(best, S.ml[2 * (k * R + row)]);
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             ml[1] = sum;
           }
         }
-        for (int d0 = 0; d0 < D; d0 += 32) {
+        for (int d0 = 0; d0 < D && ok; d0 += 32) {
           uint32_t y[32];
           __syncwarp();
           tmem_load<32>(my + W::kO + d0, y);
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           for (int i = 0; i < 32; ++i)
             scratch[tid * 32 + (i ^ lane)] =
                 (unsound && copy == 0 && own == 0.0f) ? __uint_as_float(y[i]) : __uint_as_float(y[i]) * own;
-          softmax_sync();
+          if (!(ok = softmax_sync(syncs, S))) break;
           for (int r = tid >> 3; r < rows_here; r += 16) {
             const int c4 = (tid & 7) * 4;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -687,8 +696,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
                   make_float4(v[0], v[1], v[2], v[3]);
             }
           }
-          softmax_sync();  // scratch (and, after the last run, Q and S.ml) is written again
+          ok = softmax_sync(syncs, S);  // scratch (and, after the last run, Q and S.ml) is written again
         }
+        if (!ok) break;
         if (tid == 0) S.unsound[u.ordinal % kFlags] = 0;
         fence_before();
         if (t < t_end) u.next(p);
