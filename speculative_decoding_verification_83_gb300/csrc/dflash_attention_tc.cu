@@ -98,6 +98,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// 16 bytes to shared memory as they arrive; zeros where there is nothing to read
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                : "memory");
@@ -405,10 +409,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           const size_t o = ((size_t)off + c) * 16u;
           const int row = lw * kMine + r;
           const uint32_t d = kb + (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          const int n = ((mask >> r) & 1u) ? 16 : 0;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(p.c.k + o), "r"(n) : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + W::kHalf), "l"(p.c.v + o), "r"(n)
-                       : "memory");
+          const bool there = (mask >> r) & 1u;
+          copy16(d, p.c.k + o, there);
+          copy16(d + W::kHalf, p.c.v + o, there);
         }
         if (lane == 0) {
           S.mask[st][lw] = mask;
@@ -507,17 +510,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         // ---- Q, laid out kCopies times
         const int rows_here = min(R, u.n * p.G - u.rb * R);
         constexpr int kPieces = D / 8;
-#pragma unroll 4
-        for (int i = 0; i < kPieces; ++i) {
-          const int at = i * 128 + tid, rr = at / kPieces, cc = at % kPieces, qr = rr % R;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (qr < rows_here) {
-            const int g = u.rb * R + qr, ti = g / p.G;
-            x = *reinterpret_cast<const uint4*>(p.q + 2 * ((long long)(u.first + ti) * p.q_ts +
-                                                           (long long)(u.h * p.G + g - ti * p.G) * p.q_hs + 8 * cc));
+#pragma unroll
+        for (int i = 0; i < R * kPieces / 128; ++i) {
+          const int at = i * 128 + tid, qr = at / kPieces, cc = at % kPieces;
+          const bool there = qr < rows_here;
+          const int g = u.rb * R + (there ? qr : 0), ti = g / p.G;
+          const unsigned char* src = p.q + 2 * ((long long)(u.first + ti) * p.q_ts +
+                                                (long long)(u.h * p.G + g - ti * p.G) * p.q_hs + 8 * cc);
+#pragma unroll
+          for (int k = 0; k < kCopies; ++k) {
+            const int rr = k * R + qr;
+            copy16(q_mem + (cc >> 3) * 16384 + rr * 128 + (((cc & 7) ^ (rr & 7)) << 4), src, there);
           }
-          *reinterpret_cast<uint4*>(mem + (cc >> 3) * 16384 + rr * 128 + (((cc & 7) ^ (rr & 7)) << 4)) = x;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_async_smem();
         mbar_arrive(&S.q_full);
         const int tok = (u.rb * R + row) / p.G;
@@ -623,80 +629,106 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         S.ml[2 * tid + 1] = l;
         const int unsound = *reinterpret_cast<volatile int*>(&S.unsound[u.ordinal % kFlags]);
         if (!(ok = softmax_sync(syncs, S))) break;
-        float best = kNegInf;
+        // the row's maximum and sum over its copies, and this copy's factor
+        float best = kNegInf, sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < kCopies; ++k) best = fmaxf(best, S.ml[2 * (k * R + row)]);
-        const float own = m == kNegInf ? 0.0f : ex2(m - best);
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) {
+          const float mk = S.ml[2 * (k * R + row)], lk = S.ml[2 * (k * R + row) + 1];
+          sum += mk != kNegInf ? lk * ex2(mk - best) : lk == lk ? 0.0f : lk;  // a NaN sum stays one
+        }
+        float factor = m == kNegInf ? 0.0f : ex2(m - best);
+        if (whole) factor *= sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
         const long long slot = 2LL * blockIdx.x + (u_begin == t_begin ? 0 : 1);
-        auto row_sum = [&](int r, float& top) {
-          top = kNegInf;
-#pragma unroll
-          for (int k = 0; k < kCopies; ++k) top = fmaxf(top, S.ml[2 * (k * R + r)]);
-          float s = 0.0f;
-#pragma unroll
-          for (int k = 0; k < kCopies; ++k) {
-            const float mk = S.ml[2 * (k * R + r)], lk = S.ml[2 * (k * R + r) + 1];
-            s += mk != kNegInf ? lk * ex2(mk - top) : lk == lk ? 0.0f : lk;  // a NaN sum stays one
-          }
-          return s;
-        };
-        if (tid < rows_here) {
-          float top;
-          const float sum = row_sum(tid, top);
-          if (whole) {
-            const int g = u.rb * R + tid, ti = g / p.G;
-            if (p.lse)
-              p.lse[(long long)(u.first + ti) * ((long long)p.G * p.c.kv_heads) + u.h * p.G + g - ti * p.G] =
-                  (top + log2f(sum)) * kLn2;
-          } else {
-            float* ml = reinterpret_cast<float*>(p.ws + geo.ml(p.tk.B)) + (slot * R + tid) * 2;
-            ml[0] = top;
+        const int g = u.rb * R + row, ti = g / p.G;
+        const long long q_tok = u.first + ti, q_head = u.h * p.G + g - ti * p.G;
+        const bool writes = copy == 0 && row < rows_here;  // the first copy's thread writes the row
+        unsigned char* out_row = p.out + 2 * (q_tok * p.o_ts + q_head * p.o_hs);
+        float* part_row = reinterpret_cast<float*>(p.ws + geo.o(p.tk.B)) + (slot * R + row) * D;
+        if (writes) {
+          if (!whole) {
+            float* ml = reinterpret_cast<float*>(p.ws + geo.ml(p.tk.B)) + (slot * R + row) * 2;
+            ml[0] = best;
             ml[1] = sum;
+          } else if (p.lse) {
+            p.lse[q_tok * ((long long)p.G * p.c.kv_heads) + q_head] = (best + log2f(sum)) * kLn2;
           }
         }
-        for (int d0 = 0; d0 < D && ok; d0 += 32) {
-          uint32_t y[32];
-          __syncwarp();
-          tmem_load<32>(my + W::kO + d0, y);
-          if (unsound && row < rows_here && copy == 0) {
-            // the values replaced by 0 that this row does see
-            for (int k = max(0, u.L - u.n); k < vis; ++k) {
-              if (k < (int)(u_begin - u.start) * kKeys || k >= (int)(u_end - u.start) * kKeys) continue;
-              int page, sl;
-              split_position(p.c, k, page, sl);
-              const int id = p.c.table[(long long)u.b * p.c.table_stride + page];
-              if (id < 0 || id >= p.c.num_pages) continue;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(p.c.v + (size_t)row_offset(p.c, id, u.h, sl) * 16u) + d0;
+        // The other copies leave their rows in shared memory (Q's place: as many
+        // columns at a time as it holds), the first adds them to its own. Pieces
+        // of 16 bytes are exchanged within 8 so that 8 lanes meet 8 bank groups.
+        constexpr int kRound = kCopies == 4 ? D / 2 : D;
+        for (int r0 = 0; r0 < D && ok; r0 += kRound) {
+          if (kCopies > 1) {
+            if (copy > 0) {
+              float4* dst = reinterpret_cast<float4*>(scratch) + (size_t)(tid - R) * (kRound / 4);
+#pragma unroll 1
+              for (int d = 0; d < kRound; d += 32) {
+                uint32_t y[32];
+                tmem_load<32>(my + W::kO + r0 + d, y);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (word_not_finite<T>(v[i])) y[i] = __float_as_uint(__uint_as_float(y[i]) + T::unpack(v[i]).x);
+                for (int i = 0; i < 8; ++i)
+                  dst[d / 4 + (i ^ (lane & 7))] =
+                      make_float4(__uint_as_float(y[4 * i]) * factor, __uint_as_float(y[4 * i + 1]) * factor,
+                                  __uint_as_float(y[4 * i + 2]) * factor, __uint_as_float(y[4 * i + 3]) * factor);
+              }
+            }
+            if (!(ok = softmax_sync(syncs, S))) break;
+          }
+          if (copy == 0) {
+#pragma unroll 1
+            for (int d = 0; d < kRound; d += 32) {
+              uint32_t y[32];
+              __syncwarp();
+              tmem_load<32>(my + W::kO + r0 + d, y);
+              if (unsound && writes) {
+                // the values replaced by 0 that this row does see
+                for (int k = max(0, u.L - u.n); k < vis; ++k) {
+                  if (k < (int)(u_begin - u.start) * kKeys || k >= (int)(u_end - u.start) * kKeys) continue;
+                  int page, sl;
+                  split_position(p.c, k, page, sl);
+                  const int id = p.c.table[(long long)u.b * p.c.table_stride + page];
+                  if (id < 0 || id >= p.c.num_pages) continue;
+                  const uint16_t* v =
+                      reinterpret_cast<const uint16_t*>(p.c.v + (size_t)row_offset(p.c, id, u.h, sl) * 16u) + r0 + d;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (word_not_finite<T>(v[i])) y[i] = __float_as_uint(__uint_as_float(y[i]) + T::unpack(v[i]).x);
+                }
+              }
+              float4 x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                // (an infinite value added above is kept by a copy that saw nothing else)
+                const bool raw = unsound && factor == 0.0f;
+                x[i] = make_float4(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1]),
+                                   __uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3]));
+                if (!raw) x[i] = make_float4(x[i].x * factor, x[i].y * factor, x[i].z * factor, x[i].w * factor);
+#pragma unroll
+                for (int k = 1; k < kCopies; ++k) {
+                  const float4 o = reinterpret_cast<const float4*>(scratch)[(size_t)((k - 1) * R + row) * (kRound / 4) +
+                                                                            d / 4 + (i ^ (lane & 7))];
+                  x[i] = make_float4(x[i].x + o.x, x[i].y + o.y, x[i].z + o.z, x[i].w + o.w);
+                }
+              }
+              if (writes) {
+                if (whole) {
+                  uint4* dst = reinterpret_cast<uint4*>(out_row + 2 * (r0 + d));
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    dst[i] = make_uint4(T::pack(x[2 * i].x, x[2 * i].y), T::pack(x[2 * i].z, x[2 * i].w),
+                                        T::pack(x[2 * i + 1].x, x[2 * i + 1].y), T::pack(x[2 * i + 1].z, x[2 * i + 1].w));
+                } else {
+                  float4* dst = reinterpret_cast<float4*>(part_row + r0 + d);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) dst[i] = x[i];
+                }
+              }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            scratch[tid * 32 + (i ^ lane)] =
-                (unsound && copy == 0 && own == 0.0f) ? __uint_as_float(y[i]) : __uint_as_float(y[i]) * own;
-          if (!(ok = softmax_sync(syncs, S))) break;
-          for (int r = tid >> 3; r < rows_here; r += 16) {
-            const int c4 = (tid & 7) * 4;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < kCopies; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += scratch[(k * R + r) * 32 + ((c4 + e) ^ ((k * R + r) & 31))];
-            if (whole) {
-              float top;
-              const float sum = row_sum(r, top), f = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-              const int g = u.rb * R + r, ti = g / p.G;
-              *reinterpret_cast<uint2*>(p.out + 2 * ((long long)(u.first + ti) * p.o_ts +
-                                                     (long long)(u.h * p.G + g - ti * p.G) * p.o_hs + d0 + c4)) =
-                  make_uint2(T::pack(v[0] * f, v[1] * f), T::pack(v[2] * f, v[3] * f));
-            } else {
-              *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.ws + geo.o(p.tk.B)) + (slot * R + r) * D + d0 + c4) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-            }
-          }
-          ok = softmax_sync(syncs, S);  // scratch (and, after the last run, Q and S.ml) is written again
+          // the scratch, Q and S.ml are written again
+          ok = softmax_sync(syncs, S);
         }
         if (!ok) break;
         if (tid == 0) S.unsound[u.ordinal % kFlags] = 0;
