@@ -189,12 +189,16 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
   if (bad && blockIdx.x == 0) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
   const long long total = pre[p.tk.B];
   const long long run = max((long long)kMinRun, (total + gridDim.x - 1) / gridDim.x);
-  if (blockIdx.x == 0) {
-    long long* hdr = reinterpret_cast<long long*>(p.ws);
-    for (int b = tid; b <= p.tk.B; b += kAttnThreads) hdr[1 + b] = pre[b];
-    if (tid == 0) hdr[0] = run;
-  }
+  if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<long long*>(p.ws) = run;
   const long long t_begin = (long long)blockIdx.x * run, t_end = min(total, t_begin + run);
+  if (tid == 0) {
+    SplitUnit s = {0, 0, 0, 0, 0, 0, 0};
+    if (t_begin < t_end) {
+      const Unit u = locate(p, pre, t_end - 1);
+      if (u.start >= t_begin && u.start + u.tiles > t_end) s = {u.start, u.tiles, u.h, u.rb, u.first, u.n, 0};
+    }
+    split_units(p)[blockIdx.x] = s;
+  }
   if (t_begin >= t_end) return;
 
   // ---- this warp's ring: one step = this warp's 16 keys of a tile
@@ -493,14 +497,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     const bool jok = jrow < u.n * p.G;
     const long long jtok = u.first + ji, jhead = u.h * p.G + (jrow - ji * p.G);
     const long long slot = 2LL * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
-    float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry().o(p.tk.B)) + (slot * kRows + jr) * D;
+    float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry().o()) + (slot * kRows + jr) * D;
     float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     if ((tid & 7) == 0 && jok) {
       if (whole) {
         if (p.lse) p.lse[jtok * ((long long)p.G * p.c.kv_heads) + jhead] = (top + log2f(sum)) * kLn2;
       } else {
-        float* ml = reinterpret_cast<float*>(p.ws + warp_geometry().ml(p.tk.B)) + (slot * kRows + jr) * 2;
+        float* ml = reinterpret_cast<float*>(p.ws + warp_geometry().ml()) + (slot * kRows + jr) * 2;
         ml[0] = top;
         ml[1] = sum;
       }
@@ -539,75 +543,55 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
 }
 
 // ---- joining the partial results of units that span CTAs -------------------------------
-// One warp per query row: the segments' maxima give their factors, then the
-// segments are summed in list order.
-constexpr int kJoinWarps = 4;
+// CTA (c, part): 64 columns of the unit that begins in CTA c's run. One warp per
+// query row: the segments' maxima give their factors, then the segments are
+// summed in list order.
+constexpr int kJoinWarps = 16;
 template <class T, bool kF8, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams p, const AttnGeometry geo) {
   grid_dependency_sync();
-  const int lane = threadIdx.x & 31;
-  const int Hq = p.G * p.c.kv_heads;
-  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (long long)p.tk.tokens * Hq) return;
-  const int tok = (int)(row / Hq), head = (int)(row - (long long)tok * Hq);
-  const int b = request_of_token(p.tk, tok);
-  if (b < 0 || b >= p.tk.B) return;
-  int first, n;
-  bool bad = false;
-  request_tokens(p.tk, b, first, n, bad);
-  if (tok < first || tok >= first + n) return;
-  const long long* hdr = reinterpret_cast<const long long*>(p.ws);
-  const long long run = hdr[0];
-  const int tiles = max(1, (clamped_len(p, b, bad) + geo.tile - 1) / geo.tile);
-  const int h = head / p.G, r = (tok - first) * p.G + head - h * p.G;
-  const int rbs = (int)(((long long)n * p.G + geo.rows - 1) / geo.rows);
-  const long long start = hdr[1 + b] + ((long long)h * rbs + r / geo.rows) * tiles;
-  const int c0 = (int)(start / run), c1 = (int)((start + tiles - 1) / run);
-  if (c0 == c1) return;  // one CTA had the whole unit and wrote it
-  const float* mls = reinterpret_cast<const float*>(p.ws + geo.ml(p.tk.B));
-  const float* os = reinterpret_cast<const float*>(p.ws + geo.o(p.tk.B));
-  const int jr = r % geo.rows;
-  auto slot_row = [&](int c) {
-    const long long slot = 2LL * c + (max(start, (long long)c * run) == (long long)c * run ? 0 : 1);
-    return slot * geo.rows + jr;
-  };
-  float top = kNegInf;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, mls[slot_row(c) * 2]);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  constexpr int kPer = D / 32;
-  float x[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) x[j] = 0.0f;
-  float sum = 0.0f;
-  for (int cb = c0; cb <= c1; cb += 32) {
-    const int c = cb + lane;
-    float w = 0.0f, ls = 0.0f;
-    if (c <= c1) {
-      const float2 ml = *reinterpret_cast<const float2*>(mls + slot_row(c) * 2);
-      w = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
-      ls = ml.y == ml.y ? ml.y * w : ml.y;
+  const int lane = threadIdx.x & 31, c0 = blockIdx.x, col = blockIdx.y * 64 + 2 * lane;
+  const SplitUnit u = split_units(p)[c0];
+  const long long run = *reinterpret_cast<const long long*>(p.ws);
+  if (u.tiles == 0) return;
+  const int c1 = (int)((u.start + u.tiles - 1) / run);
+  const float* mls = reinterpret_cast<const float*>(p.ws + geo.ml());
+  const float* os = reinterpret_cast<const float*>(p.ws + geo.o());
+  const long long slot0 = 2LL * c0 + (u.start == (long long)c0 * run ? 0 : 1);
+  const int rows = min(geo.rows, u.n * p.G - u.rb * geo.rows);
+  for (int jr = threadIdx.x >> 5; jr < rows; jr += kJoinWarps) {
+    auto slot_row = [&](int c) { return (c == c0 ? slot0 : 2LL * c) * geo.rows + jr; };
+    float top = kNegInf;
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, mls[slot_row(c) * 2]);
+    top = warp_max_f32(top);
+    float2 x = make_float2(0.0f, 0.0f);
+    float sum = 0.0f;
+    for (int cb = c0; cb <= c1; cb += 32) {
+      const int c = cb + lane;
+      float w = 0.0f, ls = 0.0f;
+      if (c <= c1) {
+        const float2 ml = *reinterpret_cast<const float2*>(mls + slot_row(c) * 2);
+        w = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
+        ls = ml.y == ml.y ? ml.y * w : ml.y;
+      }
+      const int cnt = min(32, c1 - cb + 1);
+#pragma unroll 8
+      for (int j = 0; j < cnt; ++j) {
+        const float2 y = *reinterpret_cast<const float2*>(os + slot_row(cb + j) * D + col);
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        sum += __shfl_sync(0xffffffffu, ls, j);
+        x.x = fmaf(y.x, wj, x.x);
+        x.y = fmaf(y.y, wj, x.y);
+      }
     }
-    const int cnt = min(32, c1 - cb + 1);
-#pragma unroll 4
-    for (int j = 0; j < cnt; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      sum += __shfl_sync(0xffffffffu, ls, j);
-      const float* src = os + slot_row(cb + j) * D + lane * kPer;
-      float y[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2) *reinterpret_cast<float2*>(y + e) = *reinterpret_cast<const float2*>(src + e);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) x[e] = fmaf(y[e], wj, x[e]);
-    }
+    float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
+    const int g = u.rb * geo.rows + jr, ti = g / p.G;
+    const long long tok = u.first + ti, head = u.h * p.G + g - ti * p.G;
+    *reinterpret_cast<uint32_t*>(p.out + 2 * (tok * p.o_ts + head * p.o_hs + col)) = T::pack(x.x * factor, x.y * factor);
+    if (lane == 0 && blockIdx.y == 0 && p.lse)
+      p.lse[tok * ((long long)p.G * p.c.kv_heads) + head] = (top + log2f(sum)) * kLn2;
   }
-  float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-  if (kF8 && p.c.v_scale) factor *= p.c.v_scale[h];
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + 2 * ((long long)tok * p.o_ts + (long long)head * p.o_hs)) +
-                  lane * (kPer / 2);
-#pragma unroll
-  for (int e = 0; e < kPer; e += 2) dst[e / 2] = T::pack(x[e] * factor, x[e + 1] * factor);
-  if (lane == 0 && p.lse) p.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
 template <class T, bool kF8, int D>
@@ -639,7 +623,7 @@ int launch(const AttnParams& p, int sms, void* stream) {
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, attention_kernel<T, kF8, D>, p);
   if (e != cudaSuccess) return (int)e;
-  return launch_join(p, warp_geometry(), std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, kF8, D, stream);
+  return launch_join(p, warp_geometry(), grid, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, kF8, D, stream);
 }
 
 template <class T, bool kF8>
@@ -650,8 +634,7 @@ int pick_dim(const AttnParams& p, int d, int sms, void* stream) {
 }
 
 template <class T, bool kF8, int D>
-int launch_join_dim(const AttnParams& p, const AttnGeometry& g, void* stream) {
-  const long long rows = (long long)p.tk.tokens * p.G * p.c.kv_heads;
+int launch_join_dim(const AttnParams& p, const AttnGeometry& g, int grid, void* stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -659,27 +642,29 @@ int launch_join_dim(const AttnParams& p, const AttnGeometry& g, void* stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = (cudaStream_t)stream;
-  cfg.gridDim = dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3((unsigned)grid, D / 64);
   cfg.blockDim = dim3(32 * kJoinWarps);
   return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, kF8, D>, p, g);
 }
 template <class T, bool kF8>
-int launch_join_type(const AttnParams& p, const AttnGeometry& g, int d, void* stream) {
-  return d == 64    ? launch_join_dim<T, kF8, 64>(p, g, stream)
-         : d == 128 ? launch_join_dim<T, kF8, 128>(p, g, stream)
-                    : launch_join_dim<T, kF8, 256>(p, g, stream);
+int launch_join_type(const AttnParams& p, const AttnGeometry& g, int grid, int d, void* stream) {
+  return d == 64    ? launch_join_dim<T, kF8, 64>(p, g, grid, stream)
+         : d == 128 ? launch_join_dim<T, kF8, 128>(p, g, grid, stream)
+                    : launch_join_dim<T, kF8, 256>(p, g, grid, stream);
 }
 
 }  // namespace
 
-int launch_join(const AttnParams& p, const AttnGeometry& g, int dtype, bool f8, int head_dim, void* stream) {
+int launch_join(const AttnParams& p, const AttnGeometry& g, int grid, int dtype, bool f8, int head_dim, void* stream) {
   if (dtype == DFLASH_BF16)
-    return f8 ? launch_join_type<Bf16, true>(p, g, head_dim, stream) : launch_join_type<Bf16, false>(p, g, head_dim, stream);
-  return f8 ? launch_join_type<F16, true>(p, g, head_dim, stream) : launch_join_type<F16, false>(p, g, head_dim, stream);
+    return f8 ? launch_join_type<Bf16, true>(p, g, grid, head_dim, stream)
+              : launch_join_type<Bf16, false>(p, g, grid, head_dim, stream);
+  return f8 ? launch_join_type<F16, true>(p, g, grid, head_dim, stream)
+            : launch_join_type<F16, false>(p, g, grid, head_dim, stream);
 }
 
-size_t attention_workspace(int B, int head_dim) {
-  const size_t a = warp_geometry().bytes(B, head_dim), b = tc_geometry(128, head_dim).bytes(B, head_dim);
+size_t attention_workspace(int head_dim) {
+  const size_t a = warp_geometry().bytes(head_dim), b = tc_geometry(128, head_dim).bytes(head_dim);
   return a > b ? a : b;
 }
 

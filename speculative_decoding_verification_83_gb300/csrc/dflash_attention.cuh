@@ -24,16 +24,26 @@ __device__ __forceinline__ float ex2(float x) {
 // the request's keys, `tile` at a time; units follow each other request by
 // request, head by head, row block by row block.
 //
-// Workspace: [0] tiles per CTA, [1 .. B + 1] tiles before each request
-// (64-bit); then for each CTA two slots of partial results, rows x (maximum,
-// sum), then rows x D.
+// The unit that begins in a CTA's run and goes on in the next CTA's (tiles 0:
+// there is none). Every split unit has exactly one such CTA.
+struct SplitUnit {
+  long long start;  // index of its first tile in the whole list
+  int tiles, h, rb, first, n, unused;
+};
+
+// Workspace: tiles per CTA (64-bit), a SplitUnit for each CTA, then for each
+// CTA two slots of partial results: rows x (maximum, sum), then rows x D. Slot
+// 0 is the segment that begins with the CTA's run, slot 1 one that begins
+// inside it.
 struct AttnGeometry {
   int rows, tile, ctas;
-  __host__ __device__ static size_t header(int B) { return ((size_t)(B + 2) * 8 + 255) & ~(size_t)255; }
-  __host__ __device__ size_t ml(int B) const { return header(B); }
-  __host__ __device__ size_t o(int B) const { return header(B) + (size_t)ctas * 2 * rows * 2 * sizeof(float); }
-  __host__ __device__ size_t bytes(int B, int D) const { return o(B) + (size_t)ctas * 2 * rows * D * sizeof(float); }
+  __host__ __device__ size_t ml() const { return 256 + ((size_t)ctas * sizeof(SplitUnit) + 255) / 256 * 256; }
+  __host__ __device__ size_t o() const { return ml() + (size_t)ctas * 2 * rows * 2 * sizeof(float); }
+  __host__ __device__ size_t bytes(int D) const { return o() + (size_t)ctas * 2 * rows * D * sizeof(float); }
 };
+__device__ __forceinline__ SplitUnit* split_units(const AttnParams& p) {
+  return reinterpret_cast<SplitUnit*>(p.ws + 256);
+}
 
 __device__ __forceinline__ int clamped_len(const AttnParams& p, int b, bool& bad) {
   const int L = p.lens[b];
@@ -53,7 +63,8 @@ __device__ __forceinline__ int row_blocks(int n, int G) {
 }
 
 // Joins the partial results of the units that span CTAs, and writes their rows.
-int launch_join(const AttnParams& p, const AttnGeometry& g, int dtype, bool f8, int head_dim, void* stream);
+// grid: the CTAs of the kernel before it.
+int launch_join(const AttnParams& p, const AttnGeometry& g, int grid, int dtype, bool f8, int head_dim, void* stream);
 
 // The tensor-memory kernel (dflash_attention_tc.cu): units of 32, 64 or 128 rows.
 AttnGeometry tc_geometry(int rows, int head_dim);

@@ -43,6 +43,9 @@ constexpr int kMmaWarp = 4;
 constexpr int kLoadWarp0 = 5, kLoadWarps = 4;
 constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
 constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the reference
+// A unit's end and the next one's beginning take a CTA about as long as this
+// many tiles: the list counts them, so that runs with many ends are shorter.
+constexpr int kEndTiles = 4;
 constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at once
 
 template <int D>
@@ -213,7 +216,8 @@ __device__ __forceinline__ bool softmax_sync(uint32_t& phase, TcShared& S) {
   return __all_sync(0xffffffffu, ok);
 }
 
-// A position in the list of units, moved on tile by tile.
+// A position in the list of units. A unit takes tiles + kEndTiles places; the
+// tiles come first.
 template <int R, int kKeys>
 struct Cursor {
   int b, h, rb, L, first, n, tiles, rbs, ordinal;
@@ -225,28 +229,37 @@ struct Cursor {
     tiles = tiles_of<kKeys>(L);
     rbs = row_blocks<R>(n, p.G);
   }
-  // the unit of tile t, request b0 being the one it falls in and pre the tiles before that
-  __device__ __forceinline__ void seek(const AttnParams& p, int b0, long long pre, long long t) {
+  // The first tile at place t or after it, before t_end (t_end: there is none);
+  // request b0 is the one t falls in, pre the places before that.
+  __device__ __forceinline__ long long seek(const AttnParams& p, int b0, long long pre, long long t, long long t_end) {
     b = b0;
     request(p);
-    const long long k = (t - pre) / tiles;
+    const long long k = (t - pre) / (tiles + kEndTiles);
     h = (int)(k / rbs);
     rb = (int)(k - (long long)h * rbs);
-    start = pre + k * tiles;
+    start = pre + k * (tiles + kEndTiles);
     ordinal = 0;
+    return t < start + tiles ? t : next(p, t_end);
   }
-  __device__ __forceinline__ long long end() const { return start + tiles; }
-  __device__ __forceinline__ void next(const AttnParams& p) {
-    start += tiles;
+  __device__ __forceinline__ long long end(long long t_end) const { return min(t_end, start + tiles); }
+  // Moves to the next unit and returns its first tile, or t_end.
+  __device__ __forceinline__ long long next(const AttnParams& p, long long t_end) {
+    if (start + tiles + kEndTiles >= t_end) return t_end;
+    start += tiles + kEndTiles;
     ++ordinal;
-    if (++rb < rbs) return;
+    if (++rb < rbs) return start;
     rb = 0;
-    if (++h < p.c.kv_heads) return;
+    if (++h < p.c.kv_heads) return start;
     h = 0;
     do {
       ++b;
       request(p);
-    } while (rbs == 0);  // a request after the list's last tile is never asked for
+    } while (rbs == 0);  // (the list goes on, so there is one)
+    return start;
+  }
+  // The tile after t, or t_end.
+  __device__ __forceinline__ long long step(const AttnParams& p, long long t, long long t_end) {
+    return t + 1 < start + tiles ? min(t + 1, t_end) : next(p, t_end);
   }
 };
 
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
   auto request_tiles = [&](int b) {
     int first, n;
     request_tokens(p.tk, b, first, n, bad);
-    return (long long)row_blocks<R>(n, p.G) * p.c.kv_heads * tiles_of<kKeys>(clamped_len(p, b, bad));
+    return (long long)row_blocks<R>(n, p.G) * p.c.kv_heads * (tiles_of<kKeys>(clamped_len(p, b, bad)) + kEndTiles);
   };
   for (int b = b_lo; b < b_hi; ++b) mine += request_tiles(b);
   before = mine;
@@ -318,13 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
   const long long run = max((long long)kMinRun, (total + gridDim.x - 1) / gridDim.x);
   const long long t_begin = (long long)blockIdx.x * run, t_end = min(total, t_begin + run);
   if (blockIdx.x == 0) {
-    long long* hdr = reinterpret_cast<long long*>(p.ws);
-    long long at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      hdr[1 + b] = at;
-      at += request_tiles(b);
-    }
-    if (tid == 0) hdr[0] = run;
+    if (tid == 0) *reinterpret_cast<long long*>(p.ws) = run;
     if (bad) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
   }
   if (t_begin < t_end && before <= t_begin && t_begin < before + mine) {
@@ -344,9 +351,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
   fence_after();
   const uint32_t tmem = S.tmem;
 
+  SplitUnit split = {0, 0, 0, 0, 0, 0, 0};
   if (t_begin < t_end) {
     Cursor<R, kKeys> u;
-    u.seek(p, S.first_b, S.first_pre, t_begin);
+    const long long t_first = u.seek(p, S.first_b, S.first_pre, t_begin, t_end);
     bool ok = true;
 
     if (warp >= kLoadWarp0) {
@@ -395,10 +403,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         }
         if (found) S.unsound[ordinal % kFlags] = 1;
       };
-      look_up(t_begin);
+      if (t_first < t_end) look_up(t_first);
       int st = 0;
       uint32_t round = 0;
-      for (long long t = t_begin; t < t_end; ++t) {
+      for (long long t = t_first; t < t_end;) {
         if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
         const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
         const uint32_t kb = ring + st * 2 * W::kHalf;
@@ -425,10 +433,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           // arrives by itself once this thread's copies have landed
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&S.full[st])) : "memory");
         }
-        if (t + 1 < t_end) {
-          if (t + 1 >= u.end()) u.next(p);
-          look_up(t + 1);
-        }
+        t = u.step(p, t, t_end);
+        if (t < t_end) look_up(t);
         if (++st == kStages) {
           st = 0;
           ++round;
@@ -442,7 +448,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         constexpr uint32_t type = std::is_same<T, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t id_s = (1u << 4) | type | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
         constexpr uint32_t id_o = (1u << 4) | type | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
-        const int count = (int)(t_end - t_begin);
         // O += P V of tile j; fresh: the unit's (or the run's) first
         auto sum_values = [&](int j, bool fresh) {
           const int st = j % kStages, buf = j & 1;
@@ -459,12 +464,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         };
         bool fresh = true, prev_fresh = true;  // of tile j, and of the last whose P V is not issued yet
         int units = 0, summed = 0;             // units begun, tiles whose P V is issued
-        for (int j = 0; j < count && ok; ++j) {
-          const long long t = t_begin + j;
-          if (j > 0 && t >= u.end()) {
-            u.next(p);
-            fresh = true;
-          }
+        int j = 0;
+        for (long long t = t_first; t < t_end && ok; ++j) {
           if (fresh) {
             // the next unit's Q comes only after the last one's sums are out
             if (j > 0 && (ok = sum_values(j - 1, prev_fresh))) summed = j;
@@ -482,10 +483,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
                    operand(kb + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16), id_s, k > 0);
           mma_commit(&S.s_full[j & 1]);
           if (summed < j && (ok = sum_values(j - 1, prev_fresh))) summed = j;
+          if (!ok) break;
           prev_fresh = fresh;
-          fresh = false;
+          const int unit = u.ordinal;
+          t = u.step(p, t, t_end);
+          fresh = u.ordinal != unit;
         }
-        if (ok) ok = sum_values(count - 1, prev_fresh);
+        if (ok && j > 0) ok = sum_values(j - 1, prev_fresh);
         mma_commit(&S.drained);  // nothing is left in flight when the tensor memory is freed
         mbar_wait_landed(&S.drained, 0);
       }
@@ -504,9 +508,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       float* scratch = reinterpret_cast<float*>(mem);  // Q's place, between units
       int j = 0;
       uint32_t syncs = 0;
-      long long t = t_begin;
+      long long t = t_first;
       while (t < t_end && ok) {
-        const long long u_end = min(t_end, u.end()), u_begin = t;
+        const long long u_end = u.end(t_end), u_begin = t;
         // ---- Q, laid out kCopies times
         const int rows_here = min(R, u.n * p.G - u.rb * R);
         constexpr int kPieces = D / 8;
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           break;
         }
         fence_after();
-        const bool whole = u_begin == u.start && u_end == u.end();
+        const bool whole = u_begin == u.start && u_end == u.start + u.tiles;
         S.ml[2 * tid] = m;
         S.ml[2 * tid + 1] = l;
         const int unsound = *reinterpret_cast<volatile int*>(&S.unsound[u.ordinal % kFlags]);
@@ -645,10 +649,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         const long long q_tok = u.first + ti, q_head = u.h * p.G + g - ti * p.G;
         const bool writes = copy == 0 && row < rows_here;  // the first copy's thread writes the row
         unsigned char* out_row = p.out + 2 * (q_tok * p.o_ts + q_head * p.o_hs);
-        float* part_row = reinterpret_cast<float*>(p.ws + geo.o(p.tk.B)) + (slot * R + row) * D;
+        float* part_row = reinterpret_cast<float*>(p.ws + geo.o()) + (slot * R + row) * D;
         if (writes) {
           if (!whole) {
-            float* ml = reinterpret_cast<float*>(p.ws + geo.ml(p.tk.B)) + (slot * R + row) * 2;
+            float* ml = reinterpret_cast<float*>(p.ws + geo.ml()) + (slot * R + row) * 2;
             ml[0] = best;
             ml[1] = sum;
           } else if (p.lse) {
@@ -733,11 +737,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         if (!ok) break;
         if (tid == 0) S.unsound[u.ordinal % kFlags] = 0;
         fence_before();
-        if (t < t_end) u.next(p);
+        if (u_begin == u.start && !whole) split = {u.start, u.tiles, u.h, u.rb, u.first, u.n, 0};
+        t = u.next(p, t_end);
       }
     }
     if (!ok && lane == 0) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
   }
+  if (tid == 0) split_units(p)[blockIdx.x] = split;
   fence_before();
   __syncthreads();
   fence_after();
@@ -765,12 +771,13 @@ int launch(const AttnParams& p, int sms, void* stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = (cudaStream_t)stream;
-  cfg.gridDim = dim3((unsigned)(sms < kTcCtas ? sms : kTcCtas));
+  const int grid = sms < kTcCtas ? sms : kTcCtas;
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = W::kSmem;
   e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, D, R>, p, geo);
   if (e != cudaSuccess) return (int)e;
-  return launch_join(p, geo, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, false, D, stream);
+  return launch_join(p, geo, grid, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, false, D, stream);
 }
 template <class T, int R>
 int pick_dim(const AttnParams& p, int d, int sms, void* stream) {

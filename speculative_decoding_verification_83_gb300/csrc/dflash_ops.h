@@ -61,7 +61,7 @@ struct AttnParams {
   unsigned char* ws;
   uint32_t* status;
 };
-size_t attention_workspace(int B, int head_dim);
+size_t attention_workspace(int head_dim);
 int launch_attention(const AttnParams& p, int dtype, int cache_dtype, int head_dim, int sms, void* stream);
 
 struct DistillParams {

@@ -191,7 +191,7 @@ int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void*
 
 size_t dflash_attention_workspace_bytes(int batch, int head_dim) {
   if (batch < 1 || batch > kOpsMaxB || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
-  return attention_workspace(batch, head_dim);
+  return attention_workspace(head_dim);
 }
 
 int dflash_paged_attention(const dflash_paged_cache* cache, const void* q, void* out, float* lse, int dtype,
@@ -214,7 +214,7 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const void* q, void*
   if (tokens == 0) return DFLASH_OK;
   if ((rc = check_rows(q, strides[0], strides[1], "q")) || (rc = check_rows(out, strides[2], strides[3], "out")))
     return rc;
-  const size_t need = attention_workspace(cache->batch, cache->head_dim);
+  const size_t need = attention_workspace(cache->head_dim);
   if (!workspace || workspace_bytes < need)
     return fail(DFLASH_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed",
                 workspace ? workspace_bytes : (size_t)0, need);
