@@ -99,11 +99,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                : "r"(a)
                : "memory");
 }
-// two e4m3 values (the low 16 bits) as two f16 values
-__device__ __forceinline__ uint32_t widen2(uint32_t v) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
-  return r;
+// four e4m3 values as two pairs of f16 values
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 
 template <bool kF8, int D>
@@ -111,11 +111,13 @@ struct Shape {
   static constexpr int kRowBytes = kF8 ? D : 2 * D;
   static constexpr int kHalfStage = kWarpKeys * kRowBytes;  // K or V of one warp's step
   static constexpr int kStageBytes = 2 * kHalfStage * kWarps;
-  static constexpr int kStages = kStageBytes >= 65536 ? 3 : (98304 / kStageBytes < 8 ? 98304 / kStageBytes : 8);
+  // CTAs per SM, and a ring that fills the SM's shared memory with them
+  static constexpr int kPerSm = kStageBytes <= 32768 ? 3 : 1;
+  static constexpr int kRing = kPerSm == 3 ? 65536 : 196608;
+  static constexpr int kStages = kRing / kStageBytes;
   static constexpr int kCols = 32;  // columns of O joined at a time
   static constexpr size_t kMerge = (size_t)kWarps * kRows * (kCols + 1) * sizeof(float);
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kMerge + 2 * kWarps * kRows * sizeof(float);
-  static constexpr int kPerSm = kSmem > 110000 ? 1 : 2;
 };
 
 // Shared-memory place of 16-byte piece c of row r: pieces of a row are
@@ -142,7 +144,9 @@ template <class T, bool kF8, int kRowBytes>
 __device__ __forceinline__ float value_at(const unsigned char* tile, int r, int d) {
   if (kF8) {
     const unsigned char b = tile[piece_at<kRowBytes>(r, d >> 4) + (d & 15)];
-    return F16::unpack(widen2(b)).x;
+    uint32_t lo, hi;
+    widen4(b, lo, hi);
+    return F16::unpack(lo).x;
   }
   return T::unpack(*reinterpret_cast<const uint16_t*>(tile + piece_at<kRowBytes>(r, d >> 3) + 2 * (d & 7))).x;
 }
@@ -345,8 +349,11 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
           ldsm4(k4, kb + piece_at<S::kRowBytes>((lane & 7) + ((lane >> 4) << 3), ks + ((lane >> 3) & 1)));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            M::mma(s[0], q[ks + j], widen2(k4[j]), widen2(k4[j] >> 16));
-            M::mma(s[1], q[ks + j], widen2(k4[2 + j]), widen2(k4[2 + j] >> 16));
+            uint32_t lo, hi;
+            widen4(k4[j], lo, hi);
+            M::mma(s[0], q[ks + j], lo, hi);
+            widen4(k4[2 + j], lo, hi);
+            M::mma(s[1], q[ks + j], lo, hi);
           }
         }
       }
@@ -455,10 +462,11 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
           ldsm4t(v4, vb + piece_at<S::kRowBytes>((lane & 7) + (((lane >> 3) & 1) << 3), ds + (lane >> 4)));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            M::mma(o[2 * (ds + j)], pa, widen2(__byte_perm(v4[2 * j], 0, 0x4420)),
-                   widen2(__byte_perm(v4[2 * j + 1], 0, 0x4420)));
-            M::mma(o[2 * (ds + j) + 1], pa, widen2(__byte_perm(v4[2 * j], 0, 0x4431)),
-                   widen2(__byte_perm(v4[2 * j + 1], 0, 0x4431)));
+            uint32_t even0, odd0, even1, odd1;
+            widen4(__byte_perm(v4[2 * j], 0, 0x3120), even0, odd0);
+            widen4(__byte_perm(v4[2 * j + 1], 0, 0x3120), even1, odd1);
+            M::mma(o[2 * (ds + j)], pa, even0, even1);
+            M::mma(o[2 * (ds + j) + 1], pa, odd0, odd1);
           }
         }
       }

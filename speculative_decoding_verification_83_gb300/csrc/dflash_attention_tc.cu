@@ -45,7 +45,7 @@ constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
 constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the reference
 // A unit's end and the next one's beginning take a CTA about as long as this
 // many tiles: the list counts them, so that runs with many ends are shorter.
-constexpr int kEndTiles = 4;
+constexpr int kEndTiles = 3;
 constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at once
 
 template <int D>

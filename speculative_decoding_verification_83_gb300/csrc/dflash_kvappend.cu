@@ -21,6 +21,7 @@ namespace dflash {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kMaxGroup = 8;  // tokens per block
 
 __device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
   uint16_t r;
@@ -60,119 +61,164 @@ __device__ __forceinline__ void store_cache(unsigned char* base, uint32_t row, i
   }
 }
 
-// One token per blockIdx.x; the token's work is split over blockIdx.y. A work
-// item is one pair of 8-value vectors (v and v + D/16) of one head: heads of
-// k, then v, then q. Half-split rotation with rot == D pairs the two vectors;
-// with rot < D the pairing is inside the first rot values, so the item's
-// vectors are chosen by the caller (vector_pair).
-template <class T, bool kF8, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
-  constexpr int kItems = D / 16;  // vector pairs per head
-  __shared__ float2 turn[D / 2];
-  grid_dependency_sync();
-  const int t = blockIdx.x;
-  const int half = p.rot >> 1;
-  const int b = request_of_token(p.tk, t);
-  if (b < 0 || b >= p.tk.B) return;
-  int first, n;
-  bool bad = false;
-  request_tokens(p.tk, b, first, n, bad);
-  if (t < first || t >= first + n) return;
-  const int len = p.lens[b];
-  // positions stay inside the page table's row
-  const long long pos64 = (long long)len + (t - first);
-  const long long cap = (long long)p.c.max_pages * p.c.page_size;
-  if (len < 0 || pos64 >= cap || pos64 > 0x7fffffffLL) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
-    return;
+// Where a token goes.
+struct Place {
+  int pos;   // -1: nowhere (it belongs to no request, or its position is bad)
+  int page;  // -1: its page is bad
+  int slot;
+};
+
+// The request that holds packed token t, by one warp: each round looks at 32
+// evenly spaced offsets.
+__device__ __forceinline__ int request_of_token_warp(const PackedTokens& k, int t) {
+  if (!k.q_start) return t / k.q_per;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = k.B;  // the first b with q_start[b] > t is in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const uint32_t over = __ballot_sync(0xffffffffu, at >= hi || k.q_start[at] > t);
+    const int f = over ? __ffs(over) - 1 : 32;  // the first place that lies beyond t
+    const int new_hi = f < 32 ? min(hi, lo + f * step) : hi;
+    lo = f > 0 ? lo + (f - 1) * step + 1 : lo;
+    hi = f > 0 ? new_hi : lo;
   }
-  if (bad && threadIdx.x == 0 && blockIdx.y == 0) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
-  const int pos = (int)pos64;
-  int page, slot;
-  split_position(p.c, pos, page, slot);
-  const int id = p.c.table[(long long)b * p.c.table_stride + page];
-  const bool have_page = id >= 0 && id < p.c.num_pages;
-  if (!have_page && threadIdx.x == 0 && blockIdx.y == 0) raise_status(p.status, DFLASH_STATUS_BAD_PAGE);
-  for (int j = threadIdx.x; j < half; j += kAppendThreads) {
-    const unsigned long long a = p.phases[j] * (unsigned long long)pos;
-    float s, c;
-    sincospif((float)(int32_t)(uint32_t)(a >> 32) * 0x1p-31f, &s, &c);
-    turn[j] = make_float2(c, s);
+  return lo - 1;
+}
+
+// A block takes `group` tokens and 256 kBatch of their work items; blockIdx.y
+// numbers its share. A work item is one pair of 8-value vectors of one head
+// (heads of k, then v, then q): the two halves of rotated pairs, or two
+// neighbours. The items' values are read before it is known where they go, so
+// that the chain of offset, length, page and slot costs no time of its own.
+template <class T, bool kF8, int D, int kBatch>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int group) {
+  constexpr int kItems = D / 16;  // vector pairs per head
+  __shared__ Place place[kMaxGroup];
+  __shared__ float2 turn[kMaxGroup * D / 2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_sync();
+  const int t0 = blockIdx.x * group, nt = min(group, p.tk.tokens - t0);
+  const int half = p.rot >> 1, rv = p.rot >> 4;
+  const int heads = 2 * p.c.kv_heads + p.q_heads, items = heads * kItems;
+
+  // ---- the values
+  uint4 x[kBatch], y[kBatch];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int w = (blockIdx.y * kBatch + k) * kAppendThreads + tid;
+    if (w >= nt * items) continue;
+    const int ti = w / items, hd = (w - ti * items) / kItems, i = w % kItems;
+    const long long t = t0 + ti;
+    const unsigned char* src = hd < p.c.kv_heads       ? p.k + 2 * (t * p.k_ts + (long long)hd * p.k_hs)
+                               : hd < 2 * p.c.kv_heads ? p.v + 2 * (t * p.v_ts + (long long)(hd - p.c.kv_heads) * p.v_hs)
+                                                       : p.q + 2 * (t * p.q_ts + (long long)(hd - 2 * p.c.kv_heads) * p.q_hs);
+    const bool split = !p.interleaved && i < rv;
+    const int va = p.interleaved || i >= rv ? 2 * i : i, vb = split ? i + rv : va + 1;
+    x[k] = reinterpret_cast<const uint4*>(src)[va];
+    y[k] = reinterpret_cast<const uint4*>(src)[vb];
+  }
+
+  // ---- where the tokens go, and their angles
+  for (int ti = warp; ti < nt; ti += kAppendThreads / 32) {
+    const int t = t0 + ti, b = request_of_token_warp(p.tk, t);
+    Place pl = {-1, -1, 0};
+    uint32_t bits = 0;
+    if (b >= 0 && b < p.tk.B) {
+      int first, n;
+      bool bad = false;
+      request_tokens(p.tk, b, first, n, bad);
+      if (t >= first && t < first + n) {
+        const int len = p.lens[b];
+        // positions stay inside the page table's row
+        const long long pos = (long long)len + (t - first), cap = (long long)p.c.max_pages * p.c.page_size;
+        if (bad) bits |= DFLASH_STATUS_BAD_LENGTH;
+        if (len < 0 || pos >= cap || pos > 0x7fffffffLL) {
+          bits |= DFLASH_STATUS_BAD_LENGTH;
+        } else {
+          int page;
+          pl.pos = (int)pos;
+          split_position(p.c, pl.pos, page, pl.slot);
+          const int id = p.c.table[(long long)b * p.c.table_stride + page];
+          if (id >= 0 && id < p.c.num_pages)
+            pl.page = id;
+          else
+            bits |= DFLASH_STATUS_BAD_PAGE;
+        }
+      }
+    }
+    if (lane == 0) {
+      place[ti] = pl;
+      if (bits && blockIdx.y == 0) raise_status(p.status, bits);
+    }
+    for (int j = lane; j < half; j += 32) {
+      const unsigned long long a = p.phases[j] * (unsigned long long)(unsigned)pl.pos;
+      float s, c;
+      sincospif((float)(int32_t)(uint32_t)(a >> 32) * 0x1p-31f, &s, &c);
+      turn[ti * half + j] = make_float2(c, s);
+    }
   }
   __syncthreads();
 
-  const int heads = 2 * p.c.kv_heads + (p.q ? p.q_heads : 0);
-  const int items = heads * kItems;
-  for (int w = blockIdx.y * kAppendThreads + threadIdx.x; w < items; w += gridDim.y * kAppendThreads) {
-    const int hd = w / kItems, i = w % kItems;
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int w = (blockIdx.y * kBatch + k) * kAppendThreads + tid;
+    if (w >= nt * items) continue;
+    const int ti = w / items, hd = (w - ti * items) / kItems, i = w % kItems;
+    const Place pl = place[ti];
+    if (pl.pos < 0) continue;
     const bool is_k = hd < p.c.kv_heads, is_v = !is_k && hd < 2 * p.c.kv_heads;
     const int head = is_k ? hd : is_v ? hd - p.c.kv_heads : hd - 2 * p.c.kv_heads;
-    const unsigned char* src =
-        is_k ? p.k + 2 * ((long long)t * p.k_ts + (long long)head * p.k_hs)
-             : is_v ? p.v + 2 * ((long long)t * p.v_ts + (long long)head * p.v_hs)
-                    : p.q + 2 * ((long long)t * p.q_ts + (long long)head * p.q_hs);
-    // the item's two vectors: a rotated pair (i < rot/16), else two of the
-    // rest, which are copied
-    const int rv = p.rot / 16;
-    int va, vb;
-    if (!p.interleaved && i < rv) {
-      va = i;
-      vb = i + rv;
-    } else if (!p.interleaved) {
-      va = 2 * rv + 2 * (i - rv);
-      vb = va + 1;
-    } else {
-      va = 2 * i;
-      vb = 2 * i + 1;
-    }
-    float x[8], y[8];
-    unpack8<T>(reinterpret_cast<const uint4*>(src)[va], x);
-    unpack8<T>(reinterpret_cast<const uint4*>(src)[vb], y);
+    const bool split = !p.interleaved && i < rv;
+    const int va = p.interleaved || i >= rv ? 2 * i : i, vb = split ? i + rv : va + 1;
+    float a[8], b[8];
+    unpack8<T>(x[k], a);
+    unpack8<T>(y[k], b);
     if (!is_v && i < rv) {
-      if (!p.interleaved) {
+      const float2* tn = turn + ti * half + 8 * i;
+      if (split) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 cs = turn[8 * i + e];
-          const float a = x[e] * cs.x - y[e] * cs.y, o = y[e] * cs.x + x[e] * cs.y;
-          x[e] = a;
-          y[e] = o;
+          const float2 cs = tn[e];
+          const float r = a[e] * cs.x - b[e] * cs.y, o = b[e] * cs.x + a[e] * cs.y;
+          a[e] = r;
+          b[e] = o;
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 cs = turn[8 * i + e], ct = turn[8 * i + 4 + e];
-          const float a = x[2 * e] * cs.x - x[2 * e + 1] * cs.y, o = x[2 * e + 1] * cs.x + x[2 * e] * cs.y;
-          x[2 * e] = a;
-          x[2 * e + 1] = o;
-          const float a2 = y[2 * e] * ct.x - y[2 * e + 1] * ct.y, o2 = y[2 * e + 1] * ct.x + y[2 * e] * ct.y;
-          y[2 * e] = a2;
-          y[2 * e + 1] = o2;
+          const float2 cs = tn[e], ct = tn[4 + e];
+          const float r = a[2 * e] * cs.x - a[2 * e + 1] * cs.y, o = a[2 * e + 1] * cs.x + a[2 * e] * cs.y;
+          a[2 * e] = r;
+          a[2 * e + 1] = o;
+          const float r2 = b[2 * e] * ct.x - b[2 * e + 1] * ct.y, o2 = b[2 * e + 1] * ct.x + b[2 * e] * ct.y;
+          b[2 * e] = r2;
+          b[2 * e + 1] = o2;
         }
       }
     }
     if (is_k || is_v) {
-      if (have_page) {
-        const uint32_t row = row_offset(p.c, id, head, slot);
+      if (pl.page >= 0) {
+        const uint32_t row = row_offset(p.c, pl.page, head, pl.slot);
         const float* sc = is_k ? p.c.k_scale : p.c.v_scale;
         const float z = kF8 && sc ? sc[head] : 1.0f;
         unsigned char* base = is_k ? p.c.k : p.c.v;
-        store_cache<T, kF8>(base, row, va, x, z);
-        store_cache<T, kF8>(base, row, vb, y, z);
+        store_cache<T, kF8>(base, row, va, a, z);
+        store_cache<T, kF8>(base, row, vb, b, z);
       }
     } else {
-      uint4* dst = reinterpret_cast<uint4*>(p.q_out + 2 * ((long long)t * p.qo_ts + (long long)head * p.qo_hs));
-      dst[va] = pack8<T>(x);
-      dst[vb] = pack8<T>(y);
+      uint4* dst =
+          reinterpret_cast<uint4*>(p.q_out + 2 * ((long long)(t0 + ti) * p.qo_ts + (long long)head * p.qo_hs));
+      dst[va] = pack8<T>(a);
+      dst[vb] = pack8<T>(b);
     }
   }
 }
 
-template <class T, bool kF8, int D>
-int launch(const AppendParams& p, void* stream) {
-  const int items = (2 * p.c.kv_heads + (p.q ? p.q_heads : 0)) * (D / 16);
-  int split = (items + kAppendThreads - 1) / kAppendThreads;
+template <class T, bool kF8, int D, int kBatch>
+int launch_batch(const AppendParams& p, int group, int items, void* stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.tk.tokens, (unsigned)split);
+  const int share = kAppendThreads * kBatch;
+  cfg.gridDim = dim3((unsigned)((p.tk.tokens + group - 1) / group), (unsigned)((group * items + share - 1) / share));
   cfg.blockDim = dim3(kAppendThreads);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
@@ -180,12 +226,24 @@ int launch(const AppendParams& p, void* stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, append_kernel<T, kF8, D>, p);
+  return (int)cudaLaunchKernelEx(&cfg, append_kernel<T, kF8, D, kBatch>, p, group);
+}
+
+// Few tokens: one item a thread, over as many blocks as that gives. Many: 4
+// items a thread and as many tokens a block as they make.
+template <class T, bool kF8, int D>
+int launch(const AppendParams& p, void* stream) {
+  const int items = (2 * p.c.kv_heads + p.q_heads) * (D / 16);
+  if ((long long)p.tk.tokens * items <= 1 << 17) return launch_batch<T, kF8, D, 1>(p, 1, items, stream);
+  const int fit = 4 * kAppendThreads / items, group = fit < 1 ? 1 : fit > kMaxGroup ? kMaxGroup : fit;
+  return launch_batch<T, kF8, D, 4>(p, group, items, stream);
 }
 
 template <class T, bool kF8>
 int pick_dim(const AppendParams& p, int d, void* stream) {
-  return d == 64 ? launch<T, kF8, 64>(p, stream) : d == 128 ? launch<T, kF8, 128>(p, stream) : launch<T, kF8, 256>(p, stream);
+  return d == 64    ? launch<T, kF8, 64>(p, stream)
+         : d == 128 ? launch<T, kF8, 128>(p, stream)
+                    : launch<T, kF8, 256>(p, stream);
 }
 
 }  // namespace

@@ -31,20 +31,6 @@ __device__ __forceinline__ void request_tokens(const PackedTokens& t, int b, int
   bad |= first != s || last != e;
 }
 
-// Request of packed token t: the largest b with q_start[b] <= t (-1: none).
-__device__ __forceinline__ int request_of_token(const PackedTokens& k, int t) {
-  if (!k.q_start) return t / k.q_per;
-  int lo = 0, hi = k.B;  // first b with q_start[b] > t, over [0, B)
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (k.q_start[mid] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo - 1;
-}
-
 // Page index and slot of a position.
 __device__ __forceinline__ void split_position(const PagedView& c, int pos, int& page, int& slot) {
   if (c.page_shift >= 0) {
