@@ -44,17 +44,18 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7]));
 }
 
-// 8 values to a cache row (16-byte units from base), at value 8 * vec
+// 8 values (e4m3: times inv, one over the head's scale) to a cache row (16-byte
+// units from base), at value 8 * vec
 template <class T, bool kF8>
 __device__ __forceinline__ void store_cache(unsigned char* base, uint32_t row, int vec, const float (&x)[8],
-                                            float scale) {
+                                            float inv) {
   unsigned char* p = base + (size_t)row * 16u;
   if (kF8) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      w[i] = (uint32_t)e4m3_pair(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
-             (uint32_t)e4m3_pair(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16;
+      w[i] = (uint32_t)e4m3_pair(x[4 * i] * inv, x[4 * i + 1] * inv) |
+             (uint32_t)e4m3_pair(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
     reinterpret_cast<uint2*>(p)[vec] = make_uint2(w[0], w[1]);
   } else {
     reinterpret_cast<uint4*>(p)[vec] = pack8<T>(x);
@@ -91,7 +92,7 @@ __device__ __forceinline__ int request_of_token_warp(const PackedTokens& k, int 
 // neighbours. The items' values are read before it is known where they go, so
 // that the chain of offset, length, page and slot costs no time of its own.
 template <class T, bool kF8, int D, int kBatch>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int group) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int group, uint32_t inv_items) {
   constexpr int kItems = D / 16;  // vector pairs per head
   __shared__ Place place[kMaxGroup];
   __shared__ float2 turn[kMaxGroup * D / 2];
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int t0 = blockIdx.x * group, nt = min(group, p.tk.tokens - t0);
   const int half = p.rot >> 1, rv = p.rot >> 4;
   const int heads = 2 * p.c.kv_heads + p.q_heads, items = heads * kItems;
+  auto token_of = [&](int w) { return (int)__umulhi((uint32_t)w, inv_items); };  // w / items
 
   // ---- the values
   uint4 x[kBatch], y[kBatch];
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   for (int k = 0; k < kBatch; ++k) {
     const int w = (blockIdx.y * kBatch + k) * kAppendThreads + tid;
     if (w >= nt * items) continue;
-    const int ti = w / items, hd = (w - ti * items) / kItems, i = w % kItems;
+    const int ti = token_of(w), hd = (w - ti * items) / kItems, i = w % kItems;
     const long long t = t0 + ti;
     const unsigned char* src = hd < p.c.kv_heads       ? p.k + 2 * (t * p.k_ts + (long long)hd * p.k_hs)
                                : hd < 2 * p.c.kv_heads ? p.v + 2 * (t * p.v_ts + (long long)(hd - p.c.kv_heads) * p.v_hs)
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       const unsigned long long a = p.phases[j] * (unsigned long long)(unsigned)pl.pos;
       float s, c;
       sincospif((float)(int32_t)(uint32_t)(a >> 32) * 0x1p-31f, &s, &c);
-      turn[ti * half + j] = make_float2(c, s);
+      turn[ti * half + (j & 7) * rv + (j >> 3)] = make_float2(c, s);  // an item's 8 pairs, rv apart
     }
   }
   __syncthreads();
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   for (int k = 0; k < kBatch; ++k) {
     const int w = (blockIdx.y * kBatch + k) * kAppendThreads + tid;
     if (w >= nt * items) continue;
-    const int ti = w / items, hd = (w - ti * items) / kItems, i = w % kItems;
+    const int ti = token_of(w), hd = (w - ti * items) / kItems, i = w % kItems;
     const Place pl = place[ti];
     if (pl.pos < 0) continue;
     const bool is_k = hd < p.c.kv_heads, is_v = !is_k && hd < 2 * p.c.kv_heads;
@@ -174,11 +176,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     unpack8<T>(x[k], a);
     unpack8<T>(y[k], b);
     if (!is_v && i < rv) {
-      const float2* tn = turn + ti * half + 8 * i;
+      const float2* tn = turn + ti * half + i;
       if (split) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 cs = tn[e];
+          const float2 cs = tn[e * rv];
           const float r = a[e] * cs.x - b[e] * cs.y, o = b[e] * cs.x + a[e] * cs.y;
           a[e] = r;
           b[e] = o;
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 cs = tn[e], ct = tn[4 + e];
+          const float2 cs = tn[e * rv], ct = tn[(4 + e) * rv];
           const float r = a[2 * e] * cs.x - a[2 * e + 1] * cs.y, o = a[2 * e + 1] * cs.x + a[2 * e] * cs.y;
           a[2 * e] = r;
           a[2 * e + 1] = o;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (pl.page >= 0) {
         const uint32_t row = row_offset(p.c, pl.page, head, pl.slot);
         const float* sc = is_k ? p.c.k_scale : p.c.v_scale;
-        const float z = kF8 && sc ? sc[head] : 1.0f;
+        const float z = kF8 && sc ? __frcp_rn(sc[head]) : 1.0f;
         unsigned char* base = is_k ? p.c.k : p.c.v;
         store_cache<T, kF8>(base, row, va, a, z);
         store_cache<T, kF8>(base, row, vb, b, z);
@@ -226,7 +228,10 @@ int launch_batch(const AppendParams& p, int group, int items, void* stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, append_kernel<T, kF8, D, kBatch>, p, group);
+  // ceil(2^32 / items): the upper half of its product with w is w / items while
+  // w * items stays below 2^32 (with one token a block there is nothing to divide)
+  const uint32_t inv_items = group == 1 ? 0u : (uint32_t)(((1ull << 32) + items - 1) / items);
+  return (int)cudaLaunchKernelEx(&cfg, append_kernel<T, kF8, D, kBatch>, p, group, inv_items);
 }
 
 // Few tokens: one item a thread, over as many blocks as that gives. Many: 4
