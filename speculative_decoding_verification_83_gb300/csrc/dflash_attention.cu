@@ -506,15 +506,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     const long long jtok = u.first + ji, jhead = u.h * p.G + (jrow - ji * p.G);
     const long long slot = 2LL * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
     float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry().o()) + (slot * kRows + jr) * D;
-    float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    // (the running maximum's own weight is 1 exactly, so l serves both ends here)
+    float factor = reciprocal_or_zero(sum);
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     if ((tid & 7) == 0 && jok) {
       if (whole) {
         if (p.lse) p.lse[jtok * ((long long)p.G * p.c.kv_heads) + jhead] = (top + log2f(sum)) * kLn2;
       } else {
-        float* ml = reinterpret_cast<float*>(p.ws + warp_geometry().ml()) + (slot * kRows + jr) * 2;
-        ml[0] = top;
-        ml[1] = sum;
+        reinterpret_cast<Part*>(p.ws + warp_geometry().ml())[slot * kRows + jr] = {top, sum, sum};
       }
     }
 #pragma unroll
@@ -563,36 +562,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams 
   const long long run = *reinterpret_cast<const long long*>(p.ws);
   if (u.tiles == 0) return;
   const int c1 = (int)((u.start + u.tiles - 1) / run);
-  const float* mls = reinterpret_cast<const float*>(p.ws + geo.ml());
+  const Part* parts = reinterpret_cast<const Part*>(p.ws + geo.ml());
   const float* os = reinterpret_cast<const float*>(p.ws + geo.o());
   const long long slot0 = 2LL * c0 + (u.start == (long long)c0 * run ? 0 : 1);
   const int rows = min(geo.rows, u.n * p.G - u.rb * geo.rows);
   for (int jr = threadIdx.x >> 5; jr < rows; jr += kJoinWarps) {
     auto slot_row = [&](int c) { return (c == c0 ? slot0 : 2LL * c) * geo.rows + jr; };
     float top = kNegInf;
-    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, mls[slot_row(c) * 2]);
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, parts[slot_row(c)].m);
     top = warp_max_f32(top);
     float2 x = make_float2(0.0f, 0.0f);
-    float sum = 0.0f;
+    float sum = 0.0f, rounded = 0.0f;
     for (int cb = c0; cb <= c1; cb += 32) {
       const int c = cb + lane;
-      float w = 0.0f, ls = 0.0f;
+      float w = 0.0f, l = 0.0f, lr = 0.0f;
       if (c <= c1) {
-        const float2 ml = *reinterpret_cast<const float2*>(mls + slot_row(c) * 2);
-        w = ml.x == kNegInf ? 0.0f : ex2(ml.x - top);
-        ls = ml.y == ml.y ? ml.y * w : ml.y;
+        const Part b = parts[slot_row(c)];
+        w = b.m == kNegInf ? 0.0f : ex2(b.m - top);
+        add_part(b, top, l, lr);
       }
       const int cnt = min(32, c1 - cb + 1);
 #pragma unroll 8
       for (int j = 0; j < cnt; ++j) {
         const float2 y = *reinterpret_cast<const float2*>(os + slot_row(cb + j) * D + col);
         const float wj = __shfl_sync(0xffffffffu, w, j);
-        sum += __shfl_sync(0xffffffffu, ls, j);
+        sum += __shfl_sync(0xffffffffu, l, j);
+        rounded += __shfl_sync(0xffffffffu, lr, j);
         x.x = fmaf(y.x, wj, x.x);
         x.y = fmaf(y.y, wj, x.y);
       }
     }
-    float factor = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    float factor = reciprocal_or_zero(rounded);
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     const int g = u.rb * geo.rows + jr, ti = g / p.G;
     const long long tok = u.first + ti, head = u.h * p.G + g - ti * p.G;

@@ -31,16 +31,31 @@ struct SplitUnit {
   int tiles, h, rb, first, n, unused;
 };
 
+// A row's statistics over some keys: the reference m of its weights 2^(x - m),
+// their sum l, and the sum of the weights as rounded for the product with V,
+// which is what the row is divided by (a row that one key rules then keeps that
+// key's value to the output's rounding). log2 of m's scale plus l gives lse.
+struct Part {
+  float m, l, rounded;
+};
+
 // Workspace: tiles per CTA (64-bit), a SplitUnit for each CTA, then for each
-// CTA two slots of partial results: rows x (maximum, sum), then rows x D. Slot
+// CTA two slots of partial results: rows x Part, then rows x D. Slot
 // 0 is the segment that begins with the CTA's run, slot 1 one that begins
 // inside it.
 struct AttnGeometry {
   int rows, tile, ctas;
   __host__ __device__ size_t ml() const { return 256 + ((size_t)ctas * sizeof(SplitUnit) + 255) / 256 * 256; }
-  __host__ __device__ size_t o() const { return ml() + (size_t)ctas * 2 * rows * 2 * sizeof(float); }
+  __host__ __device__ size_t o() const { return ml() + ((size_t)ctas * 2 * rows * sizeof(Part) + 255) / 256 * 256; }
   __host__ __device__ size_t bytes(int D) const { return o() + (size_t)ctas * 2 * rows * D * sizeof(float); }
 };
+// Part b, taken to the reference m; a sum that has seen nothing is 0, or NaN.
+__device__ __forceinline__ void add_part(const Part& b, float m, float& l, float& rounded) {
+  const float f = b.m == kNegInf ? 0.0f : ex2(b.m - m);
+  l += b.l == b.l ? b.l * f : b.l;
+  rounded += b.rounded == b.rounded ? b.rounded * f : b.rounded;
+}
+__device__ __forceinline__ float reciprocal_or_zero(float s) { return s > 0.0f ? 1.0f / s : s == 0.0f ? 0.0f : s; }
 __device__ __forceinline__ SplitUnit* split_units(const AttnParams& p) {
   return reinterpret_cast<SplitUnit*>(p.ws + 256);
 }

@@ -60,7 +60,7 @@ struct TcShape {
   static_assert(kUsed <= 512, "tensor memory");
 };
 
-struct TcShared {
+struct TcShared {  // next to the dynamic part: 227 KB in all
   uint64_t full[6], empty[6];    // per stage
   uint64_t s_full[2], p_full[2];  // per score buffer
   uint64_t pv_done, q_full, drained, together;
@@ -70,8 +70,10 @@ struct TcShared {
   uint32_t mask[6][4];           // per stage and load warp: its keys that exist
   int first_b;
   long long first_pre, sums[kTcThreads / 32];
-  float ml[2 * 128];
+  Part parts[128];
 };
+
+static_assert(TcShape<128>::kSmem + sizeof(TcShared) <= 232448, "one CTA's shared memory (227 KB)");
 
 // ---- PTX wrappers (one CTA per tensor core group) ------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         const int tok = (u.rb * R + row) / p.G;
         const int vis = row >= rows_here ? 0 : p.causal ? min(u.L, max(0, u.L - u.n + tok + 1)) : u.L;
 
-        float m = kNegInf, l = 0.0f;
+        float m = kNegInf, l = 0.0f, lr = 0.0f;  // lr: of the rounded weights
         for (; t < u_end && ok; ++t, ++j) {
           const int st = j % kStages, buf = j & 1;
           ok = tc_wait(&S.s_full[buf], (uint32_t)(j >> 1) & 1u, S);
@@ -595,6 +597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
               wait_st();
             }
             l *= f;
+            lr *= f;
             if (move) m = top;
           }
           const float ref = m == kNegInf ? 0.0f : m;
@@ -608,6 +611,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
                           b = ex2(fmaf(__uint_as_float(x[2 * i + 1]), c, -ref));
               l += a + b;
               w[i] = T::pack(a, b);
+              const float2 r = T::unpack(w[i]);
+              lr += r.x + r.y;
             }
             tmem_store<kChunk / 2>(my + W::kP + buf * (kKeys / 2) + (copy * kCols + c0) / 2, w);
           }
@@ -629,21 +634,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         }
         fence_after();
         const bool whole = u_begin == u.start && u_end == u.start + u.tiles;
-        S.ml[2 * tid] = m;
-        S.ml[2 * tid + 1] = l;
+        S.parts[tid] = {m, l, lr};
         const int unsound = *reinterpret_cast<volatile int*>(&S.unsound[u.ordinal % kFlags]);
         if (!(ok = softmax_sync(syncs, S))) break;
         // the row's maximum and sum over its copies, and this copy's factor
-        float best = kNegInf, sum = 0.0f;
+        float best = kNegInf, sum = 0.0f, rounded = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kCopies; ++k) best = fmaxf(best, S.ml[2 * (k * R + row)]);
+        for (int k = 0; k < kCopies; ++k) best = fmaxf(best, S.parts[k * R + row].m);
 #pragma unroll
-        for (int k = 0; k < kCopies; ++k) {
-          const float mk = S.ml[2 * (k * R + row)], lk = S.ml[2 * (k * R + row) + 1];
-          sum += mk != kNegInf ? lk * ex2(mk - best) : lk == lk ? 0.0f : lk;  // a NaN sum stays one
-        }
+        for (int k = 0; k < kCopies; ++k) add_part(S.parts[k * R + row], best, sum, rounded);
         float factor = m == kNegInf ? 0.0f : ex2(m - best);
-        if (whole) factor *= sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+        if (whole) factor *= reciprocal_or_zero(rounded);
         const long long slot = 2LL * blockIdx.x + (u_begin == t_begin ? 0 : 1);
         const int g = u.rb * R + row, ti = g / p.G;
         const long long q_tok = u.first + ti, q_head = u.h * p.G + g - ti * p.G;
@@ -652,9 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         float* part_row = reinterpret_cast<float*>(p.ws + geo.o()) + (slot * R + row) * D;
         if (writes) {
           if (!whole) {
-            float* ml = reinterpret_cast<float*>(p.ws + geo.ml()) + (slot * R + row) * 2;
-            ml[0] = best;
-            ml[1] = sum;
+            reinterpret_cast<Part*>(p.ws + geo.ml())[slot * R + row] = {best, sum, rounded};
           } else if (p.lse) {
             p.lse[q_tok * ((long long)p.G * p.c.kv_heads) + q_head] = (best + log2f(sum)) * kLn2;
           }
@@ -731,7 +730,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
               }
             }
           }
-          // the scratch, Q and S.ml are written again
+          // the scratch, Q and S.parts are written again
           ok = softmax_sync(syncs, S);
         }
         if (!ok) break;
