@@ -506,14 +506,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     const long long jtok = u.first + ji, jhead = u.h * p.G + (jrow - ji * p.G);
     const long long slot = 2LL * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
     float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry().o()) + (slot * kRows + jr) * D;
-    // (the running maximum's own weight is 1 exactly, so l serves both ends here)
     float factor = reciprocal_or_zero(sum);
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     if ((tid & 7) == 0 && jok) {
       if (whole) {
         if (p.lse) p.lse[jtok * ((long long)p.G * p.c.kv_heads) + jhead] = (top + log2f(sum)) * kLn2;
       } else {
-        reinterpret_cast<Part*>(p.ws + warp_geometry().ml())[slot * kRows + jr] = {top, sum, sum};
+        reinterpret_cast<Part*>(p.ws + warp_geometry().ml())[slot * kRows + jr] = {top, sum};
       }
     }
 #pragma unroll
@@ -572,14 +571,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams 
     for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, parts[slot_row(c)].m);
     top = warp_max_f32(top);
     float2 x = make_float2(0.0f, 0.0f);
-    float sum = 0.0f, rounded = 0.0f;
+    float sum = 0.0f;
     for (int cb = c0; cb <= c1; cb += 32) {
       const int c = cb + lane;
-      float w = 0.0f, l = 0.0f, lr = 0.0f;
+      float w = 0.0f, l = 0.0f;
       if (c <= c1) {
         const Part b = parts[slot_row(c)];
         w = b.m == kNegInf ? 0.0f : ex2(b.m - top);
-        add_part(b, top, l, lr);
+        l = part_sum(b, top);
       }
       const int cnt = min(32, c1 - cb + 1);
 #pragma unroll 8
@@ -587,12 +586,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams 
         const float2 y = *reinterpret_cast<const float2*>(os + slot_row(cb + j) * D + col);
         const float wj = __shfl_sync(0xffffffffu, w, j);
         sum += __shfl_sync(0xffffffffu, l, j);
-        rounded += __shfl_sync(0xffffffffu, lr, j);
         x.x = fmaf(y.x, wj, x.x);
         x.y = fmaf(y.y, wj, x.y);
       }
     }
-    float factor = reciprocal_or_zero(rounded);
+    float factor = reciprocal_or_zero(sum);
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     const int g = u.rb * geo.rows + jr, ti = g / p.G;
     const long long tok = u.first + ti, head = u.h * p.G + g - ti * p.G;

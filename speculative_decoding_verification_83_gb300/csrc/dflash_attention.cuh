@@ -31,12 +31,10 @@ struct SplitUnit {
   int tiles, h, rb, first, n, unused;
 };
 
-// A row's statistics over some keys: the reference m of its weights 2^(x - m),
-// their sum l, and the sum of the weights as rounded for the product with V,
-// which is what the row is divided by (a row that one key rules then keeps that
-// key's value to the output's rounding). log2 of m's scale plus l gives lse.
+// A row's statistics over some keys: the largest score m (in powers of 2) and
+// the sum l of the weights 2^(x - m).
 struct Part {
-  float m, l, rounded;
+  float m, l;
 };
 
 // Workspace: tiles per CTA (64-bit), a SplitUnit for each CTA, then for each
@@ -50,10 +48,8 @@ struct AttnGeometry {
   __host__ __device__ size_t bytes(int D) const { return o() + (size_t)ctas * 2 * rows * D * sizeof(float); }
 };
 // Part b, taken to the reference m; a sum that has seen nothing is 0, or NaN.
-__device__ __forceinline__ void add_part(const Part& b, float m, float& l, float& rounded) {
-  const float f = b.m == kNegInf ? 0.0f : ex2(b.m - m);
-  l += b.l == b.l ? b.l * f : b.l;
-  rounded += b.rounded == b.rounded ? b.rounded * f : b.rounded;
+__device__ __forceinline__ float part_sum(const Part& b, float m) {
+  return b.l == b.l ? (b.m == kNegInf ? 0.0f : b.l * ex2(b.m - m)) : b.l;
 }
 __device__ __forceinline__ float reciprocal_or_zero(float s) { return s > 0.0f ? 1.0f / s : s == 0.0f ? 0.0f : s; }
 __device__ __forceinline__ SplitUnit* split_units(const AttnParams& p) {

@@ -23,9 +23,12 @@
 //    two score buffers) one tile ahead of O += P V (P from tensor memory, V
 //    read in place as the transposed operand).
 //  * warps 0-3: softmax. A thread reads its scores (tcgen05.ld), takes 2^(x -
-//    m), writes P back as 16-bit pairs. m is the running maximum, but moves
-//    only when a score exceeds it by 8 (weights then stay below 2^8): moving
-//    it rescales O in tensor memory, which has to wait for the product before.
+//    m), writes P back as 16-bit pairs. When a row's running maximum m moves,
+//    its warp rescales O in tensor memory, which has to wait for the product
+//    before. Letting m lag until a score exceeds it by 8 spares most of that
+//    (220 against 224 us at the size below) but the largest weights are then no
+//    longer exactly 1, and their rounding shows: an error of 2.2e-3 of the
+//    result in bf16 against 1.8e-3 (the output's rounding alone is 1.7e-3).
 // Every wait is bounded; a CTA that gives up raises DFLASH_STATUS_TIMEOUT,
 // lets its copies land and frees its tensor memory.
 #include <cuda_runtime.h>
@@ -42,7 +45,6 @@ constexpr int kTcCtas = 160;
 constexpr int kMmaWarp = 4;
 constexpr int kLoadWarp0 = 5, kLoadWarps = 4;
 constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
-constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the reference
 // A unit's end and the next one's beginning take a CTA about as long as this
 // many tiles: the list counts them, so that runs with many ends are shorter.
 constexpr int kEndTiles = 3;
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         const int tok = (u.rb * R + row) / p.G;
         const int vis = row >= rows_here ? 0 : p.causal ? min(u.L, max(0, u.L - u.n + tok + 1)) : u.L;
 
-        float m = kNegInf, l = 0.0f, lr = 0.0f;  // lr: of the rounded weights
+        float m = kNegInf, l = 0.0f;
         for (; t < u_end && ok; ++t, ++j) {
           const int st = j % kStages, buf = j & 1;
           ok = tc_wait(&S.s_full[buf], (uint32_t)(j >> 1) & 1u, S);
@@ -575,8 +577,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             for (int i = 0; i < kChunk; ++i) top = fmaxf(top, __uint_as_float(x[i]));
           }
           top *= c;
-          // the reference moves when the weights would pass 2^kSlack
-          const bool move = top > m + kSlack || (m == kNegInf && top > m);
+          const bool move = top > m;
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? (m == kNegInf ? 0.0f : ex2(m - top)) : 1.0f;
             if (t > u_begin) {  // O holds sums: they are rescaled, after the product in flight (the one before is
@@ -597,7 +598,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
               wait_st();
             }
             l *= f;
-            lr *= f;
             if (move) m = top;
           }
           const float ref = m == kNegInf ? 0.0f : m;
@@ -611,8 +611,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
                           b = ex2(fmaf(__uint_as_float(x[2 * i + 1]), c, -ref));
               l += a + b;
               w[i] = T::pack(a, b);
-              const float2 r = T::unpack(w[i]);
-              lr += r.x + r.y;
             }
             tmem_store<kChunk / 2>(my + W::kP + buf * (kKeys / 2) + (copy * kCols + c0) / 2, w);
           }
@@ -634,17 +632,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         }
         fence_after();
         const bool whole = u_begin == u.start && u_end == u.start + u.tiles;
-        S.parts[tid] = {m, l, lr};
+        S.parts[tid] = {m, l};
         const int unsound = *reinterpret_cast<volatile int*>(&S.unsound[u.ordinal % kFlags]);
         if (!(ok = softmax_sync(syncs, S))) break;
         // the row's maximum and sum over its copies, and this copy's factor
-        float best = kNegInf, sum = 0.0f, rounded = 0.0f;
+        float best = kNegInf, sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < kCopies; ++k) best = fmaxf(best, S.parts[k * R + row].m);
 #pragma unroll
-        for (int k = 0; k < kCopies; ++k) add_part(S.parts[k * R + row], best, sum, rounded);
+        for (int k = 0; k < kCopies; ++k) sum += part_sum(S.parts[k * R + row], best);
         float factor = m == kNegInf ? 0.0f : ex2(m - best);
-        if (whole) factor *= reciprocal_or_zero(rounded);
+        if (whole) factor *= reciprocal_or_zero(sum);
         const long long slot = 2LL * blockIdx.x + (u_begin == t_begin ? 0 : 1);
         const int g = u.rb * R + row, ti = g / p.G;
         const long long q_tok = u.first + ti, q_head = u.h * p.G + g - ti * p.G;
@@ -653,7 +651,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         float* part_row = reinterpret_cast<float*>(p.ws + geo.o()) + (slot * R + row) * D;
         if (writes) {
           if (!whole) {
-            reinterpret_cast<Part*>(p.ws + geo.ml())[slot * R + row] = {best, sum, rounded};
+            reinterpret_cast<Part*>(p.ws + geo.ml())[slot * R + row] = {best, sum};
           } else if (p.lse) {
             p.lse[q_tok * ((long long)p.G * p.c.kv_heads) + q_head] = (best + log2f(sum)) * kLn2;
           }
