@@ -468,13 +468,13 @@ int dflash_distill_loss(const void* student, int64_t row_stride, int rows, int V
                         const float* row_weight, float* loss, float* row_stats, uint32_t* status, void* stream);
 
 /* The gradient for an upstream gradient of the losses ([device] float [rows],
- * NULL: 1): grad [rows, V] in the student's type, rows grad_stride elements
- * apart. grad may be student itself (same stride). A row whose upstream
+ * upstream_stride elements apart, 0 for one that all rows share; NULL: 1):
+ * grad [rows, V] in the student's type, rows grad_stride elements apart. grad may be student itself (same stride). A row whose upstream
  * gradient is 0 gives 0. */
 int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V, int dtype,
                         const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
-                        const float* row_weight, const float* row_stats, const float* upstream, void* grad,
-                        int64_t grad_stride, void* stream);
+                        const float* row_weight, const float* row_stats, const float* upstream,
+                        int64_t upstream_stride, void* grad, int64_t grad_stride, void* stream);
 
 /* Loss and gradient (of the sum of the losses) in one call, which reads the
  * logits once. grad may be student itself (same stride). */

@@ -121,7 +121,7 @@ EXPORTS = {
     "dflash_attention_workspace_bytes": ("z", "ii"),
     "dflash_paged_attention": ("i", "ppppiiipppfipzpp"),
     "dflash_distill_loss": ("i", "pliiippifppppp"),
-    "dflash_distill_grad": ("i", "pliiippifppppl" "p"),
+    "dflash_distill_grad": ("i", "pliiippifppplpl" "p"),
     "dflash_distill_loss_grad": ("i", "pliiippifpppl" "pp"),
 }
 _CT = {"i": ctypes.c_int, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float,

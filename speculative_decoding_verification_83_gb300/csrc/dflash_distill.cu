@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kGradThreads + 32) grad_kernel(const DistillPa
   const float at_edge = L.edge >= 0 ? T::load(z + (size_t)L.edge * T::kBytes) : 0.0f;
   Stat a = {p.lse[2 * r], p.lse[2 * r + 1]};
   float w = p.weight ? p.weight[r] : 1.0f;
-  if (p.upstream) w *= p.upstream[r];
+  if (p.upstream) w *= p.upstream[r * p.upstream_stride];
   if (w == 0.0f || a.s == 0.0f) {  // the statistics of a row that has no part are (0, 0)
     for (int i = L.lo + tid; i < L.hi; i += blockDim.x) T::store(g + (size_t)i * T::kBytes, 0.0f);
     return;

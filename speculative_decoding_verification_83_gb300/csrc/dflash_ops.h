@@ -71,7 +71,8 @@ struct DistillParams {
   const int32_t* ids;
   const float* teacher;
   const float* weight;    // per row, or null
-  const float* upstream;  // per row, or null (backward only)
+  const float* upstream;  // per row, upstream_stride apart, or null (backward only)
+  long long upstream_stride;
   float inv_t;
   float* loss;
   float* lse;  // [rows, 2] statistics; forward: written (or null); backward: read

@@ -266,12 +266,13 @@ int dflash_distill_loss(const void* student, int64_t row_stride, int rows, int V
 
 int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V, int dtype,
                         const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
-                        const float* row_weight, const float* lse, const float* upstream, void* grad,
-                        int64_t grad_stride, void* stream) {
+                        const float* row_weight, const float* lse, const float* upstream,
+                        int64_t upstream_stride, void* grad, int64_t grad_stride, void* stream) {
   NvtxRange nvtx_range("dflash_distill_grad");
   int rc = check_distill(student, row_stride, rows, V, dtype, teacher_ids, teacher_logits, K, temperature);
   if (rc) return rc;
   if (!lse || !grad) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
+  if (upstream_stride < 0) return fail(DFLASH_ERR_INVALID_ARG, "upstream_stride must not be negative");
   if (!aligned(grad, dtype == DFLASH_BF16 ? 2 : 4) || grad_stride < V)
     return fail(DFLASH_ERR_INVALID_ARG, "the gradient's rows must be aligned to their type and at least V apart");
   if (rows == 0) return DFLASH_OK;
@@ -286,6 +287,7 @@ int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V
   p.teacher = teacher_logits;
   p.weight = row_weight;
   p.upstream = upstream;
+  p.upstream_stride = upstream_stride;
   p.inv_t = 1.0f / temperature;
   p.lse = const_cast<float*>(lse);
   p.grad = static_cast<unsigned char*>(grad);

@@ -319,16 +319,19 @@ def _distill_function():
             return loss
 
         @staticmethod
-        @torch.autograd.function.once_differentiable
         def backward(ctx, upstream):
+            if torch.is_grad_enabled():  # create_graph: the result then refuses a second derivative
+                return torch.autograd.function.once_differentiable(DistillLoss._backward)(ctx, upstream)
+            return DistillLoss._backward(ctx, upstream)
+
+        @staticmethod
+        def _backward(ctx, upstream):
             student, ids, teacher, row_weight, stats = ctx.saved_tensors
             head, w = _distill_args(student, ids, teacher, row_weight)
-            if not upstream.is_contiguous():
-                upstream = upstream.contiguous()
             dev = student.device
             grad = torch.empty(student.shape, dtype=student.dtype, device=dev)
             _check(load().dflash_distill_grad(*head, ctx.temperature, w, stats.data_ptr(), upstream.data_ptr(),
-                                              grad.data_ptr(), head[3], _raw_stream(None, dev)))
+                                              upstream.stride(0), grad.data_ptr(), head[3], _raw_stream(None, dev)))
             return grad, None, None, None, None, None
 
     _function = DistillLoss

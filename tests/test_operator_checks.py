@@ -91,7 +91,7 @@ def test_attention_workspace(lib):
 
 
 def distill(lib, name, z=P, stride=100, rows=2, V=100, dtype=0, ids=P, teacher=P, K=4, T=1.0, tail=None):
-    tail = {"loss": (None, P, None, None, None), "grad": (None, P, None, P, 100, None),
+    tail = {"loss": (None, P, None, None, None), "grad": (None, P, None, 1, P, 100, None),
             "loss_grad": (None, P, P, 100, None, None)}[name] if tail is None else tail
     return getattr(lib, "dflash_distill_" + name)(z, stride, rows, V, dtype, ids, teacher, K, T, *tail)
 
@@ -111,8 +111,10 @@ def test_distillation_is_checked(lib, name, kw, word):
 
 def test_distillation_outputs_are_checked(lib):
     assert distill(lib, "loss", tail=(None, None, None, None, None)) == dv.ERR_INVALID_ARG
-    assert distill(lib, "grad", tail=(None, None, None, P, 100, None)) == dv.ERR_INVALID_ARG
-    assert distill(lib, "grad", tail=(None, P, None, P, 99, None)) == dv.ERR_INVALID_ARG
+    assert distill(lib, "grad", tail=(None, None, None, 1, P, 100, None)) == dv.ERR_INVALID_ARG
+    assert distill(lib, "grad", tail=(None, P, None, 1, P, 99, None))\
+        == dv.ERR_INVALID_ARG
+    assert distill(lib, "grad", tail=(None, P, P, -1, P, 100, None)) == dv.ERR_INVALID_ARG
     assert distill(lib, "loss_grad", tail=(None, P, None, 100, None, None)) == dv.ERR_INVALID_ARG
     assert distill(lib, "loss_grad", tail=(None, P, P + 1, 100, None, None)) == dv.ERR_INVALID_ARG
 
