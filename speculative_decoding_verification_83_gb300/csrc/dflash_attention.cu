@@ -99,13 +99,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                : "r"(a)
                : "memory");
 }
-// four e4m3 values as two pairs of f16 values
-__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(v));
-}
-
 template <bool kF8, int D>
 struct Shape {
   static constexpr int kRowBytes = kF8 ? D : 2 * D;
@@ -679,8 +672,8 @@ size_t attention_workspace(int head_dim) {
 int launch_attention(const AttnParams& p, int dtype, int cache_dtype, int head_dim, int sms, void* stream) {
   const bool f8 = cache_dtype == DFLASH_E4M3;
   const long long rows = (((long long)p.tk.tokens + p.tk.B - 1) / p.tk.B) * p.G;
-  if (!f8 && rows > 16)
-    return launch_attention_tc(p, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, dtype, head_dim, sms, stream);
+  if (rows > 16 && !(f8 && head_dim == 256))
+    return launch_attention_tc(p, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, dtype, f8, head_dim, sms, stream);
   if (dtype == DFLASH_BF16)
     return f8 ? pick_dim<Bf16, true>(p, head_dim, sms, stream) : pick_dim<Bf16, false>(p, head_dim, sms, stream);
   return f8 ? pick_dim<F16, true>(p, head_dim, sms, stream) : pick_dim<F16, false>(p, head_dim, sms, stream);

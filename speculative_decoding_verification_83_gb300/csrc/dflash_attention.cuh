@@ -20,6 +20,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// four e4m3 values as two pairs of f16 values
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
+
 // A unit of work is (request, key/value head, `rows` query rows) over all of
 // the request's keys, `tile` at a time; units follow each other request by
 // request, head by head, row block by row block.
@@ -79,6 +86,6 @@ int launch_join(const AttnParams& p, const AttnGeometry& g, int grid, int dtype,
 
 // The tensor-memory kernel (dflash_attention_tc.cu): units of 32, 64 or 128 rows.
 AttnGeometry tc_geometry(int rows, int head_dim);
-int launch_attention_tc(const AttnParams& p, int rows, int dtype, int head_dim, int sms, void* stream);
+int launch_attention_tc(const AttnParams& p, int rows, int dtype, bool f8, int head_dim, int sms, void* stream);
 
 }  // namespace dflash

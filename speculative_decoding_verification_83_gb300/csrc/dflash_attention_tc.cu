@@ -50,13 +50,17 @@ constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
 constexpr int kEndTiles = 3;
 constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at once
 
-template <int D>
+template <int D, bool kF8>
 struct TcShape {
   static constexpr int kKeys = D == 256 ? 64 : 128;
-  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? (kF8 ? 3 : 6) : D == 128 ? (kF8 ? 2 : 3) : 2;
+  // 8-bit caches: tiles as they lie in the cache, in flight or waiting to be widened
+  static constexpr int kRaw = !kF8 ? 0 : D == 64 ? 6 : 2;
+  static constexpr int kRawBytes = kKeys * D * 2;  // K and V
   static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kRowBytes = kF8 ? D : 2 * D;     // a cache row
   static constexpr int kHalf = kKeys * D * 2;           // K or V of a stage
-  static constexpr size_t kSmem = 1024 + (size_t)kQBytes + (size_t)kStages * 2 * kHalf;
+  static constexpr size_t kSmem = 1024 + (size_t)kQBytes + (size_t)kStages * 2 * kHalf + (size_t)kRaw * kRawBytes;
   // tensor memory columns
   static constexpr int kO = 0, kS = D, kP = kS + 2 * kKeys, kUsed = kP + kKeys;
   static_assert(kUsed <= 512, "tensor memory");
@@ -70,12 +74,15 @@ struct TcShared {  // next to the dynamic part: 227 KB in all
   volatile int failed;
   int unsound[kFlags];           // per unit (ordinal in the CTA): see load
   uint32_t mask[6][4];           // per stage and load warp: its keys that exist
+  uint32_t raw_mask[4][6];       // 8-bit caches, per load warp and raw tile: the same,
+  int raw_unit[4][6];            // and its unit, with bit 0 set if some rows see less of it than others
   int first_b;
   long long first_pre, sums[kTcThreads / 32];
   Part parts[128];
 };
 
-static_assert(TcShape<128>::kSmem + sizeof(TcShared) <= 232448, "one CTA's shared memory (227 KB)");
+static_assert(TcShape<128, false>::kSmem + sizeof(TcShared) <= 232448 && TcShape<128, true>::kSmem <= TcShape<128, false>::kSmem,
+              "one CTA's shared memory (227 KB)");
 
 // ---- PTX wrappers (one CTA per tensor core group) ------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
@@ -273,9 +280,36 @@ __device__ __forceinline__ bool word_not_finite(uint32_t w) {
   return (w & e) == e || ((w >> 16) & e) == e;
 }
 
-template <class T, int D, int R>
+// 8 e4m3 values (two words) as 8 values of T, exactly
+template <class T>
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
+  uint32_t w[4];
+  widen4(a, w[0], w[1]);
+  widen4(b, w[2], w[3]);
+  if constexpr (std::is_same<T, Bf16>::value) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = F16::unpack(w[i]);
+      w[i] = Bf16::pack(f.x, f.y);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// e4m3 NaNs (all ones below the sign) of a word become 0
+__device__ __forceinline__ bool drop_nan(uint32_t& w) {
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (((w >> (8 * i)) & 0x7fu) == 0x7fu) {
+      w &= ~(0xffu << (8 * i));
+      found = true;
+    }
+  return found;
+}
+
+template <class T, bool kF8, int D, int R>
 __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnParams p, const AttnGeometry geo) {
-  using W = TcShape<D>;
+  using W = TcShape<D, kF8>;
   constexpr int kKeys = W::kKeys, kStages = W::kStages;
   constexpr int kCopies = 128 / R, kCols = kKeys / kCopies;  // a thread's columns of a tile
   constexpr int kChunk = kCols < 64 ? kCols : 64;            // ... in registers at a time
@@ -290,7 +324,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&S.full[i], kLoadWarps * 33);  // every copying thread, and each warp's mask
+      mbar_init(&S.full[i], kLoadWarps * (kF8 ? 32 : 33));  // every loading thread, and each warp's mask
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -363,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
 
     if (warp >= kLoadWarp0) {
       // ---- loads: this warp's share of every tile's keys
-      constexpr int kPieces = D / 8;                 // 16-byte pieces of a row
+      constexpr int kPieces = W::kRowBytes / 16;     // 16-byte pieces of a row in the cache
       constexpr int kLoads = kMine * kPieces / 32;   // per lane, for K and for V each
       const int lw = warp - kLoadWarp0;
       bool bad_page = false, next_ok = false;
@@ -386,7 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       // a weight of 0 times one that is not finite would be NaN. Such a value
       // (never met in sound data) is replaced by 0 here and added at the unit's
       // end.
-      auto sanitise = [&](int st, int ordinal) {
+      [[maybe_unused]] auto sanitise = [&](int st, int ordinal) {
         const uint32_t vb = (uint32_t)(W::kQBytes + st * 2 * W::kHalf + W::kHalf);
         bool found = false;
 #pragma unroll 4
@@ -410,38 +444,110 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       if (t_first < t_end) look_up(t_first);
       int st = 0;
       uint32_t round = 0;
-      for (long long t = t_first; t < t_end;) {
-        if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
-        const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
-        const uint32_t kb = ring + st * 2 * W::kHalf;
+      auto shared_keys = [&](long long t) { return p.causal && u.n > 1 && (t - u.start + 1) * kKeys > u.L - u.n; };
+      if constexpr (!kF8) {
+        for (long long t = t_first; t < t_end;) {
+          if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
+          const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
+          const uint32_t kb = ring + st * 2 * W::kHalf;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int at = i * 32 + lane, r = at / kPieces, c = at % kPieces;
-          const uint32_t off = __shfl_sync(0xffffffffu, next_off, r);
-          const size_t o = ((size_t)off + c) * 16u;
-          const int row = lw * kMine + r;
-          const uint32_t d = kb + (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          const bool there = (mask >> r) & 1u;
-          copy16(d, p.c.k + o, there);
-          copy16(d + W::kHalf, p.c.v + o, there);
+          for (int i = 0; i < kLoads; ++i) {
+            const int at = i * 32 + lane, r = at / kPieces, c = at % kPieces;
+            const uint32_t off = __shfl_sync(0xffffffffu, next_off, r);
+            const size_t o = ((size_t)off + c) * 16u;
+            const int row = lw * kMine + r;
+            const uint32_t d = kb + (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            const bool there = (mask >> r) & 1u;
+            copy16(d, p.c.k + o, there);
+            copy16(d + W::kHalf, p.c.v + o, there);
+          }
+          if (lane == 0) {
+            S.mask[st][lw] = mask;
+            mbar_arrive(&S.full[st]);
+          }
+          if (shared_keys(t)) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            sanitise(st, u.ordinal);
+            mbar_arrive(&S.full[st]);
+          } else {
+            // arrives by itself once this thread's copies have landed
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&S.full[st]))
+                         : "memory");
+          }
+          t = u.step(p, t, t_end);
+          if (t < t_end) look_up(t);
+          if (++st == kStages) {
+            st = 0;
+            ++round;
+          }
         }
-        if (lane == 0) {
-          S.mask[st][lw] = mask;
+      } else {
+        // 8-bit caches: a thread copies its pieces as they are into a ring of
+        // its own, kRaw tiles deep, and widens them into the tile's stage
+        constexpr int kRaw = W::kRaw;
+        unsigned char* mine = mem + W::kQBytes + kStages * 2 * W::kHalf + lw * (W::kRawBytes / kLoadWarps) + lane * 16;
+        long long t = t_first;
+        int slot = 0, issued = 0, done = 0, from = 0;
+        auto issue = [&]() {
+          if (t < t_end) {
+            const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+              const int at = i * 32 + lane, r = at / kPieces, c = at % kPieces;
+              const uint32_t off = __shfl_sync(0xffffffffu, next_off, r);
+              const size_t o = ((size_t)off + c) * 16u;
+              const bool there = (mask >> r) & 1u;
+              const uint32_t d = smem_addr(mine + slot * W::kRawBytes + i * 512);
+              copy16(d, p.c.k + o, there);
+              copy16(d + kLoads * 512, p.c.v + o, there);
+            }
+            if (lane == 0) {
+              S.raw_mask[lw][slot] = mask;
+              S.raw_unit[lw][slot] = 2 * u.ordinal + (shared_keys(t) ? 1 : 0);
+            }
+            ++issued;
+            t = u.step(p, t, t_end);
+            if (t < t_end) look_up(t);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          slot = slot + 1 == kRaw ? 0 : slot + 1;
+        };
+        for (int i = 0; i < kRaw - 1; ++i) issue();
+        for (;;) {
+          issue();
+          if (done == issued) break;
+          asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
+          __syncwarp();
+          const uint32_t mask = S.raw_mask[lw][from];
+          const int unit = S.raw_unit[lw][from];
+          if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
+          unsigned char* kb = mem + W::kQBytes + st * 2 * W::kHalf;
+          bool found = false;
+#pragma unroll 4
+          for (int i = 0; i < 2 * kLoads; ++i) {
+            uint4 w = *reinterpret_cast<const uint4*>(mine + from * W::kRawBytes + i * 512);
+            const bool is_v = i >= kLoads;
+            const int at = (is_v ? i - kLoads : i) * 32 + lane, row = lw * kMine + at / kPieces, c = 2 * (at % kPieces);
+            if (is_v && (unit & 1)) {
+              found |= drop_nan(w.x);
+              found |= drop_nan(w.y);
+              found |= drop_nan(w.z);
+              found |= drop_nan(w.w);
+            }
+            unsigned char* d = kb + (is_v ? W::kHalf : 0) + (c >> 3) * (kKeys * 128) + row * 128;
+            *reinterpret_cast<uint4*>(d + (((c & 7) ^ (row & 7)) << 4)) = widen8<T>(w.x, w.y);
+            *reinterpret_cast<uint4*>(d + ((((c + 1) & 7) ^ (row & 7)) << 4)) = widen8<T>(w.z, w.w);
+          }
+          if (found) S.unsound[(unit >> 1) % kFlags] = 1;
+          if (lane == 0) S.mask[st][lw] = mask;
+          fence_async_smem();
           mbar_arrive(&S.full[st]);
-        }
-        if (p.causal && u.n > 1 && (t - u.start + 1) * kKeys > u.L - u.n) {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          sanitise(st, u.ordinal);
-          mbar_arrive(&S.full[st]);
-        } else {
-          // arrives by itself once this thread's copies have landed
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&S.full[st])) : "memory");
-        }
-        t = u.step(p, t, t_end);
-        if (t < t_end) look_up(t);
-        if (++st == kStages) {
-          st = 0;
-          ++round;
+          ++done;
+          from = from + 1 == kRaw ? 0 : from + 1;
+          if (++st == kStages) {
+            st = 0;
+            ++round;
+          }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -508,7 +614,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         for (int i = 0; i < kKeys; i += 8) st8(my + W::kP + i, zero);  // both buffers: the other copies' keys stay 0
         wait_st();
       }
-      const float c = p.scale * kLog2e;
+      float c = p.scale * kLog2e;
+      [[maybe_unused]] bool flip = false, flat = false;  // 8-bit caches: a negative, a zero scale of K
       float* scratch = reinterpret_cast<float*>(mem);  // Q's place, between units
       int j = 0;
       uint32_t syncs = 0;
@@ -532,6 +639,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (kF8) {
+          // the comparison of scores is on unscaled ones: their factor is made positive
+          c = p.scale * kLog2e * (p.c.k_scale ? p.c.k_scale[u.h] : 1.0f);
+          flip = c < 0.0f;
+          flat = c == 0.0f;
+          c = flat ? 1.0f : fabsf(c);
+        }
         fence_async_smem();
         mbar_arrive(&S.q_full);
         const int tok = (u.rb * R + row) / p.G;
@@ -555,6 +669,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           // scores of the columns from c0 on, unscaled, -inf where masked
           auto read = [&](int c0, uint32_t (&x)[kChunk]) {
             tmem_load<kChunk>(scores + c0, x);
+            if constexpr (kF8) {
+              if (flip || flat)
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) x[i] = flat ? 0u : x[i] ^ 0x80000000u;
+            }
             if (whole_tile) return;
 #pragma unroll
             for (int g = 0; g < kChunk; g += kGroup) {
@@ -642,7 +761,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
 #pragma unroll
         for (int k = 0; k < kCopies; ++k) sum += part_sum(S.parts[k * R + row], best);
         float factor = m == kNegInf ? 0.0f : ex2(m - best);
-        if (whole) factor *= reciprocal_or_zero(sum);
+        if (whole) {
+          factor *= reciprocal_or_zero(sum);
+          if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
+        }
         const long long slot = 2LL * blockIdx.x + (u_begin == t_begin ? 0 : 1);
         const int g = u.rb * R + row, ti = g / p.G;
         const long long q_tok = u.first + ti, q_head = u.h * p.G + g - ti * p.G;
@@ -691,11 +813,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
                   split_position(p.c, k, page, sl);
                   const int id = p.c.table[(long long)u.b * p.c.table_stride + page];
                   if (id < 0 || id >= p.c.num_pages) continue;
-                  const uint16_t* v =
-                      reinterpret_cast<const uint16_t*>(p.c.v + (size_t)row_offset(p.c, id, u.h, sl) * 16u) + r0 + d;
+                  const unsigned char* v =
+                      p.c.v + (size_t)row_offset(p.c, id, u.h, sl) * 16u + (kF8 ? 1 : 2) * (r0 + d);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (word_not_finite<T>(v[i])) y[i] = __float_as_uint(__uint_as_float(y[i]) + T::unpack(v[i]).x);
+                  for (int i = 0; i < 32; ++i) {
+                    if constexpr (kF8) {
+                      if ((v[i] & 0x7fu) == 0x7fu) y[i] = 0x7fffffffu;
+                    } else {
+                      const uint16_t b = reinterpret_cast<const uint16_t*>(v)[i];
+                      if (word_not_finite<T>(b)) y[i] = __float_as_uint(__uint_as_float(y[i]) + T::unpack(b).x);
+                    }
+                  }
                 }
               }
               float4 x[8];
@@ -747,9 +875,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
   if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-template <class T, int D, int R>
+template <class T, bool kF8, int D, int R>
 int launch(const AttnParams& p, int sms, void* stream) {
-  using W = TcShape<D>;
+  using W = TcShape<D, kF8>;
   const AttnGeometry geo = tc_geometry(R, D);
   static bool ready[64] = {};
   int dev = 0;
@@ -757,7 +885,8 @@ int launch(const AttnParams& p, int sms, void* stream) {
   if (e != cudaSuccess) return (int)e;
   if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(attention_tc_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kSmem);
+    e = cudaFuncSetAttribute(attention_tc_kernel<T, kF8, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)W::kSmem);
     if (e != cudaSuccess) return (int)e;
     ready[dev] = true;
   }
@@ -772,26 +901,30 @@ int launch(const AttnParams& p, int sms, void* stream) {
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = W::kSmem;
-  e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, D, R>, p, geo);
+  e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, kF8, D, R>, p, geo);
   if (e != cudaSuccess) return (int)e;
-  return launch_join(p, geo, grid, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, false, D, stream);
+  return launch_join(p, geo, grid, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, kF8, D, stream);
 }
 template <class T, int R>
-int pick_dim(const AttnParams& p, int d, int sms, void* stream) {
-  return d == 64 ? launch<T, 64, R>(p, sms, stream) : d == 128 ? launch<T, 128, R>(p, sms, stream) : launch<T, 256, R>(p, sms, stream);
-}
-template <class T>
-int pick_rows(const AttnParams& p, int rows, int d, int sms, void* stream) {
-  return rows == 32 ? pick_dim<T, 32>(p, d, sms, stream) : rows == 64 ? pick_dim<T, 64>(p, d, sms, stream) : pick_dim<T, 128>(p, d, sms, stream);
+int pick(const AttnParams& p, bool f8, int d, int sms, void* stream) {
+  if (f8) return d == 64 ? launch<T, true, 64, R>(p, sms, stream) : launch<T, true, 128, R>(p, sms, stream);
+  return d == 64    ? launch<T, false, 64, R>(p, sms, stream)
+         : d == 128 ? launch<T, false, 128, R>(p, sms, stream)
+                    : launch<T, false, 256, R>(p, sms, stream);
 }
 
 }  // namespace
 
 AttnGeometry tc_geometry(int rows, int head_dim) { return {rows, head_dim == 256 ? 64 : 128, kTcCtas}; }
 
-int launch_attention_tc(const AttnParams& p, int rows, int dtype, int head_dim, int sms, void* stream) {
-  return dtype == DFLASH_BF16 ? pick_rows<Bf16>(p, rows, head_dim, sms, stream)
-                              : pick_rows<F16>(p, rows, head_dim, sms, stream);
+int launch_attention_tc(const AttnParams& p, int rows, int dtype, bool f8, int head_dim, int sms, void* stream) {
+  if (dtype == DFLASH_BF16)
+    return rows == 32   ? pick<Bf16, 32>(p, f8, head_dim, sms, stream)
+           : rows == 64 ? pick<Bf16, 64>(p, f8, head_dim, sms, stream)
+                        : pick<Bf16, 128>(p, f8, head_dim, sms, stream);
+  return rows == 32   ? pick<F16, 32>(p, f8, head_dim, sms, stream)
+         : rows == 64 ? pick<F16, 64>(p, f8, head_dim, sms, stream)
+                      : pick<F16, 128>(p, f8, head_dim, sms, stream);
 }
 
 }  // namespace dflash

@@ -60,6 +60,10 @@ def rows(cache, table, b, L, page, scale=None):
     return x if scale is None else x * scale.double()[None, :, None]
 
 
+def rows_of(y, at):
+    return y.view(torch.uint8)[at].view(F8) if y.dtype == F8 else y[at]
+
+
 def check(dv, table, caches, q, scales, counts, lens, page, causal, scale=None, seen=None, **kw):
     D = q.shape[2]
     scale = D ** -0.5 if scale is None else scale
@@ -68,7 +72,10 @@ def check(dv, table, caches, q, scales, counts, lens, page, causal, scale=None, 
     out, lse = dv.paged_attention(pc, q, torch.tensor(lens, dtype=torch.int32, device=DEV), q_start=starts, scale=scale,
                                   causal=causal, return_lse=True, **kw)
     torch.cuda.synchronize()
-    up = U[torch.float16] if caches[0].dtype == F8 else U[q.dtype]
+    # the weights are rounded to the products' type: the tokens', or f16 for the
+    # 8-bit caches of few rows (or head_dim 256)
+    rows_each = -(-q.shape[0] // len(counts)) * (q.shape[1] // caches[0].shape[1])
+    up = U[torch.float16] if caches[0].dtype == F8 and (rows_each <= 16 or D == 256) else U[q.dtype]
     for b, s in enumerate(starts_of(counts)[:-1]):
         n, L = counts[b], lens[b]
         if n == 0:
@@ -205,28 +212,34 @@ BLOCKS = [
 
 @pytest.mark.parametrize("case", BLOCKS, ids=range(len(BLOCKS)))
 @pytest.mark.parametrize("inner", [False, True])
-def test_blocks_match_the_definition(dv, case, inner):
+@pytest.mark.parametrize("f8", [False, True])
+def test_blocks_match_the_definition(dv, case, inner, f8):
     counts, lens, Hq, Hkv, D, page, causal, dtype = case
-    table, caches, q, _ = make(len(lens) + D + page, counts, lens, Hq, Hkv, D, page, dtype, dtype, inner,
-                               fill=float("nan"))
+    table, caches, q, scales = make(len(lens) + D + page, counts, lens, Hq, Hkv, D, page, dtype, F8 if f8 else dtype,
+                                    inner, fill=float("nan"))
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
-    a = check(dv, table, caches, q, None, counts, lens, page, causal, status=st)
-    b = check(dv, table, caches, q, None, counts, lens, page, causal, status=st)
+    a = check(dv, table, caches, q, scales, counts, lens, page, causal, status=st)
+    b = check(dv, table, caches, q, scales, counts, lens, page, causal, status=st)
     assert int(st) == 0 and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-@pytest.mark.parametrize("D,rows", [(64, 32), (64, 128), (128, 32), (128, 64), (128, 128), (256, 64)])
-def test_long_blocks_are_split(dv, D, rows):
+@pytest.mark.parametrize("D,rows,cdt", [(64, 32, BF), (64, 128, BF), (128, 32, BF), (128, 64, BF), (128, 128, BF),
+                                        (256, 64, BF), (64, 64, F8), (128, 32, F8), (128, 128, F8)])
+def test_long_blocks_are_split(dv, D, rows, cdt):
     """One request over every SM, its rising scores moving the reference again and again."""
     n, lens = rows // 8, [70001]
-    table, caches, q, _ = make(D + rows, [n], lens, 16, 2, D, 64, BF, BF, False)
+    table, caches, q, scales = make(D + rows, [n], lens, 16, 2, D, 64, BF, cdt, False)
     grow = torch.linspace(0.05, 3.0, lens[0], device=DEV)
     pos = torch.arange(lens[0], device=DEV)
     y = caches[0].transpose(1, 2)
     at = table[0].long()[pos // 64], pos % 64
-    y[at] = (y[at].float() * grow[:, None, None]).to(BF)
-    a, la = check(dv, table, caches, q, None, [n], lens, 64, True)
-    b, lb = check(dv, table, caches, q, None, [n], lens, 64, True)
+    grown = (rows_of(y, at).float() * grow[:, None, None]).to(cdt)
+    if cdt == F8:
+        y.view(torch.uint8)[at] = grown.view(torch.uint8)
+    else:
+        y[at] = grown
+    a, la = check(dv, table, caches, q, scales, [n], lens, 64, True)
+    b, lb = check(dv, table, caches, q, scales, [n], lens, 64, True)
     assert torch.equal(a, b) and torch.equal(la, lb)
 
 
@@ -258,6 +271,34 @@ def test_masked_values_never_count_in_blocks(dv, dtype, D, G, bad):
     where = torch.zeros(D, dtype=torch.bool, device=DEV)
     where[1::3] = True
     assert bool((~got[:, first:].float().isfinite() == where).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_masked_nan_never_counts_in_8_bit_blocks(dv, D):
+    counts, lens, page, first, n, G = [6, 6], [140, 70], 16, 3, 6, 8
+    table, caches, q, scales = make(8, counts, lens, 2 * G, 2, D, page, BF, F8, False)
+    clean = [c.clone() for c in caches]
+    for b in range(2):
+        for i in range(first, n):
+            j = lens[b] - n + i
+            caches[1].view(torch.uint8)[int(table[b, j // page]), :, j % page, 1::3] = 0x7F if i % 2 else 0xFF
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    got, gl = dv.paged_attention(dv.PagedCache(caches[0], caches[1], table, *scales), q, ln, return_lse=True)
+    want, wl = dv.paged_attention(dv.PagedCache(clean[0], clean[1], table, *scales), q, ln, return_lse=True)
+    g, w = got.view(2, n, 2 * G, D), want.view(2, n, 2 * G, D)
+    assert torch.equal(g[:, :first], w[:, :first]) and torch.equal(gl, wl)
+    where = torch.zeros(D, dtype=torch.bool, device=DEV)
+    where[1::3] = True
+    assert bool((g[:, first:].isnan() == where).all())
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [6, 6]])
+def test_scales_of_any_sign(dv, counts):
+    """Scales below and at zero: the stored values stand for themselves times the scale."""
+    lens, page, D = [300, 77], 16, 128
+    table, caches, q, _ = make(31, counts, lens, 12, 3, D, page, BF, F8, False)
+    scales = [torch.tensor([-0.7, 0.0, 1.3], device=DEV), torch.tensor([1.1, -2.0, 0.0], device=DEV)]
+    check(dv, table, caches, q, scales, counts, lens, page, True)
 
 
 def test_blocks_with_extreme_scores(dv):
