@@ -69,7 +69,7 @@ struct TcShape {
 struct TcShared {  // next to the dynamic part: 227 KB in all
   uint64_t full[6], empty[6];    // per stage
   uint64_t s_full[2], p_full[2];  // per score buffer
-  uint64_t pv_done, q_full, drained, together;
+  uint64_t pv_done, unit_done, q_full, drained, together;
   uint32_t tmem;
   volatile int failed;
   int unsound[kFlags];           // per unit (ordinal in the CTA): see load
@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       mbar_init(&S.p_full[i], 128);
     }
     mbar_init(&S.pv_done, 1);
+    mbar_init(&S.unit_done, 1);
     mbar_init(&S.q_full, 128);
     mbar_init(&S.drained, 1);
     mbar_init(&S.together, 128);
@@ -558,8 +559,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         constexpr uint32_t type = std::is_same<T, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t id_s = (1u << 4) | type | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
         constexpr uint32_t id_o = (1u << 4) | type | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
-        // O += P V of tile j; fresh: the unit's (or the run's) first
-        auto sum_values = [&](int j, bool fresh) {
+        // O += P V of tile j; fresh, last: the unit's (or the run's) first and last tile
+        auto sum_values = [&](int j, bool fresh, bool last) {
           const int st = j % kStages, buf = j & 1;
           if (!tc_wait(&S.p_full[buf], (uint32_t)(j >> 1) & 1u, S)) return false;
           fence_after();
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             mma_ts(tmem + W::kO, tmem + W::kP + buf * (kKeys / 2) + 8 * k, operand(vb + k * 2048, kKeys * 128), id_o,
                    !fresh || k > 0);
           mma_commit(&S.empty[st]);
-          mma_commit(&S.pv_done);
+          mma_commit(last ? &S.unit_done : &S.pv_done);
           return true;
         };
         bool fresh = true, prev_fresh = true;  // of tile j, and of the last whose P V is not issued yet
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         for (long long t = t_first; t < t_end && ok; ++j) {
           if (fresh) {
             // the next unit's Q comes only after the last one's sums are out
-            if (j > 0 && (ok = sum_values(j - 1, prev_fresh))) summed = j;
+            if (j > 0 && (ok = sum_values(j - 1, prev_fresh, true))) summed = j;
             ok = ok && tc_wait(&S.q_full, (uint32_t)units & 1u, S);
             ++units;
           }
@@ -592,14 +593,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             mma_ss(tmem + W::kS + (j & 1) * kKeys, operand(q_mem + (k >> 2) * 16384 + (k & 3) * 32, 16),
                    operand(kb + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16), id_s, k > 0);
           mma_commit(&S.s_full[j & 1]);
-          if (summed < j && (ok = sum_values(j - 1, prev_fresh))) summed = j;
+          if (summed < j && (ok = sum_values(j - 1, prev_fresh, false))) summed = j;
           if (!ok) break;
           prev_fresh = fresh;
           const int unit = u.ordinal;
           t = u.step(p, t, t_end);
           fresh = u.ordinal != unit;
         }
-        if (ok && j > 0) ok = sum_values(j - 1, prev_fresh);
+        if (ok && j > 0) ok = sum_values(j - 1, prev_fresh, true);
         mma_commit(&S.drained);  // nothing is left in flight when the tensor memory is freed
         mbar_wait_landed(&S.drained, 0);
       }
@@ -617,8 +618,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       float c = p.scale * kLog2e;
       [[maybe_unused]] bool flip = false, flat = false;  // 8-bit caches: a negative, a zero scale of K
       float* scratch = reinterpret_cast<float*>(mem);  // Q's place, between units
-      int j = 0;
-      uint32_t syncs = 0;
+      int j = 0, sums = 0;  // tiles, and those of them whose product pv_done announces, before this one
+      uint32_t syncs = 0, units = 0;
       long long t = t_first;
       while (t < t_end && ok) {
         const long long u_end = u.end(t_end), u_begin = t;
@@ -699,9 +700,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           const bool move = top > m;
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? (m == kNegInf ? 0.0f : ex2(m - top)) : 1.0f;
-            if (t > u_begin) {  // O holds sums: they are rescaled, after the product in flight (the one before is
-                                // over: these scores came after it)
-              ok = tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
+            if (t > u_begin) {
+              // O holds sums: they are rescaled, after the product in flight,
+              // number sums - 1. A parity names one of two phases: the product
+              // before that is over (these scores came after it) and the one
+              // after it waits for this thread.
+              ok = tc_wait(&S.pv_done, (uint32_t)(sums - 1) & 1u, S);
               if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -736,15 +740,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           wait_st();
           fence_before();
           mbar_arrive(&S.p_full[buf]);
+          if (t + 1 < u_end) ++sums;
         }
         if (!ok) break;
 
         // ---- the unit (or this CTA's run of it) ends
-        // A parity names a phase only if the one before the last is known to be
-        // over. The last scores show the product two tiles back done, no more:
-        // another warp may still be at its weights. So both are waited for.
-        if (j > 1) ok = tc_wait(&S.pv_done, (uint32_t)j & 1u, S);
-        ok = ok && tc_wait(&S.pv_done, (uint32_t)(j - 1) & 1u, S);
+        ok = tc_wait(&S.unit_done, (uint32_t)units & 1u, S);
+        ++units;
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
