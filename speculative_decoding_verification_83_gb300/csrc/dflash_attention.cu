@@ -28,6 +28,12 @@
 //  * e4m3 caches are widened in registers, exactly, to f16. q is then scaled
 //    per row by a power of two into f16's range (exact but for values
 //    below 2^-31 of the row's largest), undone in the scores.
+// Measured on one GB300 (bytes of keys and values over time): 64 requests of up
+// to 8192 positions, 64 query and 8 key/value heads of 128, bf16: 201 us, 6.1
+// TB/s, 91% of a copy's rate; three CTAs an SM with two ring stages each beat
+// two with three (206 us). Two requests of 200001 positions in e4m3: 163 us, 5.0
+// TB/s (two CTAs an SM: 176 us): there the widening and the products' issue
+// bound it, with 12 warps an SM to hide their latency.
 // Rounding: P is rounded to the operands' type (half a step of its own
 // relative to each weight); all sums, maxima and exponents are fp32.
 #include <cuda_runtime.h>

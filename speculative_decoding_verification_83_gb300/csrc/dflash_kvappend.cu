@@ -11,6 +11,14 @@
 // bits, as a signed number of half turns in [-1, 1), go to sincospif.
 // Everything is fp32 until the one rounding to the stored type (e4m3: the
 // value over its head's scale, saturated at +-448).
+//
+// What bounds it: reading and writing each value once; for few tokens the launch
+// and the chain of offset, length, page and slot. So a block reads its values
+// first and finds out where they go while they arrive. Measured on one GB300:
+// 10223 tokens of 40 query and 8 key/value heads of 128 into an e4m3 cache, half
+// of each head rotated, 50 us (5.4 TB/s, 81% of a copy's rate), where one token a
+// block, read after its place was known, took 75 us, and two divisions an item 62
+// us. Four items a thread are best there (two 51 us, eight 57 us).
 #include <cuda_runtime.h>
 
 #include <cstdint>
