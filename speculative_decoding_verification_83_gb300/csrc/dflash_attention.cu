@@ -111,8 +111,8 @@ struct Shape {
   static constexpr int kHalfStage = kWarpKeys * kRowBytes;  // K or V of one warp's step
   static constexpr int kStageBytes = 2 * kHalfStage * kWarps;
   // CTAs per SM, and a ring that fills the SM's shared memory with them
-  static constexpr int kPerSm = kStageBytes <= 32768 ? 3 : 1;
-  static constexpr int kRing = kPerSm == 3 ? 65536 : 196608;
+  static constexpr int kPerSm = D < 256 ? 3 : kF8 ? 2 : 1;  // as registers allow: O alone takes D / 2 a thread
+  static constexpr int kRing = kPerSm == 3 ? 65536 : kPerSm == 2 ? 98304 : 196608;
   static constexpr int kStages = kRing / kStageBytes;
   static constexpr int kCols = 32;  // columns of O joined at a time
   static constexpr size_t kMerge = (size_t)kWarps * kRows * (kCols + 1) * sizeof(float);
@@ -548,55 +548,57 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
 }
 
 // ---- joining the partial results of units that span CTAs -------------------------------
-// CTA (c, part): 64 columns of the unit that begins in CTA c's run. One warp per
-// query row: the segments' maxima give their factors, then the segments are
-// summed in list order.
+// CTA (c, z): 16 rows of the unit that begins in CTA c's run, one warp each. The
+// segments' maxima give their factors, then the segments are summed in list
+// order. A chain of three loads bounds it, so every row has its warp and a warp
+// 16 segments in flight.
 constexpr int kJoinWarps = 16;
 template <class T, bool kF8, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams p, const AttnGeometry geo) {
+  constexpr int kPer = D / 32;  // columns of a lane
   grid_dependency_sync();
-  const int lane = threadIdx.x & 31, c0 = blockIdx.x, col = blockIdx.y * 64 + 2 * lane;
+  const int lane = threadIdx.x & 31, c0 = blockIdx.x, jr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   const SplitUnit u = split_units(p)[c0];
   const long long run = *reinterpret_cast<const long long*>(p.ws);
-  if (u.tiles == 0) return;
+  if (u.tiles == 0 || jr >= min(geo.rows, u.n * p.G - u.rb * geo.rows)) return;
   const int c1 = (int)((u.start + u.tiles - 1) / run);
   const Part* parts = reinterpret_cast<const Part*>(p.ws + geo.ml());
   const float* os = reinterpret_cast<const float*>(p.ws + geo.o());
   const long long slot0 = 2LL * c0 + (u.start == (long long)c0 * run ? 0 : 1);
-  const int rows = min(geo.rows, u.n * p.G - u.rb * geo.rows);
-  for (int jr = threadIdx.x >> 5; jr < rows; jr += kJoinWarps) {
-    auto slot_row = [&](int c) { return (c == c0 ? slot0 : 2LL * c) * geo.rows + jr; };
-    float top = kNegInf;
-    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, parts[slot_row(c)].m);
-    top = warp_max_f32(top);
-    float2 x = make_float2(0.0f, 0.0f);
-    float sum = 0.0f;
-    for (int cb = c0; cb <= c1; cb += 32) {
-      const int c = cb + lane;
-      float w = 0.0f, l = 0.0f;
-      if (c <= c1) {
-        const Part b = parts[slot_row(c)];
-        w = b.m == kNegInf ? 0.0f : ex2(b.m - top);
-        l = part_sum(b, top);
-      }
-      const int cnt = min(32, c1 - cb + 1);
-#pragma unroll 8
-      for (int j = 0; j < cnt; ++j) {
-        const float2 y = *reinterpret_cast<const float2*>(os + slot_row(cb + j) * D + col);
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        sum += __shfl_sync(0xffffffffu, l, j);
-        x.x = fmaf(y.x, wj, x.x);
-        x.y = fmaf(y.y, wj, x.y);
-      }
+  auto slot_row = [&](int c) { return (c == c0 ? slot0 : 2LL * c) * geo.rows + jr; };
+  Part mine = {kNegInf, 0.0f};  // this lane's segment of the first 32
+  if (c0 + lane <= c1) mine = parts[slot_row(c0 + lane)];
+  float top = mine.m;
+  for (int c = c0 + 32 + lane; c <= c1; c += 32) top = fmaxf(top, parts[slot_row(c)].m);
+  top = warp_max_f32(top);
+  float x[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
+  float sum = 0.0f;
+  for (int cb = c0; cb <= c1; cb += 32) {
+    if (cb > c0) mine = cb + lane <= c1 ? parts[slot_row(cb + lane)] : Part{kNegInf, 0.0f};
+    const float w = mine.m == kNegInf ? 0.0f : ex2(mine.m - top), l = part_sum(mine, top);
+    const int cnt = min(32, c1 - cb + 1);
+#pragma unroll 16
+    for (int j = 0; j < cnt; ++j) {
+      const float* src = os + slot_row(cb + j) * D + lane * kPer;
+      float y[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) *reinterpret_cast<float2*>(y + e) = *reinterpret_cast<const float2*>(src + e);
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      sum += __shfl_sync(0xffffffffu, l, j);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = fmaf(y[e], wj, x[e]);
     }
-    float factor = reciprocal_or_zero(sum);
-    if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
-    const int g = u.rb * geo.rows + jr, ti = g / p.G;
-    const long long tok = u.first + ti, head = u.h * p.G + g - ti * p.G;
-    *reinterpret_cast<uint32_t*>(p.out + 2 * (tok * p.o_ts + head * p.o_hs + col)) = T::pack(x.x * factor, x.y * factor);
-    if (lane == 0 && blockIdx.y == 0 && p.lse)
-      p.lse[tok * ((long long)p.G * p.c.kv_heads) + head] = (top + log2f(sum)) * kLn2;
   }
+  float factor = reciprocal_or_zero(sum);
+  if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
+  const int g = u.rb * geo.rows + jr, ti = g / p.G;
+  const long long tok = u.first + ti, head = u.h * p.G + g - ti * p.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + 2 * (tok * p.o_ts + head * p.o_hs)) + lane * (kPer / 2);
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) dst[e / 2] = T::pack(x[e] * factor, x[e + 1] * factor);
+  if (lane == 0 && p.lse) p.lse[tok * ((long long)p.G * p.c.kv_heads) + head] = (top + log2f(sum)) * kLn2;
 }
 
 template <class T, bool kF8, int D>
@@ -647,7 +649,7 @@ int launch_join_dim(const AttnParams& p, const AttnGeometry& g, int grid, void* 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = (cudaStream_t)stream;
-  cfg.gridDim = dim3((unsigned)grid, D / 64);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((g.rows + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(32 * kJoinWarps);
   return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, kF8, D>, p, g);
 }

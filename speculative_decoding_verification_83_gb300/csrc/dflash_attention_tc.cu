@@ -25,10 +25,11 @@
 //  * warps 0-3: softmax. A thread reads its scores (tcgen05.ld), takes 2^(x -
 //    m), writes P back as 16-bit pairs. When a row's running maximum m moves,
 //    its warp rescales O in tensor memory, which has to wait for the product
-//    before. Letting m lag until a score exceeds it by 8 spares most of that
-//    (220 against 224 us at the size below) but the largest weights are then no
-//    longer exactly 1, and their rounding shows: an error of 2.2e-3 of the
-//    result in bf16 against 1.8e-3 (the output's rounding alone is 1.7e-3).
+//    before. m may lag behind by 2 powers of 2 (weights up to 4), which spares
+//    most of that. The largest weights are then no longer exactly 1 and their
+//    rounding shows a little: in bf16 an error of 1.86e-3 of the result, against
+//    1.77e-3 with m exact and 2.1e-3 with a lag of 8 (the output's rounding alone:
+//    1.7e-3).
 // A unit's end costs a CTA about kEndTiles tiles (O out of tensor memory, Q in),
 // so the list of work counts it. 8-bit caches (head_dim 64 and 128) go through a
 // ring of raw tiles and are widened, exactly, into the operand tiles.
@@ -57,6 +58,7 @@ constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
 // A unit's end and the next one's beginning take a CTA about as long as this
 // many tiles: the list counts them, so that runs with many ends are shorter.
 constexpr int kEndTiles = 3;
+constexpr float kSlack = 2.0f;  // by how many powers of 2 a score may exceed its row's reference
 constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at once
 
 template <int D, bool kF8>
@@ -410,21 +412,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       constexpr int kPieces = W::kRowBytes / 16;     // 16-byte pieces of a row in the cache
       constexpr int kLoads = kMine * kPieces / 32;   // per lane, for K and for V each
       const int lw = warp - kLoadWarp0;
-      bool bad_page = false, next_ok = false;
-      uint32_t next_off = 0;
-      auto look_up = [&](long long t) {
-        const int key = (int)(t - u.start) * kKeys + lw * kMine + (lane & (kMine - 1));
-        next_ok = key < u.L;
-        int page = 0, slot = 0, id = 0;
-        if (next_ok) {
-          split_position(p.c, key, page, slot);
-          id = p.c.table[(long long)u.b * p.c.table_stride + page];
-          if (id < 0 || id >= p.c.num_pages) {
-            bad_page = true;
-            next_ok = false;
+      // The page index of a tile's keys is asked for two tiles ahead: lane l
+      // looks after key l of the warp's share.
+      struct Ahead {
+        long long t;    // the tile (t_end: none)
+        int id, slot, head, unit;  // unit: its ordinal twice, plus 1 where some rows see less of the tile than others
+        bool there;
+      };
+      bool bad_page = false;
+      auto ask = [&](long long t) {
+        Ahead a = {t, 0, 0, 0, 0, false};
+        if (t < t_end) {
+          const int key = (int)(t - u.start) * kKeys + lw * kMine + (lane & (kMine - 1));
+          a.there = key < u.L;
+          a.head = u.h;
+          a.unit = 2 * u.ordinal + (p.causal && u.n > 1 && (t - u.start + 1) * kKeys > u.L - u.n ? 1 : 0);
+          if (a.there) {
+            int page;
+            split_position(p.c, key, page, a.slot);
+            a.id = p.c.table[(long long)u.b * p.c.table_stride + page];
           }
         }
-        next_off = next_ok ? row_offset(p.c, id, u.h, slot) : 0u;
+        return a;
+      };
+      // the row's place, once the index is here
+      auto place = [&](Ahead& a) {
+        if (a.there && (a.id < 0 || a.id >= p.c.num_pages)) {
+          bad_page = true;
+          a.there = false;
+        }
+        return a.there ? row_offset(p.c, a.id, a.head, a.slot) : 0u;
+      };
+      Ahead now = ask(t_first), next = now;
+      if (t_first < t_end) next = ask(u.step(p, t_first, t_end));
+      auto move_on = [&]() {
+        now = next;
+        if (next.t < t_end) next = ask(u.step(p, next.t, t_end));
       };
       // Under a causal mask a tile may hold values that only some rows see, and
       // a weight of 0 times one that is not finite would be NaN. Such a value
@@ -451,14 +474,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         }
         if (found) S.unsound[ordinal % kFlags] = 1;
       };
-      if (t_first < t_end) look_up(t_first);
       int st = 0;
       uint32_t round = 0;
-      auto shared_keys = [&](long long t) { return p.causal && u.n > 1 && (t - u.start + 1) * kKeys > u.L - u.n; };
       if constexpr (!kF8) {
-        for (long long t = t_first; t < t_end;) {
+        while (now.t < t_end) {
+          const uint32_t next_off = place(now), mask = __ballot_sync(0xffffffffu, now.there);
           if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
-          const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
+          __syncwarp();
           const uint32_t kb = ring + st * 2 * W::kHalf;
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
@@ -475,17 +497,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             S.mask[st][lw] = mask;
             mbar_arrive(&S.full[st]);
           }
-          if (shared_keys(t)) {
+          if (now.unit & 1) {
             asm volatile("cp.async.wait_all;" ::: "memory");
-            sanitise(st, u.ordinal);
+            sanitise(st, now.unit >> 1);
             mbar_arrive(&S.full[st]);
           } else {
             // arrives by itself once this thread's copies have landed
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&S.full[st]))
                          : "memory");
           }
-          t = u.step(p, t, t_end);
-          if (t < t_end) look_up(t);
+          move_on();
           if (++st == kStages) {
             st = 0;
             ++round;
@@ -496,11 +517,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         // its own, kRaw tiles deep, and widens them into the tile's stage
         constexpr int kRaw = W::kRaw;
         unsigned char* mine = mem + W::kQBytes + kStages * 2 * W::kHalf + lw * (W::kRawBytes / kLoadWarps) + lane * 16;
-        long long t = t_first;
         int slot = 0, issued = 0, done = 0, from = 0;
         auto issue = [&]() {
-          if (t < t_end) {
-            const uint32_t mask = __ballot_sync(0xffffffffu, next_ok);
+          if (now.t < t_end) {
+            const uint32_t next_off = place(now), mask = __ballot_sync(0xffffffffu, now.there);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
               const int at = i * 32 + lane, r = at / kPieces, c = at % kPieces;
@@ -513,11 +533,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             }
             if (lane == 0) {
               S.raw_mask[lw][slot] = mask;
-              S.raw_unit[lw][slot] = 2 * u.ordinal + (shared_keys(t) ? 1 : 0);
+              S.raw_unit[lw][slot] = now.unit;
             }
             ++issued;
-            t = u.step(p, t, t_end);
-            if (t < t_end) look_up(t);
+            move_on();
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
           slot = slot + 1 == kRaw ? 0 : slot + 1;
@@ -706,7 +725,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             for (int i = 0; i < kChunk; ++i) top = fmaxf(top, __uint_as_float(x[i]));
           }
           top *= c;
-          const bool move = top > m;
+          const bool move = top > m + kSlack || (m == kNegInf && top > m);
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? (m == kNegInf ? 0.0f : ex2(m - top)) : 1.0f;
             if (t > u_begin) {
