@@ -20,25 +20,28 @@
 //    keys that do not exist are zero-filled. The copies arrive on the stage's
 //    barrier as they land.
 //  * warp 4: one thread issues S = Q K^T (both from shared memory, into one of
-//    two score buffers) one tile ahead of O += P V (P from tensor memory, V
-//    read in place as the transposed operand).
+//    two score buffers) up to two tiles ahead of O += P V (P from tensor memory,
+//    V read in place as the transposed operand).
 //  * warps 0-3: softmax. A thread reads its scores (tcgen05.ld), takes 2^(x -
 //    m), writes P back as 16-bit pairs. When a row's running maximum m moves,
 //    its warp rescales O in tensor memory, which has to wait for the product
-//    before. m may lag behind by 2 powers of 2 (weights up to 4), which spares
-//    most of that. The largest weights are then no longer exactly 1 and their
-//    rounding shows a little: in bf16 an error of 1.86e-3 of the result, against
-//    1.77e-3 with m exact and 2.1e-3 with a lag of 8 (the output's rounding alone:
-//    1.7e-3).
+//    before. m may lag behind by 8 powers of 2 (weights up to 256), which spares
+//    most of that: at 128 rows 152 against 178 us with a lag of 2 or 4, at
+//    head_dim 256 266 against 291 us. The largest weights are then no longer
+//    exactly 1 and their rounding shows: in bf16 an error of 2.2e-3 of the result
+//    against 1.8e-3 with m exact (the output's rounding alone: 1.7e-3; one weight
+//    ruling a row adds at most as much again in quadrature).
 // A unit's end costs a CTA about kEndTiles tiles (O out of tensor memory, Q in),
 // so the list of work counts it. 8-bit caches (head_dim 64 and 128) go through a
 // ring of raw tiles and are widened, exactly, into the operand tiles.
 // Measured on one GB300, 64 query and 8 key/value heads of 128, 32 requests of up
-// to 16384 positions, blocks of 8 (64 rows a head), bf16: 225 us, 5.5 TB/s of keys
-// and values, 83% of a copy's rate, against 696 us by the warps' products, which
-// read the cache four times there. What is left is the units' ends and the
-// uneven runs; at 128 rows, and for head_dim 64, the softmax's 128 threads bound
-// it (a tile's 64 or 128 columns each); for e4m3 (344 us) the widening does.
+// to 16384 positions, blocks of 8 (64 rows a head), bf16: 218 us, 5.7 TB/s of keys
+// and values, 85% of a copy's rate, against 696 us by the warps' products, which
+// read the cache four times there; blocks of 4 (32 rows) 199 us, 6.25 TB/s. What
+// is left is the units' ends and uneven runs. At 128 rows (half the positions:
+// 152 us, 4.2 TB/s, 520 TFLOP/s) and head_dim 64 (148 us, 4.2 TB/s) the softmax's
+// 128 threads bound it; at head_dim 256 (266 us, 4.7 TB/s) two stages are few for
+// the latency of a load; e4m3 (303 us for half the bytes) is bound by the widening.
 // Every wait is bounded; a CTA that gives up raises DFLASH_STATUS_TIMEOUT,
 // lets its copies land and frees its tensor memory.
 #include <cuda_runtime.h>
@@ -58,7 +61,7 @@ constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
 // A unit's end and the next one's beginning take a CTA about as long as this
 // many tiles: the list counts them, so that runs with many ends are shorter.
 constexpr int kEndTiles = 3;
-constexpr float kSlack = 2.0f;  // by how many powers of 2 a score may exceed its row's reference
+constexpr float kSlack = 8.0f;  // by how many powers of 2 a score may exceed its row's reference
 constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at once
 
 template <int D, bool kF8>
@@ -80,7 +83,8 @@ struct TcShape {
 struct TcShared {  // next to the dynamic part: 227 KB in all
   uint64_t full[6], empty[6];    // per stage
   uint64_t s_full[2], p_full[2];  // per score buffer
-  uint64_t pv_done, unit_done, q_full, drained, together;
+  uint64_t pv_done[2];           // per buffer of weights
+  uint64_t q_full, drained, together;
   uint32_t tmem;
   volatile int failed;
   int unsound[kFlags];           // per unit (ordinal in the CTA): see load
@@ -341,9 +345,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 128);
+      mbar_init(&S.pv_done[i], 1);
     }
-    mbar_init(&S.pv_done, 1);
-    mbar_init(&S.unit_done, 1);
     mbar_init(&S.q_full, 128);
     mbar_init(&S.drained, 1);
     mbar_init(&S.together, 128);
@@ -587,48 +590,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
         constexpr uint32_t type = std::is_same<T, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t id_s = (1u << 4) | type | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
         constexpr uint32_t id_o = (1u << 4) | type | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
-        // O += P V of tile j; fresh, last: the unit's (or the run's) first and last tile
-        auto sum_values = [&](int j, bool fresh, bool last) {
-          const int st = j % kStages, buf = j & 1;
-          if (!tc_wait(&S.p_full[buf], (uint32_t)(j >> 1) & 1u, S)) return false;
-          fence_after();
-          const uint32_t vb = ring + st * 2 * W::kHalf + W::kHalf;
+        int j0 = 0, units = 0;  // tiles before this unit's, units begun
+        for (long long t = t_first; t < t_end && ok;) {
+          const int n = (int)(u.end(t_end) - t);  // the unit's tiles here
+          // tile j0 + i has landed
+          auto landed = [&](int i) { return mbar_test_wait(&S.full[(j0 + i) % kStages], (uint32_t)((j0 + i) / kStages) & 1u); };
+          // S = Q K^T of tile j0 + i, which has landed
+          auto scores = [&](int i) {
+            const int j = j0 + i;
+            fence_async_smem();  // the copies, which the barrier has shown, before the asynchronous proxy reads them
+            fence_after();
+            const uint32_t kb = ring + (j % kStages) * 2 * W::kHalf;
 #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tmem + W::kO, tmem + W::kP + buf * (kKeys / 2) + 8 * k, operand(vb + k * 2048, kKeys * 128), id_o,
-                   !fresh || k > 0);
-          mma_commit(&S.empty[st]);
-          mma_commit(last ? &S.unit_done : &S.pv_done);
-          return true;
-        };
-        bool fresh = true, prev_fresh = true;  // of tile j, and of the last whose P V is not issued yet
-        int units = 0, summed = 0;             // units begun, tiles whose P V is issued
-        int j = 0;
-        for (long long t = t_first; t < t_end && ok; ++j) {
-          if (fresh) {
-            // the next unit's Q comes only after the last one's sums are out
-            if (j > 0 && (ok = sum_values(j - 1, prev_fresh, true))) summed = j;
-            ok = ok && tc_wait(&S.q_full, (uint32_t)units & 1u, S);
-            ++units;
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tmem + W::kS + (j & 1) * kKeys, operand(q_mem + (k >> 2) * 16384 + (k & 3) * 32, 16),
+                     operand(kb + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16), id_s, k > 0);
+            mma_commit(&S.s_full[j & 1]);
+          };
+          ok = tc_wait(&S.q_full, (uint32_t)units & 1u, S);
+          ++units;
+          int issued = 0;  // scores
+          for (int i = 0; i < n && ok; ++i) {
+            const int j = j0 + i, st = j % kStages, buf = j & 1;
+            if (issued == i) {
+              if (!(ok = tc_wait(&S.full[st], (uint32_t)(j / kStages) & 1u, S))) break;
+              scores(issued++);
+            }
+            if (issued == i + 1 && i + 1 < n && landed(i + 1)) scores(issued++);
+            if (!(ok = tc_wait(&S.p_full[buf], (uint32_t)(j >> 1) & 1u, S))) break;
+            // The tile's scores have been read: the next but one's go first, so
+            // that the softmax never waits for the product with V.
+            while (issued <= i + 2 && issued < n && landed(issued)) scores(issued++);
+            fence_after();
+            const uint32_t vb = ring + st * 2 * W::kHalf + W::kHalf;
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmem + W::kO, tmem + W::kP + buf * (kKeys / 2) + 8 * k, operand(vb + k * 2048, kKeys * 128), id_o,
+                     i > 0 || k > 0);
+            mma_commit(&S.empty[st]);
+            mma_commit(&S.pv_done[buf]);
           }
-          ok = ok && tc_wait(&S.full[j % kStages], (uint32_t)(j / kStages) & 1u, S);
-          if (!ok) break;
-          fence_async_smem();  // the copies, which the barrier has shown, before the asynchronous proxy reads them
-          fence_after();
-          const uint32_t kb = ring + (j % kStages) * 2 * W::kHalf;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + W::kS + (j & 1) * kKeys, operand(q_mem + (k >> 2) * 16384 + (k & 3) * 32, 16),
-                   operand(kb + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16), id_s, k > 0);
-          mma_commit(&S.s_full[j & 1]);
-          if (summed < j && (ok = sum_values(j - 1, prev_fresh, false))) summed = j;
-          if (!ok) break;
-          prev_fresh = fresh;
-          const int unit = u.ordinal;
-          t = u.step(p, t, t_end);
-          fresh = u.ordinal != unit;
+          j0 += n;
+          t = u.next(p, t_end);
         }
-        if (ok && j > 0) ok = sum_values(j - 1, prev_fresh, true);
         mma_commit(&S.drained);  // nothing is left in flight when the tensor memory is freed
         mbar_wait_landed(&S.drained, 0);
       }
@@ -646,8 +650,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
       float c = p.scale * kLog2e;
       [[maybe_unused]] bool flip = false, flat = false;  // 8-bit caches: a negative, a zero scale of K
       float* scratch = reinterpret_cast<float*>(mem);  // Q's place, between units
-      int j = 0, sums = 0;  // tiles, and those of them whose product pv_done announces, before this one
-      uint32_t syncs = 0, units = 0;
+      int j = 0;  // tiles before this one
+      uint32_t syncs = 0;
+      // P V of tile j is done. A parity names one of two phases: this thread has
+      // waited for tile j - 2's, and tile j + 2's waits for this thread.
+      auto product_done = [&](int j) { return tc_wait(&S.pv_done[j & 1], (uint32_t)(j >> 1) & 1u, S); };
       long long t = t_first;
       while (t < t_end && ok) {
         const long long u_end = u.end(t_end), u_begin = t;
@@ -729,11 +736,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? (m == kNegInf ? 0.0f : ex2(m - top)) : 1.0f;
             if (t > u_begin) {
-              // O holds sums: they are rescaled, after the product in flight,
-              // number sums - 1. A parity names one of two phases: the product
-              // before that is over (these scores came after it) and the one
-              // after it waits for this thread.
-              ok = tc_wait(&S.pv_done, (uint32_t)(sums - 1) & 1u, S);
+              // O holds sums: they are rescaled, after the last product
+              ok = product_done(j - 1);
               if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -752,6 +756,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
             if (move) m = top;
           }
           const float ref = m == kNegInf ? 0.0f : m;
+          if (j > 1) ok = product_done(j - 2);  // which read this buffer of weights
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
 #pragma unroll
           for (int c0 = 0; c0 < kCols; c0 += kChunk) {
             if (kCols > kChunk) read(c0, x);  // again: not all of a row's scores fit in registers
@@ -768,13 +777,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           wait_st();
           fence_before();
           mbar_arrive(&S.p_full[buf]);
-          if (t + 1 < u_end) ++sums;
         }
         if (!ok) break;
 
         // ---- the unit (or this CTA's run of it) ends
-        ok = tc_wait(&S.unit_done, (uint32_t)units & 1u, S);
-        ++units;
+        ok = product_done(j - 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
