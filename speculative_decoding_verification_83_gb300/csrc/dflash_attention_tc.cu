@@ -5,14 +5,13 @@
 //
 // Mathematics and work list as in dflash_attention.cu; here a unit has R = 32,
 // 64 or 128 query rows and a tile kKeys = 128 keys (64 for head_dim 256).
-// What bounds it is still the one pass over the cache: at R = 64 the products
-// take 512 of the about 2800 cycles in which a tile's 64 KB arrive, so the
-// rows that pad M to 128 cost nothing. They are put to use instead: the R rows
-// are laid out 128 / R times, and copy c takes the keys c kKeys R / 128 ... of
-// every tile as if the others were masked. Each thread of the softmax owns one
-// row of tensor memory and R / 128 of a tile's columns, so its work is the
-// same for every R, needs no exchange between lanes, and the copies' results
-// are joined once, at the end of the unit.
+// What bounds it is still the one pass over the cache: the products take about
+// 1000 of the about 2800 cycles in which a tile's 64 KB arrive, so the rows that
+// pad M to 128 cost nothing. They are put to use instead: the R rows are laid
+// out 128 / R times, and copy c takes the keys c kKeys R / 128 ... of every tile
+// as if the others were masked. Each thread of the softmax owns one row of
+// tensor memory and R / 128 of a tile's columns, which needs no exchange between
+// lanes; the copies' results are joined once, at the end of the unit.
 //
 // Roles (one CTA per SM, persistent over its run of tiles):
 //  * warps 5-8 fill a ring of stages with 16-byte asynchronous copies, placed
@@ -33,7 +32,7 @@
 //    ruling a row adds at most as much again in quadrature).
 // A unit's end costs a CTA about kEndTiles tiles (O out of tensor memory, Q in),
 // so the list of work counts it. 8-bit caches (head_dim 64 and 128) go through a
-// ring of raw tiles and are widened, exactly, into the operand tiles.
+// ring of raw tiles and are widened, exactly, into the operand tiles, by 8 warps.
 // Measured on one GB300, 64 query and 8 key/value heads of 128, 32 requests of up
 // to 16384 positions, blocks of 8 (64 rows a head), bf16: 218 us, 5.7 TB/s of keys
 // and values, 85% of a copy's rate, against 696 us by the warps' products, which
@@ -41,7 +40,8 @@
 // is left is the units' ends and uneven runs. At 128 rows (half the positions:
 // 152 us, 4.2 TB/s, 520 TFLOP/s) and head_dim 64 (148 us, 4.2 TB/s) the softmax's
 // 128 threads bound it; at head_dim 256 (266 us, 4.7 TB/s) two stages are few for
-// the latency of a load; e4m3 (303 us for half the bytes) is bound by the widening.
+// the latency of a load; e4m3 (294 us for half the bytes) has two operand stages, and
+// waits for the widening between a load and its products.
 // Every wait is bounded; a CTA that gives up raises DFLASH_STATUS_TIMEOUT,
 // lets its copies land and frees its tensor memory.
 #include <cuda_runtime.h>
@@ -56,8 +56,7 @@ namespace {
 
 constexpr int kTcCtas = 160;
 constexpr int kMmaWarp = 4;
-constexpr int kLoadWarp0 = 5, kLoadWarps = 4;
-constexpr int kTcThreads = 32 * (kLoadWarp0 + kLoadWarps);
+constexpr int kLoadWarp0 = 5, kMaxLoadWarps = 8;
 // A unit's end and the next one's beginning take a CTA about as long as this
 // many tiles: the list counts them, so that runs with many ends are shorter.
 constexpr int kEndTiles = 3;
@@ -66,6 +65,8 @@ constexpr int kFlags = 8;       // units whose "unsound" flag may be pending at 
 
 template <int D, bool kF8>
 struct TcShape {
+  static constexpr int kLoadWarps = kF8 ? 8 : 4;  // widening takes twice the warps
+  static constexpr int kThreads = 32 * (kLoadWarp0 + kLoadWarps);
   static constexpr int kKeys = D == 256 ? 64 : 128;
   static constexpr int kStages = D == 64 ? (kF8 ? 3 : 6) : D == 128 ? (kF8 ? 2 : 3) : 2;
   // 8-bit caches: tiles as they lie in the cache, in flight or waiting to be widened
@@ -88,11 +89,11 @@ struct TcShared {  // next to the dynamic part: 227 KB in all
   uint32_t tmem;
   volatile int failed;
   int unsound[kFlags];           // per unit (ordinal in the CTA): see load
-  uint32_t mask[6][4];           // per stage and load warp: its keys that exist
-  uint32_t raw_mask[4][6];       // 8-bit caches, per load warp and raw tile: the same,
-  int raw_unit[4][6];            // and its unit, with bit 0 set if some rows see less of it than others
+  uint32_t mask[6][kMaxLoadWarps];      // per stage and load warp: its keys that exist
+  uint32_t raw_mask[kMaxLoadWarps][6];  // 8-bit caches, per load warp and raw tile: the same,
+  int raw_unit[kMaxLoadWarps][6];       // and its unit, with bit 0 set if some rows see less of it than others
   int first_b;
-  long long first_pre, sums[kTcThreads / 32];
+  long long first_pre, sums[kLoadWarp0 + kMaxLoadWarps];
   Part parts[128];
 };
 
@@ -323,11 +324,12 @@ __device__ __forceinline__ bool drop_nan(uint32_t& w) {
 }
 
 template <class T, bool kF8, int D, int R>
-__global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnParams p, const AttnGeometry geo) {
+__global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_kernel(const AttnParams p, const AttnGeometry geo) {
   using W = TcShape<D, kF8>;
   constexpr int kKeys = W::kKeys, kStages = W::kStages;
   constexpr int kCopies = 128 / R, kCols = kKeys / kCopies;  // a thread's columns of a tile
   constexpr int kChunk = kCols < 64 ? kCols : 64;            // ... in registers at a time
+  constexpr int kLoadWarps = W::kLoadWarps, kTcThreads = W::kThreads;
   constexpr int kMine = kKeys / kLoadWarps;                  // a load warp's keys of a tile
   constexpr int kGroup = kChunk < kMine ? kChunk : kMine;
   constexpr uint32_t kMineMask = kMine == 32 ? 0xffffffffu : (1u << kMine) - 1u;
@@ -699,7 +701,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const AttnP
           fence_after();
           const uint32_t scores = my + W::kS + buf * kKeys + copy * kCols;
           const int key0 = (int)(t - u.start) * kKeys + copy * kCols;
-          const uint32_t all = S.mask[st][0] & S.mask[st][1] & S.mask[st][2] & S.mask[st][3];
+          uint32_t all = S.mask[st][0];
+#pragma unroll
+          for (int w = 1; w < kLoadWarps; ++w) all &= S.mask[st][w];
           const bool whole_tile = (int)(t - u.start + 1) * kKeys <= u.L - (p.causal ? u.n : 0) &&
                                   (all & kMineMask) == kMineMask;
           // scores of the columns from c0 on, unscaled, -inf where masked
@@ -936,7 +940,7 @@ int launch(const AttnParams& p, int sms, void* stream) {
   cfg.stream = (cudaStream_t)stream;
   const int grid = sms < kTcCtas ? sms : kTcCtas;
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kTcThreads);
+  cfg.blockDim = dim3(W::kThreads);
   cfg.dynamicSmemBytes = W::kSmem;
   e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, kF8, D, R>, p, geo);
   if (e != cudaSuccess) return (int)e;
