@@ -118,7 +118,7 @@ int check_rows(const void* p, int64_t token_stride, int64_t head_stride, const c
 
 int check_distill(const void* student, int64_t stride, int rows, int V, int dtype, const int32_t* ids,
                   const float* teacher, int K, float temperature) {
-  if (!student || !ids || !teacher) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
+  if (rows != 0 && (!student || !ids || !teacher)) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
   if (rows < 0 || rows > kMaxDistillRows)
     return fail(DFLASH_ERR_INVALID_ARG, "rows=%d outside [0, %d]", rows, kMaxDistillRows);
   if (V < 1) return fail(DFLASH_ERR_INVALID_ARG, "V=%d must be >= 1", V);
@@ -243,8 +243,8 @@ int dflash_distill_loss(const void* student, int64_t row_stride, int rows, int V
   NvtxRange nvtx_range("dflash_distill_loss");
   int rc = check_distill(student, row_stride, rows, V, dtype, teacher_ids, teacher_logits, K, temperature);
   if (rc) return rc;
-  if (!loss) return fail(DFLASH_ERR_INVALID_ARG, "null loss");
   if (rows == 0) return DFLASH_OK;
+  if (!loss) return fail(DFLASH_ERR_INVALID_ARG, "null loss");
   DistillParams p;
   memset(&p, 0, sizeof p);
   p.z = static_cast<const unsigned char*>(student);
@@ -271,11 +271,11 @@ int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V
   NvtxRange nvtx_range("dflash_distill_grad");
   int rc = check_distill(student, row_stride, rows, V, dtype, teacher_ids, teacher_logits, K, temperature);
   if (rc) return rc;
+  if (rows == 0) return DFLASH_OK;
   if (!lse || !grad) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
   if (upstream_stride < 0) return fail(DFLASH_ERR_INVALID_ARG, "upstream_stride must not be negative");
   if (!aligned(grad, dtype == DFLASH_BF16 ? 2 : 4) || grad_stride < V)
     return fail(DFLASH_ERR_INVALID_ARG, "the gradient's rows must be aligned to their type and at least V apart");
-  if (rows == 0) return DFLASH_OK;
   DistillParams p;
   memset(&p, 0, sizeof p);
   p.z = static_cast<const unsigned char*>(student);
@@ -302,10 +302,10 @@ int dflash_distill_loss_grad(const void* student, int64_t row_stride, int rows, 
   NvtxRange nvtx_range("dflash_distill_loss_grad");
   int rc = check_distill(student, row_stride, rows, V, dtype, teacher_ids, teacher_logits, K, temperature);
   if (rc) return rc;
+  if (rows == 0) return DFLASH_OK;
   if (!loss || !grad) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned(grad, dtype == DFLASH_BF16 ? 2 : 4) || grad_stride < V)
     return fail(DFLASH_ERR_INVALID_ARG, "the gradient's rows must be aligned to their type and at least V apart");
-  if (rows == 0) return DFLASH_OK;
   DistillParams p;
   memset(&p, 0, sizeof p);
   p.z = static_cast<const unsigned char*>(student);

@@ -71,7 +71,18 @@ def _rows(t, name, heads, dim, device, like=None):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if like is not None and (t.dtype != like.dtype or shape[0] != like.shape[0]):
         raise ValueError(f"{name} must match the tokens' dtype and count")
-    return t.data_ptr(), ts, hs
+    # an extent of one is never stepped over, whatever its stride says
+    return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the call's stream: torch's allocator orders
+    memory by the stream it is taken on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _vector(t, n, name, dtype, device):
@@ -117,7 +128,8 @@ class PagedCache:
             raise ValueError("k and v must be [pages, heads, page_size, head_dim] of one dtype and device")
         if not k.is_cuda:
             raise ValueError("the cache must be CUDA tensors")
-        if k.stride() != v.stride() or k.stride(3) != 1:
+        steps = [[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k, v)]
+        if steps[0] != steps[1] or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides, the last dimension contiguous")
         if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
             raise ValueError("page_table must be int32 [batch, max_pages] with contiguous rows")
@@ -135,7 +147,7 @@ class PagedCache:
         s = _CacheStruct(k.data_ptr(), v.data_ptr(), page_table.data_ptr(),
                          None if k_scale is None else k_scale.data_ptr(),
                          None if v_scale is None else v_scale.data_ptr(),
-                         k.stride(0), k.stride(1), k.stride(2), page_table.stride(0), self.pages, self.page_size,
+                         *steps[0], page_table.stride(0), self.pages, self.page_size,
                          self.heads, self.head_dim, codes[k.dtype], self.batch, self.max_pages)
         self.code = codes[k.dtype]
         self._struct = s
@@ -189,7 +201,7 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
         pq, qt, qh = _rows(q, "q", None, D, dev, k)
         hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n, hq, D), dtype=q.dtype, device=dev)
+            q_out = _empty((n, hq, D), q.dtype, dev, stream)
         po, ot, oh = _rows(q_out, "q_out", hq, D, dev, q)
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -228,7 +240,7 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     pq, qt, qh = _rows(q, "q", None, D, dev)
     n, hq, _ = q.shape
     if out is None:
-        out = torch.empty((n, hq, D), dtype=q.dtype, device=dev)
+        out = _empty((n, hq, D), q.dtype, dev, stream)
     po, ot, oh = _rows(out, "out", hq, D, dev, q)
     pl = None
     if lse is not None:
@@ -236,15 +248,11 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
         _on(dev, lse=lse)
         pl = _dev(lse, "lse", torch.float32)
     elif return_lse:
-        lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
+        lse = _empty((n, hq), torch.float32, dev, stream)
         pl = lse.data_ptr()
     lens, starts = _packed(cache, n, kv_lens, "kv_lens", q_start)
     if workspace is None:
-        if stream is None:
-            workspace = torch.empty((cache._ws_bytes,), dtype=torch.uint8, device=dev)
-        else:  # the allocator orders memory by the stream it is taken on
-            with torch.cuda.stream(stream):
-                workspace = torch.empty((cache._ws_bytes,), dtype=torch.uint8, device=dev)
+        workspace = _empty((cache._ws_bytes,), torch.uint8, dev, stream)
         ws, ws_bytes = workspace.data_ptr(), cache._ws_bytes
     else:
         _on(dev, workspace=workspace)
@@ -361,10 +369,10 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
     _no_grad_inputs(teacher_logits, row_weight)
     head, w = _distill_args(student, teacher_ids, teacher_logits, row_weight)
     N, V, dev = head[2], head[3], student.device
-    loss = torch.empty((N,), dtype=torch.float32, device=dev)
+    loss = _empty((N,), torch.float32, dev, stream)
     gs = V
     if grad is None:
-        grad = torch.empty((N, V), dtype=student.dtype, device=dev)
+        grad = _empty((N, V), student.dtype, dev, stream)
     else:
         _shape(grad, (N, V), "grad")
         _on(dev, grad=grad)

@@ -496,3 +496,18 @@ def test_refusals(dv):
         dv.PagedCache(caches[0], caches[1], table.long())
     with pytest.raises(ValueError):
         dv.PagedCache(caches[0], caches[1], table, k_scale=torch.ones(2, device=DEV))
+
+
+def test_extents_of_one_and_no_tokens(dv):
+    """Strides of extents of one do not matter; no tokens is no work."""
+    table, caches, q, _ = make(17, [1], [12], 1, 1, 64, 16, BF, BF, False)
+    ln = torch.tensor([12], dtype=torch.int32, device=DEV)
+    one = [c[int(table[0, 0])][None] for c in caches]
+    t0 = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    want = dv.paged_attention(dv.PagedCache(one[0], one[1], t0), q, ln)
+    odd = [c.as_strided(c.shape, (3, 5, c.stride(2), 1), c.storage_offset()) for c in one]
+    q1 = q.as_strided(q.shape, (7, 1, 1), q.storage_offset())
+    assert torch.equal(dv.paged_attention(dv.PagedCache(odd[0], one[1], t0), q1, ln), want)
+    none = dv.paged_attention(dv.PagedCache(one[0], one[1], t0), q[:0], ln)
+    assert none.shape == (0, 1, 64)
+    assert dv.kv_append(dv.PagedCache(one[0], one[1], t0), q[:0], q[:0], ln) is None

@@ -269,3 +269,29 @@ def test_refusals(dv):
     gr, = torch.autograd.grad(loss, a, create_graph=True)
     with pytest.raises(RuntimeError):
         gr.sum().backward()
+
+
+def test_no_rows(dv):
+    z = torch.zeros((0, 50), device=DEV, requires_grad=True)
+    ids, t = torch.zeros((0, 4), dtype=torch.int32, device=DEV), torch.zeros((0, 4), device=DEV)
+    loss = dv.distill_loss(z, ids, t)
+    loss.sum().backward()
+    assert loss.shape == (0,) and z.grad.shape == (0, 50)
+    loss, grad = dv.distill_loss_grad(z.detach(), ids, t)
+    assert loss.shape == (0,) and grad.shape == (0, 50)
+
+
+def test_outputs_belong_to_the_call_s_stream(dv):
+    """Tensors made by a call on another stream are not handed out again to the
+    current one while that stream still writes them."""
+    g, z, ids, t = make(16, 64, 50000, 8, BF)
+    want = dv.distill_loss_grad(z, ids, t)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        loss, grad = dv.distill_loss_grad(z, ids, t, stream=s)
+        del grad
+        torch.full_like(z, 3.0)  # would take the freed memory at once, were it this stream's
+    loss, grad = dv.distill_loss_grad(z, ids, t, stream=s)
+    s.synchronize()
+    assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])

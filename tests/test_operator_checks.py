@@ -125,6 +125,9 @@ def test_empty_calls_do_nothing(lib):
     assert attend(lib, tokens=0, q=None) == 0
     for name in ("loss", "grad", "loss_grad"):
         assert distill(lib, name, rows=0) == 0
+        assert distill(lib, name, rows=0, z=None, ids=None, teacher=None,
+                       tail={"loss": (None, None, None, None, None), "grad": (None, None, None, 1, None, 100, None),
+                             "loss_grad": (None, None, None, 100, None, None)}[name]) == 0
 
 
 def test_binding_refuses_before_the_library(lib):
