@@ -15,7 +15,7 @@ import ctypes
 import struct
 from fractions import Fraction
 
-from . import DFLASH_BF16, DFLASH_F32, ERR_INVALID_ARG, DFlashError, _check, _dev, _on, _shape, _torch, load
+from . import DFLASH_BF16, DFLASH_F32, ERR_INVALID_ARG, DFlashError, _check, _on, _shape, load
 
 DFLASH_F16, DFLASH_E4M3 = 2, 3
 STATUS_BAD_PAGE, STATUS_BAD_LENGTH = 16, 32
@@ -33,14 +33,40 @@ class _CacheStruct(ctypes.Structure):
                 ("max_pages", ctypes.c_int32)]
 
 
+_modules = []  # torch and the library, once they have been asked for: a call's checks run in microseconds
+
+
+def _torch():
+    if not _modules:
+        import torch
+
+        _modules.extend((torch, load()))
+    return _modules[0]
+
+
+def _library():
+    _torch()
+    return _modules[1]
+
+
+def _dev(t, name, dtype):
+    """Data pointer of a contiguous CUDA tensor of this type."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 _pack4, _pack8 = struct.Struct("4q").pack, struct.Struct("8q").pack  # strides, as the library reads them
 
 
 def _raw_stream(stream, device) -> int:
-    torch = _torch()
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _modules[0]._C._cuda_getCurrentRawStream(device.index)
 
 
 def _token_dtype(t, cache, what) -> int:
@@ -78,7 +104,7 @@ def _rows(t, name, heads, dim, device, like=None):
 def _empty(shape, dtype, device, stream):
     """A new tensor that belongs to the call's stream: torch's allocator orders
     memory by the stream it is taken on."""
-    torch = _torch()
+    torch = _modules[0]
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
@@ -152,7 +178,7 @@ class PagedCache:
         self.code = codes[k.dtype]
         self._struct = s
         self._ref = ctypes.byref(s)
-        self._ws_bytes = load().dflash_attention_workspace_bytes(self.batch, self.head_dim)
+        self._ws_bytes = _library().dflash_attention_workspace_bytes(self.batch, self.head_dim)
 
 
 def rope_phases(inv_freq, device=None):
@@ -212,14 +238,14 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
             raise ValueError("phases must be one-dimensional")
         rot = 2 * phases.shape[0]
         phases = _vector(phases, phases.shape[0], "phases", torch.int64, dev)
-    _check(load().dflash_kv_append(cache._ref, pk, pv, pq, po, dt, n, hq, _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens,
+    _check(_library().dflash_kv_append(cache._ref, pk, pv, pq, po, dt, n, hq, _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens,
                                    starts, phases, rot, 1 if interleaved else 0, _status_word(status, dev),
                                    _raw_stream(stream, dev)))
     return q_out
 
 
 def attention_workspace_bytes(batch: int, head_dim: int) -> int:
-    n = load().dflash_attention_workspace_bytes(batch, head_dim)
+    n = _library().dflash_attention_workspace_bytes(batch, head_dim)
     if n == 0:
         raise DFlashError(ERR_INVALID_ARG, f"no attention workspace for batch={batch}, head_dim={head_dim}")
     return n
@@ -257,7 +283,7 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     else:
         _on(dev, workspace=workspace)
         ws, ws_bytes = _dev(workspace, "workspace", torch.uint8), workspace.numel()
-    _check(load().dflash_paged_attention(
+    _check(_library().dflash_paged_attention(
         cache._ref, pq, po, pl, dt, n, hq, _pack4(qt, qh, ot, oh), lens, starts, D ** -0.5 if scale is None else scale,
         1 if causal else 0, ws, ws_bytes, _status_word(status, dev), _raw_stream(stream, dev)))
     return (out, lse) if return_lse else out
@@ -303,7 +329,7 @@ def _loss(student, ids, teacher, temperature, row_weight, status, keep):
     dev = student.device
     loss = torch.empty((head[2],), dtype=torch.float32, device=dev)
     stats = torch.empty((head[2], 2), dtype=torch.float32, device=dev) if keep else None
-    _check(load().dflash_distill_loss(*head, temperature, w, loss.data_ptr(), stats.data_ptr() if keep else None,
+    _check(_library().dflash_distill_loss(*head, temperature, w, loss.data_ptr(), stats.data_ptr() if keep else None,
                                       _status_word(status, dev), _raw_stream(None, dev)))
     return loss, stats
 
@@ -338,7 +364,7 @@ def _distill_function():
             head, w = _distill_args(student, ids, teacher, row_weight)
             dev = student.device
             grad = torch.empty(student.shape, dtype=student.dtype, device=dev)
-            _check(load().dflash_distill_grad(*head, ctx.temperature, w, stats.data_ptr(), upstream.data_ptr(),
+            _check(_library().dflash_distill_grad(*head, ctx.temperature, w, stats.data_ptr(), upstream.data_ptr(),
                                               upstream.stride(0), grad.data_ptr(), head[3], _raw_stream(None, dev)))
             return grad, None, None, None, None, None
 
@@ -381,7 +407,7 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
             raise ValueError("grad must have the student's dtype and contiguous rows")
         if N <= 1:
             gs = max(gs, V)
-    _check(load().dflash_distill_loss_grad(*head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
+    _check(_library().dflash_distill_loss_grad(*head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
                                            _status_word(status, dev), _raw_stream(stream, dev)))
     return loss, grad
 
