@@ -12,12 +12,12 @@
 // share its head, 2 n G flops per byte of a 16-bit cache, so the reads of the
 // cache bound it until n G nears 100 rows. Design:
 //  * Work is a list of units (request, head, 16 query rows), each a run of
-//    64-key tiles; the list's tiles are dealt out in equal contiguous runs,
+//    64-key tiles (128 where a row of the cache has 128 bytes or less); the list's tiles are dealt out in equal contiguous runs,
 //    one per CTA, whatever the requests' lengths. A unit that spans CTAs
 //    leaves unnormalised partial results (fp32 sum, maximum, sum of weights)
 //    in the workspace, which a second kernel joins in a fixed order: the
 //    results do not depend on timing.
-//  * In a CTA each of four warps takes its own 16 keys of every tile, with a
+//  * In a CTA each of four warps takes its own 16 (or 32) keys of every tile, with a
 //    ring of its own in shared memory filled by asynchronous 16-byte copies,
 //    which address any page size, stride and order; no barrier of the CTA is
 //    needed until the unit ends, where the warps' results are joined through
@@ -29,11 +29,16 @@
 //    per row by a power of two into f16's range (exact but for values
 //    below 2^-31 of the row's largest), undone in the scores.
 // Measured on one GB300 (bytes of keys and values over time): 64 requests of up
-// to 8192 positions, 64 query and 8 key/value heads of 128, bf16: 201 us, 6.1
-// TB/s, 91% of a copy's rate; three CTAs an SM with two ring stages each beat
-// two with three (206 us). Two requests of 200001 positions in e4m3: 163 us, 5.0
-// TB/s (two CTAs an SM: 176 us): there the widening and the products' issue
-// bound it, with 12 warps an SM to hide their latency.
+// to 8192 positions, 64 query and 8 key/value heads of 128, bf16: 199 us, 6.2
+// TB/s, 92% of a copy's rate; three CTAs an SM with two ring stages each beat
+// two with three (206 us). A step's overhead (page indexes, maxima, the rescaling
+// vote) is per warp, so rows of 128 bytes take 32 keys a step: head_dim 64 (twice
+// the positions) 204 against 274 us with 16, e4m3 at head_dim 128 (two requests of
+// 200001 positions) 144 us, 5.7 TB/s, against 164 us. There, and more so for e4m3
+// at head_dim 64 (193 us for 92 us of bytes), the warps' chain of widening,
+// products and softmax bounds it. Copies of K and V in groups of their own, each
+// reissued as its half of the stage is read, were slower (217 us): twice the waits
+// and shuffles.
 // Rounding: P is rounded to the operands' type (half a step of its own
 // relative to each weight); all sums, maxima and exponents are fp32.
 #include <cuda_runtime.h>
@@ -48,12 +53,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
-constexpr int kWarpKeys = 16;
-constexpr int kTile = kWarps * kWarpKeys;  // keys per tile
 constexpr int kRows = 16;                  // query rows per unit
 constexpr int kMaxCtas = 640;              // CTAs whose partial results the workspace holds
 
-__host__ __device__ inline AttnGeometry warp_geometry() { return {kRows, kTile, kMaxCtas}; }
+__host__ __device__ inline AttnGeometry warp_geometry(int tile) { return {kRows, tile, kMaxCtas}; }
 
 struct Unit {
   int b, h, rb, L, first, n, tiles;
@@ -61,6 +64,7 @@ struct Unit {
 };
 
 // The unit that tile t of the list belongs to (pre: tiles before each request).
+template <int kTile>
 __device__ __forceinline__ Unit locate(const AttnParams& p, const long long* pre, long long t) {
   Unit u;
   int lo = 0, hi = p.tk.B;  // largest b with pre[b] <= t
@@ -108,6 +112,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
 template <bool kF8, int D>
 struct Shape {
   static constexpr int kRowBytes = kF8 ? D : 2 * D;
+  static constexpr int kWarpKeys = kRowBytes <= 128 ? 32 : 16;  // keys of a warp's step: 4 to 16 KB of keys and values
+  static constexpr int kTile = kWarps * kWarpKeys;              // keys per tile
   static constexpr int kHalfStage = kWarpKeys * kRowBytes;  // K or V of one warp's step
   static constexpr int kStageBytes = 2 * kHalfStage * kWarps;
   // CTAs per SM, and a ring that fills the SM's shared memory with them
@@ -154,6 +160,8 @@ template <class T, bool kF8, int D>
 __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention_kernel(const AttnParams p) {
   using S = Shape<kF8, D>;
   using M = typename std::conditional<kF8, F16, T>::type;  // the products' type
+  constexpr int kWarpKeys = S::kWarpKeys, kTile = S::kTile;
+  constexpr uint32_t kAllKeys = kWarpKeys == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem;
   float* merge = reinterpret_cast<float*>(smem + (size_t)S::kStages * S::kStageBytes);
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
   if (tid == 0) {
     SplitUnit s = {0, 0, 0, 0, 0, 0, 0};
     if (t_begin < t_end) {
-      const Unit u = locate(p, pre, t_end - 1);
+      const Unit u = locate<kTile>(p, pre, t_end - 1);
       if (u.start >= t_begin && u.start + u.tiles > t_end) s = {u.start, u.tiles, u.h, u.rb, u.first, u.n, 0};
     }
     split_units(p)[blockIdx.x] = s;
@@ -208,13 +216,13 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
   const uint32_t my_ring = smem_addr(ring) + warp * 2 * S::kHalfStage;
   __shared__ uint32_t step_mask[kWarps][8];  // per stage: the keys that exist and have a page
 
-  Unit lu = locate(p, pre, t_begin);  // the unit being loaded
+  Unit lu = locate<kTile>(p, pre, t_begin);  // the unit being loaded
   long long lt = t_begin;
   int l_stage = 0;
   uint32_t next_off = 0;
   bool next_ok = false, bad_page = false;
-  auto look_up = [&]() {  // lane l < 16: the row of key l of step lt
-    const int key = (int)(lt - lu.start) * kTile + warp * kWarpKeys + (lane & 15);
+  auto look_up = [&]() {  // lane l: the row of key l of step lt
+    const int key = (int)(lt - lu.start) * kTile + warp * kWarpKeys + (lane & (kWarpKeys - 1));
     next_ok = key < lu.L;
     int page = 0, slot = 0, id = 0;
     if (next_ok) {
@@ -248,7 +256,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
       if (lane == 0) step_mask[warp][l_stage] = ok;
       ++lt;
       if (lt < t_end) {
-        if (lt >= lu.start + lu.tiles) lu = locate(p, pre, lt);
+        if (lt >= lu.start + lu.tiles) lu = locate<kTile>(p, pre, lt);
         look_up();
       }
     }
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
   int stage = 0;
   long long t = t_begin;
   while (t < t_end) {
-    const Unit u = locate(p, pre, t);
+    const Unit u = locate<kTile>(p, pre, t);
     const long long u_end = min(t_end, u.start + u.tiles);
     // ---- this thread's two query rows
     int row_tok[2], row_head[2], vis[2];
@@ -328,40 +336,44 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
       __syncwarp();
       load_step();  // into the stage whose step every lane has finished
       const uint32_t kb = my_ring + stage * S::kStageBytes, vb = kb + S::kHalfStage;
-      const uint32_t ok = step_mask[warp][stage] & 0xffffu;
+      const uint32_t ok = step_mask[warp][stage] & kAllKeys;
       // ---- S = Q K^T
-      float s[2][4];
+      float s[kWarpKeys / 8][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+      for (int i = 0; i < kWarpKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
       if (!kF8) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t k4[4];  // keys 0-7: inner 0-7, 8-15; keys 8-15: the same
-          ldsm4(k4, kb + piece_at<S::kRowBytes>((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
-          M::mma(s[0], q[ks], k4[0], k4[1]);
-          M::mma(s[1], q[ks], k4[2], k4[3]);
-        }
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int g = 0; g < kWarpKeys / 16; ++g) {
+            uint32_t k4[4];  // keys 0-7: inner 0-7, 8-15; keys 8-15: the same
+            ldsm4(k4, kb + piece_at<S::kRowBytes>(16 * g + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+            M::mma(s[2 * g], q[ks], k4[0], k4[1]);
+            M::mma(s[2 * g + 1], q[ks], k4[2], k4[3]);
+          }
       } else {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks += 2) {
-          uint32_t k4[4];  // keys 0-7: values 0-15, 16-31; keys 8-15: the same
-          ldsm4(k4, kb + piece_at<S::kRowBytes>((lane & 7) + ((lane >> 4) << 3), ks + ((lane >> 3) & 1)));
+        for (int ks = 0; ks < D / 16; ks += 2)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t lo, hi;
-            widen4(k4[j], lo, hi);
-            M::mma(s[0], q[ks + j], lo, hi);
-            widen4(k4[2 + j], lo, hi);
-            M::mma(s[1], q[ks + j], lo, hi);
+          for (int g = 0; g < kWarpKeys / 16; ++g) {
+            uint32_t k4[4];  // keys 0-7: values 0-15, 16-31; keys 8-15: the same
+            ldsm4(k4, kb + piece_at<S::kRowBytes>(16 * g + (lane & 7) + ((lane >> 4) << 3), ks + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t lo, hi;
+              widen4(k4[j], lo, hi);
+              M::mma(s[2 * g], q[ks + j], lo, hi);
+              widen4(k4[2 + j], lo, hi);
+              M::mma(s[2 * g + 1], q[ks + j], lo, hi);
+            }
           }
-        }
       }
       // ---- scale, mask, running maximum
       const int key0 = (int)(t - u.start) * kTile + warp * kWarpKeys;
-      const bool masked = ok != 0xffffu || key0 + kWarpKeys > u.L - (p.causal ? u.n : 0);
+      const bool masked = ok != kAllKeys || key0 + kWarpKeys > u.L - (p.causal ? u.n : 0);
       float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
+      for (int nb = 0; nb < kWarpKeys / 8; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x = s[nb][e] * unit_scale[e >> 1];
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
         m[e] = m_new;
         float sum = 0.0f;
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int nb = 0; nb < kWarpKeys / 8; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float w = ex2(s[nb][2 * e + j] - ref);
@@ -421,51 +433,57 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
       }
       if (unsound) {
         const unsigned char* tile = ring + (vb - smem_addr(ring));
+#pragma unroll
+        for (int nb = 0; nb < kWarpKeys / 8; ++nb)
 #pragma unroll 1
-        for (int kk = 0; kk < kWarpKeys; ++kk) {
-          float w[2];
+          for (int k8 = 0; k8 < 8; ++k8) {
+            const int kk = 8 * nb + k8;
+            float w[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float lo = (kk >> 3) ? s[1][2 * e] : s[0][2 * e], hi = (kk >> 3) ? s[1][2 * e + 1] : s[0][2 * e + 1];
-            w[e] = __shfl_sync(0xffffffffu, (kk & 1) ? hi : lo, (lane & ~3) + ((kk & 7) >> 1));
-            if (!((ok >> kk) & 1u) || key0 + kk >= vis[e]) w[e] = -1.0f;  // not seen
+            for (int e = 0; e < 2; ++e) {
+              w[e] = __shfl_sync(0xffffffffu, (k8 & 1) ? s[nb][2 * e + 1] : s[nb][2 * e], (lane & ~3) + (k8 >> 1));
+              if (!((ok >> kk) & 1u) || key0 + kk >= vis[e]) w[e] = -1.0f;  // not seen
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (w[e >> 1] >= 0.0f || w[e >> 1] != w[e >> 1]) {
+                  const int d = kF8 ? 16 * (i >> 1) + 2 * (2 * qc + (e & 1)) + (i & 1) : 8 * i + 2 * qc + (e & 1);
+                  o[i][e] += w[e >> 1] * value_at<T, kF8, S::kRowBytes>(tile, kk, d);
+                }
           }
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (w[e >> 1] >= 0.0f || w[e >> 1] != w[e >> 1]) {
-                const int d = kF8 ? 16 * (i >> 1) + 2 * (2 * qc + (e & 1)) + (i & 1) : 8 * i + 2 * qc + (e & 1);
-                o[i][e] += w[e >> 1] * value_at<T, kF8, S::kRowBytes>(tile, kk, d);
-              }
-        }
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
         continue;
       }
-      const uint32_t pa[4] = {M::pack(s[0][0], s[0][1]), M::pack(s[0][2], s[0][3]), M::pack(s[1][0], s[1][1]),
-                              M::pack(s[1][2], s[1][3])};
-      if (!kF8) {
 #pragma unroll
-        for (int ds = 0; ds < D / 16; ++ds) {
-          uint32_t v4[4];  // values 0-7: keys 0-7, 8-15; values 8-15: the same
-          ldsm4t(v4, vb + piece_at<S::kRowBytes>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * ds + (lane >> 4)));
-          M::mma(o[2 * ds], pa, v4[0], v4[1]);
-          M::mma(o[2 * ds + 1], pa, v4[2], v4[3]);
-        }
-      } else {
-        // a transposed load of byte pairs: even values in bytes 0 and 2, odd
-        // ones in 1 and 3, of two neighbouring keys
+      for (int g = 0; g < kWarpKeys / 16; ++g) {
+        const float(&a)[4] = s[2 * g], (&b)[4] = s[2 * g + 1];
+        const uint32_t pa[4] = {M::pack(a[0], a[1]), M::pack(a[2], a[3]), M::pack(b[0], b[1]), M::pack(b[2], b[3])};
+        const int vr = 16 * g + (lane & 7) + (((lane >> 3) & 1) << 3);
+        if (!kF8) {
 #pragma unroll
-        for (int ds = 0; ds < D / 16; ds += 2) {
-          uint32_t v4[4];  // values 0-15: keys 0-7, 8-15; values 16-31: the same
-          ldsm4t(v4, vb + piece_at<S::kRowBytes>((lane & 7) + (((lane >> 3) & 1) << 3), ds + (lane >> 4)));
+          for (int ds = 0; ds < D / 16; ++ds) {
+            uint32_t v4[4];  // values 0-7: keys 0-7, 8-15; values 8-15: the same
+            ldsm4t(v4, vb + piece_at<S::kRowBytes>(vr, 2 * ds + (lane >> 4)));
+            M::mma(o[2 * ds], pa, v4[0], v4[1]);
+            M::mma(o[2 * ds + 1], pa, v4[2], v4[3]);
+          }
+        } else {
+          // a transposed load of byte pairs: even values in bytes 0 and 2, odd
+          // ones in 1 and 3, of two neighbouring keys
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t even0, odd0, even1, odd1;
-            widen4(__byte_perm(v4[2 * j], 0, 0x3120), even0, odd0);
-            widen4(__byte_perm(v4[2 * j + 1], 0, 0x3120), even1, odd1);
-            M::mma(o[2 * (ds + j)], pa, even0, even1);
-            M::mma(o[2 * (ds + j) + 1], pa, odd0, odd1);
+          for (int ds = 0; ds < D / 16; ds += 2) {
+            uint32_t v4[4];  // values 0-15: keys 0-7, 8-15; values 16-31: the same
+            ldsm4t(v4, vb + piece_at<S::kRowBytes>(vr, ds + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t even0, odd0, even1, odd1;
+              widen4(__byte_perm(v4[2 * j], 0, 0x3120), even0, odd0);
+              widen4(__byte_perm(v4[2 * j + 1], 0, 0x3120), even1, odd1);
+              M::mma(o[2 * (ds + j)], pa, even0, even1);
+              M::mma(o[2 * (ds + j) + 1], pa, odd0, odd1);
+            }
           }
         }
       }
@@ -504,14 +522,14 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     const bool jok = jrow < u.n * p.G;
     const long long jtok = u.first + ji, jhead = u.h * p.G + (jrow - ji * p.G);
     const long long slot = 2LL * blockIdx.x + (seg_begin == t_begin ? 0 : 1);
-    float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry().o()) + (slot * kRows + jr) * D;
+    float* part_o = reinterpret_cast<float*>(p.ws + warp_geometry(kTile).o()) + (slot * kRows + jr) * D;
     float factor = reciprocal_or_zero(sum);
     if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
     if ((tid & 7) == 0 && jok) {
       if (whole) {
         if (p.lse) p.lse[jtok * ((long long)p.G * p.c.kv_heads) + jhead] = (top + log2f(sum)) * kLn2;
       } else {
-        reinterpret_cast<Part*>(p.ws + warp_geometry().ml())[slot * kRows + jr] = {top, sum};
+        reinterpret_cast<Part*>(p.ws + warp_geometry(kTile).ml())[slot * kRows + jr] = {top, sum};
       }
     }
 #pragma unroll
@@ -630,7 +648,7 @@ int launch(const AttnParams& p, int sms, void* stream) {
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, attention_kernel<T, kF8, D>, p);
   if (e != cudaSuccess) return (int)e;
-  return launch_join(p, warp_geometry(), grid, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, kF8, D, stream);
+  return launch_join(p, warp_geometry(S::kTile), grid, std::is_same<T, Bf16>::value ? DFLASH_BF16 : DFLASH_F16, kF8, D, stream);
 }
 
 template <class T, bool kF8>
@@ -671,7 +689,7 @@ int launch_join(const AttnParams& p, const AttnGeometry& g, int grid, int dtype,
 }
 
 size_t attention_workspace(int head_dim) {
-  const size_t a = warp_geometry().bytes(head_dim), b = tc_geometry(128, head_dim).bytes(head_dim);
+  const size_t a = warp_geometry(0).bytes(head_dim), b = tc_geometry(128, head_dim).bytes(head_dim);
   return a > b ? a : b;
 }
 
