@@ -295,3 +295,30 @@ def test_outputs_belong_to_the_call_s_stream(dv):
     loss, grad = dv.distill_loss_grad(z, ids, t, stream=s)
     s.synchronize()
     assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
+
+
+def test_backward_in_a_graph(dv):
+    """Loss and backward captured together: replays read the tensors' contents."""
+    g, z, ids, t = make(17, 6, 3000, 8, BF)
+    a = z.clone().requires_grad_(True)
+    up = torch.rand(6, generator=g, device=DEV)
+
+    def both():
+        loss = dv.distill_loss(a, ids, t)
+        return loss.detach(), torch.autograd.grad(loss, a, up)[0]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both()
+    torch.cuda.current_stream().wait_stream(s)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        loss, grad = both()
+    with torch.no_grad():
+        a.copy_(torch.randn(a.shape, generator=g, device=DEV).to(BF))
+    up.mul_(-2.0)
+    gr.replay()
+    torch.cuda.synchronize()
+    want = both()
+    assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
