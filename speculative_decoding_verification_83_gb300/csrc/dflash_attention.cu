@@ -693,12 +693,18 @@ size_t attention_workspace(int head_dim) {
   return a > b ? a : b;
 }
 
-// Query rows that share a key/value head, per request on average: up to 16 go
-// to the warps' own products, more to the tensor-memory kernel.
+// By the query rows that share a key/value head, per request on average. Up to
+// 16 rows go to the warps' own products, which read the cache once for them
+// (64 single tokens, 8 rows: 198 us; the tensor-memory kernel 207 us). From 17 on
+// they would read it again for every 16 rows: at 32 requests of up to 16384
+// positions and 8 key/value heads of 128, 32 rows take 422 us against 197 us, 64
+// rows 704 against 218 us. 8-bit caches have half the bytes to read again and the
+// widening to pay: 32 rows 204 against 252 us, 64 rows 386 against 296 us, so
+// they change over after 32; at head_dim 256 they stay with the warps.
 int launch_attention(const AttnParams& p, int dtype, int cache_dtype, int head_dim, int sms, void* stream) {
   const bool f8 = cache_dtype == DFLASH_E4M3;
   const long long rows = (((long long)p.tk.tokens + p.tk.B - 1) / p.tk.B) * p.G;
-  if (rows > 16 && !(f8 && head_dim == 256))
+  if (f8 ? rows > 32 && head_dim != 256 : rows > 16)
     return launch_attention_tc(p, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, dtype, f8, head_dim, sms, stream);
   if (dtype == DFLASH_BF16)
     return f8 ? pick_dim<Bf16, true>(p, head_dim, sms, stream) : pick_dim<Bf16, false>(p, head_dim, sms, stream);

@@ -1,6 +1,6 @@
 // dflash_attention_tc.cu -- attention over the paged cache for blocks whose
 // query rows (new tokens x heads that share a key/value head) number more than
-// 16: the products run on the 5th-generation tensor cores, with scores,
+// 16 (8-bit caches: 32): the products run on the 5th-generation tensor cores, with scores,
 // weights and sums in tensor memory.
 //
 // Mathematics and work list as in dflash_attention.cu; here a unit has R = 32,

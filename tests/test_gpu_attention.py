@@ -75,7 +75,7 @@ def check(dv, table, caches, q, scales, counts, lens, page, causal, scale=None, 
     # the weights are rounded to the products' type: the tokens', or f16 for the
     # 8-bit caches of few rows (or head_dim 256)
     rows_each = -(-q.shape[0] // len(counts)) * (q.shape[1] // caches[0].shape[1])
-    up = U[torch.float16] if caches[0].dtype == F8 and (rows_each <= 16 or D == 256) else U[q.dtype]
+    up = U[torch.float16] if caches[0].dtype == F8 and (rows_each <= 32 or D == 256) else U[q.dtype]
     for b, s in enumerate(starts_of(counts)[:-1]):
         n, L = counts[b], lens[b]
         if n == 0:
