@@ -234,6 +234,11 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcShared
     }
   }
 }
+// The same for a warp: its lanes go on together or give up together, since what
+// follows are shuffles and votes of the whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, TcShared& S) {
+  return __all_sync(0xffffffffu, tc_wait(bar, parity, S));
+}
 // A barrier of the 128 softmax threads whose wait is bounded like the others
 // (a hardware barrier would hang if one warp had given up).
 __device__ __forceinline__ bool softmax_sync(uint32_t& phase, TcShared& S) {
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
       if constexpr (!kF8) {
         while (now.t < t_end) {
           const uint32_t next_off = place(now), mask = __ballot_sync(0xffffffffu, now.there);
-          if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
+          if (round > 0 && !(ok = warp_wait(&S.empty[st], (round - 1) & 1u, S))) break;
           __syncwarp();
           const uint32_t kb = ring + st * 2 * W::kHalf;
 #pragma unroll
@@ -554,7 +559,7 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
           __syncwarp();
           const uint32_t mask = S.raw_mask[lw][from];
           const int unit = S.raw_unit[lw][from];
-          if (round > 0 && !(ok = tc_wait(&S.empty[st], (round - 1) & 1u, S))) break;
+          if (round > 0 && !(ok = warp_wait(&S.empty[st], (round - 1) & 1u, S))) break;
           unsigned char* kb = mem + W::kQBytes + st * 2 * W::kHalf;
           bool found = false;
 #pragma unroll 4
