@@ -852,8 +852,9 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
               __syncwarp();
               tmem_load<32>(my + W::kO + r0 + d, y);
               if (unsound && writes) {
-                // the values replaced by 0 that this row does see
-                for (int k = max(0, u.L - u.n); k < vis; ++k) {
+                // the values replaced by 0 that this row does see: whole tiles
+                // were gone through, from the one that holds position L - n
+                for (int k = max(0, u.L - u.n) / kKeys * kKeys; k < vis; ++k) {
                   if (k < (int)(u_begin - u.start) * kKeys || k >= (int)(u_end - u.start) * kKeys) continue;
                   int page, sl;
                   split_position(p.c, k, page, sl);

@@ -1,0 +1,75 @@
+"""dflash_paged_attention where values of the cache are not finite, and where a
+row's weights span many powers of 2: what a row sees decides its result, not
+which kernel, tile, copy or SM took the key."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, HF, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def dv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_83_gb300 as m
+
+    m.build()
+    m.load()
+    return m
+
+
+class Case:
+    """One request of L positions and n new tokens, 2 key/value heads."""
+
+    def __init__(self, seed, L, n, G, D, dtype, cdt, page=16, H=2):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        width = -(-L // page)
+        self.L, self.n, self.G, self.D, self.H, self.page, self.dtype = L, n, G, D, H, page, dtype
+        self.table = torch.randperm(width, generator=g, device=DEV).view(1, width).to(torch.int32)
+        self.k, self.v = (torch.randn((width, H, page, D), generator=g, device=DEV).to(cdt) for _ in range(2))
+        self.q = torch.randn((n, H * G, D), generator=g, device=DEV).to(dtype)
+        self.lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+
+    def put(self, cache, pos, value, head=slice(None), col=slice(None)):
+        t = cache.view(torch.uint8) if cache.dtype == F8 else cache
+        if cache.dtype == F8:
+            value = torch.tensor(value, device=DEV).to(F8).view(torch.uint8)
+        t[self.table[0, pos // self.page].long(), head, pos % self.page, col] = value
+
+    def attend(self, dv, scales=(None, None), **kw):
+        out, lse = dv.paged_attention(dv.PagedCache(self.k, self.v, self.table, *scales), self.q, self.lens,
+                                      return_lse=True, **kw)
+        return out.view(self.n, self.H, self.G, self.D), lse.view(self.n, self.H, self.G)
+
+
+# n, G: 8 rows a head (the warps' products), then units of 32, 64 and 128 rows, and two units
+ROWS = [(4, 2), (4, 6), (4, 12), (4, 24), (4, 40)]
+
+
+TYPES = [(64, BF, BF), (128, BF, BF), (128, HF, HF), (256, BF, BF)]
+TYPES8 = [(64, BF, F8), (128, HF, F8), (256, BF, F8)]
+BAD = [(t, bad, r) for t in TYPES for bad in (NAN, INF, -INF) for r in ROWS[1:]] \
+    + [(t, NAN, r) for t in TYPES8[:2] for r in ROWS[2:]]
+
+
+@pytest.mark.parametrize("types,bad,rows", BAD)
+def test_values_in_front_of_the_block_count(dv, types, bad, rows):
+    """The block's tile also holds keys in front of the block, which every row
+    sees: a value there that is not finite reaches every row."""
+    (D, dtype, cdt), (n, G), L, col = types, rows, 200, 5
+    tile = 64 if D == 256 else 128
+    block = L - n
+    for pos in (block - 1, block // tile * tile):
+        c = Case(D + G, L, n, G, D, dtype, cdt)
+        want, wl = c.attend(dv)
+        c.put(c.v, pos, bad, head=1, col=col)
+        got, gl = c.attend(dv)
+        assert torch.equal(gl, wl)
+        assert not bool(got[:, 1, :, col].float().isfinite().any()), (pos, got[:, 1, :, col])
+        got[:, 1, :, col] = want[:, 1, :, col]
+        assert torch.equal(got, want)
