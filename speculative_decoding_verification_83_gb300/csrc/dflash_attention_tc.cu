@@ -851,9 +851,26 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
               uint32_t y[32];
               __syncwarp();
               tmem_load<32>(my + W::kO + r0 + d, y);
+              float x[32];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float4 o = make_float4(__uint_as_float(y[4 * i]) * factor, __uint_as_float(y[4 * i + 1]) * factor,
+                                       __uint_as_float(y[4 * i + 2]) * factor, __uint_as_float(y[4 * i + 3]) * factor);
+#pragma unroll
+                for (int k = 1; k < kCopies; ++k) {
+                  const float4 e = reinterpret_cast<const float4*>(scratch)[(size_t)((k - 1) * R + row) * (kRound / 4) +
+                                                                            d / 4 + (i ^ (lane & 7))];
+                  o = make_float4(o.x + e.x, o.y + e.y, o.z + e.z, o.w + e.w);
+                }
+                x[4 * i] = o.x;
+                x[4 * i + 1] = o.y;
+                x[4 * i + 2] = o.z;
+                x[4 * i + 3] = o.w;
+              }
               if (unsound && writes) {
-                // the values replaced by 0 that this row does see: whole tiles
-                // were gone through, from the one that holds position L - n
+                // The values replaced by 0 that this row does see, added to the
+                // scaled sums (a factor does not change them): whole tiles were
+                // gone through, from the one that holds position L - n.
                 for (int k = max(0, u.L - u.n) / kKeys * kKeys; k < vis; ++k) {
                   if (k < (int)(u_begin - u.start) * kKeys || k >= (int)(u_end - u.start) * kKeys) continue;
                   int page, sl;
@@ -865,27 +882,12 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
 #pragma unroll
                   for (int i = 0; i < 32; ++i) {
                     if constexpr (kF8) {
-                      if ((v[i] & 0x7fu) == 0x7fu) y[i] = 0x7fffffffu;
+                      if ((v[i] & 0x7fu) == 0x7fu) x[i] = NAN;
                     } else {
                       const uint16_t b = reinterpret_cast<const uint16_t*>(v)[i];
-                      if (word_not_finite<T>(b)) y[i] = __float_as_uint(__uint_as_float(y[i]) + T::unpack(b).x);
+                      if (word_not_finite<T>(b)) x[i] += T::unpack(b).x;
                     }
                   }
-                }
-              }
-              float4 x[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                // (an infinite value added above is kept by a copy that saw nothing else)
-                const bool raw = unsound && factor == 0.0f;
-                x[i] = make_float4(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1]),
-                                   __uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3]));
-                if (!raw) x[i] = make_float4(x[i].x * factor, x[i].y * factor, x[i].z * factor, x[i].w * factor);
-#pragma unroll
-                for (int k = 1; k < kCopies; ++k) {
-                  const float4 o = reinterpret_cast<const float4*>(scratch)[(size_t)((k - 1) * R + row) * (kRound / 4) +
-                                                                            d / 4 + (i ^ (lane & 7))];
-                  x[i] = make_float4(x[i].x + o.x, x[i].y + o.y, x[i].z + o.z, x[i].w + o.w);
                 }
               }
               if (writes) {
@@ -893,12 +895,12 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
                   uint4* dst = reinterpret_cast<uint4*>(out_row + 2 * (r0 + d));
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
-                    dst[i] = make_uint4(T::pack(x[2 * i].x, x[2 * i].y), T::pack(x[2 * i].z, x[2 * i].w),
-                                        T::pack(x[2 * i + 1].x, x[2 * i + 1].y), T::pack(x[2 * i + 1].z, x[2 * i + 1].w));
+                    dst[i] = make_uint4(T::pack(x[8 * i], x[8 * i + 1]), T::pack(x[8 * i + 2], x[8 * i + 3]),
+                                        T::pack(x[8 * i + 4], x[8 * i + 5]), T::pack(x[8 * i + 6], x[8 * i + 7]));
                 } else {
                   float4* dst = reinterpret_cast<float4*>(part_row + r0 + d);
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) dst[i] = x[i];
+                  for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                 }
               }
             }

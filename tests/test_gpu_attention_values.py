@@ -73,3 +73,39 @@ def test_values_in_front_of_the_block_count(dv, types, bad, rows):
         assert not bool(got[:, 1, :, col].float().isfinite().any()), (pos, got[:, 1, :, col])
         got[:, 1, :, col] = want[:, 1, :, col]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", ROWS[1:])
+@pytest.mark.parametrize("below", [40.0, 200.0])
+def test_bad_values_of_other_rows_leave_weak_keys_alone(dv, D, n, G, below):
+    """A tile's first half weighs e^-40 or (in 32 bits) nothing against the rest,
+    and the block's last token's value is NaN: the tokens before it do not
+    notice."""
+    L = 64 if D == 256 else 128
+    c = Case(G, L, n, G, D, BF, BF)
+    c.q.zero_()
+    c.q[..., 0] = D ** 0.5
+    for pos in range(L // 2):
+        c.put(c.k, pos, -below, col=0)
+    want, wl = c.attend(dv)
+    c.put(c.v, L - 1, NAN, col=slice(0, None, 3))
+    got, gl = c.attend(dv)
+    assert torch.equal(gl, wl) and torch.equal(got[:-1], want[:-1])
+    assert bool(got[-1, :, :, ::3].isnan().all())
+    got[-1, :, :, ::3] = want[-1, :, :, ::3]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G", ROWS[2:])
+def test_bad_values_under_a_scale_of_zero(dv, D, n, G):
+    """A head's values scaled by 0: zero for the rows that see finite values only."""
+    c = Case(G, 128, n, G, D, BF, F8)
+    scales = torch.ones(2, device=DEV), torch.tensor([0.0, 0.5], device=DEV)
+    want, _ = c.attend(dv, scales)
+    assert bool((want[:, 0] == 0).all())
+    c.put(c.v, 127, NAN, col=slice(0, None, 3))
+    got, _ = c.attend(dv, scales)
+    assert torch.equal(got[:-1], want[:-1])
+    assert bool(got[-1, :, :, ::3].isnan().all())
