@@ -132,30 +132,6 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
   return kRowBytes >= 128 ? r * kRowBytes + ((c ^ (r & 7)) << 4) : r * kRowBytes + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Whether a 32-bit word of cache values holds one that is not finite.
-template <class T, bool kF8>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-  if (kF8) {  // e4m3: all ones below the sign
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (((w >> (8 * i)) & 0x7fu) == 0x7fu) return true;
-    return false;
-  }
-  constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7c00u : 0x7f80u;
-  return (w & e) == e || ((w >> 16) & e) == e;
-}
-// Value d of a cache row in shared memory.
-template <class T, bool kF8, int kRowBytes>
-__device__ __forceinline__ float value_at(const unsigned char* tile, int r, int d) {
-  if (kF8) {
-    const unsigned char b = tile[piece_at<kRowBytes>(r, d >> 4) + (d & 15)];
-    uint32_t lo, hi;
-    widen4(b, lo, hi);
-    return F16::unpack(lo).x;
-  }
-  return T::unpack(*reinterpret_cast<const uint16_t*>(tile + piece_at<kRowBytes>(r, d >> 3) + 2 * (d & 7))).x;
-}
-
 template <class T, bool kF8, int D>
 __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention_kernel(const AttnParams p) {
   using S = Shape<kF8, D>;
@@ -168,6 +144,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
   float* merge_ml = merge + S::kMerge / sizeof(float);
   long long* pre = reinterpret_cast<long long*>(merge_ml + 2 * kWarps * kRows);
   __shared__ long long warp_sum[kWarps];
+  __shared__ int replaced;  // values of the unit that are not finite have been replaced
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_sync();
 
@@ -194,7 +171,10 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
     long long before = incl - mine;
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     for (int b = lo; b < hi; ++b) pre[b] += before;
-    if (tid == 0) pre[p.tk.B] = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+    if (tid == 0) {
+      pre[p.tk.B] = warp_sum[0] + warp_sum[1] + warp_sum[2] + warp_sum[3];
+      replaced = 0;
+    }
     __syncthreads();
   }
   if (bad && blockIdx.x == 0) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
@@ -417,44 +397,30 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
         }
       }
       // ---- O += P V
-      // Under a causal mask a step may hold values that only some rows see.
-      // A product with weight 0 would turn one that is not finite into NaN,
-      // so such a step (never met in sound data) is summed key by key.
-      bool unsound = false;
+      // Under a causal mask a step may hold values that only some rows see:
+      // those that are not finite are replaced by 0.
       if (masked && p.causal && u.n > 1) {
+        uint4* own = reinterpret_cast<uint4*>(ring + (vb - smem_addr(ring))) + lane;
+        bool found = false;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(
-              ring + (vb - smem_addr(ring)) + ((size_t)(i * 32 + lane) << 4));
-          unsound |= not_finite<T, kF8>(w.x) || not_finite<T, kF8>(w.y) || not_finite<T, kF8>(w.z) ||
-                     not_finite<T, kF8>(w.w);
+          uint4 w = own[i * 32];
+          found |= drop_not_finite<T, kF8>(w.x) | drop_not_finite<T, kF8>(w.y) | drop_not_finite<T, kF8>(w.z) |
+                   drop_not_finite<T, kF8>(w.w);
         }
-        unsound = __any_sync(0xffffffffu, unsound);
-      }
-      if (unsound) {
-        const unsigned char* tile = ring + (vb - smem_addr(ring));
-#pragma unroll
-        for (int nb = 0; nb < kWarpKeys / 8; ++nb)
+        if (__builtin_expect(__any_sync(0xffffffffu, found), 0)) {
 #pragma unroll 1
-          for (int k8 = 0; k8 < 8; ++k8) {
-            const int kk = 8 * nb + k8;
-            float w[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              w[e] = __shfl_sync(0xffffffffu, (k8 & 1) ? s[nb][2 * e + 1] : s[nb][2 * e], (lane & ~3) + (k8 >> 1));
-              if (!((ok >> kk) & 1u) || key0 + kk >= vis[e]) w[e] = -1.0f;  // not seen
-            }
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (w[e >> 1] >= 0.0f || w[e >> 1] != w[e >> 1]) {
-                  const int d = kF8 ? 16 * (i >> 1) + 2 * (2 * qc + (e & 1)) + (i & 1) : 8 * i + 2 * qc + (e & 1);
-                  o[i][e] += w[e >> 1] * value_at<T, kF8, S::kRowBytes>(tile, kk, d);
-                }
+          for (int i = 0; i < kLoads; ++i) {
+            uint4 w = own[i * 32];
+            drop_not_finite<T, kF8>(w.x);
+            drop_not_finite<T, kF8>(w.y);
+            drop_not_finite<T, kF8>(w.z);
+            drop_not_finite<T, kF8>(w.w);
+            own[i * 32] = w;
           }
-        stage = stage + 1 == S::kStages ? 0 : stage + 1;
-        continue;
+          if (lane == 0) replaced = 1;
+          __syncwarp();
+        }
       }
 #pragma unroll
       for (int g = 0; g < kWarpKeys / 16; ++g) {
@@ -532,6 +498,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
         reinterpret_cast<Part*>(p.ws + warp_geometry(kTile).ml())[slot * kRows + jr] = {top, sum};
       }
     }
+    bool odd = replaced;  // or a result is not finite
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += S::kCols) {
       __syncthreads();
@@ -549,6 +516,8 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
       for (int w = 0; w < kWarps; ++w)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] += merge[(w * kRows + jr) * (S::kCols + 1) + jc + j];
+      // (a row whose sum of weights is not finite has NaN everywhere)
+      odd |= jok && sum < INFINITY && (x[0] * 0.0f + x[1] * 0.0f) + (x[2] * 0.0f + x[3] * 0.0f) != 0.0f;
       if (jok) {
         if (whole) {
           uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + 2 * (jtok * p.o_ts + jhead * p.o_hs + c0 + jc));
@@ -559,7 +528,28 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
         }
       }
     }
-    __syncthreads();  // merge_ml is written again by the next unit
+    if (__builtin_expect(__syncthreads_or(odd), 0)) {  // (merge and merge_ml are written again)
+      // results that values which are not finite decide
+      int* first = reinterpret_cast<int*>(merge);
+      for (int i = tid; i < 3 * D; i += kAttnThreads) first[i] = kNever;
+      replaced = 0;
+      __syncthreads();
+      find_not_finite<T, kF8, D>(p, u.b, u.h, (int)(seg_begin - u.start) * kTile,
+                                 (int)min((long long)u.L, (u_end - u.start) * kTile), first, tid, kAttnThreads);
+      __syncthreads();
+      if (jok && sum < INFINITY) {
+        const int jvis = p.causal ? min(u.L, max(0, u.L - u.n + ji + 1)) : u.L;
+        for (int d = tid & 7; d < D; d += 8) {
+          const float v = not_finite_value<D>(first, d, jvis);
+          if (v == 0.0f) continue;
+          if (whole)
+            reinterpret_cast<uint16_t*>(p.out + 2 * (jtok * p.o_ts + jhead * p.o_hs))[d] = (uint16_t)T::pack(v, 0.0f);
+          else
+            part_o[d] = v;
+        }
+      }
+      __syncthreads();
+    }
   }
   if (bad_page) raise_status(p.status, DFLASH_STATUS_BAD_PAGE);
   cp_wait<0>();
@@ -571,6 +561,16 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
 // order. A chain of three loads bounds it, so every row has its warp and a warp
 // 16 segments in flight.
 constexpr int kJoinWarps = 16;
+// A column of a unit whose segments' sum x is not finite: the sum of the partial
+// results that are not, whatever their segments weigh (x where all are finite).
+__device__ __forceinline__ float not_finite_sum(const float* first, const float* rest, long long step, int n, float x) {
+  float s = fabsf(*first) < INFINITY ? 0.0f : *first;
+  for (int c = 0; c < n; ++c) {
+    const float y = rest[c * step];
+    if (!(fabsf(y) < INFINITY)) s += y;
+  }
+  return s != 0.0f ? s : x;
+}
 template <class T, bool kF8, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams p, const AttnGeometry geo) {
   constexpr int kPer = D / 32;  // columns of a lane
@@ -609,6 +609,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttnParams 
       for (int e = 0; e < kPer; ++e) x[e] = fmaf(y[e], wj, x[e]);
     }
   }
+  // a partial result that is not finite counts whatever its segment weighs
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if (__builtin_expect(!(fabsf(x[e]) < INFINITY), 0))
+      x[e] = not_finite_sum(os + slot_row(c0) * D + lane * kPer + e, os + slot_row(c0 + 1) * D + lane * kPer + e, 2LL * geo.rows * D, c1 - c0, x[e]);
   float factor = reciprocal_or_zero(sum);
   if (kF8 && p.c.v_scale) factor *= p.c.v_scale[u.h];
   const int g = u.rb * geo.rows + jr, ti = g / p.G;

@@ -88,7 +88,8 @@ struct TcShared {  // next to the dynamic part: 227 KB in all
   uint64_t q_full, drained, together;
   uint32_t tmem;
   volatile int failed;
-  int unsound[kFlags];           // per unit (ordinal in the CTA): see load
+  int unsound[kFlags];           // per unit (ordinal in the CTA): values were replaced, see load
+  int odd;                       // a result of the unit is not finite
   uint32_t mask[6][kMaxLoadWarps];      // per stage and load warp: its keys that exist
   uint32_t raw_mask[kMaxLoadWarps][6];  // 8-bit caches, per load warp and raw tile: the same,
   int raw_unit[kMaxLoadWarps][6];       // and its unit, with bit 0 set if some rows see less of it than others
@@ -295,12 +296,6 @@ struct Cursor {
   }
 };
 
-template <class T>
-__device__ __forceinline__ bool word_not_finite(uint32_t w) {
-  constexpr uint32_t e = std::is_same<T, F16>::value ? 0x7c00u : 0x7f80u;
-  return (w & e) == e || ((w >> 16) & e) == e;
-}
-
 // 8 e4m3 values (two words) as 8 values of T, exactly
 template <class T>
 __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
@@ -316,18 +311,6 @@ __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// e4m3 NaNs (all ones below the sign) of a word become 0
-__device__ __forceinline__ bool drop_nan(uint32_t& w) {
-  bool found = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (((w >> (8 * i)) & 0x7fu) == 0x7fu) {
-      w &= ~(0xffu << (8 * i));
-      found = true;
-    }
-  return found;
-}
-
 template <class T, bool kF8, int D, int R>
 __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_kernel(const AttnParams p, const AttnGeometry geo) {
   using W = TcShape<D, kF8>;
@@ -358,6 +341,7 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
     mbar_init(&S.drained, 1);
     mbar_init(&S.together, 128);
     for (int i = 0; i < kFlags; ++i) S.unsound[i] = 0;
+    S.odd = 0;
     S.failed = 0;
     fence_barrier_init();
   }
@@ -459,10 +443,9 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
         now = next;
         if (next.t < t_end) next = ask(u.step(p, next.t, t_end));
       };
-      // Under a causal mask a tile may hold values that only some rows see, and
-      // a weight of 0 times one that is not finite would be NaN. Such a value
-      // (never met in sound data) is replaced by 0 here and added at the unit's
-      // end.
+      // Under a causal mask a tile may hold values that only some rows see:
+      // those that are not finite are replaced by 0 here, and the unit's end is
+      // told.
       [[maybe_unused]] auto sanitise = [&](int st, int ordinal) {
         const uint32_t vb = (uint32_t)(W::kQBytes + st * 2 * W::kHalf + W::kHalf);
         bool found = false;
@@ -472,15 +455,13 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
           uint32_t* w = reinterpret_cast<uint32_t*>(mem + vb + (c >> 3) * (kKeys * 128) + r * 128 +
                                                     (((c & 7) ^ (r & 7)) << 4));
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (word_not_finite<T>(w[e])) {
-              found = true;
-              constexpr uint32_t m = std::is_same<T, F16>::value ? 0x7c00u : 0x7f80u;
-              uint32_t x = w[e];
-              if ((x & m) == m) x &= 0xffff0000u;
-              if (((x >> 16) & m) == m) x &= 0xffffu;
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x = w[e];
+            if (drop_not_finite<T, false>(x)) {
               w[e] = x;
+              found = true;
             }
+          }
         }
         if (found) S.unsound[ordinal % kFlags] = 1;
       };
@@ -568,10 +549,10 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
             const bool is_v = i >= kLoads;
             const int at = (is_v ? i - kLoads : i) * 32 + lane, row = lw * kMine + at / kPieces, c = 2 * (at % kPieces);
             if (is_v && (unit & 1)) {
-              found |= drop_nan(w.x);
-              found |= drop_nan(w.y);
-              found |= drop_nan(w.z);
-              found |= drop_nan(w.w);
+              found |= drop_not_finite<T, true>(w.x);
+              found |= drop_not_finite<T, true>(w.y);
+              found |= drop_not_finite<T, true>(w.z);
+              found |= drop_not_finite<T, true>(w.w);
             }
             unsigned char* d = kb + (is_v ? W::kHalf : 0) + (c >> 3) * (kKeys * 128) + row * 128;
             *reinterpret_cast<uint4*>(d + (((c & 7) ^ (row & 7)) << 4)) = widen8<T>(w.x, w.y);
@@ -828,6 +809,7 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
         // columns at a time as it holds), the first adds them to its own. Pieces
         // of 16 bytes are exchanged within 8 so that 8 lanes meet 8 bank groups.
         constexpr int kRound = kCopies == 4 ? D / 2 : D;
+        float probe = 0.0f;  // NaN once a result is not finite
         for (int r0 = 0; r0 < D && ok; r0 += kRound) {
           if (kCopies > 1) {
             if (copy > 0) {
@@ -867,29 +849,8 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
                 x[4 * i + 2] = o.z;
                 x[4 * i + 3] = o.w;
               }
-              if (unsound && writes) {
-                // The values replaced by 0 that this row does see, added to the
-                // scaled sums (a factor does not change them): whole tiles were
-                // gone through, from the one that holds position L - n.
-                for (int k = max(0, u.L - u.n) / kKeys * kKeys; k < vis; ++k) {
-                  if (k < (int)(u_begin - u.start) * kKeys || k >= (int)(u_end - u.start) * kKeys) continue;
-                  int page, sl;
-                  split_position(p.c, k, page, sl);
-                  const int id = p.c.table[(long long)u.b * p.c.table_stride + page];
-                  if (id < 0 || id >= p.c.num_pages) continue;
-                  const unsigned char* v =
-                      p.c.v + (size_t)row_offset(p.c, id, u.h, sl) * 16u + (kF8 ? 1 : 2) * (r0 + d);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    if constexpr (kF8) {
-                      if ((v[i] & 0x7fu) == 0x7fu) x[i] = NAN;
-                    } else {
-                      const uint16_t b = reinterpret_cast<const uint16_t*>(v)[i];
-                      if (word_not_finite<T>(b)) x[i] += T::unpack(b).x;
-                    }
-                  }
-                }
-              }
+              for (int i = 0; i < 32; ++i) probe = fmaf(x[i], 0.0f, probe);
               if (writes) {
                 if (whole) {
                   uint4* dst = reinterpret_cast<uint4*>(out_row + 2 * (r0 + d));
@@ -905,10 +866,33 @@ __global__ void __launch_bounds__(TcShape<D, kF8>::kThreads, 1) attention_tc_ker
               }
             }
           }
+          // (a row whose sum of weights is not finite has NaN everywhere)
+          if (writes && probe != 0.0f && sum < INFINITY) S.odd = 1;
           // the scratch, Q and S.parts are written again
           ok = softmax_sync(syncs, S);
         }
         if (!ok) break;
+        if (__builtin_expect(unsound || *reinterpret_cast<volatile int*>(&S.odd), 0)) {
+          // results that values which are not finite decide
+          int* first = reinterpret_cast<int*>(scratch);
+          for (int i = tid; i < 3 * D; i += 128) first[i] = kNever;
+          if (!(ok = softmax_sync(syncs, S))) break;
+          find_not_finite<T, kF8, D>(p, u.b, u.h, (int)(u_begin - u.start) * kKeys,
+                                     (int)min((long long)u.L, (u_end - u.start) * kKeys), first, tid, 128);
+          if (!(ok = softmax_sync(syncs, S))) break;
+          if (tid == 0) S.odd = 0;
+          if (writes && sum < INFINITY) {
+            for (int d = 0; d < D; ++d) {
+              const float v = not_finite_value<D>(first, d, vis);
+              if (v == 0.0f) continue;
+              if (whole)
+                reinterpret_cast<uint16_t*>(out_row)[d] = (uint16_t)T::pack(v, 0.0f);
+              else
+                part_row[d] = v;
+            }
+          }
+          if (!(ok = softmax_sync(syncs, S))) break;
+        }
         if (tid == 0) S.unsound[u.ordinal % kFlags] = 0;
         fence_before();
         if (u_begin == u.start && !whole) split = {u.start, u.tiles, u.h, u.rb, u.first, u.n, 0};

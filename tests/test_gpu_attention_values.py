@@ -109,3 +109,63 @@ def test_bad_values_under_a_scale_of_zero(dv, D, n, G):
     got, _ = c.attend(dv, scales)
     assert torch.equal(got[:-1], want[:-1])
     assert bool(got[-1, :, :, ::3].isnan().all())
+
+
+# the rest of the forms: the warps' products
+WARPS = [(t, bad, ROWS[0]) for t in TYPES for bad in (NAN, INF, -INF)] \
+    + [(t, NAN, r) for t in TYPES8 for r in (ROWS if t[0] == 256 else ROWS[:2])]
+
+
+@pytest.mark.parametrize("types,bad,rows", WARPS)
+def test_other_results_stay_as_they_are(dv, types, bad, rows):
+    """A value that is not finite decides its own column of the rows that see it;
+    every other result keeps its bits."""
+    test_values_in_front_of_the_block_count(dv, types, bad, rows)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (128, HF), (256, BF)])
+@pytest.mark.parametrize("n,G", [(1, 4)] + ROWS)
+@pytest.mark.parametrize("L,page", [(300, 16), (70001, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_infinite_values_stay_infinite(dv, D, dtype, n, G, L, page, causal):
+    """An infinite value that a row sees, at whatever weight, makes its result
+    infinite; infinities of both signs, or a NaN, make it NaN. Over one SM and
+    over many."""
+    c = Case(D + G, L, n, G, D, dtype, dtype, page)
+    want, wl = c.attend(dv, causal=causal)
+    c.put(c.v, 3, INF, col=0)
+    c.put(c.v, L // 2 + 1, -INF, col=1)
+    c.put(c.v, 5, INF, col=2)
+    c.put(c.v, L // 2, -INF, col=2)
+    c.put(c.v, L // 3, INF, col=D - 1)
+    c.put(c.v, 7, NAN, col=D - 2)
+    got, gl = c.attend(dv, causal=causal)
+    assert torch.equal(gl, wl)
+    f = got.float()
+    assert bool((f[..., 0] == INF).all()), f[..., 0]
+    assert bool((f[..., 1] == -INF).all())
+    assert bool(f[..., 2].isnan().all())
+    assert bool((f[..., D - 1] == INF).all()) and bool(f[..., D - 2].isnan().all())
+    for col in (0, 1, 2, D - 1, D - 2):
+        got[..., col] = want[..., col]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n,G", [(1, 4)] + ROWS)
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("below", [15.0, 60.0, 300.0])
+def test_infinite_values_of_weak_keys_stay_infinite(dv, n, G, dtype, below):
+    """The key of the infinite value weighs e^-15 to e^-300 of the rest: a finite
+    score's weight is not zero, whatever type holds it."""
+    D, L = 128, 400
+    c = Case(G, L, n, G, D, dtype, dtype)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.k[..., 0] = 0.0
+    c.put(c.k, 9, -below, col=0)
+    want, wl = c.attend(dv, scale=1.0)
+    c.put(c.v, 9, INF, col=7)
+    got, gl = c.attend(dv, scale=1.0)
+    assert torch.equal(gl, wl) and bool((got[..., 7] == INF).all()), got[..., 7]
+    got[..., 7] = want[..., 7]
+    assert torch.equal(got, want)
