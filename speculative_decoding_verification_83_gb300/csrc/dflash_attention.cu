@@ -40,7 +40,8 @@
 // reissued as its half of the stage is read, were slower (217 us): twice the waits
 // and shuffles.
 // Rounding: P is rounded to the operands' type (half a step of its own
-// relative to each weight); all sums, maxima and exponents are fp32.
+// relative to each weight; f16: down to 2^-29 of a row's largest); all sums,
+// maxima and exponents are fp32.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -54,6 +55,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
 constexpr int kRows = 16;                  // query rows per unit
+// f16 holds normal numbers from 2^-14 to below 2^16: a row's reference lies this
+// many powers of 2 below its largest score, so that weights are rounded by half a
+// step of their own down to 2^-29 of the largest. (bf16 has the range of fp32.)
+constexpr float kTopF16 = 15.0f;
 constexpr int kMaxCtas = 640;              // CTAs whose partial results the workspace holds
 
 __host__ __device__ inline AttnGeometry warp_geometry(int tile) { return {kRows, tile, kMaxCtas}; }
@@ -370,6 +375,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
       for (int e = 0; e < 2; ++e) {
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        if (std::is_same<M, F16>::value) mx[e] -= kTopF16;
         const float m_new = fmaxf(m[e], mx[e]);
         moved |= m_new > m[e];
         // no key seen yet: any finite reference will do

@@ -1,9 +1,12 @@
 """dflash_paged_attention where values of the cache are not finite, and where a
 row's weights span many powers of 2: what a row sees decides its result, not
 which kernel, tile, copy or SM took the key."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
+from operator_refs import F32, U  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -169,3 +172,35 @@ def test_infinite_values_of_weak_keys_stay_infinite(dv, n, G, dtype, below):
     assert torch.equal(gl, wl) and bool((got[..., 7] == INF).all()), got[..., 7]
     got[..., 7] = want[..., 7]
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,cdt", [(HF, HF), (BF, F8), (HF, F8), (BF, BF)])
+@pytest.mark.parametrize("n,G", [(1, 4), (4, 6), (4, 12), (4, 24)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("below,sink", [(18.0, 0), (18.0, 15000), (12.0, 0)])
+def test_many_keys_far_below_one(dv, dtype, cdt, n, G, D, below, sink):
+    """One key outweighs each of 20000 others by e^12 or e^18 and has no value
+    of its own: the result is what the others add up to. Weights are rounded by
+    half a step of their own, in f16 (whose largest weight is 2^15 in the warps'
+    products, and at first 2^7 on tensor memory) by no more than 2^-25 at the least.
+    (300 requests share the pages, so that each unit lies in few SMs.)"""
+    L, B = 20001, 300
+    c = Case(1, L, n, G, D, dtype, cdt, page=64)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    for t, x in ((c.k, 0.0), (c.v, 1.0)):
+        t.copy_(torch.full(t.shape, x, device=DEV).to(t.dtype))
+    c.put(c.k, sink, below, col=0)
+    c.put(c.v, sink, 0.0)
+    c.table, c.lens, c.q = c.table.expand(B, -1).contiguous(), c.lens.expand(B).contiguous(), c.q.repeat(B, 1, 1)
+    c.n *= B
+    got, lse = c.attend(dv, scale=1.0, causal=False)
+    rest = (L - 1) * math.exp(-below)
+    want = rest / (1.0 + rest)
+    # the weights' type (8-bit caches of up to 32 rows: f16), the output's, sums of L / 16 terms a lane
+    up = U[HF] if cdt == F8 and n * G <= 32 else U[dtype]
+    small = 0.0 if up != U[HF] else 2.0 ** (-40 if n * G <= (32 if cdt == F8 else 16) else -32)
+    tol = max(up, small * math.exp(below)) + U[dtype] + 2 * ((L / 16 + 200) * F32 + 2.0 ** -21)
+    err = (got.double() / want - 1.0).abs()
+    assert float(err.max()) <= tol, (float(err.max()), tol)
+    assert float((lse.double() - (below + math.log1p(rest))).abs().max()) <= 2 * tol
