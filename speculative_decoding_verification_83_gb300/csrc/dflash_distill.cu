@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
   __syncwarp();
   a = warp_join(a);  // the same bits in every warp of every CTA of the row
   const bool active = w != 0.0f && (a.s != 0.0f || a.ref == -INFINITY);
-  if (a.ref == -INFINITY) a.s = NAN;  // no logit above -inf: the row has no distribution
+  if (fabsf(a.ref) == INFINITY) a.s = NAN;  // no logit above -inf, or +inf: the row has no distribution
   if (rank == 0 && warp == kW) {
     const float log2_s = log2f(a.s);
     float part = 0.0f;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
         p.lse[2 * r] = active ? a.ref : 0.0f;
         p.lse[2 * r + 1] = active ? a.s : 0.0f;
       }
-      if (active && (!(a.s == a.s) || a.ref == INFINITY)) raise_status(p.status, DFLASH_STATUS_BAD_ROW);
+      if (active && !(a.s == a.s)) raise_status(p.status, DFLASH_STATUS_BAD_ROW);
     }
   }
   if (kGrad) {
