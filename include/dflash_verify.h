@@ -462,7 +462,8 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const void* q, void*
  * dflash_distill_loss: loss [rows] and, where row_stats ([device] float
  * [rows, 2]) is given, each row's reference R and sum s of 2^(z / (T ln 2) -
  * R), so log sum e^(z / T) = (R + log2 s) ln 2, for the backward call (0, 0 for
- * a row that takes no part). */
+ * a row that takes no part). A row whose largest logit m is so far from 0 that
+ * |m| / (T ln 2) > 2^30 has m and minus the sum of 2^((z - m) / (T ln 2)). */
 int dflash_distill_loss(const void* student, int64_t row_stride, int rows, int V, int dtype,
                         const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
                         const float* row_weight, float* loss, float* row_stats, uint32_t* status, void* stream);

@@ -10,20 +10,22 @@
 // w_r = 0, has loss 0 and gradient 0, and its logits do not matter.
 //
 // Exponents are taken in base 2 with c = 1 / (T ln 2): the row's statistics
-// are R = fl(c max z), a plain reference, and s = sum_v 2^(c z_v - R), so that
-// q_v = 2^(c z_v - R) / s and log q_v = (c z_v - R - log2 s) ln 2, where c z_v
-// - R is one rounded multiply-add. All sums are fp32.
+// are m = max z and s = sum_v 2^(c (z_v - m)), so that q_v = 2^(c (z_v - m)) / s
+// and log q_v = (c (z_v - m) - log2 s) ln 2. The difference comes first: c z alone
+// leaves fp32's range for logits near its ends (a row that is nothing but its
+// type's lowest value), and is rounded to more than 1 from 2^24 on. All sums are
+// fp32.
 //
 // What bounds it: reading the logits and writing the gradient, once each. A row
 // is dealt out to a cluster of a few CTAs. Each moves the first 70 KB of its
 // slice into shared memory by bulk copies, reduces the pieces as they land (a
-// running reference per thread), then the rest as it streams by; it sends its
-// (R, s) to the other CTAs through distributed shared memory and writes the
+// running maximum per thread), then the rest as it streams by; it sends its
+// (m, s) to the other CTAs through distributed shared memory and writes the
 // gradient, from shared memory and, for the rest, from L2, where the logits
 // just read still are. Three CTAs share an SM, so that one's copies and stores
 // fill the time of another's reductions and barriers: that counts for more
 // than holding whole slices. Measured at 1920 x 248320 bf16, loss and
-// gradient: clusters of 4 with 70 KB held 342 us (5.57 TB/s, 83% of a copy's
+// gradient: clusters of 4 with 70 KB held 347 us (5.49 TB/s, 82% of a copy's
 // measured rate), of 8 with whole slices held 406 us, of 2 453 us (more CTAs
 // per row wait for their slowest, fewer read more again), of 4 with 110 KB and
 // two CTAs an SM 583 us. The loss alone holds nothing back, and fewer CTAs per
@@ -44,6 +46,7 @@ namespace {
 constexpr int kMaxSplit = 8;         // CTAs per row
 constexpr int kPieces = 4;          // bulk copies of a slice
 constexpr int kMaxHeld = 70 * 1024;  // bytes of a slice kept in shared memory: three fit an SM
+constexpr float kMaxReference = 0x1p30f;  // of a row's statistics, in powers of 2: good to 2^5 of them
 constexpr float kLog2eD = 1.4426950408889634f;
 constexpr float kLn2D = 0.6931471805599453f;
 
@@ -78,10 +81,10 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^(c x - R) of both values
+// 2^(c (x - m)) of both values
 __device__ __forceinline__ unsigned long long weights2(unsigned long long x, unsigned long long c2,
-                                                       unsigned long long neg_r2) {
-  const float2 a = floats_of(fma2(x, c2, neg_r2));
+                                                       unsigned long long neg_m2) {
+  const float2 a = floats_of(mul2(add2(x, neg_m2), c2));
   return pair_of(ex2d(a.x), ex2d(a.y));
 }
 
@@ -136,15 +139,16 @@ struct F32 {
   }
 };
 
-// A part of a row: the reference R (-inf: no value above -inf yet) and s.
+// A part of a row: its largest logit m (-inf: no value above -inf yet) and s.
 struct Stat {
   float ref, s;
 };
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
   Stat r;
   r.ref = fmaxf(a.ref, b.ref);
   // a side that has seen nothing carries its sum, 0 or NaN, as it is
-  const float fa = a.ref == r.ref ? 1.0f : ex2d(a.ref - r.ref), fb = b.ref == r.ref ? 1.0f : ex2d(b.ref - r.ref);
+  const float fa = a.ref == r.ref ? 1.0f : ex2d((a.ref - r.ref) * c),
+              fb = b.ref == r.ref ? 1.0f : ex2d((b.ref - r.ref) * c);
   r.s = a.s * fa + b.s * fb;
   return r;
 }
@@ -154,18 +158,18 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 // The join of the warp's 32 parts, in every lane.
-__device__ __forceinline__ Stat warp_join(const Stat& a) {
+__device__ __forceinline__ Stat warp_join(const Stat& a, float c) {
   Stat r;
   r.ref = warp_max_f32(a.ref);
-  r.s = warp_sum(a.ref == r.ref ? a.s : a.s * ex2d(a.ref - r.ref));
+  r.s = warp_sum(a.ref == r.ref ? a.s : a.s * ex2d((a.ref - r.ref) * c));
   return r;
 }
 // Two vectors into a running part: the reference moves up to their largest.
 template <class T>
 __device__ __forceinline__ void take(Stat& a, const uint4& u, const uint4& v, float c, unsigned long long c2) {
-  const float m = T::top(u, v) * c;
+  const float m = T::top(u, v);
   if (m > a.ref) {
-    a.s = a.ref == -INFINITY ? a.s : a.s * ex2d(a.ref - m);
+    a.s = a.ref == -INFINITY ? a.s : a.s * ex2d((a.ref - m) * c);
     a.ref = m;
   }
   const float neg = a.ref == -INFINITY ? 0.0f : -a.ref;
@@ -180,8 +184,7 @@ __device__ __forceinline__ void take(Stat& a, const uint4& u, const uint4& v, fl
   a.s += f.x + f.y;
 }
 __device__ __forceinline__ void take_one(Stat& a, float x, float c) {
-  const float m = x * c;
-  a = join(a, Stat{m == m ? m : -INFINITY, m == -INFINITY ? 0.0f : m == m ? 1.0f : m});
+  a = join(a, Stat{x == x ? x : -INFINITY, x == -INFINITY ? 0.0f : x == x ? 1.0f : x}, c);
 }
 
 struct Teacher {
@@ -236,10 +239,23 @@ __device__ __forceinline__ void teacher_row(const DistillParams& p, long long r,
   }
 }
 
+// The student's distribution: q = 2^(c (z - shift) + add) / s. For ordinary rows
+// shift is 0 and add = -R, R = fl(c m), with s taken to it: one rounded
+// multiply-add, the same in both gradients. Where R is rounded to too few bits
+// for that, shift is the largest logit itself.
+struct Student {
+  float shift, add, s;
+};
+__device__ __forceinline__ Student student_of(const Stat& a, float c) {
+  const float R = a.ref * c;
+  if (fabsf(R) <= kMaxReference) return {0.0f, -R, a.s * ex2d(fmaf(a.ref, c, -R))};
+  return {a.ref, 0.0f, a.s};
+}
+
 // The gradient at the teacher's tokens in [lo, hi), over what is written there.
 template <class T>
 __device__ __forceinline__ void teacher_gradient(const DistillParams& p, const Teacher& S, unsigned char* g, int lo,
-                                                 int hi, float c, const Stat& a, float coef) {
+                                                 int hi, float c, const Student& q, float coef) {
   for (int j = threadIdx.x; j < p.K; j += blockDim.x) {
     const int id = S.id[j];
     if (id < lo || id >= hi) continue;
@@ -250,7 +266,7 @@ __device__ __forceinline__ void teacher_gradient(const DistillParams& p, const T
         owner &= i >= j;
         sum += S.p[i];
       }
-    if (owner) T::store(g + (size_t)id * T::kBytes, (ex2d(fmaf(S.z[j], c, -a.ref)) / a.s - sum) * coef);
+    if (owner) T::store(g + (size_t)id * T::kBytes, (ex2d(fmaf(S.z[j] - q.shift, c, q.add)) / q.s - sum) * coef);
   }
 }
 
@@ -274,20 +290,23 @@ struct Slice {
   }
 };
 
-// The gradient's vectors: 2^(c z - R) f.
+// The gradient's vectors: 2^(c (z - shift) + add) f.
 template <class T>
 struct Writer {
-  unsigned long long c2, n2, f2;
+  unsigned long long c2, n2, a2, f2;
   unsigned char* body;
   bool aligned;
-  __device__ __forceinline__ Writer(const unsigned char* z, unsigned char* g, int head, float c, const Stat& a, float f)
-      : c2(pair_of(c, c)), n2(pair_of(-a.ref, -a.ref)), f2(pair_of(f, f)), body(g + (size_t)head * T::kBytes),
+  __device__ __forceinline__ Writer(const unsigned char* z, unsigned char* g, int head, float c, const Student& q, float f)
+      : c2(pair_of(c, c)), n2(pair_of(-q.shift, -q.shift)), a2(pair_of(q.add, q.add)), f2(pair_of(f, f)), body(g + (size_t)head * T::kBytes),
         aligned((((uintptr_t)z ^ (uintptr_t)g) & 15) == 0) {}
   __device__ __forceinline__ void put(int v, const uint4& u) const {
     unsigned long long x[T::kPer / 2];
     T::unpack(u, x);
 #pragma unroll
-    for (int i = 0; i < T::kPer / 2; ++i) x[i] = mul2(weights2(x[i], c2, n2), f2);
+    for (int i = 0; i < T::kPer / 2; ++i) {
+      const float2 e = floats_of(fma2(add2(x[i], n2), c2, a2));
+      x[i] = mul2(pair_of(ex2d(e.x), ex2d(e.y)), f2);
+    }
     if (aligned) {
       reinterpret_cast<uint4*>(body)[v] = T::pack(x);
     } else {
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
     take<T>(a, body[v], v + kThreads < L.v1 ? body[v + kThreads] : low, c, c2);
   if (L.edge >= 0) take_one(a, at_edge, c);
   if (!ok) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
-  a = warp_join(a);
+  a = warp_join(a, c);
   if (lane == 0) parts[warp] = a;
   }
   __syncwarp();
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
   if (split > 1) {
     cluster_wait();  // every CTA of the row runs
     if (warp == 0) {
-      a = warp_join(lane < kW ? parts[lane] : Stat{-INFINITY, 0.0f});
+      a = warp_join(lane < kW ? parts[lane] : Stat{-INFINITY, 0.0f}, c);
       if (S.empty) a = Stat{0.0f, 0.0f};  // a row without entries: every CTA sends (0, 0)
       if (lane < split) send_part(&slices[rank], &exchanged, lane, a);
     }
@@ -435,20 +454,21 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
     a = S.empty ? Stat{0.0f, 0.0f} : lane < kW ? parts[lane] : Stat{-INFINITY, 0.0f};
   }
   __syncwarp();
-  a = warp_join(a);  // the same bits in every warp of every CTA of the row
+  a = warp_join(a, c);  // the same bits in every warp of every CTA of the row
   const bool active = w != 0.0f && (a.s != 0.0f || a.ref == -INFINITY);
   if (fabsf(a.ref) == INFINITY) a.s = NAN;  // no logit above -inf, or +inf: the row has no distribution
   if (rank == 0 && warp == kW) {
     const float log2_s = log2f(a.s);
     float part = 0.0f;
     for (int j = lane; j < p.K; j += 32)
-      if (S.id[j] >= 0 && S.p[j] != 0.0f) part += S.p[j] * (S.log2p[j] - (fmaf(S.z[j], c, -a.ref) - log2_s));
+      if (S.id[j] >= 0 && S.p[j] != 0.0f) part += S.p[j] * (S.log2p[j] - ((S.z[j] - a.ref) * c - log2_s));
     part = warp_sum(part);
     if (lane == 0) {
       p.loss[r] = active ? part * kLn2D * w : 0.0f;
       if (p.lse) {
-        p.lse[2 * r] = active ? a.ref : 0.0f;
-        p.lse[2 * r + 1] = active ? a.s : 0.0f;
+        const Student q = student_of(a, c);
+        p.lse[2 * r] = !active ? 0.0f : q.shift == 0.0f ? -q.add : q.shift;
+        p.lse[2 * r + 1] = !active ? 0.0f : q.shift == 0.0f ? q.s : -q.s;
       }
       if (active && !(a.s == a.s)) raise_status(p.status, DFLASH_STATUS_BAD_ROW);
     }
@@ -458,15 +478,16 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
       for (int i = L.lo + tid; i < L.hi; i += blockDim.x) T::store(g + (size_t)i * T::kBytes, 0.0f);
       return;
     }
-    const float coef = w * p.inv_t, f = coef / a.s;
-    const Writer<T> out(z, g, L.head, c, a, f);
+    const Student q = student_of(a, c);
+    const float coef = w * p.inv_t, f = coef / q.s;
+    const Writer<T> out(z, g, L.head, c, q, f);
     if (warp < kW) {
       for (int v = tid; v < n_held; v += kThreads) out.put(L.v0 + v, mine[v]);
       for (int v = L.v0 + n_held + tid; v < L.v1; v += kThreads) out.put(v, body[v]);
     }
-    if (L.edge >= 0) T::store(g + (size_t)L.edge * T::kBytes, ex2d(fmaf(at_edge, c, -a.ref)) * f);
+    if (L.edge >= 0) T::store(g + (size_t)L.edge * T::kBytes, ex2d(fmaf(at_edge - q.shift, c, q.add)) * f);
     __syncthreads();  // the slice is written
-    teacher_gradient<T>(p, S, g, L.lo, L.hi, c, a, coef);
+    teacher_gradient<T>(p, S, g, L.lo, L.hi, c, q, coef);
   }
 }
 
@@ -492,7 +513,8 @@ __global__ void __launch_bounds__(kGradThreads + 32) grad_kernel(const DistillPa
     if (tid < kGradThreads && v < L.v1) u[i] = body[v];
   }
   const float at_edge = L.edge >= 0 ? T::load(z + (size_t)L.edge * T::kBytes) : 0.0f;
-  Stat a = {p.lse[2 * r], p.lse[2 * r + 1]};
+  const Stat a = {p.lse[2 * r], p.lse[2 * r + 1]};
+  const Student q = a.s < 0.0f ? Student{a.ref, 0.0f, -a.s} : Student{0.0f, -a.ref, a.s};
   float w = p.weight ? p.weight[r] : 1.0f;
   if (p.upstream) w *= p.upstream[r * p.upstream_stride];
   if (w == 0.0f || a.s == 0.0f) {  // the statistics of a row that has no part are (0, 0)
@@ -501,8 +523,8 @@ __global__ void __launch_bounds__(kGradThreads + 32) grad_kernel(const DistillPa
   }
   if (tid >= kGradThreads) teacher_row<T>(p, r, z, false, c, S);
   if (g == z) __syncthreads();  // in place: the teacher's logits are read before they are written over
-  const float coef = w * p.inv_t, f = coef / a.s;
-  const Writer<T> out(z, g, L.head, c, a, f);
+  const float coef = w * p.inv_t, f = coef / q.s;
+  const Writer<T> out(z, g, L.head, c, q, f);
   for (int v = L.v0 + tid; v < L.v1 && tid < kGradThreads; v += kGradHeld * kGradThreads) {
 #pragma unroll
     for (int i = 0; i < kGradHeld; ++i)
@@ -513,9 +535,9 @@ __global__ void __launch_bounds__(kGradThreads + 32) grad_kernel(const DistillPa
       if (n < L.v1) u[i] = body[n];
     }
   }
-  if (L.edge >= 0) T::store(g + (size_t)L.edge * T::kBytes, ex2d(fmaf(at_edge, c, -a.ref)) * f);
+  if (L.edge >= 0) T::store(g + (size_t)L.edge * T::kBytes, ex2d(fmaf(at_edge - q.shift, c, q.add)) * f);
   __syncthreads();  // the slice is written
-  teacher_gradient<T>(p, S, g, L.lo, L.hi, c, a, coef);
+  teacher_gradient<T>(p, S, g, L.lo, L.hi, c, q, coef);
 }
 
 int launch_cfg(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long grid, int threads, size_t smem,

@@ -75,7 +75,7 @@ struct DistillParams {
   long long upstream_stride;
   float inv_t;
   float* loss;
-  float* lse;  // [rows, 2] statistics; forward: written (or null); backward: read
+  float* lse;  // [rows, 2] statistics; forward: written (or null); backward: read. s < 0: about the largest logit
   unsigned char* grad;
   long long grad_stride;
   uint32_t* status;
