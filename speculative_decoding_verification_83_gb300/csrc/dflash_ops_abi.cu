@@ -128,6 +128,8 @@ int check_distill(const void* student, int64_t stride, int rows, int V, int dtyp
   if (stride < 0) return fail(DFLASH_ERR_INVALID_ARG, "the row stride must not be negative");
   if (!(temperature > 0.0f) || std::isinf(temperature))
     return fail(DFLASH_ERR_INVALID_ARG, "temperature=%g must be positive and finite", (double)temperature);
+  if (std::isinf(1.4426950408889634f * (1.0f / temperature)))  // the exponents' scale
+    return fail(DFLASH_ERR_INVALID_ARG, "temperature=%g is too small: 1 / (T ln 2) must be finite", (double)temperature);
   if (!aligned(student, dtype == DFLASH_BF16 ? 2 : 4))
     return fail(DFLASH_ERR_INVALID_ARG, "student logits are not aligned to their type");
   return DFLASH_OK;
