@@ -16,11 +16,12 @@
 // and the chain of offset, length, page and slot. So a block reads its values
 // first and finds out where they go while they arrive. Measured on one GB300:
 // 10223 tokens of 40 query and 8 key/value heads of 128 into an e4m3 cache, half
-// of each head rotated, 50 us (5.4 TB/s, 81% of a copy's rate), where one token a
+// of each head rotated, 52 us (5.2 TB/s, 78% of a copy's rate), where one token a
 // block, read after its place was known, took 75 us, and two divisions an item 62
 // us. Four items a thread are best there (two 51 us, eight 57 us).
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "dflash_paged.cuh"
@@ -52,18 +53,39 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7]));
 }
 
-// 8 values (e4m3: times inv, one over the head's scale) to a cache row (16-byte
-// units from base), at value 8 * vec
+// A head's scale z, and two reciprocals with the true one between them. Rounding
+// is monotonic: where a value's products with both round to the same e4m3 value,
+// so does its quotient; elsewhere (about one value in 2^18) it is divided.
+// Dividing every value takes 55 us where this takes 52 (the case above).
+struct Scale {
+  float z, low, high;
+};
+__device__ __forceinline__ Scale make_scale(float z) {
+  const float inv = __frcp_rn(z);
+  // no reciprocal with all its bits: 0 and infinity round apart, and all is divided
+  if (!(fabsf(inv) >= 0x1p-126f && fabsf(inv) < INFINITY)) return {z, 0.0f, INFINITY};
+  // a power of 2 has its own
+  if ((__float_as_uint(z) & 0x7fffffu) == 0u) return {z, inv, inv};
+  return {z, inv * (1.0f - 0x1p-22f), inv * (1.0f + 0x1p-22f)};
+}
+__device__ __forceinline__ uint32_t e4m3_4(const float (&x)[8], int i, float f) {
+  return (uint32_t)e4m3_pair(x[i] * f, x[i + 1] * f) | (uint32_t)e4m3_pair(x[i + 2] * f, x[i + 3] * f) << 16;
+}
+
+// 8 values (e4m3: over the head's scale) to a cache row (16-byte units from base),
+// at value 8 * vec
 template <class T, bool kF8>
 __device__ __forceinline__ void store_cache(unsigned char* base, uint32_t row, int vec, const float (&x)[8],
-                                            float inv) {
+                                            const Scale& s) {
   unsigned char* p = base + (size_t)row * 16u;
   if (kF8) {
-    uint32_t w[2];
+    uint32_t w[2] = {e4m3_4(x, 0, s.low), e4m3_4(x, 4, s.low)};
+    if (__builtin_expect((w[0] ^ e4m3_4(x, 0, s.high)) | (w[1] ^ e4m3_4(x, 4, s.high)), 0)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      w[i] = (uint32_t)e4m3_pair(x[4 * i] * inv, x[4 * i + 1] * inv) |
-             (uint32_t)e4m3_pair(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+      for (int i = 0; i < 2; ++i)
+        w[i] = (uint32_t)e4m3_pair(x[4 * i] / s.z, x[4 * i + 1] / s.z) |
+               (uint32_t)e4m3_pair(x[4 * i + 2] / s.z, x[4 * i + 3] / s.z) << 16;
+    }
     reinterpret_cast<uint2*>(p)[vec] = make_uint2(w[0], w[1]);
   } else {
     reinterpret_cast<uint4*>(p)[vec] = pack8<T>(x);
@@ -210,7 +232,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (pl.page >= 0) {
         const uint32_t row = row_offset(p.c, pl.page, head, pl.slot);
         const float* sc = is_k ? p.c.k_scale : p.c.v_scale;
-        const float z = kF8 && sc ? __frcp_rn(sc[head]) : 1.0f;
+        const Scale z = make_scale(kF8 && sc ? sc[head] : 1.0f);
         unsigned char* base = is_k ? p.c.k : p.c.v;
         store_cache<T, kF8>(base, row, va, a, z);
         store_cache<T, kF8>(base, row, vb, b, z);
