@@ -417,7 +417,8 @@ typedef struct dflash_paged_cache {
  * (modulo 1), which keeps the angle exact at any position. rot_dim: a
  * multiple of 16, 0 for no rotation. The arithmetic is fp32, rounded once to
  * the cache's type (e4m3: over the head's scale, saturated at +-448).
- * strides: k's token and head stride, then v's, q's, q_out's. */
+ * Tokens of a bad length, and rows of no request, leave their place in q_out as
+ * it is. strides: k's token and head stride, then v's, q's, q_out's. */
 int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out,
                      int dtype, int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens,
                      const int32_t* q_start, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,

@@ -189,6 +189,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       turn[ti * half + (j & 7) * rv + (j >> 3)] = make_float2(c, s);  // an item's 8 pairs, rv apart
     }
   }
+  // Offsets and lengths that no token meets are reported, too: by one block,
+  // beginning with the warps that have no token to place.
+  if (p.status && blockIdx.x == 0 && blockIdx.y == 0) {
+    const long long cap = (long long)p.c.max_pages * p.c.page_size;
+    bool bad = false;
+    for (int b = kAppendThreads - 1 - tid; b < p.tk.B; b += kAppendThreads) {
+      int first, n;
+      request_tokens(p.tk, b, first, n, bad);
+      bad |= p.lens[b] < 0 || p.lens[b] > cap;
+    }
+    if (bad) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
+  }
   __syncthreads();
 
 #pragma unroll

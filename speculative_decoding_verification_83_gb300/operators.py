@@ -214,7 +214,8 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     [batch] int32 tokens, the keys (and ``q`` [tokens, q_heads, head_dim])
     rotated by ``phases`` (``rope_phases``; None: no rotation). Requests' tokens
     are packed at ``q_start`` [batch + 1] int32, or tokens / batch each. Returns
-    the rotated q (a new tensor, or ``q_out``, which may be ``q``), or None."""
+    the rotated q (a new tensor, or ``q_out``, which may be ``q``), or None; its
+    rows of no request, or of a bad length, are not written."""
     torch = _torch()
     dev, D = cache.device, cache.head_dim
     dt = _token_dtype(k, cache, "tokens")

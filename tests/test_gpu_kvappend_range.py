@@ -1,4 +1,5 @@
-"""dflash_kv_append: values over their scale."""
+"""dflash_kv_append: values over their scale, and what its status word says of
+offsets and lengths."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -62,3 +63,48 @@ def test_quotients_of_any_size(dv, unit):
     want = (x.float() / z[:, None]).clamp(-448, 448).to(F8)
     for c in caches:
         assert torch.equal(c[0].transpose(0, 1).view(torch.uint8), want.view(torch.uint8))
+
+
+def cache_of(dv, batch, pages=4, page=16, D=64, H=2):
+    c = [torch.zeros((batch * pages, H, page, D), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    t = torch.arange(batch * pages, device=DEV, dtype=torch.int32).view(batch, pages)
+    return c, dv.PagedCache(c[0], c[1], t)
+
+
+@pytest.mark.parametrize("starts,cached,bad", [
+    ([0, 4, 8], [0, 3], False), ([0, 0, 8], [0, 3], False), ([2, 4, 6], [0, 3], False), ([0, 8, 8], [0, 64], False),
+    ([0, 8, 100], [0, 3], True), ([0, 6, 4, 8], [0, 3, 1], True), ([-3, 4, 8], [0, 3], True), ([0, 9, 9], [0, 3], True),
+    ([0, 8, 8], [0, 65], True), ([0, 8, 8], [0, -1], True), ([0, 4, 8], [0, 61], True),
+])
+@pytest.mark.parametrize("spare", [0, 600])
+def test_status_names_bad_offsets_and_lengths(dv, starts, cached, bad, spare):
+    """Offsets that do not ascend inside the packed tokens, and lengths outside
+    the page table, are reported whether or not a token meets them."""
+    B = len(cached)
+    starts, cached = starts + [starts[-1]] * spare, cached + [0] * spare
+    c, pc = cache_of(dv, B + spare)
+    x = torch.randn((8, 2, 64), device=DEV).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dv.kv_append(pc, x, x, torch.tensor(cached, dtype=torch.int32, device=DEV), status=st,
+                 q_start=torch.tensor(starts, dtype=torch.int32, device=DEV))
+    assert int(st) == (dv.STATUS_BAD_LENGTH if bad else 0)
+
+
+def test_nothing_outside_is_touched(dv):
+    """Negative lengths write nothing; clamped offsets write the tokens that are
+    there and nothing else."""
+    x = torch.randn((12, 2, 64), device=DEV).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c, pc = cache_of(dv, 3)
+    dv.kv_append(pc, x, x, torch.tensor([-1, -5, -2 ** 31], dtype=torch.int32, device=DEV), status=st)
+    assert int(st) == dv.STATUS_BAD_LENGTH and all(bool((t == 0).all()) for t in c)
+    st.zero_()
+    dv.kv_append(pc, x, x, torch.tensor([0, 14, 3], dtype=torch.int32, device=DEV), status=st,
+                 q_start=torch.tensor([0, 4, 100, 200], dtype=torch.int32, device=DEV))
+    assert int(st) == dv.STATUS_BAD_LENGTH
+    for t in c:
+        want = torch.zeros_like(t)
+        want[0, :, :4] = x[:4].transpose(0, 1)
+        want[4, :, 14:16] = x[4:6].transpose(0, 1)
+        want[5, :, :6] = x[6:12].transpose(0, 1)
+        assert torch.equal(t, want)
