@@ -136,6 +136,20 @@ def _status_word(status, device):
     return _dev(status, "status", _torch().int32)
 
 
+def _carries_no_gradient(cache, **tensors):
+    """These calls have no backward pass: a gradient they would drop is refused,
+    unless the caller has switched gradients off."""
+    if not _modules[0].is_grad_enabled():
+        return
+    if cache is not None:
+        for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+            if t is not None and t.requires_grad:
+                raise ValueError("the cache has no gradient here: detach it, or call under torch.no_grad()")
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{name} has no gradient here: detach it, or call under torch.no_grad()")
+
+
 class PagedCache:
     """A paged key/value cache as the calls take it: ``k`` and ``v`` [pages,
     heads, page_size, head_dim] (views with any outer strides, the same for
@@ -213,12 +227,14 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     heads, head_dim] into the cache behind each request's ``cached_lens``
     [batch] int32 tokens, the keys (and ``q`` [tokens, q_heads, head_dim])
     rotated by ``phases`` (``rope_phases``; None: no rotation). Requests' tokens
-    are packed at ``q_start`` [batch + 1] int32, or tokens / batch each. Returns
+    are packed at ``q_start`` [batch + 1] int32, or tokens / batch each. There is
+    no backward pass (tensors that require a gradient are refused). Returns
     the rotated q (a new tensor, or ``q_out``, which may be ``q``), or None; its
     rows of no request, or of a bad length, are not written."""
     torch = _torch()
     dev, D = cache.device, cache.head_dim
     dt = _token_dtype(k, cache, "tokens")
+    _carries_no_gradient(cache, k=k, v=v, q=q, q_out=q_out)
     pk, kt, kh = _rows(k, "k", cache.heads, D, dev)
     pv, vt, vh = _rows(v, "v", cache.heads, D, dev, k)
     n = k.shape[0]
@@ -257,13 +273,15 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     """dflash_paged_attention: ``q`` [tokens, q_heads, head_dim] over the cache,
     which already holds the new tokens (``kv_lens`` [batch] int32 counts them).
     ``scale`` defaults to 1 / sqrt(head_dim). causal: each new token sees the
-    positions up to its own; otherwise all of its request's. Returns ``out``
-    like q, with ``return_lse`` (out, lse [tokens, q_heads] fp32). ``workspace``:
-    a uint8 tensor of ``attention_workspace_bytes``; None takes one from
-    torch's allocator for the call."""
+    positions up to its own; otherwise all of its request's. There is no backward
+    pass (tensors that require a gradient are refused). Returns ``out`` like q,
+    with ``return_lse`` (out, lse [tokens, q_heads] fp32). ``workspace``: a uint8
+    tensor of ``attention_workspace_bytes``; None takes one from torch's allocator
+    for the call."""
     torch = _torch()
     dev, D = cache.device, cache.head_dim
     dt = _token_dtype(q, cache, "queries")
+    _carries_no_gradient(cache, q=q, out=out, lse=lse)
     pq, qt, qh = _rows(q, "q", None, D, dev)
     n, hq, _ = q.shape
     if out is None:
@@ -394,6 +412,7 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
     training loops that carry the gradient on themselves, without autograd."""
     torch = _torch()
     _no_grad_inputs(teacher_logits, row_weight)
+    _carries_no_gradient(None, grad=grad)
     head, w = _distill_args(student, teacher_ids, teacher_logits, row_weight)
     N, V, dev = head[2], head[3], student.device
     loss = _empty((N,), torch.float32, dev, stream)
