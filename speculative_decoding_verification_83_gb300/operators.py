@@ -150,6 +150,12 @@ def _carries_no_gradient(cache, **tensors):
             raise ValueError(f"{name} has no gradient here: detach it, or call under torch.no_grad()")
 
 
+def _written(*tensors):
+    """Tells torch which of the caller's tensors a call has written over: a
+    backward pass that kept one of them then fails instead of reading it."""
+    _modules[0].autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 class PagedCache:
     """A paged key/value cache as the calls take it: ``k`` and ``v`` [pages,
     heads, page_size, head_dim] (views with any outer strides, the same for
@@ -239,6 +245,7 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     pv, vt, vh = _rows(v, "v", cache.heads, D, dev, k)
     n = k.shape[0]
     pq = po = None
+    new_q = q_out is None
     hq = qt = qh = ot = oh = 0
     if q is not None:
         pq, qt, qh = _rows(q, "q", None, D, dev, k)
@@ -258,6 +265,7 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     _check(_library().dflash_kv_append(cache._ref, pk, pv, pq, po, dt, n, hq, _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens,
                                    starts, phases, rot, 1 if interleaved else 0, _status_word(status, dev),
                                    _raw_stream(stream, dev)))
+    _written(cache.k, cache.v, None if new_q else q_out)
     return q_out
 
 
@@ -284,10 +292,12 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     _carries_no_gradient(cache, q=q, out=out, lse=lse)
     pq, qt, qh = _rows(q, "q", None, D, dev)
     n, hq, _ = q.shape
-    if out is None:
+    given_out = out is not None
+    if not given_out:
         out = _empty((n, hq, D), q.dtype, dev, stream)
     po, ot, oh = _rows(out, "out", hq, D, dev, q)
     pl = None
+    given = out if given_out else None, lse
     if lse is not None:
         _shape(lse, (n, hq), "lse")
         _on(dev, lse=lse)
@@ -305,6 +315,7 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     _check(_library().dflash_paged_attention(
         cache._ref, pq, po, pl, dt, n, hq, _pack4(qt, qh, ot, oh), lens, starts, D ** -0.5 if scale is None else scale,
         1 if causal else 0, ws, ws_bytes, _status_word(status, dev), _raw_stream(stream, dev)))
+    _written(*given)
     return (out, lse) if return_lse else out
 
 
@@ -416,7 +427,7 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
     head, w = _distill_args(student, teacher_ids, teacher_logits, row_weight)
     N, V, dev = head[2], head[3], student.device
     loss = _empty((N,), torch.float32, dev, stream)
-    gs = V
+    gs, given = V, grad
     if grad is None:
         grad = _empty((N, V), student.dtype, dev, stream)
     else:
@@ -429,6 +440,7 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
             gs = max(gs, V)
     _check(_library().dflash_distill_loss_grad(*head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
                                            _status_word(status, dev), _raw_stream(stream, dev)))
+    _written(given)
     return loss, grad
 
 

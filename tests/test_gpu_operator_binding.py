@@ -58,3 +58,38 @@ def test_gradients_are_not_dropped_in_silence(dv):
     with torch.no_grad():
         dv.distill_loss_grad(z, ids, t, grad=z)
     dv.distill_loss_grad(z, ids, t)
+
+
+def test_tensors_written_in_place_are_known_to_autograd(dv):
+    """A tensor that autograd keeps for a backward pass and a call then writes
+    over is an error of the backward pass, as it is for torch's own operations."""
+    pc, q, (k, v), ln = setup(dv)
+    w = torch.ones((), device=DEV, requires_grad=True)
+
+    def refused(t, write):
+        y = (t * w).float().sum()
+        write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+
+    refused(pc.k, lambda: dv.kv_append(pc, k, v, ln))
+    refused(pc.v, lambda: dv.kv_append(pc, k, v, ln))
+    refused(q, lambda: dv.kv_append(pc, k, v, ln, q=q, q_out=q))
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)
+    refused(out, lambda: dv.paged_attention(pc, q, ln, out=out, lse=lse))
+    refused(lse, lambda: dv.paged_attention(pc, q, ln, out=out, lse=lse))
+    z = torch.randn((2, 50), device=DEV)
+    ids, t = torch.zeros((2, 3), dtype=torch.int32, device=DEV), torch.zeros((2, 3), device=DEV)
+    refused(z, lambda: dv.distill_loss_grad(z, ids, t, grad=z))
+    # the loss's own saved logits
+    a = torch.randn((2, 50), device=DEV, requires_grad=True)
+    b = a * 1
+    loss = dv.distill_loss(b, ids, t).sum()
+    with torch.no_grad():
+        dv.distill_loss_grad(b, ids, t, grad=b)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():  # tensors without a version are written as ever
+        pi, qi, (ki, vi), li = setup(dv)
+        dv.kv_append(pi, ki, vi, li)
+        dv.paged_attention(pi, qi, li + 1)
