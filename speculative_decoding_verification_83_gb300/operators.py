@@ -69,6 +69,17 @@ def _raw_stream(stream, device) -> int:
     return _modules[0]._C._cuda_getCurrentRawStream(device.index)
 
 
+def _call(device, function, *args):
+    """A call of the library, which launches on the thread's current device: the
+    tensors' is made that for the call, if it is not."""
+    cuda = _modules[0].cuda
+    if cuda.current_device() == device.index:
+        _check(function(*args))
+    else:
+        with cuda.device(device):
+            _check(function(*args))
+
+
 def _token_dtype(t, cache, what) -> int:
     torch = _torch()
     dt = t.dtype
@@ -262,9 +273,9 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
             raise ValueError("phases must be one-dimensional")
         rot = 2 * phases.shape[0]
         phases = _vector(phases, phases.shape[0], "phases", torch.int64, dev)
-    _check(_library().dflash_kv_append(cache._ref, pk, pv, pq, po, dt, n, hq, _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens,
-                                   starts, phases, rot, 1 if interleaved else 0, _status_word(status, dev),
-                                   _raw_stream(stream, dev)))
+    _call(dev, _library().dflash_kv_append, cache._ref, pk, pv, pq, po, dt, n, hq,
+          _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens, starts, phases, rot, 1 if interleaved else 0,
+          _status_word(status, dev), _raw_stream(stream, dev))
     _written(cache.k, cache.v, None if new_q else q_out)
     return q_out
 
@@ -312,9 +323,9 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     else:
         _on(dev, workspace=workspace)
         ws, ws_bytes = _dev(workspace, "workspace", torch.uint8), workspace.numel()
-    _check(_library().dflash_paged_attention(
-        cache._ref, pq, po, pl, dt, n, hq, _pack4(qt, qh, ot, oh), lens, starts, D ** -0.5 if scale is None else scale,
-        1 if causal else 0, ws, ws_bytes, _status_word(status, dev), _raw_stream(stream, dev)))
+    _call(dev, _library().dflash_paged_attention, cache._ref, pq, po, pl, dt, n, hq, _pack4(qt, qh, ot, oh), lens,
+          starts, D ** -0.5 if scale is None else scale, 1 if causal else 0, ws, ws_bytes, _status_word(status, dev),
+          _raw_stream(stream, dev))
     _written(*given)
     return (out, lse) if return_lse else out
 
@@ -359,8 +370,8 @@ def _loss(student, ids, teacher, temperature, row_weight, status, keep):
     dev = student.device
     loss = torch.empty((head[2],), dtype=torch.float32, device=dev)
     stats = torch.empty((head[2], 2), dtype=torch.float32, device=dev) if keep else None
-    _check(_library().dflash_distill_loss(*head, temperature, w, loss.data_ptr(), stats.data_ptr() if keep else None,
-                                      _status_word(status, dev), _raw_stream(None, dev)))
+    _call(dev, _library().dflash_distill_loss, *head, temperature, w, loss.data_ptr(),
+          stats.data_ptr() if keep else None, _status_word(status, dev), _raw_stream(None, dev))
     return loss, stats
 
 
@@ -394,8 +405,8 @@ def _distill_function():
             head, w = _distill_args(student, ids, teacher, row_weight)
             dev = student.device
             grad = torch.empty(student.shape, dtype=student.dtype, device=dev)
-            _check(_library().dflash_distill_grad(*head, ctx.temperature, w, stats.data_ptr(), upstream.data_ptr(),
-                                              upstream.stride(0), grad.data_ptr(), head[3], _raw_stream(None, dev)))
+            _call(dev, _library().dflash_distill_grad, *head, ctx.temperature, w, stats.data_ptr(),
+                  upstream.data_ptr(), upstream.stride(0), grad.data_ptr(), head[3], _raw_stream(None, dev))
             return grad, None, None, None, None, None
 
     _function = DistillLoss
@@ -438,8 +449,8 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
             raise ValueError("grad must have the student's dtype and contiguous rows")
         if N <= 1:
             gs = max(gs, V)
-    _check(_library().dflash_distill_loss_grad(*head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
-                                           _status_word(status, dev), _raw_stream(stream, dev)))
+    _call(dev, _library().dflash_distill_loss_grad, *head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
+          _status_word(status, dev), _raw_stream(stream, dev))
     _written(given)
     return loss, grad
 
