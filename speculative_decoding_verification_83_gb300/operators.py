@@ -7,7 +7,9 @@ drafter's training: ``distill_loss`` (autograd) and ``distill_loss_grad``, the
 divergence from the target's top logits and its gradient.
 
 Argument marshalling only, as in the rest of the binding: the work is done by
-the kernels behind ``include/dflash_verify.h``.
+the kernels behind ``include/dflash_verify.h``. A call with ``stream`` runs
+there: the caller orders it after what made its inputs (``wait_stream``), what it
+returns belongs to that stream, and its inputs may be let go of at once.
 """
 from __future__ import annotations
 
@@ -161,6 +163,15 @@ def _carries_no_gradient(cache, **tensors):
             raise ValueError(f"{name} has no gradient here: detach it, or call under torch.no_grad()")
 
 
+def _used_on(stream, *tensors):
+    """Tensors that a call on a stream of its own reads or writes: torch hands
+    their memory out again only once that stream is past the call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _written(*tensors):
     """Tells torch which of the caller's tensors a call has written over: a
     backward pass that kept one of them then fails instead of reading it."""
@@ -198,6 +209,7 @@ class PagedCache:
                 _shape(t, (k.shape[1],), name)
                 _dev(t, name, torch.float32)
         self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
+        self.tensors = k, v, page_table, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.batch, self.max_pages = page_table.shape
         self.device, self.dtype = k.device, k.dtype
@@ -256,7 +268,7 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     pv, vt, vh = _rows(v, "v", cache.heads, D, dev, k)
     n = k.shape[0]
     pq = po = None
-    new_q = q_out is None
+    new_q, phase_table = q_out is None, phases
     hq = qt = qh = ot = oh = 0
     if q is not None:
         pq, qt, qh = _rows(q, "q", None, D, dev, k)
@@ -276,6 +288,7 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
     _call(dev, _library().dflash_kv_append, cache._ref, pk, pv, pq, po, dt, n, hq,
           _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens, starts, phases, rot, 1 if interleaved else 0,
           _status_word(status, dev), _raw_stream(stream, dev))
+    _used_on(stream, *cache.tensors, k, v, q, None if new_q else q_out, cached_lens, q_start, phase_table, status)
     _written(cache.k, cache.v, None if new_q else q_out)
     return q_out
 
@@ -317,6 +330,7 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
         lse = _empty((n, hq), torch.float32, dev, stream)
         pl = lse.data_ptr()
     lens, starts = _packed(cache, n, kv_lens, "kv_lens", q_start)
+    given_workspace = workspace
     if workspace is None:
         workspace = _empty((cache._ws_bytes,), torch.uint8, dev, stream)
         ws, ws_bytes = workspace.data_ptr(), cache._ws_bytes
@@ -326,6 +340,7 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     _call(dev, _library().dflash_paged_attention, cache._ref, pq, po, pl, dt, n, hq, _pack4(qt, qh, ot, oh), lens,
           starts, D ** -0.5 if scale is None else scale, 1 if causal else 0, ws, ws_bytes, _status_word(status, dev),
           _raw_stream(stream, dev))
+    _used_on(stream, *cache.tensors, q, *given, kv_lens, q_start, given_workspace, status)
     _written(*given)
     return (out, lse) if return_lse else out
 
@@ -451,6 +466,7 @@ def distill_loss_grad(student, teacher_ids, teacher_logits, temperature: float =
             gs = max(gs, V)
     _call(dev, _library().dflash_distill_loss_grad, *head, float(temperature), w, loss.data_ptr(), grad.data_ptr(), gs,
           _status_word(status, dev), _raw_stream(stream, dev))
+    _used_on(stream, student, teacher_ids, teacher_logits, row_weight, given, status)
     _written(given)
     return loss, grad
 

@@ -93,3 +93,28 @@ def test_tensors_written_in_place_are_known_to_autograd(dv):
         pi, qi, (ki, vi), li = setup(dv)
         dv.kv_append(pi, ki, vi, li)
         dv.paged_attention(pi, qi, li + 1)
+
+
+def test_inputs_outlive_a_call_on_another_stream(dv):
+    """A call on another stream still reads its inputs when Python has let go of
+    them: their memory is not handed out before."""
+    pc, q, (k, v), ln = setup(dv, B=64, Hq=64, H=8, D=128)
+    want = dv.paged_attention(pc, q, ln)
+    s = torch.cuda.Stream()
+    z = torch.randn((64, 20000), device=DEV)
+    ids = torch.randint(0, 20000, (64, 8), device=DEV, dtype=torch.int32)
+    t = torch.randn((64, 8), device=DEV)
+    wl, wg = dv.distill_loss_grad(z, ids, t)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        q1, z1 = q.clone(), z.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)  # the calls wait in the stream for about 10 ms
+        got = dv.paged_attention(pc, q1, ln, stream=s)
+        loss, grad = dv.distill_loss_grad(z1, ids, t, stream=s)
+        del q1, z1
+        over = [torch.full_like(q, 3.0), torch.full_like(z, 3.0)]  # at once in the freed memory, were it free
+        s.synchronize()
+        assert torch.equal(got, want) and torch.equal(loss, wl) and torch.equal(grad, wg)
+        del over
