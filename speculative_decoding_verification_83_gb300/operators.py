@@ -199,7 +199,8 @@ class PagedCache:
         steps = [[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)] for t in (k, v)]
         if steps[0] != steps[1] or k.stride(3) != 1 or v.stride(3) != 1:
             raise ValueError("k and v must have the same strides, the last dimension contiguous")
-        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 \
+                or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
             raise ValueError("page_table must be int32 [batch, max_pages] with contiguous rows")
         _on(k.device, page_table=page_table, k_scale=k_scale, v_scale=v_scale)
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):

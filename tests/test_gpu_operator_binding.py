@@ -118,3 +118,13 @@ def test_inputs_outlive_a_call_on_another_stream(dv):
         s.synchronize()
         assert torch.equal(got, want) and torch.equal(loss, wl) and torch.equal(grad, wg)
         del over
+
+
+def test_tables_of_one_column(dv):
+    """Extents of one in a page table are never stepped over."""
+    pc, q, (k, v), ln = setup(dv, pages=1)
+    ln = torch.full((2,), 9, dtype=torch.int32, device=DEV)
+    want = dv.paged_attention(pc, q, ln)
+    column = torch.stack([pc.page_table[:, 0]] * 3).t()[:, :1]
+    assert column.stride(1) != 1 and column.shape == (2, 1)
+    assert torch.equal(dv.paged_attention(dv.PagedCache(pc.k, pc.v, column), q, ln), want)
