@@ -96,9 +96,10 @@ def _token_dtype(t, cache, what) -> int:
     return code
 
 
-def _rows(t, name, heads, dim, device, like=None):
+def _rows(t, name, heads, dim, device, like=None, written=False):
     """Data pointer, token stride and head stride of a [tokens, heads, dim] view
-    whose last dimension is contiguous."""
+    whose last dimension is contiguous (and, where it is written, whose rows are
+    places of their own)."""
     shape = t.shape
     if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have shape [tokens, {'heads' if heads is None else heads}, {dim}], "
@@ -110,6 +111,8 @@ def _rows(t, name, heads, dim, device, like=None):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if like is not None and (t.dtype != like.dtype or shape[0] != like.shape[0]):
         raise ValueError(f"{name} must match the tokens' dtype and count")
+    if written and (ts < dim and shape[0] > 1 or hs < dim and shape[1] > 1):
+        raise ValueError(f"{name}: rows that are written must not share memory")
     # an extent of one is never stepped over, whatever its stride says
     return t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
 
@@ -276,7 +279,7 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
         hq = q.shape[1]
         if q_out is None:
             q_out = _empty((n, hq, D), q.dtype, dev, stream)
-        po, ot, oh = _rows(q_out, "q_out", hq, D, dev, q)
+        po, ot, oh = _rows(q_out, "q_out", hq, D, dev, q, True)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     lens, starts = _packed(cache, n, cached_lens, "cached_lens", q_start)
@@ -320,7 +323,7 @@ def paged_attention(cache: PagedCache, q, kv_lens, q_start=None, scale=None, cau
     given_out = out is not None
     if not given_out:
         out = _empty((n, hq, D), q.dtype, dev, stream)
-    po, ot, oh = _rows(out, "out", hq, D, dev, q)
+    po, ot, oh = _rows(out, "out", hq, D, dev, q, True)
     pl = None
     given = out if given_out else None, lse
     if lse is not None:

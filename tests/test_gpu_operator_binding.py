@@ -128,3 +128,16 @@ def test_tables_of_one_column(dv):
     column = torch.stack([pc.page_table[:, 0]] * 3).t()[:, :1]
     assert column.stride(1) != 1 and column.shape == (2, 1)
     assert torch.equal(dv.paged_attention(dv.PagedCache(pc.k, pc.v, column), q, ln), want)
+
+
+def test_outputs_whose_rows_share_memory_are_refused(dv):
+    """As torch's own operations refuse them: which row's result stays would be
+    left to chance."""
+    pc, q, (k, v), ln = setup(dv)
+    for shared in (torch.zeros((1, 4, 64), dtype=BF, device=DEV).expand(2, 4, 64),
+                   torch.zeros((2, 1, 64), dtype=BF, device=DEV).expand(2, 4, 64),
+                   torch.zeros(1000, dtype=BF, device=DEV).as_strided((2, 4, 64), (256, 32, 1))):
+        with pytest.raises(ValueError, match="share memory"):
+            dv.paged_attention(pc, q, ln, out=shared)
+        with pytest.raises(ValueError, match="share memory"):
+            dv.kv_append(pc, k, v, ln, q=q, q_out=shared)
