@@ -248,6 +248,8 @@ def rope_phases(inv_freq, device=None):
 
 def _packed(cache, n_tokens, lens, lens_name, q_start):
     torch = _torch()
+    if cache.batch == 0:
+        raise DFlashError(ERR_INVALID_ARG, "batch=0: the page table has no requests")
     if q_start is None and n_tokens % cache.batch:
         raise ValueError(f"{n_tokens} tokens do not divide evenly over {cache.batch} requests: q_start is needed")
     return (_vector(lens, cache.batch, lens_name, torch.int32, cache.device),

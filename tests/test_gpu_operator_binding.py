@@ -141,3 +141,11 @@ def test_outputs_whose_rows_share_memory_are_refused(dv):
             dv.paged_attention(pc, q, ln, out=shared)
         with pytest.raises(ValueError, match="share memory"):
             dv.kv_append(pc, k, v, ln, q=q, q_out=shared)
+
+
+def test_a_cache_without_requests_is_refused(dv):
+    pc, q, (k, v), ln = setup(dv)
+    none = dv.PagedCache(pc.k, pc.v, pc.page_table[:0])
+    for call in (lambda: dv.paged_attention(none, q, ln[:0]), lambda: dv.kv_append(none, k, v, ln[:0])):
+        with pytest.raises(dv.DFlashError, match="batch=0"):
+            call()
