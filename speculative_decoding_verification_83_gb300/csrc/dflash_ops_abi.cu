@@ -161,6 +161,10 @@ int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void*
   if ((q == nullptr) != (q_out == nullptr))
     return fail(DFLASH_ERR_INVALID_ARG, "q and q_out are given together or not at all");
   if (q && q_heads < 1) return fail(DFLASH_ERR_INVALID_ARG, "q_heads=%d must be positive", q_heads);
+  // pieces of 16 values of a token's heads: a grid's second extent times a block's
+  if ((2LL * cache->kv_heads + (q ? q_heads : 0)) * (cache->head_dim / 16) > 65535LL * 256)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%d query and %d key/value heads of %d are more than a token may have",
+                q ? q_heads : 0, cache->kv_heads, cache->head_dim);
   if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16)
     return fail(DFLASH_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16 in [0, head_dim=%d]", rot_dim,
                 cache->head_dim);
