@@ -117,6 +117,9 @@ __device__ __forceinline__ bool drop_not_finite(uint32_t& w) {
   return found;
 }
 
+__device__ __forceinline__ void note(int* first, int key) {
+  if (key < *first) atomicMin(first, key);  // (a cache of nothing else meets the atomic rarely)
+}
 // first[c * D + d]: the first key of [k0, k1) of request b and head h whose value
 // d is +inf (c = 0), -inf (1) or NaN (2). `threads` threads share the work.
 template <class T, bool kF8, int D>
@@ -151,13 +154,13 @@ __device__ __noinline__ void find_not_finite(const AttnParams& p, int b, int h, 
       for (int e = 0; e < 4; ++e) {
         if (kF8) {
           for (int k = 0; k < 4; ++k)
-            if (((word[e] >> (8 * k)) & 0x7fu) == 0x7fu) atomicMin(first + 2 * D + 16 * c + 4 * e + k, key[j]);
+            if (((word[e] >> (8 * k)) & 0x7fu) == 0x7fu) note(first + 2 * D + 16 * c + 4 * e + k, key[j]);
         } else if (word_not_finite<T>(word[e])) {
           const float2 f = T::unpack(word[e]);
           const float v[2] = {f.x, f.y};
           for (int k = 0; k < 2; ++k)
             if (!(fabsf(v[k]) < INFINITY))
-              atomicMin(first + (v[k] > 0.0f ? 0 : v[k] < 0.0f ? 1 : 2) * D + 8 * c + 2 * e + k, key[j]);
+              note(first + (v[k] > 0.0f ? 0 : v[k] < 0.0f ? 1 : 2) * D + 8 * c + 2 * e + k, key[j]);
         }
       }
     }
