@@ -37,6 +37,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "dflash_paged.cuh"
 
@@ -299,12 +300,13 @@ struct Writer {
   __device__ __forceinline__ Writer(const unsigned char* z, unsigned char* g, int head, float c, const Student& q, float f)
       : c2(pair_of(c, c)), n2(pair_of(-q.shift, -q.shift)), a2(pair_of(q.add, q.add)), f2(pair_of(f, f)), body(g + (size_t)head * T::kBytes),
         aligned((((uintptr_t)z ^ (uintptr_t)g) & 15) == 0) {}
+  template <bool kShifted>
   __device__ __forceinline__ void put(int v, const uint4& u) const {
     unsigned long long x[T::kPer / 2];
     T::unpack(u, x);
 #pragma unroll
     for (int i = 0; i < T::kPer / 2; ++i) {
-      const float2 e = floats_of(fma2(add2(x[i], n2), c2, a2));
+      const float2 e = floats_of(fma2(kShifted ? add2(x[i], n2) : x[i], c2, a2));
       x[i] = mul2(pair_of(ex2d(e.x), ex2d(e.y)), f2);
     }
     if (aligned) {
@@ -422,22 +424,22 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
   if (warp == kW) {
     teacher_row<T>(p, r, z, rank == 0 && w != 0.0f, c, S);
   } else {
-  bool ok = true;
-  const uint4 low = T::kBytes == 2 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
-                                   : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);  // -inf
-  for (int i = 0; i < kPieces; ++i) {
-    const int at = min(n_held, i * piece), end = min(n_held, at + piece);
-    if (end <= at) break;
-    ok &= mbar_wait_landed(&landed[i], 0);
-    for (int v = at + tid; v < end; v += 2 * kThreads)
-      take<T>(a, mine[v], v + kThreads < end ? mine[v + kThreads] : low, c, c2);
-  }
-  for (int v = L.v0 + n_held + tid; v < L.v1; v += 2 * kThreads)
-    take<T>(a, body[v], v + kThreads < L.v1 ? body[v + kThreads] : low, c, c2);
-  if (L.edge >= 0) take_one(a, at_edge, c);
-  if (!ok) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
-  a = warp_join(a, c);
-  if (lane == 0) parts[warp] = a;
+    bool ok = true;
+    const uint4 low = T::kBytes == 2 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
+                                     : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);  // -inf
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = min(n_held, i * piece), end = min(n_held, at + piece);
+      if (end <= at) break;
+      ok &= mbar_wait_landed(&landed[i], 0);
+      for (int v = at + tid; v < end; v += 2 * kThreads)
+        take<T>(a, mine[v], v + kThreads < end ? mine[v + kThreads] : low, c, c2);
+    }
+    for (int v = L.v0 + n_held + tid; v < L.v1; v += 2 * kThreads)
+      take<T>(a, body[v], v + kThreads < L.v1 ? body[v + kThreads] : low, c, c2);
+    if (L.edge >= 0) take_one(a, at_edge, c);
+    if (!ok) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
+    a = warp_join(a, c);
+    if (lane == 0) parts[warp] = a;
   }
   __syncwarp();
   parts_ready<kThreads + 32>(warp == 0 || split == 1);
@@ -481,9 +483,15 @@ __global__ void __launch_bounds__(kThreads + 32, 1152 / (kThreads + 32))
     const Student q = student_of(a, c);
     const float coef = w * p.inv_t, f = coef / q.s;
     const Writer<T> out(z, g, L.head, c, q, f);
+    auto write = [&](auto shifted) {
+      for (int v = tid; v < n_held; v += kThreads) out.template put<decltype(shifted)::value>(L.v0 + v, mine[v]);
+      for (int v = L.v0 + n_held + tid; v < L.v1; v += kThreads) out.template put<decltype(shifted)::value>(v, body[v]);
+    };
     if (warp < kW) {
-      for (int v = tid; v < n_held; v += kThreads) out.put(L.v0 + v, mine[v]);
-      for (int v = L.v0 + n_held + tid; v < L.v1; v += kThreads) out.put(v, body[v]);
+      if (__builtin_expect(q.shift != 0.0f, 0))
+        write(std::true_type());
+      else
+        write(std::false_type());
     }
     if (L.edge >= 0) T::store(g + (size_t)L.edge * T::kBytes, ex2d(fmaf(at_edge - q.shift, c, q.add)) * f);
     __syncthreads();  // the slice is written
@@ -525,16 +533,22 @@ __global__ void __launch_bounds__(kGradThreads + 32) grad_kernel(const DistillPa
   if (g == z) __syncthreads();  // in place: the teacher's logits are read before they are written over
   const float coef = w * p.inv_t, f = coef / q.s;
   const Writer<T> out(z, g, L.head, c, q, f);
-  for (int v = L.v0 + tid; v < L.v1 && tid < kGradThreads; v += kGradHeld * kGradThreads) {
+  auto write = [&](auto shifted) {
+    for (int v = L.v0 + tid; v < L.v1 && tid < kGradThreads; v += kGradHeld * kGradThreads) {
 #pragma unroll
-    for (int i = 0; i < kGradHeld; ++i)
-      if (v + i * kGradThreads < L.v1) out.put(v + i * kGradThreads, u[i]);
+      for (int i = 0; i < kGradHeld; ++i)
+        if (v + i * kGradThreads < L.v1) out.template put<decltype(shifted)::value>(v + i * kGradThreads, u[i]);
 #pragma unroll
-    for (int i = 0; i < kGradHeld; ++i) {
-      const int n = v + (kGradHeld + i) * kGradThreads;
-      if (n < L.v1) u[i] = body[n];
+      for (int i = 0; i < kGradHeld; ++i) {
+        const int n = v + (kGradHeld + i) * kGradThreads;
+        if (n < L.v1) u[i] = body[n];
+      }
     }
-  }
+  };
+  if (__builtin_expect(q.shift != 0.0f, 0))
+    write(std::true_type());
+  else
+    write(std::false_type());
   if (L.edge >= 0) T::store(g + (size_t)L.edge * T::kBytes, ex2d(fmaf(at_edge - q.shift, c, q.add)) * f);
   __syncthreads();  // the slice is written
   teacher_gradient<T>(p, S, g, L.lo, L.hi, c, q, coef);
