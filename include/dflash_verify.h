@@ -432,8 +432,12 @@ int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void*
  * of n sees the first kv_len - n + i + 1 positions (the target's
  * verification); otherwise every one (a drafter that attends over its whole
  * block). Keys a row does not see take no part, whatever they hold; a row
- * that sees none gives 0 and -inf. strides: q's token and head stride, then
- * out's.
+ * that sees none gives 0 and -inf. A value that is not finite decides its column
+ * of the rows that see it, at any weight (infinities of both signs: NaN).
+ * Weights relative to a row's largest are rounded to 16 bits for the product
+ * with the values: the tokens' type, or f16 for an 8-bit cache in the kernel for
+ * few rows (up to 32 that share a head, or head_dim 256). strides: q's token and
+ * head stride, then out's.
  * workspace [device], 256-byte aligned, of dflash_attention_workspace_bytes();
  * it needs no preparation, and calls that share one must be ordered. The
  * result does not depend on how the GPU schedules the work. */
@@ -456,9 +460,10 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const void* q, void*
  * [device] float [rows, K], 1 <= K <= 256, row_weight [device] float [rows] or
  * NULL (1). Entries with id -1 take no part; other ids outside [0, V) neither
  * (DFLASH_STATUS_BAD_TOKEN). A row without entries, or of weight 0, has loss
- * and gradient 0 whatever its logits. A row with a NaN, or whose largest
- * student logit or used teacher logit is infinite, gives NaN
- * (DFLASH_STATUS_BAD_ROW). Ids may repeat.
+ * and gradient 0 whatever its logits; a row whose used teacher logits are all
+ * -inf is one without entries. A row with a NaN, without a student logit above
+ * -inf, or with one or a used teacher logit of +inf, gives NaN
+ * (DFLASH_STATUS_BAD_ROW). Ids may repeat. 1 / (T ln 2) must be finite.
  *
  * dflash_distill_loss: loss [rows] and, where row_stats ([device] float
  * [rows, 2]) is given, each row's reference R and sum s of 2^(z / (T ln 2) -
@@ -471,8 +476,8 @@ int dflash_distill_loss(const void* student, int64_t row_stride, int rows, int V
 
 /* The gradient for an upstream gradient of the losses ([device] float [rows],
  * upstream_stride elements apart, 0 for one that all rows share; NULL: 1):
- * grad [rows, V] in the student's type, rows grad_stride elements apart. grad may be student itself (same stride). A row whose upstream
- * gradient is 0 gives 0. */
+ * grad [rows, V] in the student's type, rows grad_stride elements apart. grad may
+ * be student itself (same stride). A row whose upstream gradient is 0 gives 0. */
 int dflash_distill_grad(const void* student, int64_t row_stride, int rows, int V, int dtype,
                         const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
                         const float* row_weight, const float* row_stats, const float* upstream,

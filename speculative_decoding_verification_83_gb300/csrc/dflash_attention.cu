@@ -12,8 +12,9 @@
 // share its head, 2 n G flops per byte of a 16-bit cache, so the reads of the
 // cache bound it until n G nears 100 rows. Design:
 //  * Work is a list of units (request, head, 16 query rows), each a run of
-//    64-key tiles (128 where a row of the cache has 128 bytes or less); the list's tiles are dealt out in equal contiguous runs,
-//    one per CTA, whatever the requests' lengths. A unit that spans CTAs
+//    64-key tiles (128 where a row of the cache has 128 bytes or less); the list's
+//    tiles are dealt out in equal contiguous runs, one per CTA, whatever the
+//    requests' lengths. A unit that spans CTAs
 //    leaves unnormalised partial results (fp32 sum, maximum, sum of weights)
 //    in the workspace, which a second kernel joins in a fixed order: the
 //    results do not depend on timing.
@@ -33,10 +34,12 @@
 // TB/s, 92% of a copy's rate; three CTAs an SM with two ring stages each beat
 // two with three (206 us). A step's overhead (page indexes, maxima, the rescaling
 // vote) is per warp, so rows of 128 bytes take 32 keys a step: head_dim 64 (twice
-// the positions) 204 against 274 us with 16, e4m3 at head_dim 128 (two requests of
-// 200001 positions) 144 us, 5.7 TB/s, against 164 us. There, and more so for e4m3
-// at head_dim 64 (193 us for 92 us of bytes), the warps' chain of widening,
-// products and softmax bounds it. Copies of K and V in groups of their own, each
+// the positions) 196 against 274 us with 16, e4m3 at head_dim 128 (two requests of
+// 200001 positions) 145 us, 5.6 TB/s, against 164 us. There, and more so for e4m3
+// at head_dim 64 (131 us for 92 us of bytes), the warps' chain of widening,
+// products and softmax bounds it. At head_dim 256 O alone takes 128 registers a
+// thread, which leaves 4 warps an SM (e4m3: 8): 264 us for 181 us of bytes (64
+// requests of up to 4096 positions), e4m3 285 us for 192 (8192). Copies of K and V in groups of their own, each
 // reissued as its half of the stage is read, were slower (217 us): twice the waits
 // and shuffles.
 // Rounding: P is rounded to the operands' type (half a step of its own
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kAttnThreads, Shape<kF8, D>::kPerSm) attention
   }
   if (t_begin >= t_end) return;
 
-  // ---- this warp's ring: one step = this warp's 16 keys of a tile
+  // ---- this warp's ring: one step = this warp's kWarpKeys keys of a tile
   const uint32_t my_ring = smem_addr(ring) + warp * 2 * S::kHalfStage;
   __shared__ uint32_t step_mask[kWarps][8];  // per stage: the keys that exist and have a page
 

@@ -1,7 +1,7 @@
 // dflash_attention_tc.cu -- attention over the paged cache for blocks whose
 // query rows (new tokens x heads that share a key/value head) number more than
-// 16 (8-bit caches: 32): the products run on the 5th-generation tensor cores, with scores,
-// weights and sums in tensor memory.
+// 16 (8-bit caches: 32): the products run on the 5th-generation tensor cores, with
+// scores, weights and sums in tensor memory.
 //
 // Mathematics and work list as in dflash_attention.cu; here a unit has R = 32,
 // 64 or 128 query rows and a tile kKeys = 128 keys (64 for head_dim 256).
@@ -34,13 +34,13 @@
 // so the list of work counts it. 8-bit caches (head_dim 64 and 128) go through a
 // ring of raw tiles and are widened, exactly, into the operand tiles, by 8 warps.
 // Measured on one GB300, 64 query and 8 key/value heads of 128, 32 requests of up
-// to 16384 positions, blocks of 8 (64 rows a head), bf16: 218 us, 5.7 TB/s of keys
-// and values, 85% of a copy's rate, against 696 us by the warps' products, which
-// read the cache four times there; blocks of 4 (32 rows) 199 us, 6.25 TB/s. What
+// to 16384 positions, blocks of 8 (64 rows a head), bf16: 219 us, 5.5 TB/s of keys
+// and values, 82% of a copy's rate, against 696 us by the warps' products, which
+// read the cache four times there; blocks of 4 (32 rows) 197 us, 6.1 TB/s. What
 // is left is the units' ends and uneven runs. At 128 rows (half the positions:
-// 152 us, 4.2 TB/s, 520 TFLOP/s) and head_dim 64 (148 us, 4.2 TB/s) the softmax's
-// 128 threads bound it; at head_dim 256 (266 us, 4.7 TB/s) two stages are few for
-// the latency of a load; e4m3 (294 us for half the bytes) has two operand stages, and
+// 150 us, 4.1 TB/s, 520 TFLOP/s) and head_dim 64 (150 us, 4.0 TB/s) the softmax's
+// 128 threads bound it; at head_dim 256 (266 us, 4.5 TB/s) two stages are few for
+// the latency of a load; e4m3 (297 us for half the bytes) has two operand stages, and
 // waits for the widening between a load and its products.
 // Every wait is bounded; a CTA that gives up raises DFLASH_STATUS_TIMEOUT,
 // lets its copies land and frees its tensor memory.

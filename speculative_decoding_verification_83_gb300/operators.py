@@ -9,7 +9,10 @@ divergence from the target's top logits and its gradient.
 Argument marshalling only, as in the rest of the binding: the work is done by
 the kernels behind ``include/dflash_verify.h``. A call with ``stream`` runs
 there: the caller orders it after what made its inputs (``wait_stream``), what it
-returns belongs to that stream, and its inputs may be let go of at once.
+returns belongs to that stream, and its inputs may be let go of at once. Bad
+pages, lengths and rows, and waits on the GPU that gave up (STATUS_TIMEOUT: the
+outputs are unspecified), are reported in ``status``, an int32 word on the
+device, and nowhere else.
 """
 from __future__ import annotations
 
@@ -438,9 +441,11 @@ def distill_loss(student, teacher_ids, teacher_logits, temperature: float = 1.0,
     """dflash_distill_loss: per row the divergence of softmax(student / T) over
     the whole vocabulary from the teacher's softmax over its top logits, times
     ``row_weight``. ``student`` [rows, V] bf16 or fp32; ``teacher_ids`` int32 and
-    ``teacher_logits`` fp32 [rows, K], id -1 for an empty entry. Returns the
-    losses [rows] fp32, differentiable in ``student``. Runs on the current
-    stream."""
+    ``teacher_logits`` fp32 [rows, K], id -1 for an empty entry; a row whose used
+    teacher logits are all -inf counts as one without entries. Returns the losses
+    [rows] fp32, differentiable in ``student``. Runs on the current stream. A
+    backward pass may be captured into a graph once no eager graph of the same
+    leaves is alive."""
     _no_grad_inputs(teacher_logits, row_weight)
     if not (student.requires_grad and _torch().is_grad_enabled()):
         return _loss(student, teacher_ids, teacher_logits, float(temperature), row_weight, status, False)[0]
