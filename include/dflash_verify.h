@@ -424,6 +424,17 @@ int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void*
                      const int32_t* q_start, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,
                      void* stream);
 
+/* dflash_kv_append with norms: before the rotation each key and query head x
+ * becomes x w / sqrt(mean x^2 + eps) over its head_dim values, in fp32 (squares
+ * that leave fp32's range make the head 0 or NaN), with one rounding behind the
+ * rotation. q_weight and k_weight [device] [head_dim], in the tokens' dtype or
+ * DFLASH_F32 (weight_dtype), NULL: 1. eps: finite, not negative. */
+int dflash_kv_append_norm(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out,
+                          int dtype, int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens,
+                          const int32_t* q_start, const void* q_weight, const void* k_weight, int weight_dtype,
+                          float eps, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,
+                          void* stream);
+
 /* Attention of the new tokens over the cache, which already holds them:
  * kv_lens [device] int32 [batch] counts every position, the new tokens last.
  * Query head h reads key/value head h / (q_heads / kv_heads). out [tokens,
@@ -489,6 +500,98 @@ int dflash_distill_loss_grad(const void* student, int64_t row_stride, int rows, 
                              const int32_t* teacher_ids, const float* teacher_logits, int K, float temperature,
                              const float* row_weight, float* loss, void* grad, int64_t grad_stride, uint32_t* status,
                              void* stream);
+
+/* ---- training a drafter: norms with rotation ------------------------------------------------
+ * Layers whose queries and keys are normed head by head before their rotation, for
+ * whole batches and with gradients (dflash_kv_append_norm is the same on the way
+ * into a cache).
+ * For each head x of q [tokens, q_heads, head_dim] and k [tokens, k_heads,
+ * head_dim] (bf16 or f16): y = R(n) (x w / sqrt(mean x^2 + eps)), R the rotation of
+ * dflash_kv_append by the token's position n = positions[token] ([device] int32,
+ * any sign), all in fp32, rounded once. 0 heads: that array is left out.
+ * head_dim 64, 128 or 256; weights as for dflash_kv_append_norm; rot_dim a
+ * multiple of 16, 0 for no rotation. strides [host]: token and head stride of q,
+ * k, q_out, k_out, in elements, multiples of 16 bytes. q_out may be q, k_out k. */
+int dflash_norm_rotate(const void* q, const void* k, void* q_out, void* k_out, int dtype, int tokens, int q_heads,
+                       int k_heads, int head_dim, const int64_t* strides, const void* q_weight, const void* k_weight,
+                       int weight_dtype, float eps, const int32_t* positions, const uint64_t* phases, int rot_dim,
+                       int interleaved, void* stream);
+
+/* Its gradients: dq and dk from dq_out and dk_out, and (where given) the weights'
+ * gradients, summed over tokens and heads in fp32 in a fixed order, in
+ * weight_dtype. strides: q, k, dq_out, dk_out, dq, dk. dq may be dq_out, dk
+ * dk_out. workspace [device], 256-byte aligned, needs no preparation. */
+size_t dflash_norm_workspace_bytes(int head_dim);
+int dflash_norm_rotate_grad(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                            int dtype, int tokens, int q_heads, int k_heads, int head_dim, const int64_t* strides,
+                            const void* q_weight, const void* k_weight, void* dq_weight, void* dk_weight, int weight_dtype,
+                            float eps, const int32_t* positions, const uint64_t* phases, int rot_dim, int interleaved,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- attention over packed sequences ----------------------------------------------------------
+ * Prompts, and the sequences a drafter is trained on, without a cache. Sequence
+ * b's queries are rows q_start[b] .. q_start[b + 1] - 1 of q and out [q_tokens,
+ * q_heads, head_dim], its keys and values rows kv_start[b] .. of k and v
+ * [kv_tokens, kv_heads, head_dim] ([device] int32 [batch + 1]; kv_start may be
+ * q_start). out = softmax(scale q k^T) v over the keys a row sees, lse
+ * ([device] float [q_tokens, q_heads], contiguous, or NULL) = log sum e^(scale q k).
+ * causal: query i of n sees the first m - n + i + 1 of m keys; otherwise all.
+ * A row that sees none gives 0 and -inf. What a row does not see takes no part,
+ * whatever it holds; a value that is not finite decides its column of the rows
+ * that see it, at any weight (infinities of both signs: NaN). Rows of no sequence are left
+ * as they are, or with `fill` set to 0 (lse: -inf). Offsets that leave the arrays
+ * or do not ascend are clamped (DFLASH_STATUS_BAD_LENGTH; the outputs are
+ * unspecified). bf16 or f16, head_dim 64 or 128, batch <= 2048, tokens <= 2^24,
+ * q_heads <= 1024. strides [host]: token and head stride of q, k, v, out, in elements,
+ * multiples of 16 bytes, the last dimension contiguous. workspace [device],
+ * 256-byte aligned, needs no preparation; calls that share one must be
+ * ordered. The results do not depend on how the GPU schedules the work. */
+typedef struct dflash_packed_batch {
+  const int32_t* q_start;  /* [device] [batch + 1] */
+  const int32_t* kv_start; /* [device] [batch + 1] */
+  int32_t batch, q_tokens, kv_tokens, q_heads, kv_heads, head_dim, dtype, causal;
+  float scale;
+} dflash_packed_batch;
+size_t dflash_packed_workspace_bytes(const dflash_packed_batch* batch, int backward);
+int dflash_packed_attention(const dflash_packed_batch* batch, const void* q, const void* k, const void* v, void* out,
+                            const int64_t* strides, float* lse, int fill, void* workspace, size_t workspace_bytes,
+                            uint32_t* status, void* stream);
+
+/* Its gradients for dout, from the forward call's out and lse (bf16 only). Heads
+ * that share a key add up. strides: q, k, v, out, dout, dq, dk, dv. */
+int dflash_packed_attention_grad(const dflash_packed_batch* batch, const void* q, const void* k, const void* v,
+                                 const void* out, const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                                 const int64_t* strides, int fill, void* workspace, size_t workspace_bytes,
+                                 uint32_t* status, void* stream);
+
+/* ---- cross entropy through the vocabulary projection --------------------------------------------
+ * A drafter's training on the target's tokens (or any labels): per row
+ *   loss = w (log sum_v e^(z_v) - z_label), z = h W^T,
+ * for hidden states h [rows, K] and the projection W [V, K] of
+ * dflash_lmhead_logits (bf16, rows h_stride and w_stride elements apart, multiples
+ * of 16 bytes, 16-byte aligned), labels [device] int32 [rows], row_weight
+ * [device] float [rows] or NULL (1). The logits are never stored as a whole. K:
+ * a multiple of 8 up to 2^16; rows <= 2^20, V <= 2^24. A row with label -1 or of weight 0
+ * takes no part (loss and gradient 0, whatever h holds); another label outside
+ * [0, V) neither (DFLASH_STATUS_BAD_TOKEN). A row whose loss is NaN sets
+ * DFLASH_STATUS_BAD_ROW. row_stats ([device] float [rows, 2], or NULL): the
+ * largest logit m and the sum of e^(z - m), for the backward call. workspace
+ * [device], 256-byte aligned, needs no preparation; calls that share one must be
+ * ordered. Every sum has a fixed order. */
+size_t dflash_linear_entropy_workspace_bytes(int rows, int V, int K, int backward);
+int dflash_linear_entropy(const void* h, int64_t h_stride, const void* w, int64_t w_stride, int rows, int V, int K,
+                          const int32_t* labels, const float* row_weight, float* loss, float* row_stats, void* workspace,
+                          size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* Its gradients for an upstream gradient of the losses ([device] float [rows],
+ * upstream_stride elements apart, 0 for one that all rows share; NULL: 1): dh
+ * [rows, K] and dw [V, K] (bf16, contiguous; NULL: not computed). The logits'
+ * gradients go to the products as bf16, in pieces of the vocabulary. A row whose
+ * upstream gradient is 0 takes no part. */
+int dflash_linear_entropy_grad(const void* h, int64_t h_stride, const void* w, int64_t w_stride, int rows, int V, int K,
+                               const int32_t* labels, const float* row_weight, const float* row_stats,
+                               const float* upstream, int64_t upstream_stride, void* dh, void* dw, void* workspace,
+                               size_t workspace_bytes, uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

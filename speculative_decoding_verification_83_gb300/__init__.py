@@ -21,9 +21,11 @@ LIB_PATH = os.path.join(_BUILD, "libdflash_verify.so")
 SOURCES = ["dflash_sweep.cu", "dflash_fullvocab.cu", "dflash_fvtp.cu", "dflash_candidates.cu", "dflash_lmhead.cu",
            "dflash_abi.cu",
            "dflash_noalloc.cu", "dflash_kvappend.cu", "dflash_attention.cu", "dflash_attention_tc.cu",
-           "dflash_distill.cu", "dflash_ops_abi.cu"]
+           "dflash_distill.cu", "dflash_ops_abi.cu", "dflash_norm.cu", "dflash_packed.cu", "dflash_entropy.cu",
+           "dflash_train_abi.cu"]
 HEADERS = ["dflash_device.cuh", "dflash_internal.h", "dflash_rule.cuh", "dflash_ff.cuh", "dflash_ops.h",
-           "dflash_paged.cuh", "dflash_attention.cuh"]
+           "dflash_paged.cuh", "dflash_attention.cuh", "dflash_norm.cuh", "dflash_packed.cuh", "dflash_tcgen05.cuh",
+           "dflash_train.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -118,11 +120,21 @@ EXPORTS = {
     "dflash_lmhead_logits": ("i", "ppiiippp"),
     "dflash_lmhead_verify": ("i", "ppiiiippifQppppzpp"),
     "dflash_kv_append": ("i", "pppppiiippppiipp"),
+    "dflash_kv_append_norm": ("i", "pppppiiippp" "ppifpiipp"),
     "dflash_attention_workspace_bytes": ("z", "ii"),
     "dflash_paged_attention": ("i", "ppppiiipppfipzpp"),
     "dflash_distill_loss": ("i", "pliiippifppppp"),
     "dflash_distill_grad": ("i", "pliiippifppplpl" "p"),
     "dflash_distill_loss_grad": ("i", "pliiippifpppl" "pp"),
+    "dflash_norm_rotate": ("i", "ppppiiiiip" "ppif" "ppii" "p"),
+    "dflash_norm_workspace_bytes": ("z", "i"),
+    "dflash_norm_rotate_grad": ("i", "ppppppiiiiip" "ppppif" "ppii" "pzp"),
+    "dflash_packed_workspace_bytes": ("z", "pi"),
+    "dflash_packed_attention": ("i", "pppppppi" "pzpp"),
+    "dflash_packed_attention_grad": ("i", "ppppppppppp" "i" "pzpp"),
+    "dflash_linear_entropy_workspace_bytes": ("z", "iiii"),
+    "dflash_linear_entropy": ("i", "plpliii" "pppp" "pzpp"),
+    "dflash_linear_entropy_grad": ("i", "plpliii" "pppplpp" "pzpp"),
 }
 _CT = {"i": ctypes.c_int, "p": ctypes.c_void_p, "z": ctypes.c_size_t, "f": ctypes.c_float,
        "Q": ctypes.c_uint64, "l": ctypes.c_int64, "s": ctypes.c_char_p, "": None}
@@ -619,10 +631,12 @@ def verify_host(target, draft, draft_tokens, temperature, top_k, top_p, seed, ou
 
 from .operators import *  # noqa: E402,F401,F403
 from .operators import __all__ as _operators  # noqa: E402
+from .training import *  # noqa: E402,F401,F403
+from .training import __all__ as _training  # noqa: E402
 
 __all__ = [
     "build", "load", "verify", "verify_det", "verify_greedy", "shard_candidates", "gather_records",
     "verify_candidates", "verify_vocab_sharded", "candidates_words", "filter_rows", "sample_rows", "uniforms",
     "verify_host", "Workspace", "workspace_bytes", "rows_workspace_bytes", "host_staging_bytes",
-    "DFlashError", "LIB_PATH", "EXPORTS", *_operators,
+    "DFlashError", "LIB_PATH", "EXPORTS", *_operators, *_training,
 ]

@@ -10,7 +10,9 @@
 // 2^-65, whatever the position, without 64-bit floating point; its upper 32
 // bits, as a signed number of half turns in [-1, 1), go to sincospif.
 // Everything is fp32 until the one rounding to the stored type (e4m3: the
-// value over its head's scale, saturated at +-448).
+// value over its head's scale, saturated at +-448). With norms, keys and queries
+// are first taken to x w / sqrt(mean x^2 + eps) over their head's values, which
+// the head's D / 16 lanes sum by shuffles.
 //
 // What bounds it: reading and writing each value once; for few tokens the launch
 // and the chain of offset, length, page and slot. So a block reads its values
@@ -24,6 +26,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "dflash_norm.cuh"
 #include "dflash_paged.cuh"
 
 namespace dflash {
@@ -36,21 +39,6 @@ __device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-template <class T>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = T::unpack(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-template <class T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(T::pack(x[0], x[1]), T::pack(x[2], x[3]), T::pack(x[4], x[5]), T::pack(x[6], x[7]));
 }
 
 // A head's scale z, and two reciprocals with the true one between them. Rounding
@@ -121,7 +109,7 @@ __device__ __forceinline__ int request_of_token_warp(const PackedTokens& k, int 
 // (heads of k, then v, then q): the two halves of rotated pairs, or two
 // neighbours. The items' values are read before it is known where they go, so
 // that the chain of offset, length, page and slot costs no time of its own.
-template <class T, bool kF8, int D, int kBatch>
+template <class T, bool kF8, int D, int kBatch, bool kNorm>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p, int group, uint32_t inv_items) {
   constexpr int kItems = D / 16;  // vector pairs per head
   __shared__ Place place[kMaxGroup];
@@ -217,6 +205,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     float a[8], b[8];
     unpack8<T>(x[k], a);
     unpack8<T>(y[k], b);
+    if (kNorm && !is_v) {
+      // (a head's lanes are all here: they share its token and its range)
+      float sum = 0.0f, w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += a[e] * a[e] + b[e] * b[e];
+      const float inv = rsqrtf(head_sum<kItems>(sum) * (1.0f / D) + p.eps);
+      const void* weight = is_k ? p.k_weight : p.q_weight;
+      weight8<T>(weight, p.weight_f32, va, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] *= inv * w[e];
+      weight8<T>(weight, p.weight_f32, vb, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] *= inv * w[e];
+    }
     if (!is_v && i < rv) {
       const float2* tn = turn + ti * half + i;
       if (split) {
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   }
 }
 
-template <class T, bool kF8, int D, int kBatch>
+template <class T, bool kF8, int D, int kBatch, bool kNorm>
 int launch_batch(const AppendParams& p, int group, int items, void* stream) {
   cudaLaunchConfig_t cfg = {};
   const int share = kAppendThreads * kBatch;
@@ -273,24 +275,28 @@ int launch_batch(const AppendParams& p, int group, int items, void* stream) {
   // ceil(2^32 / items): the upper half of its product with w is w / items while
   // w * items stays below 2^32 (with one token a block there is nothing to divide)
   const uint32_t inv_items = group == 1 ? 0u : (uint32_t)(((1ull << 32) + items - 1) / items);
-  return (int)cudaLaunchKernelEx(&cfg, append_kernel<T, kF8, D, kBatch>, p, group, inv_items);
+  return (int)cudaLaunchKernelEx(&cfg, append_kernel<T, kF8, D, kBatch, kNorm>, p, group, inv_items);
 }
 
 // Few tokens: one item a thread, over as many blocks as that gives. Many: 4
 // items a thread and as many tokens a block as they make.
-template <class T, bool kF8, int D>
+template <class T, bool kF8, int D, bool kNorm>
 int launch(const AppendParams& p, void* stream) {
   const int items = (2 * p.c.kv_heads + p.q_heads) * (D / 16);
-  if ((long long)p.tk.tokens * items <= 1 << 17) return launch_batch<T, kF8, D, 1>(p, 1, items, stream);
+  if ((long long)p.tk.tokens * items <= 1 << 17) return launch_batch<T, kF8, D, 1, kNorm>(p, 1, items, stream);
   const int fit = 4 * kAppendThreads / items, group = fit < 1 ? 1 : fit > kMaxGroup ? kMaxGroup : fit;
-  return launch_batch<T, kF8, D, 4>(p, group, items, stream);
+  return launch_batch<T, kF8, D, 4, kNorm>(p, group, items, stream);
 }
 
-template <class T, bool kF8>
+template <class T, bool kF8, bool kNorm>
 int pick_dim(const AppendParams& p, int d, void* stream) {
-  return d == 64    ? launch<T, kF8, 64>(p, stream)
-         : d == 128 ? launch<T, kF8, 128>(p, stream)
-                    : launch<T, kF8, 256>(p, stream);
+  return d == 64    ? launch<T, kF8, 64, kNorm>(p, stream)
+         : d == 128 ? launch<T, kF8, 128, kNorm>(p, stream)
+                    : launch<T, kF8, 256, kNorm>(p, stream);
+}
+template <class T, bool kF8>
+int pick_norm(const AppendParams& p, int d, void* stream) {
+  return p.norm ? pick_dim<T, kF8, true>(p, d, stream) : pick_dim<T, kF8, false>(p, d, stream);
 }
 
 }  // namespace
@@ -298,8 +304,8 @@ int pick_dim(const AppendParams& p, int d, void* stream) {
 int launch_kv_append(const AppendParams& p, int dtype, int cache_dtype, int head_dim, void* stream) {
   const bool f8 = cache_dtype == DFLASH_E4M3;
   if (dtype == DFLASH_BF16)
-    return f8 ? pick_dim<Bf16, true>(p, head_dim, stream) : pick_dim<Bf16, false>(p, head_dim, stream);
-  return f8 ? pick_dim<F16, true>(p, head_dim, stream) : pick_dim<F16, false>(p, head_dim, stream);
+    return f8 ? pick_norm<Bf16, true>(p, head_dim, stream) : pick_norm<Bf16, false>(p, head_dim, stream);
+  return f8 ? pick_norm<F16, true>(p, head_dim, stream) : pick_norm<F16, false>(p, head_dim, stream);
 }
 
 }  // namespace dflash

@@ -43,6 +43,10 @@ struct AppendParams {
   const int32_t* lens;
   const unsigned long long* phases;  // turns per token, 64-bit fixed point
   int rot, interleaved;
+  int norm;                            // keys and queries are normed first,
+  const void *q_weight, *k_weight;     // with weights [head_dim] (null: 1)
+  int weight_f32;                      // in fp32, or in the tokens' type
+  float eps;
   uint32_t* status;
 };
 int launch_kv_append(const AppendParams& p, int dtype, int cache_dtype, int head_dim, void* stream);

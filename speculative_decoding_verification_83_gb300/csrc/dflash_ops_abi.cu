@@ -148,13 +148,10 @@ int sms_here(int* sms) {
 
 extern "C" {
 
-int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out,
-                     int dtype, int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens,
-                     const int32_t* q_start, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,
-                     void* stream) {
-  NvtxRange nvtx_range("dflash_kv_append");
-  AppendParams p;
-  memset(&p, 0, sizeof p);
+static int append(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out, int dtype,
+                  int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens, const int32_t* q_start,
+                  const uint64_t* phases, int rot_dim, int interleaved, AppendParams p, uint32_t* status,
+                  void* stream) {
   int rc = bind_cache(cache, dtype, &p.c);
   if (rc || (rc = bind_tokens(cache, q_start, tokens, &p.tk))) return rc;
   if (!strides || !cached_lens) return fail(DFLASH_ERR_INVALID_ARG, "null pointer argument");
@@ -193,6 +190,39 @@ int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void*
   p.interleaved = interleaved != 0;
   p.status = status;
   return launched(launch_kv_append(p, dtype, cache->dtype, cache->head_dim, stream), "the key/value append");
+}
+
+int dflash_kv_append(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out,
+                     int dtype, int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens,
+                     const int32_t* q_start, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,
+                     void* stream) {
+  NvtxRange nvtx_range("dflash_kv_append");
+  AppendParams p;
+  memset(&p, 0, sizeof p);
+  return append(cache, k, v, q, q_out, dtype, tokens, q_heads, strides, cached_lens, q_start, phases, rot_dim,
+                interleaved, p, status, stream);
+}
+
+int dflash_kv_append_norm(const dflash_paged_cache* cache, const void* k, const void* v, const void* q, void* q_out,
+                          int dtype, int tokens, int q_heads, const int64_t* strides, const int32_t* cached_lens,
+                          const int32_t* q_start, const void* q_weight, const void* k_weight, int weight_dtype,
+                          float eps, const uint64_t* phases, int rot_dim, int interleaved, uint32_t* status,
+                          void* stream) {
+  NvtxRange nvtx_range("dflash_kv_append_norm");
+  AppendParams p;
+  memset(&p, 0, sizeof p);
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(DFLASH_ERR_INVALID_ARG, "eps=%g must be finite and not negative", (double)eps);
+  if (weight_dtype != dtype && weight_dtype != DFLASH_F32)
+    return fail(DFLASH_ERR_INVALID_ARG, "weight_dtype=%d is neither the tokens' dtype=%d nor fp32", weight_dtype, dtype);
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return fail(DFLASH_ERR_INVALID_ARG, "the norms' weights must be 16-byte aligned");
+  p.norm = 1;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.weight_f32 = weight_dtype == DFLASH_F32;
+  p.eps = eps;
+  return append(cache, k, v, q, q_out, dtype, tokens, q_heads, strides, cached_lens, q_start, phases, rot_dim,
+                interleaved, p, status, stream);
 }
 
 size_t dflash_attention_workspace_bytes(int batch, int head_dim) {

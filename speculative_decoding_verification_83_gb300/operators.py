@@ -249,6 +249,14 @@ def rope_phases(inv_freq, device=None):
     return torch.tensor(table, dtype=torch.int64, device="cuda" if device is None else device)
 
 
+def _norm_weights(q_weight, k_weight, dim, dtype, code, device):
+    """Data pointers of the norms' weights and their type's code."""
+    f32 = _modules[0].float32
+    kind = f32 if f32 in (getattr(q_weight, "dtype", None), getattr(k_weight, "dtype", None)) else dtype
+    return (_vector(q_weight, dim, "q_weight", kind, device), _vector(k_weight, dim, "k_weight", kind, device),
+            DFLASH_F32 if kind == f32 else code)
+
+
 def _packed(cache, n_tokens, lens, lens_name, q_start):
     torch = _torch()
     if cache.batch == 0:
@@ -260,19 +268,21 @@ def _packed(cache, n_tokens, lens, lens_name, q_start):
 
 
 def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases=None, interleaved=False,
-              q_out=None, status=None, stream=None):
+              q_out=None, status=None, stream=None, q_weight=None, k_weight=None, eps=None):
     """dflash_kv_append: the new tokens' keys ``k`` and values ``v`` [tokens,
     heads, head_dim] into the cache behind each request's ``cached_lens``
     [batch] int32 tokens, the keys (and ``q`` [tokens, q_heads, head_dim])
     rotated by ``phases`` (``rope_phases``; None: no rotation). Requests' tokens
-    are packed at ``q_start`` [batch + 1] int32, or tokens / batch each. There is
-    no backward pass (tensors that require a gradient are refused). Returns
-    the rotated q (a new tensor, or ``q_out``, which may be ``q``), or None; its
+    are packed at ``q_start`` [batch + 1] int32, or tokens / batch each. With
+    ``eps`` keys and queries are normed head by head before the rotation
+    (dflash_kv_append_norm; weights [head_dim] in the tokens' type or fp32, None:
+    1). There is no backward pass (tensors that require a gradient are refused).
+    Returns the rotated q (a new tensor, or ``q_out``, which may be ``q``), or None; its
     rows of no request, or of a bad length, are not written."""
     torch = _torch()
     dev, D = cache.device, cache.head_dim
     dt = _token_dtype(k, cache, "tokens")
-    _carries_no_gradient(cache, k=k, v=v, q=q, q_out=q_out)
+    _carries_no_gradient(cache, k=k, v=v, q=q, q_out=q_out, q_weight=q_weight, k_weight=k_weight)
     pk, kt, kh = _rows(k, "k", cache.heads, D, dev)
     pv, vt, vh = _rows(v, "v", cache.heads, D, dev, k)
     n = k.shape[0]
@@ -294,10 +304,19 @@ def kv_append(cache: PagedCache, k, v, cached_lens, q_start=None, q=None, phases
             raise ValueError("phases must be one-dimensional")
         rot = 2 * phases.shape[0]
         phases = _vector(phases, phases.shape[0], "phases", torch.int64, dev)
-    _call(dev, _library().dflash_kv_append, cache._ref, pk, pv, pq, po, dt, n, hq,
-          _pack8(kt, kh, vt, vh, qt, qh, ot, oh), lens, starts, phases, rot, 1 if interleaved else 0,
-          _status_word(status, dev), _raw_stream(stream, dev))
-    _used_on(stream, *cache.tensors, k, v, q, None if new_q else q_out, cached_lens, q_start, phase_table, status)
+    strides = _pack8(kt, kh, vt, vh, qt, qh, ot, oh)
+    rest = phases, rot, 1 if interleaved else 0, _status_word(status, dev), _raw_stream(stream, dev)
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("the norms' weights need eps")
+        _call(dev, _library().dflash_kv_append, cache._ref, pk, pv, pq, po, dt, n, hq, strides, lens, starts, *rest)
+    else:
+        wq, wk, code = _norm_weights(q_weight, k_weight, D, k.dtype, dt, dev)
+        library = _library()
+        _call(dev, library.dflash_kv_append_norm, cache._ref, pk, pv, pq, po, dt, n, hq, strides, lens, starts, wq, wk,
+              code, eps, *rest)
+    _used_on(stream, *cache.tensors, k, v, q, None if new_q else q_out, cached_lens, q_start, phase_table, status,
+             q_weight, k_weight)
     _written(cache.k, cache.v, None if new_q else q_out)
     return q_out
 
