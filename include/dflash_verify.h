@@ -554,15 +554,18 @@ typedef struct dflash_packed_batch {
 } dflash_packed_batch;
 size_t dflash_packed_workspace_bytes(const dflash_packed_batch* batch, int backward);
 int dflash_packed_attention(const dflash_packed_batch* batch, const void* q, const void* k, const void* v, void* out,
-                            const int64_t* strides, float* lse, int fill, void* workspace, size_t workspace_bytes,
-                            uint32_t* status, void* stream);
+                            const int64_t* strides, float* lse, int8_t* out_low, int fill, void* workspace,
+                            size_t workspace_bytes, uint32_t* status, void* stream);
 
 /* Its gradients for dout, from the forward call's out and lse (bf16 only). Heads
- * that share a key add up. strides: q, k, v, out, dout, dq, dk, dv. */
+ * that share a key add up. out_low ([device] int8 [q_tokens, q_heads, head_dim],
+ * contiguous, or NULL): 8 further bits of each output, written by the forward call
+ * for this one, which needs sum dout out; without it the outputs' rounding reaches
+ * dq and dk. strides: q, k, v, out, dout, dq, dk, dv. */
 int dflash_packed_attention_grad(const dflash_packed_batch* batch, const void* q, const void* k, const void* v,
-                                 const void* out, const float* lse, const void* dout, void* dq, void* dk, void* dv,
-                                 const int64_t* strides, int fill, void* workspace, size_t workspace_bytes,
-                                 uint32_t* status, void* stream);
+                                 const void* out, const float* lse, const int8_t* out_low, const void* dout, void* dq,
+                                 void* dk, void* dv, const int64_t* strides, int fill, void* workspace,
+                                 size_t workspace_bytes, uint32_t* status, void* stream);
 
 /* ---- cross entropy through the vocabulary projection --------------------------------------------
  * A drafter's training on the target's tokens (or any labels): per row

@@ -130,8 +130,8 @@ EXPORTS = {
     "dflash_norm_workspace_bytes": ("z", "i"),
     "dflash_norm_rotate_grad": ("i", "ppppppiiiiip" "ppppif" "ppii" "pzp"),
     "dflash_packed_workspace_bytes": ("z", "pi"),
-    "dflash_packed_attention": ("i", "pppppppi" "pzpp"),
-    "dflash_packed_attention_grad": ("i", "ppppppppppp" "i" "pzpp"),
+    "dflash_packed_attention": ("i", "ppppppppi" "pzpp"),
+    "dflash_packed_attention_grad": ("i", "pppppppppppp" "i" "pzpp"),
     "dflash_linear_entropy_workspace_bytes": ("z", "iiii"),
     "dflash_linear_entropy": ("i", "plpliii" "pppp" "pzpp"),
     "dflash_linear_entropy_grad": ("i", "plpliii" "pppplpp" "pzpp"),

@@ -85,6 +85,9 @@ __global__ void __launch_bounds__(32 * kWarps) rows_forward_kernel(const PackedP
       if (p.fill) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) put<T>(out, lane + 32 * i, 0.0f);
+        if (p.low)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) p.low[r * D + lane + 32 * i] = 0;
         if (p.lse && lane == 0) p.lse[r] = -INFINITY;
       }
       continue;
@@ -125,7 +128,9 @@ __global__ void __launch_bounds__(32 * kWarps) rows_forward_kernel(const PackedP
     for (int i = 0; i < D / 32; ++i) {
       float y = acc[i] * inv;
       if (odd[i] && y == y) y = odd[i] == 1u ? INFINITY : odd[i] == 2u ? -INFINITY : NAN;
-      put<T>(out, lane + 32 * i, y);
+      const uint32_t hi = T::pack(y, 0.0f) & 0xffffu;
+      reinterpret_cast<uint16_t*>(out)[lane + 32 * i] = (uint16_t)hi;
+      if (p.low) p.low[r * D + lane + 32 * i] = low_bits(y, hi);
     }
     if (p.lse && lane == 0) p.lse[r] = sum == 0.0f ? -INFINITY : top + logf(sum);
   }
@@ -144,10 +149,15 @@ __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p
     const uint4 a = reinterpret_cast<const uint4*>(row_of(p.o, t, head))[lane];
     const uint4 g = reinterpret_cast<const uint4*>(row_of(p.d_o, t, head))[lane];
     const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {g.x, g.y, g.z, g.w};
+    uint2 l = make_uint2(0u, 0u);
+    if (p.low) l = reinterpret_cast<const uint2*>(p.low + r * D)[lane];
+    const uint32_t low[2] = {l.x, l.y};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 u = T::unpack(x[e]), v = T::unpack(y[e]);
-      s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+      const uint32_t b = low[e >> 1] >> (16 * (e & 1));
+      const float2 v = T::unpack(y[e]);
+      s = fmaf(with_low(x[e] & 0xffffu, (int8_t)(b & 0xffu)), v.x,
+               fmaf(with_low(x[e] >> 16, (int8_t)((b >> 8) & 0xffu)), v.y, s));
     }
   }
 #pragma unroll
@@ -295,6 +305,7 @@ unsigned blocks_for(long long rows) {
 template <class T>
 int forward(const PackedParams& p, int d, const uint32_t* redo, cudaStream_t st) {
   const unsigned grid = blocks_for((long long)p.q_tokens * p.q_heads);
+  if (!grid) return 0;
   if (d == 64)
     rows_forward_kernel<T, 64><<<grid, 32 * kWarps, 0, st>>>(p, redo);
   else
@@ -303,8 +314,9 @@ int forward(const PackedParams& p, int d, const uint32_t* redo, cudaStream_t st)
 }
 template <int D>
 int grad(const PackedParams& p, const uint32_t* redo_q, const uint32_t* redo_kv, cudaStream_t st) {
-  rows_dq_kernel<Bf16, D><<<blocks_for((long long)p.q_tokens * p.q_heads), 32 * kWarps, 0, st>>>(p, redo_q);
-  rows_dkv_kernel<Bf16, D><<<blocks_for((long long)p.kv_tokens * p.kv_heads), 32 * kWarps, 0, st>>>(p, redo_kv);
+  const unsigned grid_q = blocks_for((long long)p.q_tokens * p.q_heads), grid_kv = blocks_for((long long)p.kv_tokens * p.kv_heads);
+  if (grid_q) rows_dq_kernel<Bf16, D><<<grid_q, 32 * kWarps, 0, st>>>(p, redo_q);
+  if (grid_kv) rows_dkv_kernel<Bf16, D><<<grid_kv, 32 * kWarps, 0, st>>>(p, redo_kv);
   return (int)cudaGetLastError();
 }
 
@@ -317,6 +329,7 @@ int launch_rows_forward(const PackedParams& p, int dtype, int head_dim, const ui
 int launch_delta(const PackedParams& p, int head_dim, void* stream) {
   const long long threads = (long long)p.q_tokens * p.q_heads * (head_dim / 8);
   const unsigned grid = (unsigned)((threads + 32 * kWarps - 1) / (32 * kWarps));
+  if (!grid) return 0;
   if (head_dim == 64)
     delta_kernel<Bf16, 64><<<grid, 32 * kWarps, 0, (cudaStream_t)stream>>>(p);
   else

@@ -38,6 +38,19 @@ __device__ __forceinline__ int seen_keys(int causal, int n, int m, int i) {
 // The first query of n that sees key j of m (causal).
 __device__ __forceinline__ int first_query(int causal, int n, int m, int j) { return causal ? max(0, j - (m - n)) : 0; }
 
+// A bf16 output's next 8 bits: the rounding's remainder in units of 2^-8 of the
+// output's last place, from the two numbers' bit patterns (of one sign). The backward
+// pass needs sum dout out more exactly than bf16 outputs give it: with short
+// sequences the outputs' rounding would add as much to dq and dk as all else.
+__device__ __forceinline__ int8_t low_bits(float y, uint32_t hi) {
+  const int d = ((int)(__float_as_uint(y) - (hi << 16)) + 128) >> 8;
+  return (int8_t)max(-128, min(127, d));
+}
+__device__ __forceinline__ float with_low(uint32_t hi, int low) {
+  const bool finite = (hi & 0x7f80u) != 0x7f80u;
+  return __uint_as_float((hi << 16) + (finite ? (uint32_t)(low * 256) : 0u));
+}
+
 // Rows one by one (dflash_packed.cu): every row, or with `redo` those of the tiles
 // whose flag is set that hold a value which is not finite.
 int launch_rows_forward(const PackedParams& p, int dtype, int head_dim, const uint32_t* redo, void* stream);

@@ -60,6 +60,7 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream);
 // q_start[b + 1] - 1, its keys and values rows kv_start[b] .. kv_start[b + 1] - 1.
 struct PackedParams {
   HeadRows q, k, v, o;
+  int8_t* low;               // [q_tokens, q_heads, head_dim] or null: what the outputs' rounding left, see out_low
   float* lse;                // [q_tokens, q_heads]
   HeadRows d_o, dq, dk, dv;  // backward
   float* delta;              // backward: [q_tokens, q_heads], sum of d_o o

@@ -229,8 +229,8 @@ size_t dflash_packed_workspace_bytes(const dflash_packed_batch* batch, int backw
 }
 
 int dflash_packed_attention(const dflash_packed_batch* batch, const void* q, const void* k, const void* v, void* out,
-                            const int64_t* strides, float* lse, int fill, void* workspace, size_t workspace_bytes,
-                            uint32_t* status, void* stream) {
+                            const int64_t* strides, float* lse, int8_t* out_low, int fill, void* workspace,
+                            size_t workspace_bytes, uint32_t* status, void* stream) {
   NvtxRange nvtx_range("dflash_packed_attention");
   PackedParams p;
   int rc = bind_packed(batch, &p);
@@ -244,8 +244,11 @@ int dflash_packed_attention(const dflash_packed_batch* batch, const void* q, con
   if (p.kv_tokens && ((rc = bind_rows(k, strides + 2, p.kv_tokens, p.kv_heads, d, "k", &p.k)) ||
                       (rc = bind_rows(v, strides + 4, p.kv_tokens, p.kv_heads, d, "v", &p.v))))
     return rc;
+  if (out_low && (batch->dtype != DFLASH_BF16 || !aligned(out_low, 16)))
+    return fail(DFLASH_ERR_INVALID_ARG, "out_low is for bf16 and must be 16-byte aligned");
   if ((rc = check_workspace(workspace, workspace_bytes, packed_bytes(batch, false)))) return rc;
   p.lse = lse;
+  p.low = out_low;
   p.fill = fill != 0;
   p.ws = static_cast<unsigned char*>(workspace);
   p.status = status;
@@ -255,9 +258,9 @@ int dflash_packed_attention(const dflash_packed_batch* batch, const void* q, con
 }
 
 int dflash_packed_attention_grad(const dflash_packed_batch* batch, const void* q, const void* k, const void* v,
-                                 const void* out, const float* lse, const void* dout, void* dq, void* dk, void* dv,
-                                 const int64_t* strides, int fill, void* workspace, size_t workspace_bytes,
-                                 uint32_t* status, void* stream) {
+                                 const void* out, const float* lse, const int8_t* out_low, const void* dout, void* dq,
+                                 void* dk, void* dv, const int64_t* strides, int fill, void* workspace,
+                                 size_t workspace_bytes, uint32_t* status, void* stream) {
   NvtxRange nvtx_range("dflash_packed_attention_grad");
   PackedParams p;
   int rc = bind_packed(batch, &p);
@@ -278,7 +281,9 @@ int dflash_packed_attention_grad(const dflash_packed_batch* batch, const void* q
     return rc;
   if (p.q_tokens && !lse) return fail(DFLASH_ERR_INVALID_ARG, "null lse");
   if ((rc = check_workspace(workspace, workspace_bytes, packed_bytes(batch, true)))) return rc;
+  if (!aligned(out_low, 16)) return fail(DFLASH_ERR_INVALID_ARG, "out_low must be 16-byte aligned");
   p.lse = const_cast<float*>(lse);
+  p.low = const_cast<int8_t*>(out_low);
   p.fill = fill != 0;
   p.ws = static_cast<unsigned char*>(workspace);
   p.status = status;

@@ -249,7 +249,7 @@ def _size(function, *args):
     return n
 
 
-def _attend(q, k, v, q_start, kv_start, scale, causal, keep, status):
+def _attend(q, k, v, q_start, kv_start, scale, causal, keep, status, train=False):
     torch, lib = _ops._modules
     batch, pq, pk, pv = _batch(q, k, v, q_start, kv_start, scale, causal)
     dev = q.device
@@ -257,12 +257,13 @@ def _attend(q, k, v, q_start, kv_start, scale, causal, keep, status):
     n, hq, D = q.shape
     out = torch.empty((n, hq, D), dtype=q.dtype, device=dev)
     lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if keep else None
+    low = torch.empty((n, hq, D), dtype=torch.int8, device=dev) if train else None
     size = _size(lib.dflash_packed_workspace_bytes, ctypes.byref(batch), 0)
     ws = _workspace(size, dev)
     _ops._call(dev, lib.dflash_packed_attention, ctypes.byref(batch), pq[0], pk[0], pv[0], out.data_ptr(),
-               _pack8(*pq[1:], *pk[1:], *pv[1:], hq * D, D), lse.data_ptr() if keep else None, 1, ws.data_ptr(), size,
-               word, _ops._raw_stream(None, dev))
-    return out, lse
+               _pack8(*pq[1:], *pk[1:], *pv[1:], hq * D, D), lse.data_ptr() if keep else None,
+               low.data_ptr() if train else None, 1, ws.data_ptr(), size, word, _ops._raw_stream(None, dev))
+    return out, lse, low
 
 
 def _attention_function():
@@ -272,7 +273,7 @@ def _attention_function():
     torch = _ops._torch()
 
     def backward(ctx, dout, _):
-        q, k, v, q_start, kv_start, out, lse, status = ctx.saved_tensors
+        q, k, v, q_start, kv_start, out, lse, low, status = ctx.saved_tensors
         lib, dev = _ops._library(), q.device
         batch, pq, pk, pv = _batch(q, k, v, q_start, kv_start, ctx.scale, ctx.causal)
         dout = _usable(dout, q)
@@ -280,7 +281,7 @@ def _attention_function():
         size = _size(lib.dflash_packed_workspace_bytes, ctypes.byref(batch), 1)
         ws = _workspace(size, dev)
         _ops._call(dev, lib.dflash_packed_attention_grad, ctypes.byref(batch), pq[0], pk[0], pv[0], out.data_ptr(),
-                   lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                   lse.data_ptr(), low.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                    _pack16(*pq[1:], *pk[1:], *pv[1:], *out.stride()[:2], *dout.stride()[:2], *dq.stride()[:2],
                            *dk.stride()[:2], *dv.stride()[:2]), 1, ws.data_ptr(), size,
                    _ops._status_word(status, dev), _ops._raw_stream(None, dev))
@@ -289,8 +290,8 @@ def _attention_function():
     class PackedAttention(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, v, q_start, kv_start, scale, causal, status):
-            out, lse = _attend(q, k, v, q_start, kv_start, scale, causal, True, status)
-            ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, status)
+            out, lse, low = _attend(q, k, v, q_start, kv_start, scale, causal, True, status, True)
+            ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, low, status)
             ctx.scale, ctx.causal = scale, causal
             ctx.mark_non_differentiable(lse)
             return out, lse
@@ -319,7 +320,7 @@ def packed_attention(q, k, v, q_start, kv_start=None, scale=None, causal=True, r
                             "or call under torch.no_grad()")
         out, lse = _attention_function().apply(*args, status)
     else:
-        out, lse = _attend(*args, return_lse, status)
+        out, lse, _ = _attend(*args, return_lse, status)
     return (out, lse) if return_lse else out
 
 
