@@ -21,10 +21,11 @@ LIB_PATH = os.path.join(_BUILD, "libdflash_verify.so")
 SOURCES = ["dflash_sweep.cu", "dflash_fullvocab.cu", "dflash_fvtp.cu", "dflash_candidates.cu", "dflash_lmhead.cu",
            "dflash_abi.cu",
            "dflash_noalloc.cu", "dflash_kvappend.cu", "dflash_attention.cu", "dflash_attention_tc.cu",
-           "dflash_distill.cu", "dflash_ops_abi.cu", "dflash_norm.cu", "dflash_packed.cu", "dflash_entropy.cu",
-           "dflash_train_abi.cu"]
+           "dflash_distill.cu", "dflash_ops_abi.cu", "dflash_norm.cu", "dflash_packed.cu", "dflash_packed_fwd.cu",
+           "dflash_packed_bwd.cu", "dflash_entropy.cu", "dflash_train_abi.cu"]
 HEADERS = ["dflash_device.cuh", "dflash_internal.h", "dflash_rule.cuh", "dflash_ff.cuh", "dflash_ops.h",
-           "dflash_paged.cuh", "dflash_attention.cuh", "dflash_norm.cuh", "dflash_packed.cuh", "dflash_tcgen05.cuh",
+           "dflash_paged.cuh", "dflash_attention.cuh", "dflash_norm.cuh", "dflash_packed.cuh", "dflash_packed_mma.cuh",
+           "dflash_tcgen05.cuh",
            "dflash_train.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

@@ -1,4 +1,5 @@
-// dflash_packed.cu -- attention over packed sequences, row by row.
+// dflash_packed.cu -- attention over packed sequences: the formulas, the lists of
+// work, and the rows that are gone through one by one.
 //
 // out_i = sum_j e^(s q_i k_j) v_j / sum_j e^(s q_i k_j) over the keys j that row i
 // sees, lse_i = log of that sum. Backward, with p_ij = e^(s q_i k_j - lse_i) and
@@ -7,9 +8,11 @@
 //   dq_i = s sum_j ds_ij k_j, dk_j = s sum_i ds_ij q_i,
 // i over the rows, of all query heads that share the key's head, that see key j.
 //
-// One warp takes a row: 32 keys (queries) at a time, a score per lane, then
-// D / 32 columns per lane. Pairs that do not see each other take no part,
-// whatever they hold.
+// The products run on the tensor cores (dflash_packed_fwd.cu, dflash_packed_bwd.cu),
+// where a masked pair counts as a weight of 0, and 0 times a value that is not
+// finite is NaN. So they flag what came out not finite, and here one warp takes
+// each such row: 32 keys (queries) at a time, a score per lane, then D / 32 columns
+// per lane; pairs that do not see each other take no part, whatever they hold.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -66,80 +69,109 @@ __device__ __forceinline__ bool row_not_finite(const unsigned char* row) {
   return __any_sync(kAll, found);
 }
 
+// Row t of the outputs: query i of n over m keys from kv0 on. One warp; q_row: its
+// D values of shared memory.
 template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps) rows_forward_kernel(const PackedParams p, const uint32_t* redo) {
-  __shared__ float q_row[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = (long long)p.q_tokens * p.q_heads;
-  for (long long r = (long long)blockIdx.x * kWarps + warp; r < rows; r += (long long)gridDim.x * kWarps) {
-    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
-    unsigned char* out = row_of(p.o, t, head);
-    const int b = sequence_of(p.q_start, p.B, t);
-    int first = 0, n = 0, kv0 = 0, m = 0;
-    bool bad = false;
-    if (b >= 0) {
-      extent(p.q_start, p.q_tokens, b, first, n, bad);
-      extent(p.kv_start, p.kv_tokens, b, kv0, m, bad);
-    }
-    if (b < 0 || t < first || t >= first + n) {
-      if (p.fill) {
+__device__ void attend_row(const PackedParams& p, int t, int head, int i, int n, int kv0, int m, float* q_row) {
+  const int lane = threadIdx.x & 31, kh = head / p.G, vis = seen_keys(p.causal, n, m, i);
+  const long long r = (long long)t * p.q_heads + head;
+  const unsigned char* q = row_of(p.q, t, head);
+  unsigned char* out = row_of(p.o, t, head);
+  __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) put<T>(out, lane + 32 * i, 0.0f);
-        if (p.low)
+  for (int c = 0; c < D / 32; ++c) q_row[lane + 32 * c] = value<T>(q, lane + 32 * c);
+  __syncwarp();
+  float top = -INFINITY, sum = 0.0f, acc[D / 32] = {};
+  uint32_t odd[D / 32] = {};  // values seen that are not finite: +inf (1), -inf (2), NaN (4)
+  for (int j0 = 0; j0 < vis; j0 += 32) {
+    const int j = j0 + lane, count = min(32, vis - j0);
+    float x = -INFINITY;
+    if (j < vis) x = dot<T, D>(q_row, row_of(p.k, kv0 + j, kh)) * p.scale;
+    const float m1 = warp_max_f32(fmaxf(x, top)), ref = m1 == -INFINITY ? 0.0f : m1;
+    const float f = expf(top - ref), w = expf(x - ref);  // (a score that is NaN leaves NaN)
+    sum = sum * f + warp_sum(w);
+    top = m1;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) p.low[r * D + lane + 32 * i] = 0;
-        if (p.lse && lane == 0) p.lse[r] = -INFINITY;
-      }
-      continue;
-    }
-    const int kh = head / p.G, vis = seen_keys(p.causal, n, m, t - first);
-    const unsigned char* q = row_of(p.q, t, head);
-    __syncwarp();
+    for (int c = 0; c < D / 32; ++c) acc[c] *= f;
+    for (int k = 0; k < count; ++k) {
+      const float wk = __shfl_sync(kAll, w, k);
+      const unsigned char* v = row_of(p.v, kv0 + j0 + k, kh);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) q_row[warp][lane + 32 * i] = value<T>(q, lane + 32 * i);
-    __syncwarp();
-    float top = -INFINITY, sum = 0.0f, acc[D / 32] = {};
-    uint32_t odd[D / 32] = {};  // values seen that are not finite: +inf (1), -inf (2), NaN (4)
-    for (int j0 = 0; j0 < vis; j0 += 32) {
-      const int j = j0 + lane, count = min(32, vis - j0);
-      float x = -INFINITY;
-      if (j < vis) x = dot<T, D>(q_row[warp], row_of(p.k, kv0 + j, kh)) * p.scale;
-      const float m1 = warp_max_f32(fmaxf(x, top)), ref = m1 == -INFINITY ? 0.0f : m1;
-      const float f = expf(top - ref), w = expf(x - ref);  // (a score that is NaN leaves NaN)
-      sum = sum * f + warp_sum(w);
-      top = m1;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] *= f;
-      for (int k = 0; k < count; ++k) {
-        const float wk = __shfl_sync(kAll, w, k);
-        const unsigned char* v = row_of(p.v, kv0 + j0 + k, kh);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const float y = value<T>(v, lane + 32 * i);
-          if (fabsf(y) < INFINITY)
-            acc[i] = fmaf(wk, y, acc[i]);
-          else
-            odd[i] |= y > 0.0f ? 1u : y < 0.0f ? 2u : 4u;
-        }
+      for (int c = 0; c < D / 32; ++c) {
+        const float y = value<T>(v, lane + 32 * c);
+        if (fabsf(y) < INFINITY)
+          acc[c] = fmaf(wk, y, acc[c]);
+        else
+          odd[c] |= y > 0.0f ? 1u : y < 0.0f ? 2u : 4u;
       }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      float y = acc[i] * inv;
-      if (odd[i] && y == y) y = odd[i] == 1u ? INFINITY : odd[i] == 2u ? -INFINITY : NAN;
-      const uint32_t hi = T::pack(y, 0.0f) & 0xffffu;
-      reinterpret_cast<uint16_t*>(out)[lane + 32 * i] = (uint16_t)hi;
-      if (p.low) p.low[r * D + lane + 32 * i] = low_bits(y, hi);
-    }
-    if (p.lse && lane == 0) p.lse[r] = sum == 0.0f ? -INFINITY : top + logf(sum);
   }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float y = acc[c] * inv;
+    if (odd[c] && y == y) y = odd[c] == 1u ? INFINITY : odd[c] == 2u ? -INFINITY : NAN;
+    const uint32_t hi = T::pack(y, 0.0f) & 0xffffu;
+    reinterpret_cast<uint16_t*>(out)[lane + 32 * c] = (uint16_t)hi;
+    if (p.low) p.low[r * D + lane + 32 * c] = low_bits(y, hi);
+  }
+  if (p.lse && lane == 0) p.lse[r] = sum == 0.0f ? -INFINITY : top + logf(sum);
 }
 
-// sum over d of dout out, per row
+// Goes through the flags; row(t, head, i, unit) is called by one warp for every row
+// of a flagged 32. kSame flags in a row stand for the same 32.
+template <int kPer, int kSame, class F>
+__device__ __forceinline__ void each_flagged(const PackedList& list, const uint8_t* flags, int heads, F row) {
+  const long long total = (long long)*list.count * heads * kPer;
+  const int warp = threadIdx.x >> 5;
+  for (long long base = (long long)blockIdx.x * blockDim.x; base < total; base += (long long)gridDim.x * blockDim.x) {
+    const long long at = base + threadIdx.x;
+    if (!__syncthreads_or(at < total && flags[at])) continue;
+    for (long long f = base; f < min(total, base + blockDim.x); ++f) {
+      if (!flags[f]) continue;
+      const int part = (int)(f % kPer) / kSame, head = (int)(f / kPer % heads);
+      const PackedUnit u = list.units[f / kPer / heads];
+      for (int r = 32 * part + warp; r < min(u.rows, 32 * part + 32); r += kWarps) row(u.row0 + r, head, u.i0 + r, u);
+    }
+  }
+}
+// Rows of no sequence: pieces of 8 values set to 0.
+template <int D, class F>
+__device__ __forceinline__ void each_spare(const int32_t* start, int B, int tokens, int heads, F piece) {
+  const int lo = min(max(start[0], 0), tokens), hi = max(lo, min(max(start[B], 0), tokens));
+  const long long n = (long long)(lo + tokens - hi) * heads * (D / 8);
+  for (long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x; at < n; at += (long long)gridDim.x * blockDim.x) {
+    const int c = (int)(at % (D / 8)), head = (int)(at / (D / 8) % heads), r = (int)(at / (D / 8) / heads);
+    piece(r < lo ? r : hi + r - lo, head, c);
+  }
+}
+__device__ __forceinline__ void clear8(const HeadRows& h, int t, int head, int c) {
+  reinterpret_cast<uint4*>(row_of(h, t, head))[c] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kWarps)
+    redo_forward_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
+  __shared__ float q_row[kWarps][D];
+  grid_dependency_sync();
+  each_flagged<kForwardFlags, 1>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+    if (row_not_finite<T, D>(row_of(p.o, t, head)))
+      attend_row<T, D>(p, t, head, i, u.n, u.other0, u.m, q_row[threadIdx.x >> 5]);
+  });
+  if (!p.fill) return;
+  each_spare<D>(p.q_start, p.B, p.q_tokens, p.q_heads, [&](int t, int head, int c) {
+    clear8(p.o, t, head, c);
+    const long long r = (long long)t * p.q_heads + head;
+    if (p.low) reinterpret_cast<uint2*>(p.low + r * D)[c] = make_uint2(0u, 0u);
+    if (p.lse && c == 0) p.lse[r] = -INFINITY;
+  });
+}
+
+// delta, the sum over d of dout out, and lse as the products' kernels read them
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p) {
   constexpr int kLanes = D / 8;  // 8 values each
+  grid_dependency_sync();
   const int lane = threadIdx.x % kLanes;
   const long long rows = (long long)p.q_tokens * p.q_heads;
   const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
@@ -162,197 +194,325 @@ __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p
   }
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  if (r < rows && lane == 0) p.delta[r] = s;
+  if (r < rows && lane == 0) {
+    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
+    const float lse = p.lse[r];
+    p.row_stats[(size_t)head * p.stat_pitch + t] = make_float2(lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f, s);
+  }
 }
 
+// Row t of the queries' gradients.
 template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps) rows_dq_kernel(const PackedParams p, const uint32_t* redo) {
-  __shared__ float q_row[kWarps][D], g_row[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = (long long)p.q_tokens * p.q_heads;
-  for (long long r = (long long)blockIdx.x * kWarps + warp; r < rows; r += (long long)gridDim.x * kWarps) {
-    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
-    unsigned char* out = row_of(p.dq, t, head);
-    const int b = sequence_of(p.q_start, p.B, t);
-    int first = 0, n = 0, kv0 = 0, m = 0;
-    bool bad = false;
-    if (b >= 0) {
-      extent(p.q_start, p.q_tokens, b, first, n, bad);
-      extent(p.kv_start, p.kv_tokens, b, kv0, m, bad);
-    }
-    if (b < 0 || t < first || t >= first + n) {
-      if (p.fill)
+__device__ void dq_row(const PackedParams& p, int t, int head, int i, int n, int kv0, int m, float* q_row, float* g_row) {
+  const int lane = threadIdx.x & 31, kh = head / p.G, vis = seen_keys(p.causal, n, m, i);
+  const long long r = (long long)t * p.q_heads + head;
+  __syncwarp();
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) put<T>(out, lane + 32 * i, 0.0f);
-      continue;
+  for (int c = 0; c < D / 32; ++c) {
+    q_row[lane + 32 * c] = value<T>(row_of(p.q, t, head), lane + 32 * c);
+    g_row[lane + 32 * c] = value<T>(row_of(p.d_o, t, head), lane + 32 * c);
+  }
+  __syncwarp();
+  const float lse = p.lse[r], delta = p.row_stats[(size_t)head * p.stat_pitch + t].y;
+  float acc[D / 32] = {};
+  for (int j0 = 0; j0 < vis; j0 += 32) {
+    const int j = j0 + lane, count = min(32, vis - j0);
+    float ds = 0.0f;
+    if (j < vis) {
+      const float x = dot<T, D>(q_row, row_of(p.k, kv0 + j, kh)) * p.scale;
+      ds = expf(x - lse) * (dot<T, D>(g_row, row_of(p.v, kv0 + j, kh)) - delta) * p.scale;
     }
-    const int kh = head / p.G, vis = seen_keys(p.causal, n, m, t - first);
-    __syncwarp();
+    for (int k = 0; k < count; ++k) {
+      const float w = __shfl_sync(kAll, ds, k);
+      const unsigned char* row = row_of(p.k, kv0 + j0 + k, kh);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      q_row[warp][lane + 32 * i] = value<T>(row_of(p.q, t, head), lane + 32 * i);
-      g_row[warp][lane + 32 * i] = value<T>(row_of(p.d_o, t, head), lane + 32 * i);
+      for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(w, value<T>(row, lane + 32 * c), acc[c]);
     }
-    __syncwarp();
-    const float lse = p.lse[r], delta = p.delta[r];
-    float acc[D / 32] = {};
-    for (int j0 = 0; j0 < vis; j0 += 32) {
-      const int j = j0 + lane, count = min(32, vis - j0);
-      float ds = 0.0f;
-      if (j < vis) {
-        const float x = dot<T, D>(q_row[warp], row_of(p.k, kv0 + j, kh)) * p.scale;
-        ds = expf(x - lse) * (dot<T, D>(g_row[warp], row_of(p.v, kv0 + j, kh)) - delta) * p.scale;
+    bool lost = true;  // every column is NaN: nothing brings it back
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) lost &= acc[c] != acc[c];
+    if (__all_sync(kAll, lost)) break;
+  }
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) put<T>(row_of(p.dq, t, head), lane + 32 * c, lse == -INFINITY ? 0.0f : acc[c]);
+}
+
+// Row t of the keys' and values' gradients: key j of m, n queries from q0 on.
+template <class T, int D>
+__device__ void dkv_row(const PackedParams& p, int t, int kh, int j, int m, int q0, int n, float* k_row, float* v_row) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    k_row[lane + 32 * c] = value<T>(row_of(p.k, t, kh), lane + 32 * c);
+    v_row[lane + 32 * c] = value<T>(row_of(p.v, t, kh), lane + 32 * c);
+  }
+  __syncwarp();
+  float ak[D / 32] = {}, av[D / 32] = {};
+  const int i_first = first_query(p.causal, n, m, j);
+  bool lost = false;
+  for (int g = 0; g < p.G && !lost; ++g) {
+    const int head = kh * p.G + g;
+    for (int i0 = i_first; i0 < n && !lost; i0 += 32) {
+      const int i = i0 + lane, count = min(32, n - i0);
+      float w = 0.0f, ds = 0.0f;
+      if (i < n) {
+        const long long at = (long long)(q0 + i) * p.q_heads + head;
+        const float x = dot<T, D>(k_row, row_of(p.q, q0 + i, head)) * p.scale, lse = p.lse[at];
+        w = lse == -INFINITY ? 0.0f : expf(x - lse);
+        ds = w * (dot<T, D>(v_row, row_of(p.d_o, q0 + i, head)) - p.row_stats[(size_t)head * p.stat_pitch + q0 + i].y) * p.scale;
       }
       for (int k = 0; k < count; ++k) {
-        const float w = __shfl_sync(kAll, ds, k);
-        const unsigned char* row = row_of(p.k, kv0 + j0 + k, kh);
+        const float wk = __shfl_sync(kAll, w, k), dsk = __shfl_sync(kAll, ds, k);
+        const unsigned char *qr = row_of(p.q, q0 + i0 + k, head), *gr = row_of(p.d_o, q0 + i0 + k, head);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(w, value<T>(row, lane + 32 * i), acc[i]);
+        for (int e = 0; e < D / 32; ++e) {
+          av[e] = fmaf(wk, value<T>(gr, lane + 32 * e), av[e]);
+          ak[e] = fmaf(dsk, value<T>(qr, lane + 32 * e), ak[e]);
+        }
       }
-      bool lost = true;  // every column is NaN: nothing brings it back
+      bool gone = true;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) lost &= acc[i] != acc[i];
-      if (__all_sync(kAll, lost)) break;
+      for (int e = 0; e < D / 32; ++e) gone &= av[e] != av[e] && ak[e] != ak[e];
+      lost = __all_sync(kAll, gone);
     }
+  }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) put<T>(out, lane + 32 * i, lse == -INFINITY ? 0.0f : acc[i]);
+  for (int e = 0; e < D / 32; ++e) {
+    put<T>(row_of(p.dk, t, kh), lane + 32 * e, ak[e]);
+    put<T>(row_of(p.dv, t, kh), lane + 32 * e, av[e]);
   }
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps) rows_dkv_kernel(const PackedParams p, const uint32_t* redo) {
-  __shared__ float k_row[kWarps][D], v_row[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = (long long)p.kv_tokens * p.kv_heads;
-  for (long long r = (long long)blockIdx.x * kWarps + warp; r < rows; r += (long long)gridDim.x * kWarps) {
-    const int t = (int)(r / p.kv_heads), kh = (int)(r - (long long)t * p.kv_heads);
-    const int b = sequence_of(p.kv_start, p.B, t);
-    int first = 0, n = 0, kv0 = 0, m = 0;
-    bool bad = false;
-    if (b >= 0) {
-      extent(p.q_start, p.q_tokens, b, first, n, bad);
-      extent(p.kv_start, p.kv_tokens, b, kv0, m, bad);
-    }
-    unsigned char *dk = row_of(p.dk, t, kh), *dv = row_of(p.dv, t, kh);
-    if (b < 0 || t < kv0 || t >= kv0 + m) {
-      if (p.fill)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          put<T>(dk, lane + 32 * i, 0.0f);
-          put<T>(dv, lane + 32 * i, 0.0f);
-        }
-      continue;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      k_row[warp][lane + 32 * i] = value<T>(row_of(p.k, t, kh), lane + 32 * i);
-      v_row[warp][lane + 32 * i] = value<T>(row_of(p.v, t, kh), lane + 32 * i);
-    }
-    __syncwarp();
-    float ak[D / 32] = {}, av[D / 32] = {};
-    const int i_first = first_query(p.causal, n, m, t - kv0);
-    bool lost = false;
-    for (int g = 0; g < p.G && !lost; ++g) {
-      const int head = kh * p.G + g;
-      for (int i0 = i_first; i0 < n && !lost; i0 += 32) {
-        const int i = i0 + lane, count = min(32, n - i0);
-        float w = 0.0f, ds = 0.0f;
-        if (i < n) {
-          const long long at = (long long)(first + i) * p.q_heads + head;
-          const float x = dot<T, D>(k_row[warp], row_of(p.q, first + i, head)) * p.scale, lse = p.lse[at];
-          w = lse == -INFINITY ? 0.0f : expf(x - lse);
-          ds = w * (dot<T, D>(v_row[warp], row_of(p.d_o, first + i, head)) - p.delta[at]) * p.scale;
-        }
-        for (int k = 0; k < count; ++k) {
-          const float wk = __shfl_sync(kAll, w, k), dsk = __shfl_sync(kAll, ds, k);
-          const unsigned char *qr = row_of(p.q, first + i0 + k, head), *gr = row_of(p.d_o, first + i0 + k, head);
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            av[e] = fmaf(wk, value<T>(gr, lane + 32 * e), av[e]);
-            ak[e] = fmaf(dsk, value<T>(qr, lane + 32 * e), ak[e]);
-          }
-        }
-        bool gone = true;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) gone &= av[e] != av[e] && ak[e] != ak[e];
-        lost = __all_sync(kAll, gone);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      put<T>(dk, lane + 32 * e, ak[e]);
-      put<T>(dv, lane + 32 * e, av[e]);
-    }
-  }
+__global__ void __launch_bounds__(32 * kWarps)
+    redo_dq_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
+  __shared__ float rows[kWarps][2][D];
+  grid_dependency_sync();
+  const int warp = threadIdx.x >> 5;
+  each_flagged<kGradFlags, 2>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+    if (!row_not_finite<T, D>(row_of(p.dq, t, head))) return;
+    dq_row<T, D>(p, t, head, i, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
+  });
+  if (p.fill)
+    each_spare<D>(p.q_start, p.B, p.q_tokens, p.q_heads, [&](int t, int head, int c) { clear8(p.dq, t, head, c); });
+}
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kWarps)
+    redo_dkv_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
+  __shared__ float rows[kWarps][2][D];
+  grid_dependency_sync();
+  const int warp = threadIdx.x >> 5;
+  each_flagged<kGradFlags, 2>(list, flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
+    if (!row_not_finite<T, D>(row_of(p.dk, t, head)) && !row_not_finite<T, D>(row_of(p.dv, t, head))) return;
+    dkv_row<T, D>(p, t, head, j, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
+  });
+  if (p.fill)
+    each_spare<D>(p.kv_start, p.B, p.kv_tokens, p.kv_heads, [&](int t, int head, int c) {
+      clear8(p.dk, t, head, c);
+      clear8(p.dv, t, head, c);
+    });
 }
 
-// Offsets that leave the arrays or do not ascend are reported once.
-__global__ void check_kernel(const PackedParams p) {
+// The list of units: counted and sorted by one block. Work goes by how many of the
+// other array's rows the unit's last (queries) or first (keys) row meets; units of equal work keep
+// no order among themselves, which no result depends on.
+constexpr int kListThreads = 1024, kBuckets = 1024;
+__global__ void __launch_bounds__(kListThreads)
+    list_kernel(const PackedParams p, const int keys, const int rows, const PackedList list) {
+  __shared__ int before[kMaxBatch + 1], warp_sum_[32], bucket[kBuckets];
+  grid_dependency_sync();
+  const int32_t *sa = keys ? p.kv_start : p.q_start, *sb = keys ? p.q_start : p.kv_start;
+  const int ta = keys ? p.kv_tokens : p.q_tokens, tb = keys ? p.q_tokens : p.kv_tokens;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    int first, n;
-    extent(p.q_start, p.q_tokens, b, first, n, bad);
-    extent(p.kv_start, p.kv_tokens, b, first, n, bad);
+  // units before each sequence
+  int done = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kListThreads) {
+    const int b = b0 + tid;
+    int mine = 0;
+    if (b < p.B) {
+      int first, n;
+      extent(sb, tb, b, first, n, bad);
+      extent(sa, ta, b, first, n, bad);
+      mine = (n + rows - 1) / rows;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum_[warp] = incl;
+    __syncthreads();
+    int pre = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) pre += warp_sum_[w];
+      all += warp_sum_[w];
+    }
+    if (b < p.B) before[b] = done + pre + incl - mine;
+    done += all;
+    __syncthreads();
+  }
+  // offsets that do not ascend may name more units than the list holds
+  const int total = min(done, most_units(ta, p.B, rows));
+  if (tid == 0) {
+    before[p.B] = done;
+    *list.count = total;
+  }
+  for (int i = tid; i < kBuckets; i += kListThreads) bucket[i] = 0;
+  __syncthreads();
+  auto unit_at = [&](int k, int& work) {
+    int lo = 0, hi = p.B;  // the last b with before[b] <= k
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= k)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    PackedUnit u = {};
+    int first, fb;
+    extent(sa, ta, lo, first, u.n, bad);
+    extent(sb, tb, lo, fb, u.m, bad);
+    u.i0 = (k - before[lo]) * rows;
+    u.row0 = first + u.i0;
+    u.rows = min(rows, u.n - u.i0);
+    u.other0 = fb;
+    const int meets = keys ? u.m - first_query(p.causal, u.m, u.n, u.i0) : seen_keys(p.causal, u.n, u.m, u.i0 + u.rows - 1);
+    work = kBuckets - 1 - min(kBuckets - 1, (max(0, meets) + 127) / 128);  // most work: bucket 0
+    return u;
+  };
+  for (int k = tid; k < total; k += kListThreads) {
+    int work;
+    unit_at(k, work);
+    atomicAdd(&bucket[work], 1);
+  }
+  __syncthreads();
+  {
+    const int mine = bucket[tid];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum_[warp] = incl;
+    __syncthreads();
+    int pre = 0;
+    for (int w = 0; w < warp; ++w) pre += warp_sum_[w];
+    bucket[tid] = pre + incl - mine;
+  }
+  __syncthreads();
+  for (int k = tid; k < total; k += kListThreads) {
+    int work;
+    const PackedUnit u = unit_at(k, work);
+    list.units[atomicAdd(&bucket[work], 1)] = u;
   }
   if (bad) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
 }
 
-unsigned blocks_for(long long rows) {
-  const long long n = (rows + kWarps - 1) / kWarps;
-  return (unsigned)(n < 152 * 64 ? n : 152 * 64);
+template <class... A>
+int launch(void (*kernel)(A...), unsigned grid, unsigned threads, void* stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-template <class T>
-int forward(const PackedParams& p, int d, const uint32_t* redo, cudaStream_t st) {
-  const unsigned grid = blocks_for((long long)p.q_tokens * p.q_heads);
-  if (!grid) return 0;
-  if (d == 64)
-    rows_forward_kernel<T, 64><<<grid, 32 * kWarps, 0, st>>>(p, redo);
-  else
-    rows_forward_kernel<T, 128><<<grid, 32 * kWarps, 0, st>>>(p, redo);
-  return (int)cudaGetLastError();
-}
-template <int D>
-int grad(const PackedParams& p, const uint32_t* redo_q, const uint32_t* redo_kv, cudaStream_t st) {
-  const unsigned grid_q = blocks_for((long long)p.q_tokens * p.q_heads), grid_kv = blocks_for((long long)p.kv_tokens * p.kv_heads);
-  if (grid_q) rows_dq_kernel<Bf16, D><<<grid_q, 32 * kWarps, 0, st>>>(p, redo_q);
-  if (grid_kv) rows_dkv_kernel<Bf16, D><<<grid_kv, 32 * kWarps, 0, st>>>(p, redo_kv);
-  return (int)cudaGetLastError();
+// Blocks for the flags' kernels: a thread a flag, which in sound data is all they do.
+unsigned redo_blocks(long long flags) {
+  const long long n = (flags + 32 * kWarps - 1) / (32 * kWarps);
+  return (unsigned)(n < 1 ? 1 : n < 304 ? n : 304);
 }
 
 }  // namespace
 
-int launch_rows_forward(const PackedParams& p, int dtype, int head_dim, const uint32_t* redo, void* stream) {
-  return dtype == DFLASH_BF16 ? forward<Bf16>(p, head_dim, redo, (cudaStream_t)stream)
-                              : forward<F16>(p, head_dim, redo, (cudaStream_t)stream);
+int launch_list(const PackedParams& p, bool keys, int rows, const PackedList& list, void* stream) {
+  return launch(list_kernel, 1u, (unsigned)kListThreads, stream, p, (int)keys, rows, list);
+}
+int launch_redo_forward(const PackedParams& p, int dtype, int d, const PackedList& list, const uint8_t* flags,
+                        void* stream) {
+  const unsigned grid = redo_blocks((long long)most_units(p.q_tokens, p.B, kForwardRows) * p.q_heads * kForwardFlags);
+  if (dtype == DFLASH_BF16)
+    return d == 64 ? launch(redo_forward_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p, list, flags)
+                   : launch(redo_forward_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p, list, flags);
+  return d == 64 ? launch(redo_forward_kernel<F16, 64>, grid, 32u * kWarps, stream, p, list, flags)
+                 : launch(redo_forward_kernel<F16, 128>, grid, 32u * kWarps, stream, p, list, flags);
+}
+int launch_redo_dq(const PackedParams& p, int d, const PackedList& list, const uint8_t* flags, void* stream) {
+  const unsigned grid = redo_blocks((long long)most_units(p.q_tokens, p.B, kGradRows) * p.q_heads * kGradFlags);
+  return d == 64 ? launch(redo_dq_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p, list, flags)
+                 : launch(redo_dq_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p, list, flags);
+}
+int launch_redo_dkv(const PackedParams& p, int d, const PackedList& list, const uint8_t* flags, void* stream) {
+  const unsigned grid = redo_blocks((long long)most_units(p.kv_tokens, p.B, kGradRows) * p.kv_heads * kGradFlags);
+  return d == 64 ? launch(redo_dkv_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p, list, flags)
+                 : launch(redo_dkv_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p, list, flags);
 }
 int launch_delta(const PackedParams& p, int head_dim, void* stream) {
   const long long threads = (long long)p.q_tokens * p.q_heads * (head_dim / 8);
   const unsigned grid = (unsigned)((threads + 32 * kWarps - 1) / (32 * kWarps));
   if (!grid) return 0;
-  if (head_dim == 64)
-    delta_kernel<Bf16, 64><<<grid, 32 * kWarps, 0, (cudaStream_t)stream>>>(p);
-  else
-    delta_kernel<Bf16, 128><<<grid, 32 * kWarps, 0, (cudaStream_t)stream>>>(p);
-  return (int)cudaGetLastError();
-}
-int launch_rows_grad(const PackedParams& p, int head_dim, const uint32_t* redo_q, const uint32_t* redo_kv, void* stream) {
-  return head_dim == 64 ? grad<64>(p, redo_q, redo_kv, (cudaStream_t)stream)
-                        : grad<128>(p, redo_q, redo_kv, (cudaStream_t)stream);
+  return head_dim == 64 ? launch(delta_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p)
+                        : launch(delta_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p);
 }
 
+// ---- workspaces
+// Forward: the list of queries, their flags. Backward: delta, both lists, both sets of flags.
+namespace {
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+size_t flag_bytes(int tokens, int B, int rows, int heads) { return up((size_t)most_units(tokens, B, rows) * heads * 8); }
+static_assert(kForwardFlags == 8 && kGradFlags == 8, "flags of a unit and head");
+// Pairs of a head: an even count, and room behind the last row for a whole tile's pairs.
+int stat_pitch(int tokens) { return (tokens + 131) / 2 * 2; }
+}  // namespace
+
 size_t packed_workspace(int B, int q_tokens, int kv_tokens, int q_heads, int kv_heads, int head_dim, bool backward) {
-  return backward ? ((size_t)q_tokens * q_heads * sizeof(float) + 255) / 256 * 256 + 256 : 256;
+  if (!backward) return list_bytes(q_tokens, B, kForwardRows) + flag_bytes(q_tokens, B, kForwardRows, q_heads);
+  return up((size_t)stat_pitch(q_tokens) * q_heads * sizeof(float2)) + list_bytes(q_tokens, B, kGradRows) +
+         flag_bytes(q_tokens, B, kGradRows, q_heads) + list_bytes(kv_tokens, B, kGradRows) +
+         flag_bytes(kv_tokens, B, kGradRows, kv_heads);
 }
+
 int launch_packed(const PackedParams& p, int dtype, int head_dim, int sms, void* stream) {
-  check_kernel<<<1, 256, 0, (cudaStream_t)stream>>>(p);
-  return launch_rows_forward(p, dtype, head_dim, nullptr, stream);
+  const PackedList list = list_at(p.ws);
+  uint8_t* flags = p.ws + list_bytes(p.q_tokens, p.B, kForwardRows);
+  int e = launch_list(p, false, kForwardRows, list, stream);
+  if (!e) e = launch_forward_tc(p, dtype, head_dim, list, flags, sms, stream);
+  return e ? e : launch_redo_forward(p, dtype, head_dim, list, flags, stream);
 }
-int launch_packed_grad(const PackedParams& p, int head_dim, int sms, void* stream) {
-  PackedParams q = p;
-  q.delta = reinterpret_cast<float*>(p.ws);
-  const int e = launch_delta(q, head_dim, stream);
-  return e ? e : launch_rows_grad(q, head_dim, nullptr, nullptr, stream);
+
+int launch_packed_grad(const PackedParams& p0, int head_dim, int sms, void* stream) {
+  PackedParams p = p0;
+  unsigned char* ws = p.ws;
+  p.row_stats = reinterpret_cast<float2*>(ws);
+  p.stat_pitch = stat_pitch(p.q_tokens);
+  ws += up((size_t)p.stat_pitch * p.q_heads * sizeof(float2));
+  const PackedList queries = list_at(ws);
+  ws += list_bytes(p.q_tokens, p.B, kGradRows);
+  uint8_t* q_flags = ws;
+  ws += flag_bytes(p.q_tokens, p.B, kGradRows, p.q_heads);
+  const PackedList keys = list_at(ws);
+  ws += list_bytes(p.kv_tokens, p.B, kGradRows);
+  uint8_t* kv_flags = ws;
+  int e = launch_delta(p, head_dim, stream);
+  if (!e && p.q_tokens) {
+    e = launch_list(p, false, kGradRows, queries, stream);
+    if (!e) e = launch_dq_tc(p, head_dim, queries, q_flags, sms, stream);
+    if (!e) e = launch_redo_dq(p, head_dim, queries, q_flags, stream);
+  }
+  if (!e && p.kv_tokens) {
+    e = launch_list(p, true, kGradRows, keys, stream);
+    if (!e) e = launch_dkv_tc(p, head_dim, keys, kv_flags, sms, stream);
+    if (!e) e = launch_redo_dkv(p, head_dim, keys, kv_flags, stream);
+  }
+  return e;
 }
 
 }  // namespace dflash

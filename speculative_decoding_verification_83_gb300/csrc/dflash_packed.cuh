@@ -51,10 +51,44 @@ __device__ __forceinline__ float with_low(uint32_t hi, int low) {
   return __uint_as_float((hi << 16) + (finite ? (uint32_t)(low * 256) : 0u));
 }
 
-// Rows one by one (dflash_packed.cu): every row, or with `redo` those of the tiles
-// whose flag is set that hold a value which is not finite.
-int launch_rows_forward(const PackedParams& p, int dtype, int head_dim, const uint32_t* redo, void* stream);
-int launch_rows_grad(const PackedParams& p, int head_dim, const uint32_t* redo_q, const uint32_t* redo_kv, void* stream);
+// ---- units of work: a run of rows of one sequence, for each head
+struct PackedUnit {
+  int row0, rows;  // the unit's first row in its array, its rows
+  int i0, n;       // that row's place in its sequence, the sequence's rows
+  int other0, m;   // the sequence's rows in the other array: keys of queries, queries of keys
+  int unused0, unused1;
+};
+// The list of the tiles of `rows` queries (or keys), those with the most work first;
+// the first word counts them.
+struct PackedList {
+  int* count;
+  PackedUnit* units;
+};
+__host__ __device__ inline int most_units(int tokens, int B, int rows) { return tokens / rows + (B < tokens ? B : tokens); }
+inline size_t list_bytes(int tokens, int B, int rows) {
+  return 256 + ((size_t)most_units(tokens, B, rows) * sizeof(PackedUnit) + 255) / 256 * 256;
+}
+inline PackedList list_at(unsigned char* p) { return {reinterpret_cast<int*>(p), reinterpret_cast<PackedUnit*>(p + 256)}; }
+int launch_list(const PackedParams& p, bool keys, int rows, const PackedList& list, void* stream);
+
+// The tensor cores' kernels leave rows whose masked keys or queries hold values that
+// are not finite as NaN (0 times such a value), and a flag for 32 rows with a result that is
+// not finite, 8 for each unit and head. These kernels go through the flagged rows
+// one by one, with exact masks, and set the rows of no sequence to 0.
+int launch_redo_forward(const PackedParams& p, int dtype, int head_dim, const PackedList& list, const uint8_t* flags,
+                        void* stream);
+int launch_redo_dq(const PackedParams& p, int head_dim, const PackedList& list, const uint8_t* flags, void* stream);
+int launch_redo_dkv(const PackedParams& p, int head_dim, const PackedList& list, const uint8_t* flags, void* stream);
 int launch_delta(const PackedParams& p, int head_dim, void* stream);
+
+// The products (dflash_packed_fwd.cu, dflash_packed_bwd.cu).
+int launch_forward_tc(const PackedParams& p, int dtype, int head_dim, const PackedList& list, uint8_t* flags, int sms,
+                      void* stream);
+int launch_dq_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, int sms, void* stream);
+int launch_dkv_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, int sms, void* stream);
+constexpr int kForwardRows = 256, kGradRows = 128;  // of a unit
+constexpr int kForwardFlags = 8;  // of a unit and head: one for each 32 rows
+constexpr int kGradFlags = 8;     // ... two for each 32 rows, one for each half of the columns
+constexpr int kMaxBatch = 2048;
 
 }  // namespace dflash

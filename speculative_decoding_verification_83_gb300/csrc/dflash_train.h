@@ -5,6 +5,8 @@
 // points and their argument checks are in dflash_train_abi.cu.
 #pragma once
 
+#include <vector_types.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -63,7 +65,9 @@ struct PackedParams {
   int8_t* low;               // [q_tokens, q_heads, head_dim] or null: what the outputs' rounding left, see out_low
   float* lse;                // [q_tokens, q_heads]
   HeadRows d_o, dq, dk, dv;  // backward
-  float* delta;              // backward: [q_tokens, q_heads], sum of d_o o
+  // backward: by head, stat_pitch rows each: lse log2 e (a row that sees nothing: +inf) and delta = sum of d_o o
+  float2* row_stats;
+  int stat_pitch;
   const int32_t *q_start, *kv_start;
   int B, q_tokens, kv_tokens, q_heads, kv_heads, G;
   float scale;

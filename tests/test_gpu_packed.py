@@ -176,20 +176,24 @@ def test_rows_of_no_sequence(dv):
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_values_that_are_not_seen(dv, bad):
-    """What a sequence holds that is not finite does not reach its neighbours, nor rows before it (causal)."""
+    """What a sequence holds that is not finite does not reach its neighbours, nor rows before it (causal). (The
+    rows beside it come from another kernel, so they are held to the definition, not to equal bits.)"""
     cq = [100, 70, 130]
     q, k, v, do = inputs(9, 300, 300, 4, 2, 64, BF)
-    clean = dv.packed_attention(q, k, v, starts(cq), return_lse=True)
     k[100:170], v[100:170], q[100:170] = bad, bad, bad
-    v[250, 1, 5] = bad
     out, lse = dv.packed_attention(q, k, v, starts(cq), return_lse=True)
-    assert torch.equal(out[:100], clean[0][:100]) and torch.equal(lse[:100], clean[1][:100])
-    assert torch.equal(out[170:250], clean[0][170:250]) and torch.equal(lse[170:], clean[1][170:])
-    rest = torch.ones((50, 4, 64), device=DEV, dtype=torch.bool)
-    rest[:, 2:, 5] = False
-    near = (out[250:].float() - clean[0][250:].float()).abs()[rest]  # (by another kernel where a value is odd)
-    assert (near <= 2.0 ** -6 * clean[0][250:].float().abs().amax()).all()
-    hit = out[250:, 2:, 5].float()
+    for lo, hi in ((0, 100), (170, 300)):
+        check(out[lo:hi], lse[lo:hi], None, q[lo:hi], k[lo:hi], v[lo:hi], do, [hi - lo], [hi - lo], 0.125, True)
+    v[250, 1, 5] = bad
+    odd, lse2 = dv.packed_attention(q, k, v, starts(cq), return_lse=True)
+    assert ((lse2[170:] - lse[170:]).abs() <= 2.0 ** -18 * (1 + lse[170:].abs())).all()
+    v[250, 1, 5] = 0.0  # beside it, all is as with any other value there
+    o, _, e, _, _, _ = refs.attention64(q[170:].double(), k[170:].double(), v[170:].double(), 0.125,
+                                        refs.sees(130, 130, True).to(DEV), refs.U[BF])
+    rest = torch.ones((130, 4, 64), device=DEV, dtype=torch.bool)
+    rest[80:, 2:, 5] = False
+    assert ((odd[170:].double() - o).abs() <= refs.rounded(o, e, BF))[rest].all()
+    hit = odd[250:, 2:, 5].float()
     assert hit.isnan().all() if math.isnan(bad) else (hit == bad).all()
 
 
