@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   tc::cluster_sync();  // both CTAs' barriers are there before a load or an arrival reaches them
   tc::fence_after();
-  const uint32_t tmem = S.tmem;
+  constexpr uint32_t tmem = 0;  // (all of it is ours, so it begins at 0)
 
   if (warp == 0) {
     if (lane == 0) {
@@ -194,21 +194,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
         (void)wait_from(&S.empty[q % kStages], (uint32_t)((q / kStages) & 1), t1);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t id = tc::idesc<Bf16>(kTile, kTile, kAMn, kBMn);
-      long long it = 0;
-      int lt = 0;
+      const uint32_t lead = tc::elect();
+      int slot = 0, s = 0, use = 0;  // accumulator, stage
+      uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += pairs, ++lt) {
-        const int slot = lt & 1, use = lt >> 1, steps = tile_at(p, t).steps;
-        if (use > 0 && !wait_bar_cluster(&S.acc_empty[slot], (uint32_t)((use - 1) & 1), S)) {
+      for (int t = first; t < tiles && ok; t += pairs) {
+        const int steps = tile_at(p, t).steps;
+        if (use > 0 && !__all_sync(0xffffffffu, wait_bar_cluster(&S.acc_empty[slot], (uint32_t)((use - 1) & 1), S))) {
           ok = false;
           break;
         }
         tc::fence_after();
-        for (int ks = 0; ks < steps; ++ks, ++it) {
-          const int s = (int)(it % kStages);
-          if (!wait_bar(&S.full[s], (uint32_t)((it / kStages) & 1), S)) {
+        for (int ks = 0; ks < steps; ++ks) {
+          if (!__all_sync(0xffffffffu, wait_bar(&S.full[s], phase, S))) {
             ok = false;
             break;
           }
@@ -217,11 +217,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           const uint64_t bd = tc::operand(b_mem(s), kBMn ? kOperandBytes / 2 : 16u);
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)  // 16 inner values: 32 bytes of a row, or 16 rows
-            tc::mma_pair(tmem + (uint32_t)(slot * kTile), ad + (uint64_t)(kAMn ? 128 : 2) * kk,
-                         bd + (uint64_t)(kBMn ? 128 : 2) * kk, id, (ks | kk) != 0);
-          tc::commit_pair(&S.empty[s]);
+            tc::mma_pair((uint32_t)(slot * kTile), ad + (uint64_t)((kAMn ? 128 : 2) * kk),
+                         bd + (uint64_t)((kBMn ? 128 : 2) * kk), id, (ks | kk) != 0, lead);
+          tc::commit_pair(&S.empty[s], lead);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
         }
-        if (ok) tc::commit_pair(&S.acc_full[slot]);
+        if (ok) tc::commit_pair(&S.acc_full[slot], lead);
+        use += slot;
+        slot ^= 1;
       }
       if (!ok) S.failed = 1;
     }

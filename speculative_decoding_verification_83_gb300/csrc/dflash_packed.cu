@@ -119,8 +119,8 @@ __device__ void attend_row(const PackedParams& p, int t, int head, int i, int n,
 }
 
 // Goes through the flags; row(t, head, i, unit) is called by one warp for every row
-// of a flagged 32. kSame flags in a row stand for the same 32.
-template <int kPer, int kSame, class F>
+// of a flagged 32, for either half's flag.
+template <int kPer, class F>
 __device__ __forceinline__ void each_flagged(const PackedList& list, const uint8_t* flags, int heads, F row) {
   const long long total = (long long)*list.count * heads * kPer;
   const int warp = threadIdx.x >> 5;
@@ -129,7 +129,7 @@ __device__ __forceinline__ void each_flagged(const PackedList& list, const uint8
     if (!__syncthreads_or(at < total && flags[at])) continue;
     for (long long f = base; f < min(total, base + blockDim.x); ++f) {
       if (!flags[f]) continue;
-      const int part = (int)(f % kPer) / kSame, head = (int)(f / kPer % heads);
+      const int part = (int)(f % kPer) / 2, head = (int)(f / kPer % heads);
       const PackedUnit u = list.units[f / kPer / heads];
       for (int r = 32 * part + warp; r < min(u.rows, 32 * part + 32); r += kWarps) row(u.row0 + r, head, u.i0 + r, u);
     }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     redo_forward_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
   __shared__ float q_row[kWarps][D];
   grid_dependency_sync();
-  each_flagged<kForwardFlags, 1>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+  each_flagged<kForwardFlags>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
     if (row_not_finite<T, D>(row_of(p.o, t, head)))
       attend_row<T, D>(p, t, head, i, u.n, u.other0, u.m, q_row[threadIdx.x >> 5]);
   });
@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p
   if (r < rows && lane == 0) {
     const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
     const float lse = p.lse[r];
-    p.row_stats[(size_t)head * p.stat_pitch + t] = make_float2(lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f, s);
+    float* st = p.row_stats + (size_t)head * 2 * p.stat_pitch;
+    st[t] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    st[p.stat_pitch + t] = s;
   }
 }
 
@@ -213,7 +215,7 @@ __device__ void dq_row(const PackedParams& p, int t, int head, int i, int n, int
     g_row[lane + 32 * c] = value<T>(row_of(p.d_o, t, head), lane + 32 * c);
   }
   __syncwarp();
-  const float lse = p.lse[r], delta = p.row_stats[(size_t)head * p.stat_pitch + t].y;
+  const float lse = p.lse[r], delta = p.row_stats[((size_t)head * 2 + 1) * p.stat_pitch + t];
   float acc[D / 32] = {};
   for (int j0 = 0; j0 < vis; j0 += 32) {
     const int j = j0 + lane, count = min(32, vis - j0);
@@ -260,7 +262,7 @@ __device__ void dkv_row(const PackedParams& p, int t, int kh, int j, int m, int 
         const long long at = (long long)(q0 + i) * p.q_heads + head;
         const float x = dot<T, D>(k_row, row_of(p.q, q0 + i, head)) * p.scale, lse = p.lse[at];
         w = lse == -INFINITY ? 0.0f : expf(x - lse);
-        ds = w * (dot<T, D>(v_row, row_of(p.d_o, q0 + i, head)) - p.row_stats[(size_t)head * p.stat_pitch + q0 + i].y) * p.scale;
+        ds = w * (dot<T, D>(v_row, row_of(p.d_o, q0 + i, head)) - p.row_stats[((size_t)head * 2 + 1) * p.stat_pitch + q0 + i]) * p.scale;
       }
       for (int k = 0; k < count; ++k) {
         const float wk = __shfl_sync(kAll, w, k), dsk = __shfl_sync(kAll, ds, k);
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   __shared__ float rows[kWarps][2][D];
   grid_dependency_sync();
   const int warp = threadIdx.x >> 5;
-  each_flagged<kGradFlags, 2>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+  each_flagged<kGradFlags>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
     if (!row_not_finite<T, D>(row_of(p.dq, t, head))) return;
     dq_row<T, D>(p, t, head, i, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
   });
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   __shared__ float rows[kWarps][2][D];
   grid_dependency_sync();
   const int warp = threadIdx.x >> 5;
-  each_flagged<kGradFlags, 2>(list, flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
+  each_flagged<kGradFlags>(list, flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
     if (!row_not_finite<T, D>(row_of(p.dk, t, head)) && !row_not_finite<T, D>(row_of(p.dv, t, head))) return;
     dkv_row<T, D>(p, t, head, j, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
   });
@@ -467,15 +469,16 @@ int launch_delta(const PackedParams& p, int head_dim, void* stream) {
 // Forward: the list of queries, their flags. Backward: delta, both lists, both sets of flags.
 namespace {
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
-size_t flag_bytes(int tokens, int B, int rows, int heads) { return up((size_t)most_units(tokens, B, rows) * heads * 8); }
-static_assert(kForwardFlags == 8 && kGradFlags == 8, "flags of a unit and head");
-// Pairs of a head: an even count, and room behind the last row for a whole tile's pairs.
-int stat_pitch(int tokens) { return (tokens + 131) / 2 * 2; }
+size_t flag_bytes(int tokens, int B, int rows, int heads) {
+  return up((size_t)most_units(tokens, B, rows) * heads * (rows / 16));
+}
+// Rows of a head's statistics: a multiple of 4, and room behind the last row for a whole tile.
+int stat_pitch(int tokens) { return (tokens + 131) / 4 * 4; }
 }  // namespace
 
 size_t packed_workspace(int B, int q_tokens, int kv_tokens, int q_heads, int kv_heads, int head_dim, bool backward) {
   if (!backward) return list_bytes(q_tokens, B, kForwardRows) + flag_bytes(q_tokens, B, kForwardRows, q_heads);
-  return up((size_t)stat_pitch(q_tokens) * q_heads * sizeof(float2)) + list_bytes(q_tokens, B, kGradRows) +
+  return up((size_t)stat_pitch(q_tokens) * q_heads * 2 * sizeof(float)) + list_bytes(q_tokens, B, kGradRows) +
          flag_bytes(q_tokens, B, kGradRows, q_heads) + list_bytes(kv_tokens, B, kGradRows) +
          flag_bytes(kv_tokens, B, kGradRows, kv_heads);
 }
@@ -491,9 +494,9 @@ int launch_packed(const PackedParams& p, int dtype, int head_dim, int sms, void*
 int launch_packed_grad(const PackedParams& p0, int head_dim, int sms, void* stream) {
   PackedParams p = p0;
   unsigned char* ws = p.ws;
-  p.row_stats = reinterpret_cast<float2*>(ws);
+  p.row_stats = reinterpret_cast<float*>(ws);
   p.stat_pitch = stat_pitch(p.q_tokens);
-  ws += up((size_t)p.stat_pitch * p.q_heads * sizeof(float2));
+  ws += up((size_t)p.stat_pitch * p.q_heads * 2 * sizeof(float));
   const PackedList queries = list_at(ws);
   ws += list_bytes(p.q_tokens, p.B, kGradRows);
   uint8_t* q_flags = ws;

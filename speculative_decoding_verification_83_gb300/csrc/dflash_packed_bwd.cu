@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 320, kMmaWarp = 8, kLoadWarp = 9, kWorkWarps = 8;
 constexpr int kTileRows = 128;
-constexpr uint32_t kStatBytes = 1040;  // 130 pairs: 128 from an even place on, or from the one after it
+constexpr uint32_t kStatBytes = 1024;  // 128 of lse and 128 of delta
 
 template <int D>
 struct GradShape {
@@ -45,7 +45,6 @@ struct GradShared {
   uint64_t own_full, own_empty;       // the unit's own two tiles
   uint64_t full1[5], empty1[5], full2[4], empty2[4];
   uint64_t s_full[2], dp_full, p_full, ds_full, acc_full, drained;
-  uint64_t met[4];
   uint32_t tmem;
   volatile int failed;
 };
@@ -53,13 +52,15 @@ template <int D>
 constexpr size_t kGradSmem = GradShape<D>::kBars + sizeof(GradShared);
 static_assert(kGradSmem<128> <= 232448, "one CTA's shared memory (227 KB)");
 
-__device__ __forceinline__ const float2* stats_of(const PackedParams& p, int head) {
-  return p.row_stats + (size_t)head * p.stat_pitch;
+// A head's statistics: lse, then (delta_at further on) delta
+__device__ __forceinline__ const float* stats_of(const PackedParams& p, int head) {
+  return p.row_stats + (size_t)head * 2 * p.stat_pitch;
 }
 
-// What all roles of both kernels begin with: barriers, tensor memory.
+// What all roles of both kernels begin with: barriers, tensor memory (all of it, so it
+// begins at 0).
 template <int D>
-__device__ __forceinline__ uint32_t begin(GradShared& S, int warp, uint32_t second_readers) {
+__device__ __forceinline__ void begin(GradShared& S, int warp, uint32_t second_readers) {
   using W = GradShape<D>;
   if (threadIdx.x == 0) {
     mbar_init(&S.own_full, 1);
@@ -78,7 +79,6 @@ __device__ __forceinline__ uint32_t begin(GradShared& S, int warp, uint32_t seco
     mbar_init(&S.ds_full, kWorkWarps);
     mbar_init(&S.acc_full, 1);
     mbar_init(&S.drained, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&S.met[i], 2);
     S.failed = 0;
     fence_barrier_init();
   }
@@ -86,15 +86,13 @@ __device__ __forceinline__ uint32_t begin(GradShared& S, int warp, uint32_t seco
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = S.tmem;
   grid_dependency_sync();
-  return tmem;
 }
-__device__ __forceinline__ void end(const PackedParams& p, GradShared& S, uint32_t tmem, int warp) {
+__device__ __forceinline__ void end(const PackedParams& p, GradShared& S, int warp) {
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == kMmaWarp) tc::dealloc(tmem, 512);
+  if (warp == kMmaWarp) tc::dealloc(0, 512);
   if (threadIdx.x == 0 && S.failed) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
 }
 
@@ -104,65 +102,80 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
 #pragma unroll
   for (int d = 0; d < D; d += 64) tc::load_3d(dst + (uint32_t)d * 256u, map, d, head, row, bar);
 }
-// D (+)= A B^T over D inner values, both tiles as they lie
+// D (+)= A B^T over D inner values, both tiles as they lie (addresses count in 16 bytes)
 template <int D>
-__device__ __forceinline__ void mma_inner(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_inner(uint32_t d, uint32_t a, uint32_t b, uint32_t lead) {
   constexpr uint32_t id = tc::idesc<Bf16>(128, 128, false, false);
+  const uint64_t ad = tc::operand(a), bd = tc::operand(b);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k)
-    tc::mma_ss(d, tc::operand(a + (uint32_t)((k >> 2) * 16384 + (k & 3) * 32)),
-               tc::operand(b + (uint32_t)((k >> 2) * 16384 + (k & 3) * 32)), id, k > 0);
+    tc::mma_ss(d, ad + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), bd + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), id, k > 0,
+               lead);
 }
 // D (+)= A B over 128 rows of B; A in tensor memory
+// (each half of A's columns lies over that half of the scores)
 template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool add) {
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool add, uint32_t lead) {
   constexpr uint32_t id = tc::idesc<Bf16>(128, D, false, true);
+  const uint64_t bd = tc::operand(b, 16384u);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) tc::mma_ts(d, a + 8 * k, tc::operand(b + k * 2048u, 16384u), id, add || k > 0);
+  for (int k = 0; k < 8; ++k) tc::mma_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, bd + (uint64_t)(k * 128), id, add || k > 0, lead);
 }
+// A tile of a ring of kSlots: its place, and the parity of its round
+template <int kSlots>
+struct RingAt {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
-// The two warps of a lane quarter have both read; bounded like every wait.
-__device__ __forceinline__ bool meet(GradShared& S, int quarter, uint32_t& phase) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&S.met[quarter]);
-  const bool ok = bounded_warp_wait(&S.met[quarter], phase & 1u, &S.failed);
-  ++phase;
-  return ok;
-}
-
-// 32 sums of this thread's row times `factor` to memory as bf16; whether all are finite
-__device__ __forceinline__ bool store32(uint32_t taddr, float factor, bool zero, bool there, unsigned char* dst) {
-  uint32_t y[32], w[16];
-  tc::ld32(taddr, y);
-  tc::wait_ld32(y);
+// Half of a warp's 32 rows of sums times `factor` to memory as bf16 (rows where `zero`
+// holds: 0, whatever the products left there); whether this lane's are finite
+template <int D>
+__device__ __forceinline__ bool store_half(uint32_t taddr, float factor, bool zero, unsigned char* dst, long long stride,
+                                           int rows, int lane) {
+  constexpr int kPieces = D / 16;
+  uint32_t w[4 * kPieces];
   bool fine = true;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    // (a row that sees nothing is 0, whatever the products left there)
-    const float a = zero ? 0.0f : __uint_as_float(y[2 * i]) * factor, b = zero ? 0.0f : __uint_as_float(y[2 * i + 1]) * factor;
-    w[i] = Bf16::pack(a, b);
-    fine &= fabsf(a) < INFINITY && fabsf(b) < INFINITY;
-  }
-  if (there)
+  for (int d = 0; d < D / 2; d += 32) {
+    uint32_t y[32];
+    tc::ld32(taddr + d, y);
+    tc::wait_ld32(y);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < 16; ++i) {
+      const float a = zero ? 0.0f : __uint_as_float(y[2 * i]) * factor, b = zero ? 0.0f : __uint_as_float(y[2 * i + 1]) * factor;
+      w[d / 2 + i] = Bf16::pack(a, b);
+      fine &= fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+    }
+  }
+  store_rows<kPieces>(w, dst, stride, rows, lane);
   return fine;
 }
-__device__ __forceinline__ void clear32(bool there, unsigned char* dst) {
-  if (there)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0u, 0u, 0u, 0u);
+template <int D>
+__device__ __forceinline__ void clear_half(unsigned char* dst, long long stride, int rows, int lane) {
+  constexpr int kPieces = D / 16;
+  uint32_t w[4 * kPieces] = {};
+  store_rows<kPieces>(w, dst, stride, rows, lane);
 }
 
 // ---- keys and values
-// A unit's queries: from i0 on, `tiles` tiles for each of the heads that share the key.
+// A unit's queries: from i0 on, `tiles` tiles for each of the heads that share the
+// key. The first row is a multiple of 4, so that four statistics are one load; up to 3
+// queries in front of the first (or rows of the sequence before) count as masked.
 struct QuerySpan {
   int i0, tiles;
 };
 __device__ __forceinline__ QuerySpan query_span(const PackedUnit& u, int causal) {
   const int i0 = first_query(causal, u.m, u.n, u.i0);  // (u.m queries, u.n keys)
-  return {i0, max(0, (u.m - i0 + kTileRows - 1) / kTileRows)};
+  if (i0 >= u.m) return {0, 0};
+  const int at = i0 - ((u.other0 + i0) & 3);
+  return {at, (u.m - at + kTileRows - 1) / kTileRows};
 }
 
 template <int D>
@@ -179,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   GradShared& S = *reinterpret_cast<GradShared*>(raw + W::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t tmem = begin<D>(S, warp, 1 + kWorkWarps);
-  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + D;
+  begin<D>(S, warp, 1 + kWorkWarps);
+  constexpr uint32_t t_s = 0, t_dp = 128, t_dv = 256, t_dk = 256 + D;
   const uint32_t k_mem = base, v_mem = base + W::kTile;
   const long long work = (long long)*list.count * p.kv_heads;
 
@@ -212,7 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(&S.full2[s2], W::kTile + kStatBytes);
           load_tile<D>(base + W::kRing2 + s2 * W::kTile, &map_do, head, row, &S.full2[s2]);
-          bulk_load(raw + W::kStats + s2 * kStatBytes, stats_of(p, head) + (row & ~1), kStatBytes, &S.full2[s2]);
+          bulk_load(raw + W::kStats + s2 * kStatBytes, stats_of(p, head) + row, kStatBytes / 2, &S.full2[s2]);
+          bulk_load(raw + W::kStats + s2 * kStatBytes + kStatBytes / 2, stats_of(p, head) + p.stat_pitch + row,
+                    kStatBytes / 2, &S.full2[s2]);
         }
       }
       // every copy has landed before the CTA may end
@@ -224,57 +239,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      long long it = 0;  // tiles so far
-      int units = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t phase) {
-        if (!bounded_wait(bar, phase & 1u, &S.failed)) return false;
-        tc::fence_after();
-        return true;
-      };
-      auto q_mem = [&](long long i) { return base + W::kRing1 + (uint32_t)(i % W::kFirst) * W::kTile; };
-      auto do_mem = [&](long long i) { return base + W::kRing2 + (uint32_t)(i % W::kSecond) * W::kTile; };
-      auto scores = [&](long long i) {
-        if (!wait(&S.full1[i % W::kFirst], (uint32_t)(i / W::kFirst))) return false;
-        mma_inner<D>(t_s, k_mem, q_mem(i));
-        tc::commit(&S.s_full[0]);
-        return true;
-      };
-      auto products = [&](long long i) {
-        if (!wait(&S.full2[i % W::kSecond], (uint32_t)(i / W::kSecond))) return false;
-        mma_inner<D>(t_dp, v_mem, do_mem(i));
-        tc::commit(&S.dp_full);
-        return true;
-      };
-      for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
-        const PackedUnit u = list.units[w / p.kv_heads];
-        const QuerySpan q = query_span(u, p.causal);
-        const int n = p.G * q.tiles;
-        if (!n) continue;
-        if (!(ok = wait(&S.own_full, (uint32_t)units))) break;
-        ++units;
-        if (!(ok = scores(it)) || !(ok = products(it))) break;
-        if (n == 1) tc::commit(&S.own_empty);
-        for (int j = 0; j < n; ++j) {
-          const long long i = it + j;
-          if (!(ok = wait(&S.p_full, (uint32_t)i))) break;
-          mma_rows<D>(t_dv, t_s, do_mem(i), j > 0);
-          tc::commit(&S.empty2[i % W::kSecond]);
-          if (j + 1 < n && !(ok = scores(i + 1))) break;
-          if (!(ok = wait(&S.ds_full, (uint32_t)i))) break;
-          mma_rows<D>(t_dk, t_dp, q_mem(i), j > 0);
-          tc::commit(&S.empty1[i % W::kFirst]);
-          if (j + 1 < n && !(ok = products(i + 1))) break;
-          if (j + 2 == n) tc::commit(&S.own_empty);
-        }
-        if (!ok) break;
-        tc::commit(&S.acc_full);
-        it += n;
+    const uint32_t lead = tc::elect();
+    RingAt<W::kFirst> q1, q2;     // the tiles of Q of the next scores, and of the next dK
+    RingAt<W::kSecond> d1, d2;    // the tiles of dO of the next products with V, and of the next dV
+    uint32_t units = 0, it = 0;   // units and tiles so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool done = bounded_warp_wait(bar, parity & 1u, &S.failed);
+      tc::fence_after();
+      return done;
+    };
+    auto q_mem = [&](int slot) { return base + W::kRing1 + (uint32_t)slot * W::kTile; };
+    auto do_mem = [&](int slot) { return base + W::kRing2 + (uint32_t)slot * W::kTile; };
+    auto scores = [&] {
+      if (!wait(&S.full1[q1.slot], q1.phase)) return false;
+      mma_inner<D>(t_s, k_mem, q_mem(q1.slot), lead);
+      tc::commit(&S.s_full[0], lead);
+      q1.advance();
+      return true;
+    };
+    auto products = [&] {
+      if (!wait(&S.full2[d1.slot], d1.phase)) return false;
+      mma_inner<D>(t_dp, v_mem, do_mem(d1.slot), lead);
+      tc::commit(&S.dp_full, lead);
+      d1.advance();
+      return true;
+    };
+    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+      const PackedUnit u = list.units[w / p.kv_heads];
+      const int n = tc::uniform(p.G * query_span(u, p.causal).tiles);
+      if (!n) continue;
+      if (!(ok = wait(&S.own_full, units))) break;
+      ++units;
+      if (!(ok = scores()) || !(ok = products())) break;
+      if (n == 1) tc::commit(&S.own_empty, lead);
+      for (int j = 0; j < n; ++j, ++it) {
+        if (!(ok = wait(&S.p_full, it))) break;
+        mma_rows<D>(t_dv, t_s, do_mem(d2.slot), j > 0, lead);
+        tc::commit(&S.empty2[d2.slot], lead);
+        d2.advance();
+        if (j + 1 < n && !(ok = scores())) break;
+        if (!(ok = wait(&S.ds_full, it))) break;
+        mma_rows<D>(t_dk, t_dp, q_mem(q2.slot), j > 0, lead);
+        tc::commit(&S.empty1[q2.slot], lead);
+        q2.advance();
+        if (j + 1 < n && !(ok = products())) break;
+        if (j + 2 == n) tc::commit(&S.own_empty, lead);
       }
-      tc::commit(&S.drained);  // nothing is left in flight when the tensor memory is freed
-      (void)mbar_wait_landed(&S.drained, 0);
+      if (!ok) break;
+      tc::commit(&S.acc_full, lead);
     }
+    tc::commit(&S.drained, lead);  // nothing is left in flight when the tensor memory is freed
+    (void)mbar_wait_landed(&S.drained, 0);
     __syncwarp();
   } else {
     const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
@@ -282,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale * kLog2e;
     long long it = 0;
     int units = 0;
-    uint32_t meets = 0;
     bool ok = true;
     for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
       const PackedUnit u = list.units[w / p.kv_heads];
@@ -294,10 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int last = first_query(p.causal, u.m, u.n, u.i0 + kTileRows - 1);  // the unit's last key's
       for (int j = 0; j < n; ++j, ++it) {
         const int i0 = q.i0 + (j % q.tiles) * kTileRows, s2 = (int)(it % W::kSecond);
-        const int first_row = u.other0 + i0;
-        const bool border = i0 < last || i0 + kTileRows > u.m;
+        const bool border = i0 < max(last, 0) || i0 + kTileRows > u.m;
         const int lo = mine - i0 - half * 64, hi = u.m - i0 - half * 64;  // of the half's columns
-        const float2* st = reinterpret_cast<const float2*>(raw + W::kStats + s2 * kStatBytes) + (first_row & 1) + half * 64;
+        const float4* lse4 = reinterpret_cast<const float4*>(raw + W::kStats + s2 * kStatBytes) + half * 16;
+        const float4* delta4 = lse4 + 32;
         if (!(ok = bounded_warp_wait(&S.full2[s2], (uint32_t)(it / W::kSecond) & 1u, &S.failed))) break;
         if (!(ok = bounded_warp_wait(&S.s_full[0], (uint32_t)it & 1u, &S.failed))) break;
         tc::fence_after();
@@ -306,16 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld32(t_s + lanes + half * 64 + 32, x + 32);
         tc::wait_ld32(x);
         tc::wait_ld32(x + 32);
-        if (!(ok = meet(S, quarter, meets))) break;
 #pragma unroll
         for (int k = 0; k < 64; k += 32) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float a = ex2_approx(fmaf(__uint_as_float(x[k + e]), c, -st[k + e].x));
-            const float b = ex2_approx(fmaf(__uint_as_float(x[k + e + 1]), c, -st[k + e + 1].x));
-            x[k + e] = __float_as_uint(a);
-            x[k + e + 1] = __float_as_uint(b);
+          for (int e = 0; e < 32; e += 4) {
+            const float4 s4 = lse4[(k + e) / 4];
+            x[k + e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e]), c, -s4.x)));
+            x[k + e + 1] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 1]), c, -s4.y)));
+            x[k + e + 2] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 2]), c, -s4.z)));
+            x[k + e + 3] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 3]), c, -s4.w)));
           }
           if (border) {
 #pragma unroll
@@ -325,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             pk[e] = Bf16::pack(__uint_as_float(x[k + 2 * e]), __uint_as_float(x[k + 2 * e + 1]));
-          tc::st16(t_s + lanes + half * 32 + k / 2, pk);
+          tc::st16(t_s + lanes + half * 64 + k / 2, pk);
         }
         tc::wait_st();
         tc::fence_before();
@@ -339,13 +354,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld32(t_dp + lanes + half * 64 + 32, y + 32);
         tc::wait_ld32(y);
         tc::wait_ld32(y + 32);
-        if (!(ok = meet(S, quarter, meets))) break;
 #pragma unroll
         for (int k = 0; k < 64; k += 32) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            y[k + e] = __float_as_uint(__uint_as_float(x[k + e]) * (__uint_as_float(y[k + e]) - st[k + e].y));
+          for (int e = 0; e < 32; e += 4) {
+            const float4 s4 = delta4[(k + e) / 4];
+            y[k + e] = __float_as_uint(__uint_as_float(x[k + e]) * (__uint_as_float(y[k + e]) - s4.x));
+            y[k + e + 1] = __float_as_uint(__uint_as_float(x[k + e + 1]) * (__uint_as_float(y[k + e + 1]) - s4.y));
+            y[k + e + 2] = __float_as_uint(__uint_as_float(x[k + e + 2]) * (__uint_as_float(y[k + e + 2]) - s4.z));
+            y[k + e + 3] = __float_as_uint(__uint_as_float(x[k + e + 3]) * (__uint_as_float(y[k + e + 3]) - s4.w));
+          }
           if (border) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             pk[e] = Bf16::pack(__uint_as_float(y[k + 2 * e]), __uint_as_float(y[k + 2 * e + 1]));
-          tc::st16(t_dp + lanes + half * 32 + k / 2, pk);
+          tc::st16(t_dp + lanes + half * 64 + k / 2, pk);
         }
         tc::wait_st();
         tc::fence_before();
@@ -367,30 +386,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
 
       // ---- the keys' ends: half of the columns each
-      unsigned char* dk = p.dk.p + 2 * ((long long)(u.row0 + row) * p.dk.ts + (long long)kh * p.dk.hs);
-      unsigned char* dv = p.dv.p + 2 * ((long long)(u.row0 + row) * p.dv.ts + (long long)kh * p.dv.hs);
+      const int rows = u.rows - quarter * 32;  // of this warp's 32
+      const long long tok0 = u.row0 + quarter * 32;
+      unsigned char* dk = p.dk.p + 2 * (tok0 * p.dk.ts + (long long)kh * p.dk.hs) + half * D;
+      unsigned char* dv = p.dv.p + 2 * (tok0 * p.dv.ts + (long long)kh * p.dv.hs) + half * D;
       bool fine = true;
       if (n > 0) {
         if (!(ok = bounded_warp_wait(&S.acc_full, (uint32_t)units & 1u, &S.failed))) break;
         ++units;
         tc::fence_after();
-      }
-#pragma unroll 1
-      for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
-        if (n > 0) {
-          fine &= store32(t_dv + lanes + d, 1.0f, false, there, dv + 2 * d);
-          fine &= store32(t_dk + lanes + d, p.scale, false, there, dk + 2 * d);
-        } else {
-          clear32(there, dv + 2 * d);
-          clear32(there, dk + 2 * d);
-        }
+        fine &= store_half<D>(t_dv + lanes + half * (D / 2), 1.0f, false, dv, 2 * p.dv.ts, rows, lane);
+        fine &= store_half<D>(t_dk + lanes + half * (D / 2), p.scale, false, dk, 2 * p.dk.ts, rows, lane);
+      } else {
+        clear_half<D>(dv, 2 * p.dv.ts, rows, lane);
+        clear_half<D>(dk, 2 * p.dk.ts, rows, lane);
       }
       const bool odd = __any_sync(0xffffffffu, there && !fine);
       if (lane == 0) flags[w * kGradFlags + 2 * quarter + half] = odd;
       tc::fence_before();
     }
   }
-  end(p, S, tmem, warp);
+  end(p, S, warp);
 }
 
 // ---- queries
@@ -408,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   GradShared& S = *reinterpret_cast<GradShared*>(raw + W::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t tmem = begin<D>(S, warp, 1);
-  const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
+  begin<D>(S, warp, 1);
+  constexpr uint32_t t_s = 0, t_dp = 256, t_dq = 384;
   const uint32_t q_mem = base, do_mem = base + W::kTile;
   const long long work = (long long)*list.count * p.q_heads;
   auto tiles_of = [&](const PackedUnit& u) {
@@ -453,68 +469,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      long long it = 0;
-      int units = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t phase) {
-        if (!bounded_wait(bar, phase & 1u, &S.failed)) return false;
-        tc::fence_after();
-        return true;
-      };
-      auto k_mem = [&](long long i) { return base + W::kRing1 + (uint32_t)(i % W::kFirst) * W::kTile; };
-      // scores and products of the ring's tile i, which takes buffer i % 2
-      auto scores = [&](long long i) {
-        if (!wait(&S.full1[i % W::kFirst], (uint32_t)(i / W::kFirst))) return false;
-        mma_inner<D>(t_s + (uint32_t)(i & 1) * 128u, q_mem, k_mem(i));
-        tc::commit(&S.s_full[i & 1]);
-        return true;
-      };
-      auto products = [&](long long i) {
-        if (!wait(&S.full2[i % W::kSecond], (uint32_t)(i / W::kSecond))) return false;
-        mma_inner<D>(t_dp, do_mem, base + W::kRing2 + (uint32_t)(i % W::kSecond) * W::kTile);
-        tc::commit(&S.dp_full);
-        tc::commit(&S.empty2[i % W::kSecond]);
-        return true;
-      };
-      for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
-        const PackedUnit u = list.units[w / p.q_heads];
-        const int n = tiles_of(u);
-        if (!n) continue;
-        if (!(ok = wait(&S.own_full, (uint32_t)units))) break;
-        ++units;
-        if (!(ok = scores(it)) || !(ok = products(it))) break;
-        if (n == 1) tc::commit(&S.own_empty);
-        int issued = 1;  // scores
-        if (n > 1) {
-          if (!(ok = scores(it + 1))) break;
-          issued = 2;
+    const uint32_t lead = tc::elect();
+    RingAt<W::kFirst> k1, k2;   // the tiles of K of the next scores, and of the next dQ
+    RingAt<W::kSecond> v1;
+    uint32_t units = 0, it = 0, ahead = 0;  // units, tiles and tiles of scores so far (scores take buffer ahead % 2)
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool done = bounded_warp_wait(bar, parity & 1u, &S.failed);
+      tc::fence_after();
+      return done;
+    };
+    auto k_mem = [&](int slot) { return base + W::kRing1 + (uint32_t)slot * W::kTile; };
+    auto scores = [&] {
+      if (!wait(&S.full1[k1.slot], k1.phase)) return false;
+      mma_inner<D>(t_s + (ahead & 1u) * 128u, q_mem, k_mem(k1.slot), lead);
+      tc::commit(&S.s_full[ahead & 1u], lead);
+      k1.advance();
+      ++ahead;
+      return true;
+    };
+    auto products = [&] {
+      if (!wait(&S.full2[v1.slot], v1.phase)) return false;
+      mma_inner<D>(t_dp, do_mem, base + W::kRing2 + (uint32_t)v1.slot * W::kTile, lead);
+      tc::commit(&S.dp_full, lead);
+      tc::commit(&S.empty2[v1.slot], lead);
+      v1.advance();
+      return true;
+    };
+    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+      const PackedUnit u = list.units[w / p.q_heads];
+      const int n = tc::uniform(tiles_of(u));
+      if (!n) continue;
+      if (!(ok = wait(&S.own_full, units))) break;
+      ++units;
+      if (!(ok = scores()) || !(ok = products())) break;
+      if (n == 1) tc::commit(&S.own_empty, lead);
+      if (n > 1 && !(ok = scores())) break;
+      for (int j = 0; j < n; ++j, ++it) {
+        if (!(ok = wait(&S.ds_full, it))) break;
+        if (j + 1 < n) {
+          // (scores that could not go ahead of the product before)
+          if (ahead == it + 1 && !(ok = scores())) break;
+          if (!(ok = products())) break;
+          if (j + 2 == n) tc::commit(&S.own_empty, lead);
         }
-        for (int j = 0; j < n; ++j) {
-          const long long i = it + j;
-          if (!(ok = wait(&S.ds_full, (uint32_t)i))) break;
-          if (j + 1 < n) {
-            if (issued == j + 1) {  // these scores could not go ahead of the product before
-              if (!(ok = scores(i + 1))) break;
-              ++issued;
-            }
-            if (!(ok = products(i + 1))) break;
-            if (j + 2 == n) tc::commit(&S.own_empty);
-          }
-          mma_rows<D>(t_dq, t_s + (uint32_t)(i & 1) * 128u, k_mem(i), j > 0);
-          tc::commit(&S.empty1[i % W::kFirst]);
-          if (j + 2 < n && mbar_test_wait(&S.full1[(i + 2) % W::kFirst], (uint32_t)((i + 2) / W::kFirst) & 1u)) {
-            if (!(ok = scores(i + 2))) break;
-            issued = j + 3;
-          }
-        }
-        if (!ok) break;
-        tc::commit(&S.acc_full);
-        it += n;
+        mma_rows<D>(t_dq, t_s + (it & 1u) * 128u, k_mem(k2.slot), j > 0, lead);
+        tc::commit(&S.empty1[k2.slot], lead);
+        k2.advance();
+        if (j + 2 < n && __all_sync(0xffffffffu, mbar_test_wait(&S.full1[k1.slot], k1.phase)) && !(ok = scores())) break;
       }
-      tc::commit(&S.drained);
-      (void)mbar_wait_landed(&S.drained, 0);
+      if (!ok) break;
+      tc::commit(&S.acc_full, lead);
     }
+    tc::commit(&S.drained, lead);
+    (void)mbar_wait_landed(&S.drained, 0);
     __syncwarp();
   } else {
     const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
@@ -522,14 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale * kLog2e;
     long long it = 0;
     int units = 0;
-    uint32_t meets = 0;
     bool ok = true;
     for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
       const PackedUnit u = list.units[w / p.q_heads];
       const int head = (int)(w % p.q_heads), n = tiles_of(u);
       const bool there = row < u.rows;
       const int vis = there ? seen_keys(p.causal, u.n, u.m, u.i0 + row) : 0, vis0 = seen_keys(p.causal, u.n, u.m, u.i0);
-      const float2 st = there ? stats_of(p, head)[u.row0 + row] : make_float2(INFINITY, 0.0f);
+      const float lse = there ? stats_of(p, head)[u.row0 + row] : INFINITY;
+      const float delta = there ? stats_of(p, head)[p.stat_pitch + u.row0 + row] : 0.0f;
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t buf = t_s + (uint32_t)(it & 1) * 128u + lanes;
         const int left = (j + 1) * kTileRows > vis0 ? vis - j * kTileRows - half * 64 : 64;
@@ -541,10 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::wait_ld32(x);
         tc::wait_ld32(x + 32);
 #pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -st.x)));
+        for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -lse)));
         if (!(ok = bounded_warp_wait(&S.dp_full, (uint32_t)it & 1u, &S.failed))) break;
         tc::fence_after();
-        if (!(ok = meet(S, quarter, meets))) break;
 #pragma unroll
         for (int k = 0; k < 64; k += 32) {
           uint32_t y[32], pk[16];
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_ld32(y);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            y[e] = __float_as_uint(__uint_as_float(x[k + e]) * (__uint_as_float(y[e]) - st.y));
+            y[e] = __float_as_uint(__uint_as_float(x[k + e]) * (__uint_as_float(y[e]) - delta));
           if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = Bf16::pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-          tc::st16(buf + half * 32 + k / 2, pk);
+          tc::st16(buf + half * 64 + k / 2, pk);
         }
         tc::wait_st();
         tc::fence_before();
@@ -569,26 +576,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      unsigned char* dq = p.dq.p + 2 * ((long long)(u.row0 + row) * p.dq.ts + (long long)head * p.dq.hs);
+      const int rows = u.rows - quarter * 32;
+      const long long tok0 = u.row0 + quarter * 32;
+      unsigned char* dq = p.dq.p + 2 * (tok0 * p.dq.ts + (long long)head * p.dq.hs) + half * D;
       bool fine = true;
       if (n > 0) {
         if (!(ok = bounded_warp_wait(&S.acc_full, (uint32_t)units & 1u, &S.failed))) break;
         ++units;
         tc::fence_after();
-      }
-#pragma unroll 1
-      for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
-        if (n > 0)
-          fine &= store32(t_dq + lanes + d, p.scale, vis <= 0, there, dq + 2 * d);
-        else
-          clear32(there, dq + 2 * d);
+        fine = store_half<D>(t_dq + lanes + half * (D / 2), p.scale, vis <= 0, dq, 2 * p.dq.ts, rows, lane);
+      } else {
+        clear_half<D>(dq, 2 * p.dq.ts, rows, lane);
       }
       const bool odd = __any_sync(0xffffffffu, there && !fine);
       if (lane == 0) flags[w * kGradFlags + 2 * quarter + half] = odd;
       tc::fence_before();
     }
   }
-  end(p, S, tmem, warp);
+  end(p, S, warp);
 }
 
 template <class K>

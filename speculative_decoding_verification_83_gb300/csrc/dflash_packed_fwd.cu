@@ -8,17 +8,19 @@
 //
 // What bounds it: the products, 2 x 128 x 128 x D multiply-adds per tile of keys
 // and of queries, against 128 x 128 exponentials. So the two tiles alternate: while
-// the tensor cores work on one, 128 threads, a row each, turn the other's scores
-// into weights. A thread reads its row of scores for the maximum, then 2^(x - m) goes
-// back over the scores as 16-bit pairs, from where the product with V reads them
-// (half a row stays in registers between the two; a whole one spills). m may lag behind by kSlack powers of 2, so that
-// the sums in tensor memory are rarely rescaled; they are quiet then anyway, since
-// the product before was issued ahead of these scores.
-//  * warp 9: loads. Queries, and the tiles of keys and values in a ring, by TMA; tiles
+// the tensor cores work on one, the other's scores are turned into weights by 8 warps,
+// two for each quarter of the lanes, half of the columns each (with one thread a
+// row the chain of load, maximum, exponentials and store took longer than the products
+// of both tiles: 492 against XXX us at 8192 tokens). The two exchange a
+// row's maximum through shared memory; 2^(x - m) goes back over the thread's own scores as
+// 16-bit pairs, from where the product with V reads them. m may lag behind by kSlack
+// powers of 2, so that the sums in tensor memory are rarely rescaled; they are quiet
+// then anyway, since the product before was issued ahead of these scores.
+//  * warp 17: loads. Queries, and the tiles of keys and values in a ring, by TMA; tiles
 //    that reach past a sequence's end hold the next one's rows, which count as masked.
-//  * warp 8: products. For each tile of keys and each tile of queries: O += P V, then
+//  * warp 16: products. For each tile of keys and each tile of queries: O += P V, then
 //    the next S = Q K^T over the scores that P has replaced.
-//  * warps 0-3 and 4-7: the weights of the first and the second tile, and the rows'
+//  * warps 0-7 and 8-15: the weights of the first and the second tile, and the rows'
 //    ends.
 // Rows with a result that is not finite are flagged (see dflash_packed.cuh). Every
 // wait is bounded; a CTA that gives up raises DFLASH_STATUS_TIMEOUT.
@@ -32,7 +34,7 @@
 namespace dflash {
 namespace {
 
-constexpr int kThreads = 320, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 576, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kKeys = 128;
 constexpr float kSlack = 8.0f;
 // Where the reference lies below the score that last moved it: f16 holds normal
@@ -44,16 +46,20 @@ template <int D>
 struct FwdShape {
   static constexpr int kSlots = D == 128 ? 5 : 10;            // tiles of keys or values
   static constexpr uint32_t kTileBytes = 128u * D * 2u;       // of 128 rows
-  static constexpr size_t kSmem = 1024 + (2 + kSlots) * (size_t)kTileBytes;
+  static constexpr size_t kTiles = (2 + kSlots) * (size_t)kTileBytes;
   static constexpr int kS = 0, kO = 256;                      // tensor memory: S0, S1, O0, O1
 };
 struct FwdShared {
   uint64_t q_full, q_empty, full[10], empty[10];
   uint64_t s_full[2], p_full[2], o_full[2], drained;
+  uint64_t met[2][4];        // of the two warps that share rows
+  float row[2][2][128];      // what they exchange: a row's largest score, at a unit's end its sum
   uint32_t tmem;
   volatile int failed;
 };
-static_assert(FwdShape<128>::kSmem + sizeof(FwdShared) <= 232448, "one CTA's shared memory (227 KB)");
+template <int D>
+constexpr size_t kFwdSmem = FwdShape<D>::kTiles + sizeof(FwdShared);
+static_assert(kFwdSmem<128> <= 232448 && kFwdSmem<64> <= 232448, "one CTA's shared memory (227 KB)");
 
 // Tiles of keys that rows r0 .. of a unit see.
 __device__ __forceinline__ int key_tiles(const PackedUnit& u, int causal, int r0) {
@@ -69,9 +75,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using W = FwdShape<D>;
   constexpr int kSlots = W::kSlots;
   constexpr uint32_t kTile = W::kTileBytes;
-  extern __shared__ unsigned char raw[];
-  __shared__ FwdShared S;
-  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, ring = base + 2 * kTile;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  FwdShared& S = *reinterpret_cast<FwdShared*>(raw + W::kTiles);
+  const uint32_t base = smem_addr(raw), ring = base + 2 * kTile;
+  if (base & 1023u) {  // (the dynamic part begins on such a boundary)
+    if (threadIdx.x == 0) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -83,7 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&S.s_full[s], 1);
-      mbar_init(&S.p_full[s], 128);
+      mbar_init(&S.p_full[s], 8);
+      for (int q = 0; q < 4; ++q) mbar_init(&S.met[s][q], 2);
       mbar_init(&S.o_full[s], 1);
     }
     mbar_init(&S.drained, 1);
@@ -94,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = S.tmem;
+  constexpr uint32_t tmem = 0;  // (all of it is ours, so it begins at 0)
   grid_dependency_sync();
   const long long work = (long long)*list.count * p.q_heads;
 
@@ -141,73 +152,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc::idesc<T>(128, kKeys, false, false), id_o = tc::idesc<T>(128, D, false, true);
-      int units = 0, t = 0;     // units with keys, ring tiles before this unit
-      int weights[2] = {0, 0};  // tiles of weights taken so far
-      bool ok = true;
-      auto full = [&](int i) {
-        if (!bounded_wait(&S.full[i % kSlots], (uint32_t)(i / kSlots) & 1u, &S.failed)) return false;
-        tc::fence_after();
-        return true;
-      };
-      auto scores = [&](int s, int i) {
-        const uint32_t qa = base + (uint32_t)s * kTile, ka = ring + (uint32_t)(i % kSlots) * kTile;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_ss(tmem + W::kS + s * 128, tc::operand(qa + (uint32_t)((k >> 2) * 16384 + (k & 3) * 32)),
-                     tc::operand(ka + (uint32_t)((k >> 2) * 16384 + (k & 3) * 32)), id_s, k > 0);
-        tc::commit(&S.s_full[s]);
-      };
-      for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
-        const PackedUnit u = list.units[w / p.q_heads];
-        const int n[2] = {key_tiles(u, p.causal, 0), key_tiles(u, p.causal, 128)}, tiles = max(n[0], n[1]);
-        if (!tiles) continue;
-        if (!(ok = bounded_wait(&S.q_full, (uint32_t)units & 1u, &S.failed)) || !(ok = full(t))) break;
-        ++units;
-        for (int s = 0; s < 2; ++s)
-          if (n[s] > 0) scores(s, t);
-        tc::commit(&S.empty[t % kSlots]);
-        if (tiles == 1) tc::commit(&S.q_empty);
-        for (int j = 0; j < tiles && ok; ++j) {
-          const int v = t + 2 * j + 1, next = t + 2 * j + 2;
-          if (!(ok = full(v))) break;
-          const uint32_t va = ring + (uint32_t)(v % kSlots) * kTile;
-          bool loaded = false;
-          for (int s = 0; s < 2 && ok; ++s) {
-            if (j < n[s]) {
-              if (!(ok = bounded_wait(&S.p_full[s], (uint32_t)weights[s] & 1u, &S.failed))) break;
-              ++weights[s];
-              tc::fence_after();
-#pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                tc::mma_ts(tmem + W::kO + s * 128, tmem + W::kS + s * 128 + 8 * k, tc::operand(va + k * 2048u, 16384u), id_o,
-                           j > 0 || k > 0);
-              if (j == n[s] - 1) tc::commit(&S.o_full[s]);
-            }
-            if (j + 1 < n[s]) {
-              if (!loaded && !(ok = full(next))) break;
-              loaded = true;
-              scores(s, next);
-            }
-          }
-          if (!ok) break;
-          tc::commit(&S.empty[v % kSlots]);
-          if (j + 1 < tiles) tc::commit(&S.empty[next % kSlots]);
-          if (j + 2 == tiles) tc::commit(&S.q_empty);
-        }
-        t += 2 * tiles;
+    const uint32_t lead = tc::elect();
+    constexpr uint32_t id_s = tc::idesc<T>(128, kKeys, false, false), id_o = tc::idesc<T>(128, D, false, true);
+    int units = 0;            // units with keys
+    int slot = 0;             // the ring's next tile, and the parity of its round
+    uint32_t phase = 0;
+    int weights[2] = {0, 0};  // tiles of weights taken so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool done = bounded_warp_wait(bar, parity, &S.failed);
+      tc::fence_after();
+      return done;
+    };
+    auto advance = [&] {
+      if (++slot == kSlots) {
+        slot = 0;
+        phase ^= 1u;
       }
-      tc::commit(&S.drained);  // nothing is left in flight when the tensor memory is freed
-      (void)mbar_wait_landed(&S.drained, 0);
+    };
+    auto scores = [&](int s, uint32_t ka) {
+      const uint32_t qa = base + (uint32_t)s * kTile;
+      const uint64_t q = tc::operand(qa), k = tc::operand(ka);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)  // (addresses count in 16 bytes)
+        tc::mma_ss(W::kS + s * 128, q + (uint64_t)((i >> 2) * 1024 + (i & 3) * 2), k + (uint64_t)((i >> 2) * 1024 + (i & 3) * 2),
+                   id_s, i > 0, lead);
+      tc::commit(&S.s_full[s], lead);
+    };
+    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+      const PackedUnit u = list.units[w / p.q_heads];
+      const int n[2] = {tc::uniform(key_tiles(u, p.causal, 0)), tc::uniform(key_tiles(u, p.causal, 128))};
+      const int tiles = max(n[0], n[1]);
+      if (!tiles) continue;
+      if (!(ok = wait(&S.q_full, (uint32_t)units & 1u)) || !(ok = wait(&S.full[slot], phase))) break;
+      ++units;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (n[s] > 0) scores(s, ring + (uint32_t)slot * kTile);
+      tc::commit(&S.empty[slot], lead);
+      if (tiles == 1) tc::commit(&S.q_empty, lead);
+      advance();
+      for (int j = 0; j < tiles; ++j) {
+        // this tile's values, then the next one's keys
+        const int v = slot;
+        if (!(ok = wait(&S.full[v], phase))) break;
+        advance();
+        const bool more = j + 1 < tiles;
+        const uint64_t vd = tc::operand(ring + (uint32_t)v * kTile, 16384u);
+        bool loaded = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (ok && j < n[s]) {
+            if (!(ok = wait(&S.p_full[s], (uint32_t)weights[s] & 1u))) break;
+            ++weights[s];
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i)
+              tc::mma_ts(W::kO + s * 128, W::kS + s * 128 + (i >> 2) * 64 + (i & 3) * 8, vd + (uint64_t)(i * 128), id_o,
+                         j > 0 || i > 0, lead);
+            if (j == n[s] - 1) tc::commit(&S.o_full[s], lead);
+          }
+          if (ok && j + 1 < n[s]) {
+            if (!loaded && !(ok = wait(&S.full[slot], phase))) break;
+            loaded = true;
+            scores(s, ring + (uint32_t)slot * kTile);
+          }
+        }
+        if (!ok) break;
+        tc::commit(&S.empty[v], lead);
+        if (more) {
+          tc::commit(&S.empty[slot], lead);
+          advance();
+        }
+        if (j + 2 == tiles) tc::commit(&S.q_empty, lead);
+      }
     }
+    tc::commit(&S.drained, lead);  // nothing is left in flight when the tensor memory is freed
+    (void)mbar_wait_landed(&S.drained, 0);
     __syncwarp();
   } else {
-    const int s = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t my = tmem + ((uint32_t)((warp & 3) * 32) << 16), scores = my + W::kS + s * 128, sums = my + W::kO + s * 128;
+    const int s = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t scores = my + W::kS + s * 128 + half * 64, sums = my + W::kO + s * 128 + half * (D / 2);
     const float c = p.scale * kLog2e;
     int tile = 0, ends = 0;  // of this tile of queries: score tiles and units so far
+    uint32_t meets = 0;
     bool ok = true;
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.met[s][quarter]);
+      return bounded_warp_wait(&S.met[s][quarter], meets++ & 1u, &S.failed);
+    };
     for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
       const PackedUnit u = list.units[w / p.q_heads];
       const int head = (int)(w % p.q_heads), r = s * 128 + row;
@@ -219,43 +253,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n; ++j, ++tile) {
         if (!(ok = bounded_warp_wait(&S.s_full[s], (uint32_t)tile & 1u, &S.failed))) break;
         tc::fence_after();
-        // half a row of scores at a time; the first half stays in registers
-        const int left = (j + 1) * kKeys > vis0 ? vis - j * kKeys : kKeys;
-        uint32_t x[64];
+        const int left = (j + 1) * kKeys > vis0 ? vis - j * kKeys - half * 64 : 64;
+        uint32_t x[32];
         auto read = [&](int c0) {
           tc::ld32(scores + c0, x);
-          tc::ld32(scores + c0 + 32, x + 32);
           tc::wait_ld32(x);
-          tc::wait_ld32(x + 32);
-          if (__any_sync(0xffffffffu, left < kKeys)) {
+          if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < 32; ++i)
               if (c0 + i >= left) x[i] = 0xff800000u;
           }
         };
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c0 = 64; c0 >= 0; c0 -= 64) {
+        for (int c0 = 32; c0 >= 0; c0 -= 32) {
           read(c0);
 #pragma unroll
-          for (int i = 0; i < 64; i += 4)
+          for (int i = 0; i < 32; i += 4)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], __uint_as_float(x[i + e]));
         }
-        const float top = fmaf(fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])), c, -kTop<T>);
+        float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        // (written again only when the partner has given its weights of this tile)
+        S.row[s][half][row] = top;
+        if (!(ok = meet())) break;
+        top = fmaf(fmaxf(top, S.row[s][half ^ 1][row]), c, -kTop<T>);
         const bool move = top > m + kSlack || (m == -INFINITY && top > m);
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? (m == -INFINITY ? 0.0f : ex2_approx(m - top)) : 1.0f;
           if (j > 0) {
             // the product before was issued ahead of these scores, so it is done
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t y[32];
-              tc::ld32(sums + d, y);
-              tc::wait_ld32(y);
+            for (int d = 0; d < D / 2; d += 16) {
+              uint32_t y[16];
+              tc::ld16(sums + d, y);
+              tc::wait_ld16(y);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              tc::st32(sums + d, y);
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              tc::st16(sums + d, y);
             }
           }
           l2.x *= f;
@@ -265,76 +300,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = m == -INFINITY ? 0.0f : m;
         const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 64) {
-          if (c0) read(c0);  // (the weights of the first half replace scores of the first half)
+        for (int i = 0; i < 64; i += 32) {
+          if (i) read(i);  // (the weights of the first 32 lie over scores of the first 32)
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 64; i += 32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y =
-                  fma2(make_float2(__uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1])), c2, r2);
-              const float2 wt = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-              l2 = add2(l2, wt);
-              pk[e] = T::pack(wt.x, wt.y);
-            }
-            tc::st16(scores + (c0 + i) / 2, pk);
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, r2);
+            const float2 wt = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            l2 = add2(l2, wt);
+            pk[e] = T::pack(wt.x, wt.y);
           }
+          tc::st16(scores + i / 2, pk);
         }
         tc::wait_st();
         tc::fence_before();
-        mbar_arrive(&S.p_full[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[s]);
       }
       if (!ok) break;
 
-      // ---- the rows' ends
-      const bool there = r < u.rows;
-      const long long tok = u.row0 + r, at = tok * p.q_heads + head;
-      unsigned char* out = p.o.p + 2 * (tok * p.o.ts + (long long)head * p.o.hs);
-      const float l = l2.x + l2.y;
-      bool odd = false;
+      // ---- the rows' ends: half of the columns each
+      if (!(ok = meet())) break;  // the partner has read the last tile's maximum
+      S.row[s][half][row] = l2.x + l2.y;
+      if (!(ok = meet())) break;
+      const float l = S.row[s][0][row] + S.row[s][1][row];
+      if (!(ok = meet())) break;  // ... and the sums
       if (n > 0) {
         if (!(ok = bounded_warp_wait(&S.o_full[s], (uint32_t)ends & 1u, &S.failed))) break;
         ++ends;
         tc::fence_after();
       }
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int rows = u.rows - s * 128 - quarter * 32;  // of this warp's 32
+      const long long tok0 = u.row0 + s * 128 + quarter * 32;
+      unsigned char* out = p.o.p + 2 * (tok0 * p.o.ts + (long long)head * p.o.hs) + half * D;
+      unsigned char* low_out = reinterpret_cast<unsigned char*>(p.low) + (tok0 * p.q_heads + head) * D + half * (D / 2);
+      bool odd = false;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        uint32_t y[32];
+      for (int d = 0; d < D / 2; d += 32) {
+        uint32_t y[32], o[16], low[8];
         if (n > 0) {
           tc::ld32(sums + d, y);
           tc::wait_ld32(y);
         }
-        if (!there) continue;
-        uint32_t w32[16], low[8];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           // (a row that sees nothing is 0, whatever the products left there)
           const float a = l == 0.0f ? 0.0f : __uint_as_float(y[2 * i]) * inv,
                       b = l == 0.0f ? 0.0f : __uint_as_float(y[2 * i + 1]) * inv;
-          w32[i] = T::pack(a, b);
+          o[i] = T::pack(a, b);
           odd |= !(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY);
-          if (p.low) {
-            const uint32_t two = (uint32_t)(uint8_t)low_bits(a, w32[i] & 0xffffu) |
-                                 (uint32_t)(uint8_t)low_bits(b, w32[i] >> 16) << 8;
-            low[i >> 1] = i & 1 ? low[i >> 1] | two << 16 : two;
-          }
+          const uint32_t two =
+              (uint32_t)(uint8_t)low_bits(a, o[i] & 0xffffu) | (uint32_t)(uint8_t)low_bits(b, o[i] >> 16) << 8;
+          low[i >> 1] = i & 1 ? low[i >> 1] | two << 16 : two;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<uint4*>(out + 2 * d)[i] = make_uint4(w32[4 * i], w32[4 * i + 1], w32[4 * i + 2], w32[4 * i + 3]);
-        if (p.low)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            reinterpret_cast<uint4*>(p.low + at * D + d)[i] =
-                make_uint4(low[4 * i], low[4 * i + 1], low[4 * i + 2], low[4 * i + 3]);
+        store_rows<4>(o, out + 2 * d, 2 * p.o.ts, rows, lane);
+        if (p.low) store_rows<2>(low, low_out + d, (long long)p.q_heads * D, rows, lane);
       }
-      if (there && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      tc::fence_before();
+      const bool there = r < u.rows;
+      if (there && half == 0 && p.lse)
+        p.lse[(tok0 + lane) * p.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       // (a sum of weights that is not finite leaves NaN everywhere, which nothing mends)
       odd = __any_sync(0xffffffffu, odd && there && l < INFINITY);
-      if (lane == 0) flags[w * kForwardFlags + warp] = odd;
-      tc::fence_before();
+      if (lane == 0) flags[w * kForwardFlags + s * 8 + 2 * quarter + half] = odd;
     }
   }
   tc::fence_before();
@@ -354,7 +383,7 @@ int launch(const PackedParams& p, const PackedList& list, uint8_t* flags, int sm
   if (e != cudaSuccess) return (int)e;
   if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(forward_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kSmem);
+    e = cudaFuncSetAttribute(forward_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem<D>);
     if (e != cudaSuccess) return (int)e;
     ready[dev] = true;
   }
@@ -374,7 +403,7 @@ int launch(const PackedParams& p, const PackedList& list, uint8_t* flags, int sm
   cfg.stream = stream;
   cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = W::kSmem;
+  cfg.dynamicSmemBytes = kFwdSmem<D>;
   return (int)cudaLaunchKernelEx(&cfg, forward_kernel<T, D>, q, k, v, p, list, flags);
 }
 

@@ -56,6 +56,41 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// Inside each group of P lanes, lane t holds the P 16-byte pieces of row t (piece q in
+// words 4q .. 4q + 3); afterwards it holds piece t of the group's row i in words 4i ..
+// 4i + 3, so that a store's lanes write neighbouring pieces of a few rows.
+template <int P>
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[4 * P], int lane) {
+#pragma unroll
+  for (int m = P / 2; m > 0; m >>= 1) {
+    const bool hi = (lane & m) != 0;
+#pragma unroll
+    for (int a = 0; a < P; ++a) {
+      if (a & m) continue;
+      const int b = a | m;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? w[4 * a + e] : w[4 * b + e], m);
+        if (hi)
+          w[4 * a + e] = got;
+        else
+          w[4 * b + e] = got;
+      }
+    }
+  }
+}
+// Writes a warp's 32 rows, P pieces of 16 bytes each (lane t's are row t's), to
+// dst + row * stride; rows from `rows` on are left out.
+template <int P>
+__device__ __forceinline__ void store_rows(uint32_t (&w)[4 * P], unsigned char* dst, long long stride, int rows, int lane) {
+  transpose_pieces<P>(w, lane);
+  const int r0 = lane & ~(P - 1), t = lane & (P - 1);
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (r0 + i < rows)
+      *reinterpret_cast<uint4*>(dst + (r0 + i) * stride + 16 * t) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
 // A [tokens, heads, head_dim] array in boxes of `rows` tokens x 64 values of one head.
 inline bool map_heads(CUtensorMap* map, bool bf16, const HeadRows& h, int tokens, int heads, int head_dim, int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tc::encode_fn();
