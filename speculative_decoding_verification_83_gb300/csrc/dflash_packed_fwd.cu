@@ -12,10 +12,10 @@
 // two for each quarter of the lanes, half of the columns each (with one thread a
 // row the chain of load, maximum, exponentials and store took longer than the products
 // of both tiles: 492 against XXX us at 8192 tokens). The two exchange a
-// row's maximum through shared memory; 2^(x - m) goes back over the thread's own scores as
-// 16-bit pairs, from where the product with V reads them. m may lag behind by kSlack
-// powers of 2, so that the sums in tensor memory are rarely rescaled; they are quiet
-// then anyway, since the product before was issued ahead of these scores.
+// row's maximum through shared memory; 2^(x - m) goes back to tensor memory as 16-bit
+// pairs (over the thread's own scores, or beside them), from where the product with V
+// reads them, beginning with the first half that is there. m may lag behind by kSlack
+// powers of 2, so that the sums in tensor memory are rarely rescaled.
 //  * warp 17: loads. Queries, and the tiles of keys and values in a ring, by TMA; tiles
 //    that reach past a sequence's end hold the next one's rows, which count as masked.
 //  * warp 16: products. For each tile of keys and each tile of queries: O += P V, then
@@ -47,11 +47,15 @@ struct FwdShape {
   static constexpr int kSlots = D == 128 ? 5 : 10;            // tiles of keys or values
   static constexpr uint32_t kTileBytes = 128u * D * 2u;       // of 128 rows
   static constexpr size_t kTiles = (2 + kSlots) * (size_t)kTileBytes;
-  static constexpr int kS = 0, kO = 256;                      // tensor memory: S0, S1, O0, O1
+  // Tensor memory: S0, S1, then O0, O1. With head_dim 64 there is room for the weights beside
+  // the scores, so that the next scores are issued as soon as these have been read.
+  static constexpr bool kBeside = D == 64;
+  static constexpr int kS = 0, kO = 256, kOStep = kBeside ? 64 : 128;
+  static constexpr int kP = kBeside ? 384 : 0, kPStep = kBeside ? 64 : 128, kPHalf = kBeside ? 32 : 64;
 };
 struct FwdShared {
   uint64_t q_full, q_empty, full[10], empty[10];
-  uint64_t s_full[2], p_full[2], o_full[2], drained;
+  uint64_t s_full[2], s_read[2], p_half[2], p_full[2], pv_done[2], o_full[2], drained;
   uint64_t met[2][4];        // of the two warps that share rows
   float row[2][2][128];      // what they exchange: a row's largest score, at a unit's end its sum
   uint32_t tmem;
@@ -93,7 +97,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&S.s_full[s], 1);
+      mbar_init(&S.s_read[s], 8);
+      mbar_init(&S.p_half[s], 8);
       mbar_init(&S.p_full[s], 8);
+      mbar_init(&S.pv_done[s], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&S.met[s][q], 2);
       mbar_init(&S.o_full[s], 1);
     }
@@ -193,29 +200,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles == 1) tc::commit(&S.q_empty, lead);
       advance();
       for (int j = 0; j < tiles; ++j) {
-        // this tile's values, then the next one's keys
+        // this tile's values and the next one's keys, ahead of the waits for weights
         const int v = slot;
         if (!(ok = wait(&S.full[v], phase))) break;
         advance();
         const bool more = j + 1 < tiles;
+        if (more && !(ok = wait(&S.full[slot], phase))) break;
         const uint64_t vd = tc::operand(ring + (uint32_t)v * kTile, 16384u);
-        bool loaded = false;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (ok && j < n[s]) {
-            if (!(ok = wait(&S.p_full[s], (uint32_t)weights[s] & 1u))) break;
-            ++weights[s];
+          if (!ok || j >= n[s]) continue;
+          const uint32_t parity = (uint32_t)weights[s] & 1u;
+          ++weights[s];
+          // a quarter of the keys' weights of each half: keys 0-31 and 64-95, then the rest
+          auto product = [&](int part) {
 #pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              tc::mma_ts(W::kO + s * 128, W::kS + s * 128 + (i >> 2) * 64 + (i & 3) * 8, vd + (uint64_t)(i * 128), id_o,
-                         j > 0 || i > 0, lead);
-            if (j == n[s] - 1) tc::commit(&S.o_full[s], lead);
-          }
-          if (ok && j + 1 < n[s]) {
-            if (!loaded && !(ok = wait(&S.full[slot], phase))) break;
-            loaded = true;
+            for (int i = 0; i < 4; ++i) {
+              const int k = (i >> 1) * 4 + 2 * part + (i & 1);  // 16 keys
+              tc::mma_ts(W::kO + s * W::kOStep, W::kP + s * W::kPStep + (k >> 2) * W::kPHalf + (k & 3) * 8,
+                         vd + (uint64_t)(k * 128), id_o, j > 0 || part > 0 || i > 0, lead);
+            }
+          };
+          if (W::kBeside && j + 1 < n[s]) {
+            if (!(ok = wait(&S.s_read[s], parity))) continue;
             scores(s, ring + (uint32_t)slot * kTile);
           }
+          if (!(ok = wait(&S.p_half[s], parity))) continue;
+          product(0);
+          if (!(ok = wait(&S.p_full[s], parity))) continue;
+          product(1);
+          if (W::kBeside) tc::commit(&S.pv_done[s], lead);
+          if (j == n[s] - 1) tc::commit(&S.o_full[s], lead);
+          if (!W::kBeside && j + 1 < n[s]) scores(s, ring + (uint32_t)slot * kTile);
         }
         if (!ok) break;
         tc::commit(&S.empty[v], lead);
@@ -232,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int s = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t scores = my + W::kS + s * 128 + half * 64, sums = my + W::kO + s * 128 + half * (D / 2);
+    const uint32_t scores = my + W::kS + s * 128 + half * 64, sums = my + W::kO + s * W::kOStep + half * (D / 2);
+    const uint32_t weights = my + W::kP + s * W::kPStep + half * W::kPHalf;
     const float c = p.scale * kLog2e;
     int tile = 0, ends = 0;  // of this tile of queries: score tiles and units so far
     uint32_t meets = 0;
@@ -254,10 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = bounded_warp_wait(&S.s_full[s], (uint32_t)tile & 1u, &S.failed))) break;
         tc::fence_after();
         const int left = (j + 1) * kKeys > vis0 ? vis - j * kKeys - half * 64 : 64;
-        uint32_t x[32];
-        auto read = [&](int c0) {
-          tc::ld32(scores + c0, x);
-          tc::wait_ld32(x);
+        uint32_t x[32];  // (64 do not fit beside the rest of a thread's 96 registers)
+        auto mask = [&](int c0) {
           if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -267,7 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c0 = 32; c0 >= 0; c0 -= 32) {
-          read(c0);
+          tc::ld32(scores + c0, x);
+          tc::wait_ld32(x);
+          mask(c0);
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
 #pragma unroll
@@ -279,10 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = meet())) break;
         top = fmaf(fmaxf(top, S.row[s][half ^ 1][row]), c, -kTop<T>);
         const bool move = top > m + kSlack || (m == -INFINITY && top > m);
+        // the product before: where the weights lie over the scores it was issued ahead of these, so it is done
+        if (W::kBeside && tile > 0 && !(ok = bounded_warp_wait(&S.pv_done[s], (uint32_t)(tile - 1) & 1u, &S.failed))) break;
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? (m == -INFINITY ? 0.0f : ex2_approx(m - top)) : 1.0f;
           if (j > 0) {
-            // the product before was issued ahead of these scores, so it is done
+            if (W::kBeside) tc::fence_after();
 #pragma unroll 1
             for (int d = 0; d < D / 2; d += 16) {
               uint32_t y[16];
@@ -301,21 +320,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
 #pragma unroll
         for (int i = 0; i < 64; i += 32) {
-          if (i) read(i);  // (the weights of the first 32 lie over scores of the first 32)
-          uint32_t pk[16];
+          if (i) {
+            tc::ld32(scores + i, x);  // (what lies over the scores so far are weights of the first 32)
+            tc::wait_ld32(x);
+            if (W::kBeside) {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.s_read[s]);
+            }
+            mask(i);
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, r2);
             const float2 wt = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             l2 = add2(l2, wt);
-            pk[e] = T::pack(wt.x, wt.y);
+            x[e] = T::pack(wt.x, wt.y);  // (pairs take the place of what has been read)
           }
-          tc::st16(scores + i / 2, pk);
+          tc::st16(weights + i / 2, x);
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(i ? &S.p_full[s] : &S.p_half[s]);
         }
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[s]);
       }
       if (!ok) break;
 
