@@ -195,16 +195,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   begin<D>(S, warp, 1 + kWorkWarps);
   constexpr uint32_t t_s = 0, t_dp = 128, t_dv = 256, t_dk = 256 + D;
   const uint32_t k_mem = base, v_mem = base + W::kTile;
-  const long long work = (long long)*list.count * p.kv_heads;
+  const int work = *list.count * p.kv_heads;  // (below 2^28)
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
       long long it = 0;
       int units = 0;
       bool ok = true;
-      for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+      for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
         const PackedUnit u = list.units[w / p.kv_heads];
-        const int kh = (int)(w % p.kv_heads);
+        const int kh = w % p.kv_heads;
         const QuerySpan q = query_span(u, p.causal);
         if (!q.tiles) continue;
         if (units > 0 && !(ok = bounded_wait(&S.own_empty, (uint32_t)(units - 1) & 1u, &S.failed))) break;
@@ -252,38 +254,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto q_mem = [&](int slot) { return base + W::kRing1 + (uint32_t)slot * W::kTile; };
     auto do_mem = [&](int slot) { return base + W::kRing2 + (uint32_t)slot * W::kTile; };
     auto scores = [&] {
-      if (!wait(&S.full1[q1.slot], q1.phase)) return false;
       mma_inner<D>(t_s, k_mem, q_mem(q1.slot), lead);
       tc::commit(&S.s_full[0], lead);
       q1.advance();
-      return true;
     };
     auto products = [&] {
-      if (!wait(&S.full2[d1.slot], d1.phase)) return false;
       mma_inner<D>(t_dp, v_mem, do_mem(d1.slot), lead);
       tc::commit(&S.dp_full, lead);
       d1.advance();
-      return true;
     };
-    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+    for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
       const PackedUnit u = list.units[w / p.kv_heads];
       const int n = tc::uniform(p.G * query_span(u, p.causal).tiles);
       if (!n) continue;
-      if (!(ok = wait(&S.own_full, units))) break;
+      if (!(ok = wait(&S.own_full, units)) || !(ok = wait(&S.full1[q1.slot], q1.phase))) break;
       ++units;
-      if (!(ok = scores()) || !(ok = products())) break;
+      scores();
+      if (!(ok = wait(&S.full2[d1.slot], d1.phase))) break;
+      products();
       if (n == 1) tc::commit(&S.own_empty, lead);
       for (int j = 0; j < n; ++j, ++it) {
+        // (operands are waited for ahead of what the threads make)
+        const bool more = j + 1 < n;
+        if (more && !(ok = wait(&S.full1[q1.slot], q1.phase))) break;
         if (!(ok = wait(&S.p_full, it))) break;
         mma_rows<D>(t_dv, t_s, do_mem(d2.slot), j > 0, lead);
         tc::commit(&S.empty2[d2.slot], lead);
         d2.advance();
-        if (j + 1 < n && !(ok = scores())) break;
+        if (more) scores();
+        if (more && !(ok = wait(&S.full2[d1.slot], d1.phase))) break;
         if (!(ok = wait(&S.ds_full, it))) break;
         mma_rows<D>(t_dk, t_dp, q_mem(q2.slot), j > 0, lead);
         tc::commit(&S.empty1[q2.slot], lead);
         q2.advance();
-        if (j + 1 < n && !(ok = products())) break;
+        if (more) products();
         if (j + 2 == n) tc::commit(&S.own_empty, lead);
       }
       if (!ok) break;
@@ -299,9 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long it = 0;
     int units = 0;
     bool ok = true;
-    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+    for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
       const PackedUnit u = list.units[w / p.kv_heads];
-      const int kh = (int)(w % p.kv_heads);
+      const int kh = w % p.kv_heads;
       const QuerySpan q = query_span(u, p.causal);
       const int n = p.G * q.tiles;
       const bool there = row < u.rows;
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         clear_half<D>(dk, 2 * p.dk.ts, rows, lane);
       }
       const bool odd = __any_sync(0xffffffffu, there && !fine);
-      if (lane == 0) flags[w * kGradFlags + 2 * quarter + half] = odd;
+      if (lane == 0) flags[(size_t)w * kGradFlags + 2 * quarter + half] = odd;
       tc::fence_before();
     }
   }
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   begin<D>(S, warp, 1);
   constexpr uint32_t t_s = 0, t_dp = 256, t_dq = 384;
   const uint32_t q_mem = base, do_mem = base + W::kTile;
-  const long long work = (long long)*list.count * p.q_heads;
+  const int work = *list.count * p.q_heads;  // (below 2^27)
   auto tiles_of = [&](const PackedUnit& u) {
     return (seen_keys(p.causal, u.n, u.m, u.i0 + u.rows - 1) + kTileRows - 1) / kTileRows;
   };
@@ -437,9 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long it = 0;
       int units = 0;
       bool ok = true;
-      for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+      for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
         const PackedUnit u = list.units[w / p.q_heads];
-        const int head = (int)(w % p.q_heads), kh = head / p.G, n = tiles_of(u);
+        const int head = w % p.q_heads, kh = head / p.G, n = tiles_of(u);
         if (!n) continue;
         if (units > 0 && !(ok = bounded_wait(&S.own_empty, (uint32_t)(units - 1) & 1u, &S.failed))) break;
         ++units;
@@ -481,42 +491,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto k_mem = [&](int slot) { return base + W::kRing1 + (uint32_t)slot * W::kTile; };
     auto scores = [&] {
-      if (!wait(&S.full1[k1.slot], k1.phase)) return false;
       mma_inner<D>(t_s + (ahead & 1u) * 128u, q_mem, k_mem(k1.slot), lead);
       tc::commit(&S.s_full[ahead & 1u], lead);
       k1.advance();
       ++ahead;
-      return true;
     };
     auto products = [&] {
-      if (!wait(&S.full2[v1.slot], v1.phase)) return false;
       mma_inner<D>(t_dp, do_mem, base + W::kRing2 + (uint32_t)v1.slot * W::kTile, lead);
       tc::commit(&S.dp_full, lead);
       tc::commit(&S.empty2[v1.slot], lead);
       v1.advance();
-      return true;
     };
-    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+    for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
       const PackedUnit u = list.units[w / p.q_heads];
       const int n = tc::uniform(tiles_of(u));
       if (!n) continue;
-      if (!(ok = wait(&S.own_full, units))) break;
+      if (!(ok = wait(&S.own_full, units)) || !(ok = wait(&S.full1[k1.slot], k1.phase))) break;
       ++units;
-      if (!(ok = scores()) || !(ok = products())) break;
+      scores();
+      if (!(ok = wait(&S.full2[v1.slot], v1.phase))) break;
+      products();
       if (n == 1) tc::commit(&S.own_empty, lead);
-      if (n > 1 && !(ok = scores())) break;
       for (int j = 0; j < n; ++j, ++it) {
-        if (!(ok = wait(&S.ds_full, it))) break;
         if (j + 1 < n) {
-          // (scores that could not go ahead of the product before)
-          if (ahead == it + 1 && !(ok = scores())) break;
-          if (!(ok = products())) break;
-          if (j + 2 == n) tc::commit(&S.own_empty, lead);
+          // (operands are waited for ahead of what the threads make)
+          if (ahead == it + 1) {
+            if (!(ok = wait(&S.full1[k1.slot], k1.phase))) break;
+            scores();
+          }
+          if (!(ok = wait(&S.full2[v1.slot], v1.phase))) break;
         }
+        if (!(ok = wait(&S.ds_full, it))) break;
+        if (j + 1 < n) products();
+        if (j + 2 == n) tc::commit(&S.own_empty, lead);
         mma_rows<D>(t_dq, t_s + (it & 1u) * 128u, k_mem(k2.slot), j > 0, lead);
         tc::commit(&S.empty1[k2.slot], lead);
         k2.advance();
-        if (j + 2 < n && __all_sync(0xffffffffu, mbar_test_wait(&S.full1[k1.slot], k1.phase)) && !(ok = scores())) break;
+        if (j + 2 < n && __all_sync(0xffffffffu, mbar_test_wait(&S.full1[k1.slot], k1.phase))) {
+          tc::fence_after();
+          scores();
+        }
       }
       if (!ok) break;
       tc::commit(&S.acc_full, lead);
@@ -531,9 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long it = 0;
     int units = 0;
     bool ok = true;
-    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+    for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
       const PackedUnit u = list.units[w / p.q_heads];
-      const int head = (int)(w % p.q_heads), n = tiles_of(u);
+      const int head = w % p.q_heads, n = tiles_of(u);
       const bool there = row < u.rows;
       const int vis = there ? seen_keys(p.causal, u.n, u.m, u.i0 + row) : 0, vis0 = seen_keys(p.causal, u.n, u.m, u.i0);
       const float lse = there ? stats_of(p, head)[u.row0 + row] : INFINITY;
@@ -589,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         clear_half<D>(dq, 2 * p.dq.ts, rows, lane);
       }
       const bool odd = __any_sync(0xffffffffu, there && !fine);
-      if (lane == 0) flags[w * kGradFlags + 2 * quarter + half] = odd;
+      if (lane == 0) flags[(size_t)w * kGradFlags + 2 * quarter + half] = odd;
       tc::fence_before();
     }
   }

@@ -114,16 +114,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   constexpr uint32_t tmem = 0;  // (all of it is ours, so it begins at 0)
   grid_dependency_sync();
-  const long long work = (long long)*list.count * p.q_heads;
+  const int work = *list.count * p.q_heads;  // (below 2^27)
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
       int slot = 0, units = 0;
-      uint32_t round = 0;
+      uint32_t rounds = 0;  // of the ring
       long long issued = 0;
       bool ok = true;
       auto load = [&](const CUtensorMap* map, int head, int row) {
-        if (round > 0 && !(ok = bounded_wait(&S.empty[slot], (round - 1) & 1u, &S.failed))) return;
+        if (rounds > 0 && !(ok = bounded_wait(&S.empty[slot], (rounds - 1) & 1u, &S.failed))) return;
         mbar_arrive_expect_tx(&S.full[slot], kTile);
         const uint32_t dst = ring + (uint32_t)slot * kTile;
 #pragma unroll
@@ -131,12 +131,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++issued;
         if (++slot == kSlots) {
           slot = 0;
-          ++round;
+          ++rounds;
         }
       };
-      for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
-        const PackedUnit u = list.units[w / p.q_heads];
-        const int head = (int)(w % p.q_heads), kh = head / p.G;
+      PackedUnit next = {};
+      if (blockIdx.x < work) next = list.units[blockIdx.x / p.q_heads];
+      for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
+        const PackedUnit u = next;
+        if (unit_of(round + 1) < work) next = list.units[unit_of(round + 1) / p.q_heads];
+        const int head = w % p.q_heads, kh = head / p.G;
         const int tiles = max(key_tiles(u, p.causal, 0), key_tiles(u, p.causal, 128));
         if (!tiles) continue;
         if (units > 0 && !(ok = bounded_wait(&S.q_empty, (uint32_t)(units - 1) & 1u, &S.failed))) break;
@@ -186,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                    id_s, i > 0, lead);
       tc::commit(&S.s_full[s], lead);
     };
-    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+    for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
       const PackedUnit u = list.units[w / p.q_heads];
       const int n[2] = {tc::uniform(key_tiles(u, p.causal, 0)), tc::uniform(key_tiles(u, p.causal, 128))};
       const int tiles = max(n[0], n[1]);
@@ -254,29 +261,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile = 0, ends = 0;  // of this tile of queries: score tiles and units so far
     uint32_t meets = 0;
     bool ok = true;
-    auto meet = [&] {
+    // The two warps that share rows: `come` says that this one has written or read what
+    // they exchange, `meet` waits for the other to have said so.
+    auto come = [&] {
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.met[s][quarter]);
-      return bounded_warp_wait(&S.met[s][quarter], meets++ & 1u, &S.failed);
     };
-    for (long long w = blockIdx.x; w < work && ok; w += gridDim.x) {
+    auto meet = [&] { return bounded_warp_wait(&S.met[s][quarter], meets++ & 1u, &S.failed); };
+    come();  // nothing is read yet
+    for (int round = 0; ok; ++round) {
+      const int w = unit_of(round);
+      if (w >= work) break;
       const PackedUnit u = list.units[w / p.q_heads];
-      const int head = (int)(w % p.q_heads), r = s * 128 + row;
+      const int head = w % p.q_heads, r = s * 128 + row;
       const int n = key_tiles(u, p.causal, s * 128);
       const int vis = r < u.rows ? seen_keys(p.causal, u.n, u.m, u.i0 + r) : 0;
       const int vis0 = seen_keys(p.causal, u.n, u.m, u.i0 + s * 128);  // the tile's first row sees least
       float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
+      if (!(ok = meet())) break;  // the sums of the unit before are read
       for (int j = 0; j < n; ++j, ++tile) {
         if (!(ok = bounded_warp_wait(&S.s_full[s], (uint32_t)tile & 1u, &S.failed))) break;
         tc::fence_after();
-        const int left = (j + 1) * kKeys > vis0 ? vis - j * kKeys - half * 64 : 64;
+        const bool border = (j + 1) * kKeys > vis0;  // some row does not see all of the tile
         uint32_t x[32];  // (64 do not fit beside the rest of a thread's 96 registers)
         auto mask = [&](int c0) {
-          if (__any_sync(0xffffffffu, left < 64)) {
+          if (border) {
+            const int left = vis - j * kKeys - half * 64 - c0;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c0 + i >= left) x[i] = 0xff800000u;
+              if (i >= left) x[i] = 0xff800000u;
           }
         };
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -291,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], __uint_as_float(x[i + e]));
         }
         float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-        // (written again only when the partner has given its weights of this tile)
+        // (written again only when the partner has given its weights of this tile, so it has read)
         S.row[s][half][row] = top;
+        come();
         if (!(ok = meet())) break;
         top = fmaf(fmaxf(top, S.row[s][half ^ 1][row]), c, -kTop<T>);
         const bool move = top > m + kSlack || (m == -INFINITY && top > m);
@@ -347,50 +362,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
 
       // ---- the rows' ends: half of the columns each
-      if (!(ok = meet())) break;  // the partner has read the last tile's maximum
+      come();
+      if (!(ok = meet())) break;  // the last maximum is read
       S.row[s][half][row] = l2.x + l2.y;
+      come();
       if (!(ok = meet())) break;
       const float l = S.row[s][0][row] + S.row[s][1][row];
-      if (!(ok = meet())) break;  // ... and the sums
+      come();  // the sums are read
       if (n > 0) {
         if (!(ok = bounded_warp_wait(&S.o_full[s], (uint32_t)ends & 1u, &S.failed))) break;
         ++ends;
         tc::fence_after();
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
       const int rows = u.rows - s * 128 - quarter * 32;  // of this warp's 32
       const long long tok0 = u.row0 + s * 128 + quarter * 32;
       unsigned char* out = p.o.p + 2 * (tok0 * p.o.ts + (long long)head * p.o.hs) + half * D;
       unsigned char* low_out = reinterpret_cast<unsigned char*>(p.low) + (tok0 * p.q_heads + head) * D + half * (D / 2);
-      bool odd = false;
+      float2 probe = make_float2(0.0f, 0.0f);  // NaN once a result is not finite
+      const bool none = l == 0.0f;
 #pragma unroll 1
       for (int d = 0; d < D / 2; d += 32) {
-        uint32_t y[32], o[16], low[8];
+        uint32_t y[32], o[16];
         if (n > 0) {
           tc::ld32(sums + d, y);
           tc::wait_ld32(y);
         }
+        if (__any_sync(0xffffffffu, none)) {  // a row that sees nothing is 0, whatever the products left there
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = none ? 0u : y[i];
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          // (a row that sees nothing is 0, whatever the products left there)
-          const float a = l == 0.0f ? 0.0f : __uint_as_float(y[2 * i]) * inv,
-                      b = l == 0.0f ? 0.0f : __uint_as_float(y[2 * i + 1]) * inv;
-          o[i] = T::pack(a, b);
-          odd |= !(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY);
-          const uint32_t two =
-              (uint32_t)(uint8_t)low_bits(a, o[i] & 0xffffu) | (uint32_t)(uint8_t)low_bits(b, o[i] >> 16) << 8;
-          low[i >> 1] = i & 1 ? low[i >> 1] | two << 16 : two;
+          const float2 f = mul2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(inv, inv));
+          o[i] = T::pack(f.x, f.y);
+          y[2 * i] = __float_as_uint(f.x);
+          y[2 * i + 1] = __float_as_uint(f.y);
+          probe = fma2(f, make_float2(0.0f, 0.0f), probe);
+        }
+        if (p.low) {
+          uint32_t low[8];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t two = (uint32_t)(uint8_t)low_bits(__uint_as_float(y[2 * i]), o[i] & 0xffffu) |
+                                 (uint32_t)(uint8_t)low_bits(__uint_as_float(y[2 * i + 1]), o[i] >> 16) << 8;
+            low[i >> 1] = i & 1 ? low[i >> 1] | two << 16 : two;
+          }
+          store_rows<2>(low, low_out + d, (long long)p.q_heads * D, rows, lane);
         }
         store_rows<4>(o, out + 2 * d, 2 * p.o.ts, rows, lane);
-        if (p.low) store_rows<2>(low, low_out + d, (long long)p.q_heads * D, rows, lane);
       }
       tc::fence_before();
       const bool there = r < u.rows;
       if (there && half == 0 && p.lse)
         p.lse[(tok0 + lane) * p.q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       // (a sum of weights that is not finite leaves NaN everywhere, which nothing mends)
-      odd = __any_sync(0xffffffffu, odd && there && l < INFINITY);
-      if (lane == 0) flags[w * kForwardFlags + s * 8 + 2 * quarter + half] = odd;
+      const bool odd = __any_sync(0xffffffffu, probe.x + probe.y != 0.0f && there && l < INFINITY);
+      if (lane == 0) flags[(size_t)w * kForwardFlags + s * 8 + 2 * quarter + half] = odd;
     }
   }
   tc::fence_before();

@@ -30,6 +30,11 @@ __device__ __forceinline__ bool bounded_warp_wait(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, failed));
 }
 
+// A CTA's units: every gridDim-th of the list, in turn from either end of a round,
+// since the list begins with the largest.
+__device__ __forceinline__ int unit_of(int round) {
+  return round * (int)gridDim.x + (int)(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
 // Two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
