@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   });
 }
 
-// delta, the sum over d of dout out, and lse as the products' kernels read them
+// delta, the sum over d of dout out, and lse as the products' kernels read them; behind
+// the last row a tile's worth of zeros
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p) {
   constexpr int kLanes = D / 8;  // 8 values each
@@ -176,6 +177,11 @@ __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p
   const long long rows = (long long)p.q_tokens * p.q_heads;
   const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
   float s = 0.0f;
+  for (long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x; at < (p.stat_pitch - p.q_tokens) * 2ll * p.q_heads;
+       at += (long long)gridDim.x * blockDim.x) {
+    const int spare = p.stat_pitch - p.q_tokens;
+    p.row_stats[at / spare * p.stat_pitch + p.q_tokens + at % spare] = 0.0f;
+  }
   if (r < rows) {
     const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
     const uint4 a = reinterpret_cast<const uint4*>(row_of(p.o, t, head))[lane];

@@ -16,7 +16,8 @@
 // of the lanes, half of the columns each; since the results take the scores' place, the
 // two meet once they have read (`met`). The rows' lse and delta lie as pairs by head,
 // made with delta ahead of the kernels; for the keys' kernel 128 of them come with each
-// tile of dO. Masks select P = 0 and dS = 0 in tiles at a border only. Rows with a result that is not
+// tile of dO. Masks select P = 0 in tiles at a border only (dS is then 0 times
+// something, which is 0 or mended with the rest). Rows with a result that is not
 // finite are flagged (see dflash_packed.cuh). Every wait is bounded; a CTA that gives up
 // raises DFLASH_STATUS_TIMEOUT.
 #include <cuda_runtime.h>
@@ -31,15 +32,15 @@ namespace {
 
 constexpr int kThreads = 320, kMmaWarp = 8, kLoadWarp = 9, kWorkWarps = 8;
 constexpr int kTileRows = 128;
-constexpr uint32_t kStatBytes = 1024;  // 128 of lse and 128 of delta
+constexpr uint32_t kStatBytes = 512;  // of a tile of queries: lse comes with Q, delta with dO
 
 template <int D>
 struct GradShape {
   static constexpr uint32_t kTile = 128u * D * 2u;
   // keys: K, V; tiles of Q and of dO. queries: Q, dO; tiles of K and of V.
   static constexpr int kFirst = D == 128 ? 3 : 5, kSecond = D == 128 ? 2 : 4;
-  static constexpr uint32_t kRing1 = 2 * kTile, kRing2 = kRing1 + kFirst * kTile, kStats = kRing2 + kSecond * kTile;
-  static constexpr uint32_t kBars = (kStats + kSecond * kStatBytes + 15u) / 16u * 16u;
+  static constexpr uint32_t kRing1 = 2 * kTile, kRing2 = kRing1 + kFirst * kTile, kLse = kRing2 + kSecond * kTile;
+  static constexpr uint32_t kDelta = kLse + kFirst * kStatBytes, kBars = kDelta + kSecond * kStatBytes;
 };
 struct GradShared {
   uint64_t own_full, own_empty;       // the unit's own two tiles
@@ -199,12 +200,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      long long it = 0;
-      int units = 0;
+      RingAt<W::kFirst> r1;
+      RingAt<W::kSecond> r2;
+      int units = 0, it = 0;
       bool ok = true;
       for (int round = 0; ok; ++round) {
-      const int w = unit_of(round);
-      if (w >= work) break;
+        const int w = unit_of(round);
+        if (w >= work) break;
         const PackedUnit u = list.units[w / p.kv_heads];
         const int kh = w % p.kv_heads;
         const QuerySpan q = query_span(u, p.causal);
@@ -214,29 +216,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&S.own_full, 2 * W::kTile);
         load_tile<D>(k_mem, &map_k, kh, u.row0, &S.own_full);
         load_tile<D>(v_mem, &map_v, kh, u.row0, &S.own_full);
-        for (int t = 0; t < p.G * q.tiles && ok; ++t, ++it) {
-          const int head = kh * p.G + t / q.tiles, row = u.other0 + q.i0 + (t % q.tiles) * kTileRows;
-          const int s1 = (int)(it % W::kFirst), s2 = (int)(it % W::kSecond);
-          const uint32_t r1 = (uint32_t)(it / W::kFirst), r2 = (uint32_t)(it / W::kSecond);
-          if (r1 > 0 && !(ok = bounded_wait(&S.empty1[s1], (r1 - 1) & 1u, &S.failed))) break;
-          mbar_arrive_expect_tx(&S.full1[s1], W::kTile);
-          load_tile<D>(base + W::kRing1 + s1 * W::kTile, &map_q, head, row, &S.full1[s1]);
-          if (r2 > 0 && !(ok = bounded_wait(&S.empty2[s2], (r2 - 1) & 1u, &S.failed))) {
-            (void)mbar_wait_landed(&S.full1[s1], r1 & 1u);
-            break;
+        for (int head = kh * p.G; head < (kh + 1) * p.G && ok; ++head)
+          for (int t = 0; t < q.tiles && ok; ++t, ++it) {
+            const int row = u.other0 + q.i0 + t * kTileRows;
+            const float* st = stats_of(p, head) + row;
+            if (it >= W::kFirst && !(ok = bounded_wait(&S.empty1[r1.slot], r1.phase ^ 1u, &S.failed))) break;
+            mbar_arrive_expect_tx(&S.full1[r1.slot], W::kTile + kStatBytes);
+            load_tile<D>(base + W::kRing1 + r1.slot * W::kTile, &map_q, head, row, &S.full1[r1.slot]);
+            bulk_load(raw + W::kLse + r1.slot * kStatBytes, st, kStatBytes, &S.full1[r1.slot]);
+            if (it >= W::kSecond && !(ok = bounded_wait(&S.empty2[r2.slot], r2.phase ^ 1u, &S.failed))) {
+              (void)mbar_wait_landed(&S.full1[r1.slot], r1.phase);
+              break;
+            }
+            mbar_arrive_expect_tx(&S.full2[r2.slot], W::kTile + kStatBytes);
+            load_tile<D>(base + W::kRing2 + r2.slot * W::kTile, &map_do, head, row, &S.full2[r2.slot]);
+            bulk_load(raw + W::kDelta + r2.slot * kStatBytes, st + p.stat_pitch, kStatBytes, &S.full2[r2.slot]);
+            r1.advance();
+            r2.advance();
           }
-          mbar_arrive_expect_tx(&S.full2[s2], W::kTile + kStatBytes);
-          load_tile<D>(base + W::kRing2 + s2 * W::kTile, &map_do, head, row, &S.full2[s2]);
-          bulk_load(raw + W::kStats + s2 * kStatBytes, stats_of(p, head) + row, kStatBytes / 2, &S.full2[s2]);
-          bulk_load(raw + W::kStats + s2 * kStatBytes + kStatBytes / 2, stats_of(p, head) + p.stat_pitch + row,
-                    kStatBytes / 2, &S.full2[s2]);
-        }
       }
       // every copy has landed before the CTA may end
       if (units) (void)mbar_wait_landed(&S.own_full, (uint32_t)(units - 1) & 1u);
-      for (long long i = it > W::kFirst ? it - W::kFirst : 0; i < it; ++i)
+      for (int i = it > W::kFirst ? it - W::kFirst : 0; i < it; ++i)
         (void)mbar_wait_landed(&S.full1[i % W::kFirst], (uint32_t)(i / W::kFirst) & 1u);
-      for (long long i = it > W::kSecond ? it - W::kSecond : 0; i < it; ++i)
+      for (int i = it > W::kSecond ? it - W::kSecond : 0; i < it; ++i)
         (void)mbar_wait_landed(&S.full2[i % W::kSecond], (uint32_t)(i / W::kSecond) & 1u);
     }
     __syncwarp();
@@ -302,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float c = p.scale * kLog2e;
-    long long it = 0;
-    int units = 0;
+    uint32_t it = 0, units = 0;  // tiles and units so far
+    RingAt<W::kFirst> r1;
+    RingAt<W::kSecond> r2;
     bool ok = true;
     for (int round = 0; ok; ++round) {
       const int w = unit_of(round);
@@ -315,14 +319,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool there = row < u.rows;
       const int mine = first_query(p.causal, u.m, u.n, u.i0 + row);          // this key's first query
       const int last = first_query(p.causal, u.m, u.n, u.i0 + kTileRows - 1);  // the unit's last key's
+      int i0 = q.i0, t = 0;  // this tile's first query and its number
       for (int j = 0; j < n; ++j, ++it) {
-        const int i0 = q.i0 + (j % q.tiles) * kTileRows, s2 = (int)(it % W::kSecond);
-        const bool border = i0 < max(last, 0) || i0 + kTileRows > u.m;
+        const bool from_front = i0 < max(last, 0), at_end = i0 + kTileRows > u.m;  // some keys are not seen by all
         const int lo = mine - i0 - half * 64, hi = u.m - i0 - half * 64;  // of the half's columns
-        const float4* lse4 = reinterpret_cast<const float4*>(raw + W::kStats + s2 * kStatBytes) + half * 16;
-        const float4* delta4 = lse4 + 32;
-        if (!(ok = bounded_warp_wait(&S.full2[s2], (uint32_t)(it / W::kSecond) & 1u, &S.failed))) break;
-        if (!(ok = bounded_warp_wait(&S.s_full[0], (uint32_t)it & 1u, &S.failed))) break;
+        const float4* lse4 = reinterpret_cast<const float4*>(raw + W::kLse + r1.slot * kStatBytes) + half * 16;
+        const float4* delta4 = reinterpret_cast<const float4*>(raw + W::kDelta + r2.slot * kStatBytes) + half * 16;
+        i0 += kTileRows;
+        if (++t == q.tiles) {
+          t = 0;
+          i0 = q.i0;
+        }
+        if (!(ok = bounded_warp_wait(&S.full1[r1.slot], r1.phase, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.s_full[0], it & 1u, &S.failed))) break;
         tc::fence_after();
         uint32_t x[64];
         tc::ld32(t_s + lanes + half * 64, x);
@@ -340,10 +349,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[k + e + 2] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 2]), c, -s4.z)));
             x[k + e + 3] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 3]), c, -s4.w)));
           }
-          if (border) {
+          if (from_front) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (k + e < lo || k + e >= hi) x[k + e] = 0u;
+              if (k + e < lo) x[k + e] = 0u;
+          }
+          if (at_end) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (k + e >= hi) x[k + e] = 0u;
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -355,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full);
 
-        if (!(ok = bounded_warp_wait(&S.dp_full, (uint32_t)it & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.full2[r2.slot], r2.phase, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.dp_full, it & 1u, &S.failed))) break;
         tc::fence_after();
         uint32_t y[64];
         tc::ld32(t_dp + lanes + half * 64, y);
@@ -373,11 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             y[k + e + 2] = __float_as_uint(__uint_as_float(x[k + e + 2]) * (__uint_as_float(y[k + e + 2]) - s4.z));
             y[k + e + 3] = __float_as_uint(__uint_as_float(x[k + e + 3]) * (__uint_as_float(y[k + e + 3]) - s4.w));
           }
-          if (border) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k + e < lo || k + e >= hi) y[k + e] = 0u;
-          }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             pk[e] = Bf16::pack(__uint_as_float(y[k + 2 * e]), __uint_as_float(y[k + 2 * e + 1]));
@@ -388,8 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&S.ds_full);
-          mbar_arrive(&S.empty2[s2]);  // the statistics are read
+          mbar_arrive(&S.empty2[r2.slot]);  // delta is read
         }
+        r1.advance();
+        r2.advance();
       }
       if (!ok) break;
 
@@ -400,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* dv = p.dv.p + 2 * (tok0 * p.dv.ts + (long long)kh * p.dv.hs) + half * D;
       bool fine = true;
       if (n > 0) {
-        if (!(ok = bounded_warp_wait(&S.acc_full, (uint32_t)units & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.acc_full, units & 1u, &S.failed))) break;
         ++units;
         tc::fence_after();
         fine &= store_half<D>(t_dv + lanes + half * (D / 2), 1.0f, false, dv, 2 * p.dv.ts, rows, lane);
@@ -442,12 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      long long it = 0;
-      int units = 0;
+      RingAt<W::kFirst> r1;
+      RingAt<W::kSecond> r2;
+      int units = 0, it = 0;
       bool ok = true;
       for (int round = 0; ok; ++round) {
-      const int w = unit_of(round);
-      if (w >= work) break;
+        const int w = unit_of(round);
+        if (w >= work) break;
         const PackedUnit u = list.units[w / p.q_heads];
         const int head = w % p.q_heads, kh = head / p.G, n = tiles_of(u);
         if (!n) continue;
@@ -458,23 +471,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_tile<D>(do_mem, &map_do, head, u.row0, &S.own_full);
         for (int t = 0; t < n && ok; ++t, ++it) {
           const int row = u.other0 + t * kTileRows;
-          const int s1 = (int)(it % W::kFirst), s2 = (int)(it % W::kSecond);
-          const uint32_t r1 = (uint32_t)(it / W::kFirst), r2 = (uint32_t)(it / W::kSecond);
-          if (r1 > 0 && !(ok = bounded_wait(&S.empty1[s1], (r1 - 1) & 1u, &S.failed))) break;
-          mbar_arrive_expect_tx(&S.full1[s1], W::kTile);
-          load_tile<D>(base + W::kRing1 + s1 * W::kTile, &map_k, kh, row, &S.full1[s1]);
-          if (r2 > 0 && !(ok = bounded_wait(&S.empty2[s2], (r2 - 1) & 1u, &S.failed))) {
-            (void)mbar_wait_landed(&S.full1[s1], r1 & 1u);
+          if (it >= W::kFirst && !(ok = bounded_wait(&S.empty1[r1.slot], r1.phase ^ 1u, &S.failed))) break;
+          mbar_arrive_expect_tx(&S.full1[r1.slot], W::kTile);
+          load_tile<D>(base + W::kRing1 + r1.slot * W::kTile, &map_k, kh, row, &S.full1[r1.slot]);
+          if (it >= W::kSecond && !(ok = bounded_wait(&S.empty2[r2.slot], r2.phase ^ 1u, &S.failed))) {
+            (void)mbar_wait_landed(&S.full1[r1.slot], r1.phase);
             break;
           }
-          mbar_arrive_expect_tx(&S.full2[s2], W::kTile);
-          load_tile<D>(base + W::kRing2 + s2 * W::kTile, &map_v, kh, row, &S.full2[s2]);
+          mbar_arrive_expect_tx(&S.full2[r2.slot], W::kTile);
+          load_tile<D>(base + W::kRing2 + r2.slot * W::kTile, &map_v, kh, row, &S.full2[r2.slot]);
+          r1.advance();
+          r2.advance();
         }
       }
       if (units) (void)mbar_wait_landed(&S.own_full, (uint32_t)(units - 1) & 1u);
-      for (long long i = it > W::kFirst ? it - W::kFirst : 0; i < it; ++i)
+      for (int i = it > W::kFirst ? it - W::kFirst : 0; i < it; ++i)
         (void)mbar_wait_landed(&S.full1[i % W::kFirst], (uint32_t)(i / W::kFirst) & 1u);
-      for (long long i = it > W::kSecond ? it - W::kSecond : 0; i < it; ++i)
+      for (int i = it > W::kSecond ? it - W::kSecond : 0; i < it; ++i)
         (void)mbar_wait_landed(&S.full2[i % W::kSecond], (uint32_t)(i / W::kSecond) & 1u);
     }
     __syncwarp();
@@ -544,8 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float c = p.scale * kLog2e;
-    long long it = 0;
-    int units = 0;
+    uint32_t it = 0, units = 0;  // tiles and units so far
     bool ok = true;
     for (int round = 0; ok; ++round) {
       const int w = unit_of(round);
@@ -557,9 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lse = there ? stats_of(p, head)[u.row0 + row] : INFINITY;
       const float delta = there ? stats_of(p, head)[p.stat_pitch + u.row0 + row] : 0.0f;
       for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t buf = t_s + (uint32_t)(it & 1) * 128u + lanes;
+        const uint32_t buf = t_s + (it & 1u) * 128u + lanes;
         const int left = (j + 1) * kTileRows > vis0 ? vis - j * kTileRows - half * 64 : 64;
-        if (!(ok = bounded_warp_wait(&S.s_full[it & 1], (uint32_t)(it >> 1) & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.s_full[it & 1], (it >> 1) & 1u, &S.failed))) break;
         tc::fence_after();
         uint32_t x[64];
         tc::ld32(buf + half * 64, x);
@@ -568,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::wait_ld32(x + 32);
 #pragma unroll
         for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -lse)));
-        if (!(ok = bounded_warp_wait(&S.dp_full, (uint32_t)it & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.dp_full, it & 1u, &S.failed))) break;
         tc::fence_after();
 #pragma unroll
         for (int k = 0; k < 64; k += 32) {
@@ -599,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* dq = p.dq.p + 2 * (tok0 * p.dq.ts + (long long)head * p.dq.hs) + half * D;
       bool fine = true;
       if (n > 0) {
-        if (!(ok = bounded_warp_wait(&S.acc_full, (uint32_t)units & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait(&S.acc_full, units & 1u, &S.failed))) break;
         ++units;
         tc::fence_after();
         fine = store_half<D>(t_dq + lanes + half * (D / 2), p.scale, vis <= 0, dq, 2 * p.dq.ts, rows, lane);
