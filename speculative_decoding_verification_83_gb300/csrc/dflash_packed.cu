@@ -119,8 +119,8 @@ __device__ void attend_row(const PackedParams& p, int t, int head, int i, int n,
 }
 
 // Goes through the flags; row(t, head, i, unit) is called by one warp for every row
-// of a flagged 32, for either half's flag.
-template <int kPer, class F>
+// of a flagged 32, for any of its kSame flags.
+template <int kPer, int kSame, class F>
 __device__ __forceinline__ void each_flagged(const PackedList& list, const uint8_t* flags, int heads, F row) {
   const long long total = (long long)*list.count * heads * kPer;
   const int warp = threadIdx.x >> 5;
@@ -129,7 +129,7 @@ __device__ __forceinline__ void each_flagged(const PackedList& list, const uint8
     if (!__syncthreads_or(at < total && flags[at])) continue;
     for (long long f = base; f < min(total, base + blockDim.x); ++f) {
       if (!flags[f]) continue;
-      const int part = (int)(f % kPer) / 2, head = (int)(f / kPer % heads);
+      const int part = (int)(f % kPer) / kSame, head = (int)(f / kPer % heads);
       const PackedUnit u = list.units[f / kPer / heads];
       for (int r = 32 * part + warp; r < min(u.rows, 32 * part + 32); r += kWarps) row(u.row0 + r, head, u.i0 + r, u);
     }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     redo_forward_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
   __shared__ float q_row[kWarps][D];
   grid_dependency_sync();
-  each_flagged<kForwardFlags>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+  each_flagged<kForwardFlags, 2>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
     if (row_not_finite<T, D>(row_of(p.o, t, head)))
       attend_row<T, D>(p, t, head, i, u.n, u.other0, u.m, q_row[threadIdx.x >> 5]);
   });
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   __shared__ float rows[kWarps][2][D];
   grid_dependency_sync();
   const int warp = threadIdx.x >> 5;
-  each_flagged<kGradFlags>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+  each_flagged<kGradFlags, 4>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
     if (!row_not_finite<T, D>(row_of(p.dq, t, head))) return;
     dq_row<T, D>(p, t, head, i, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
   });
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   __shared__ float rows[kWarps][2][D];
   grid_dependency_sync();
   const int warp = threadIdx.x >> 5;
-  each_flagged<kGradFlags>(list, flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
+  each_flagged<kGradFlags, 4>(list, flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
     if (!row_not_finite<T, D>(row_of(p.dk, t, head)) && !row_not_finite<T, D>(row_of(p.dv, t, head))) return;
     dkv_row<T, D>(p, t, head, j, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
   });
@@ -476,7 +476,7 @@ int launch_delta(const PackedParams& p, int head_dim, void* stream) {
 namespace {
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 size_t flag_bytes(int tokens, int B, int rows, int heads) {
-  return up((size_t)most_units(tokens, B, rows) * heads * (rows / 16));
+  return up((size_t)most_units(tokens, B, rows) * heads * (rows == kForwardRows ? kForwardFlags : kGradFlags));
 }
 // Rows of a head's statistics: a multiple of 4, and room behind the last row for a whole tile.
 int stat_pitch(int tokens) { return (tokens + 131) / 4 * 4; }

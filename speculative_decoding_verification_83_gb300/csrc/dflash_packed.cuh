@@ -73,7 +73,7 @@ int launch_list(const PackedParams& p, bool keys, int rows, const PackedList& li
 
 // The tensor cores' kernels leave rows whose masked keys or queries hold values that
 // are not finite as NaN (0 times such a value), and a flag for 32 rows with a result that is
-// not finite, two for each 32 rows (the columns' halves). These kernels go through the flagged rows
+// not finite, two or four for each 32 rows (parts of the columns). These kernels go through the flagged rows
 // one by one, with exact masks, and set the rows of no sequence to 0.
 int launch_redo_forward(const PackedParams& p, int dtype, int head_dim, const PackedList& list, const uint8_t* flags,
                         void* stream);
@@ -87,7 +87,7 @@ int launch_forward_tc(const PackedParams& p, int dtype, int head_dim, const Pack
 int launch_dq_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, int sms, void* stream);
 int launch_dkv_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, int sms, void* stream);
 constexpr int kForwardRows = 256, kGradRows = 128;  // of a unit
-constexpr int kForwardFlags = kForwardRows / 16, kGradFlags = kGradRows / 16;  // of a unit and head
+constexpr int kForwardFlags = kForwardRows / 16, kGradFlags = kGradRows / 8;  // of a unit and head
 constexpr int kMaxBatch = 2048;
 
 }  // namespace dflash

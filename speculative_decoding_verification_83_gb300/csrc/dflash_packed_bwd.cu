@@ -30,7 +30,9 @@
 namespace dflash {
 namespace {
 
-constexpr int kThreads = 320, kMmaWarp = 8, kLoadWarp = 9, kWorkWarps = 8;
+constexpr int kThreads = 576, kMmaWarp = 16, kLoadWarp = 17, kWorkWarps = 16;
+constexpr int kParts = kWorkWarps / 4;   // warps that share rows
+constexpr int kCols = 128 / kParts;      // columns of a tile for each
 constexpr int kTileRows = 128;
 constexpr uint32_t kStatBytes = 512;  // of a tile of queries: lse comes with Q, delta with dO
 
@@ -114,13 +116,13 @@ __device__ __forceinline__ void mma_inner(uint32_t d, uint32_t a, uint32_t b, ui
                lead);
 }
 // D (+)= A B over 128 rows of B; A in tensor memory
-// (each half of A's columns lies over that half of the scores)
+// (each part of A's columns lies over that part of the scores)
 template <int D>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool add, uint32_t lead) {
   constexpr uint32_t id = tc::idesc<Bf16>(128, D, false, true);
   const uint64_t bd = tc::operand(b, 16384u);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) tc::mma_ts(d, a + (k >> 2) * 64 + (k & 3) * 8, bd + (uint64_t)(k * 128), id, add || k > 0, lead);
+  for (int k = 0; k < 8; ++k) tc::mma_ts(d, a + (k >> 1) * 32 + (k & 1) * 8, bd + (uint64_t)(k * 128), id, add || k > 0, lead);
 }
 // A tile of a ring of kSlots: its place, and the parity of its round
 template <int kSlots>
@@ -135,32 +137,34 @@ struct RingAt {
   }
 };
 
-// Half of a warp's 32 rows of sums times `factor` to memory as bf16 (rows where `zero`
+// A part of a warp's 32 rows of sums times `factor` to memory as bf16 (rows where `zero`
 // holds: 0, whatever the products left there); whether this lane's are finite
 template <int D>
-__device__ __forceinline__ bool store_half(uint32_t taddr, float factor, bool zero, unsigned char* dst, long long stride,
+__device__ __forceinline__ bool store_part(uint32_t taddr, float factor, bool zero, unsigned char* dst, long long stride,
                                            int rows, int lane) {
-  constexpr int kPieces = D / 16;
-  uint32_t w[4 * kPieces];
-  bool fine = true;
-#pragma unroll
-  for (int d = 0; d < D / 2; d += 32) {
-    uint32_t y[32];
-    tc::ld32(taddr + d, y);
+  constexpr int kMine = D / kParts, kPieces = kMine / 8;
+  uint32_t y[kMine], w[4 * kPieces];
+  if constexpr (kMine == 32) {
+    tc::ld32(taddr, y);
     tc::wait_ld32(y);
+  } else {
+    tc::ld16(taddr, y);
+    tc::wait_ld16(y);
+  }
+  float2 probe = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = zero ? 0.0f : __uint_as_float(y[2 * i]) * factor, b = zero ? 0.0f : __uint_as_float(y[2 * i + 1]) * factor;
-      w[d / 2 + i] = Bf16::pack(a, b);
-      fine &= fabsf(a) < INFINITY && fabsf(b) < INFINITY;
-    }
+  for (int i = 0; i < kMine / 2; ++i) {
+    float2 f = mul2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(factor, factor));
+    if (zero) f = make_float2(0.0f, 0.0f);
+    w[i] = Bf16::pack(f.x, f.y);
+    probe = fma2(f, make_float2(0.0f, 0.0f), probe);
   }
   store_rows<kPieces>(w, dst, stride, rows, lane);
-  return fine;
+  return probe.x + probe.y == 0.0f;
 }
 template <int D>
-__device__ __forceinline__ void clear_half(unsigned char* dst, long long stride, int rows, int lane) {
-  constexpr int kPieces = D / 16;
+__device__ __forceinline__ void clear_part(unsigned char* dst, long long stride, int rows, int lane) {
+  constexpr int kPieces = D / kParts / 8;
   uint32_t w[4 * kPieces] = {};
   store_rows<kPieces>(w, dst, stride, rows, lane);
 }
@@ -302,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     (void)mbar_wait_landed(&S.drained, 0);
     __syncwarp();
   } else {
-    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
+    const uint32_t mine = ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kCols);
     const float c = p.scale * kLog2e;
     uint32_t it = 0, units = 0;  // tiles and units so far
     RingAt<W::kFirst> r1;
@@ -317,82 +321,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const QuerySpan q = query_span(u, p.causal);
       const int n = p.G * q.tiles;
       const bool there = row < u.rows;
-      const int mine = first_query(p.causal, u.m, u.n, u.i0 + row);          // this key's first query
-      const int last = first_query(p.causal, u.m, u.n, u.i0 + kTileRows - 1);  // the unit's last key's
+      const int first = first_query(p.causal, u.m, u.n, u.i0 + row);          // that sees this key
+      const int last = first_query(p.causal, u.m, u.n, u.i0 + kTileRows - 1);  // ... the unit's last
       int i0 = q.i0, t = 0;  // this tile's first query and its number
       for (int j = 0; j < n; ++j, ++it) {
         const bool from_front = i0 < max(last, 0), at_end = i0 + kTileRows > u.m;  // some keys are not seen by all
-        const int lo = mine - i0 - half * 64, hi = u.m - i0 - half * 64;  // of the half's columns
-        const float4* lse4 = reinterpret_cast<const float4*>(raw + W::kLse + r1.slot * kStatBytes) + half * 16;
-        const float4* delta4 = reinterpret_cast<const float4*>(raw + W::kDelta + r2.slot * kStatBytes) + half * 16;
+        const int lo = first - i0 - part * kCols, hi = u.m - i0 - part * kCols;    // of this part's columns
+        const float4* lse4 = reinterpret_cast<const float4*>(raw + W::kLse + r1.slot * kStatBytes) + part * (kCols / 4);
+        const float4* delta4 = reinterpret_cast<const float4*>(raw + W::kDelta + r2.slot * kStatBytes) + part * (kCols / 4);
         i0 += kTileRows;
         if (++t == q.tiles) {
           t = 0;
           i0 = q.i0;
         }
-        if (!(ok = bounded_warp_wait(&S.full1[r1.slot], r1.phase, &S.failed))) break;
-        if (!(ok = bounded_warp_wait(&S.s_full[0], it & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait2(&S.s_full[0], it & 1u, &S.full1[r1.slot], r1.phase, &S.failed))) break;
         tc::fence_after();
-        uint32_t x[64];
-        tc::ld32(t_s + lanes + half * 64, x);
-        tc::ld32(t_s + lanes + half * 64 + 32, x + 32);
+        uint32_t x[kCols], pk[kCols / 2];
+        tc::ld32(t_s + mine, x);
         tc::wait_ld32(x);
-        tc::wait_ld32(x + 32);
 #pragma unroll
-        for (int k = 0; k < 64; k += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 s4 = lse4[(k + e) / 4];
-            x[k + e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e]), c, -s4.x)));
-            x[k + e + 1] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 1]), c, -s4.y)));
-            x[k + e + 2] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 2]), c, -s4.z)));
-            x[k + e + 3] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[k + e + 3]), c, -s4.w)));
-          }
-          if (from_front) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k + e < lo) x[k + e] = 0u;
-          }
-          if (at_end) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k + e >= hi) x[k + e] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = Bf16::pack(__uint_as_float(x[k + 2 * e]), __uint_as_float(x[k + 2 * e + 1]));
-          tc::st16(t_s + lanes + half * 64 + k / 2, pk);
+        for (int e = 0; e < kCols; e += 4) {
+          const float4 s4 = lse4[e / 4];
+          x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -s4.x)));
+          x[e + 1] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e + 1]), c, -s4.y)));
+          x[e + 2] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e + 2]), c, -s4.z)));
+          x[e + 3] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e + 3]), c, -s4.w)));
         }
+        if (from_front) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (e < lo) x[e] = 0u;
+        }
+        if (at_end) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (e >= hi) x[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < kCols / 2; ++e) pk[e] = Bf16::pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+        tc::st16(t_s + mine, pk);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_full);
 
-        if (!(ok = bounded_warp_wait(&S.full2[r2.slot], r2.phase, &S.failed))) break;
-        if (!(ok = bounded_warp_wait(&S.dp_full, it & 1u, &S.failed))) break;
+        if (!(ok = bounded_warp_wait2(&S.dp_full, it & 1u, &S.full2[r2.slot], r2.phase, &S.failed))) break;
         tc::fence_after();
-        uint32_t y[64];
-        tc::ld32(t_dp + lanes + half * 64, y);
-        tc::ld32(t_dp + lanes + half * 64 + 32, y + 32);
+        uint32_t y[kCols];
+        tc::ld32(t_dp + mine, y);
         tc::wait_ld32(y);
-        tc::wait_ld32(y + 32);
 #pragma unroll
-        for (int k = 0; k < 64; k += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 s4 = delta4[(k + e) / 4];
-            y[k + e] = __float_as_uint(__uint_as_float(x[k + e]) * (__uint_as_float(y[k + e]) - s4.x));
-            y[k + e + 1] = __float_as_uint(__uint_as_float(x[k + e + 1]) * (__uint_as_float(y[k + e + 1]) - s4.y));
-            y[k + e + 2] = __float_as_uint(__uint_as_float(x[k + e + 2]) * (__uint_as_float(y[k + e + 2]) - s4.z));
-            y[k + e + 3] = __float_as_uint(__uint_as_float(x[k + e + 3]) * (__uint_as_float(y[k + e + 3]) - s4.w));
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = Bf16::pack(__uint_as_float(y[k + 2 * e]), __uint_as_float(y[k + 2 * e + 1]));
-          tc::st16(t_dp + lanes + half * 64 + k / 2, pk);
+        for (int e = 0; e < kCols; e += 4) {
+          const float4 s4 = delta4[e / 4];
+          pk[e / 2] = Bf16::pack(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - s4.x),
+                                 __uint_as_float(x[e + 1]) * (__uint_as_float(y[e + 1]) - s4.y));
+          pk[e / 2 + 1] = Bf16::pack(__uint_as_float(x[e + 2]) * (__uint_as_float(y[e + 2]) - s4.z),
+                                     __uint_as_float(x[e + 3]) * (__uint_as_float(y[e + 3]) - s4.w));
         }
+        tc::st16(t_dp + mine, pk);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -405,24 +391,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      // ---- the keys' ends: half of the columns each
+      // ---- the keys' ends: a part of the columns each
       const int rows = u.rows - quarter * 32;  // of this warp's 32
       const long long tok0 = u.row0 + quarter * 32;
-      unsigned char* dk = p.dk.p + 2 * (tok0 * p.dk.ts + (long long)kh * p.dk.hs) + half * D;
-      unsigned char* dv = p.dv.p + 2 * (tok0 * p.dv.ts + (long long)kh * p.dv.hs) + half * D;
+      constexpr int kMine = D / kParts;
+      unsigned char* dk = p.dk.p + 2 * (tok0 * p.dk.ts + (long long)kh * p.dk.hs + part * kMine);
+      unsigned char* dv = p.dv.p + 2 * (tok0 * p.dv.ts + (long long)kh * p.dv.hs + part * kMine);
+      const uint32_t sums = ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kMine);
       bool fine = true;
       if (n > 0) {
         if (!(ok = bounded_warp_wait(&S.acc_full, units & 1u, &S.failed))) break;
         ++units;
         tc::fence_after();
-        fine &= store_half<D>(t_dv + lanes + half * (D / 2), 1.0f, false, dv, 2 * p.dv.ts, rows, lane);
-        fine &= store_half<D>(t_dk + lanes + half * (D / 2), p.scale, false, dk, 2 * p.dk.ts, rows, lane);
+        fine &= store_part<D>(t_dv + sums, 1.0f, false, dv, 2 * p.dv.ts, rows, lane);
+        fine &= store_part<D>(t_dk + sums, p.scale, false, dk, 2 * p.dk.ts, rows, lane);
       } else {
-        clear_half<D>(dv, 2 * p.dv.ts, rows, lane);
-        clear_half<D>(dk, 2 * p.dk.ts, rows, lane);
+        clear_part<D>(dv, 2 * p.dv.ts, rows, lane);
+        clear_part<D>(dk, 2 * p.dk.ts, rows, lane);
       }
       const bool odd = __any_sync(0xffffffffu, there && !fine);
-      if (lane == 0) flags[(size_t)w * kGradFlags + 2 * quarter + half] = odd;
+      if (lane == 0) flags[(size_t)w * kGradFlags + kParts * quarter + part] = odd;
       tc::fence_before();
     }
   }
@@ -554,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     (void)mbar_wait_landed(&S.drained, 0);
     __syncwarp();
   } else {
-    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
+    const uint32_t mine = ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kCols);
     const float c = p.scale * kLog2e;
     uint32_t it = 0, units = 0;  // tiles and units so far
     bool ok = true;
@@ -569,36 +557,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lse = there ? stats_of(p, head)[u.row0 + row] : INFINITY;
       const float delta = there ? stats_of(p, head)[p.stat_pitch + u.row0 + row] : 0.0f;
       for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t buf = t_s + (it & 1u) * 128u + lanes;
-        const int left = (j + 1) * kTileRows > vis0 ? vis - j * kTileRows - half * 64 : 64;
-        if (!(ok = bounded_warp_wait(&S.s_full[it & 1], (it >> 1) & 1u, &S.failed))) break;
+        const uint32_t buf = t_s + (it & 1u) * 128u + mine;
+        if (!(ok = bounded_warp_wait(&S.s_full[it & 1u], (it >> 1) & 1u, &S.failed))) break;
         tc::fence_after();
-        uint32_t x[64];
-        tc::ld32(buf + half * 64, x);
-        tc::ld32(buf + half * 64 + 32, x + 32);
+        uint32_t x[kCols], y[kCols], pk[kCols / 2];
+        tc::ld32(buf, x);
         tc::wait_ld32(x);
-        tc::wait_ld32(x + 32);
 #pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -lse)));
+        for (int e = 0; e < kCols; ++e) x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -lse)));
+        if ((j + 1) * kTileRows > vis0) {  // some row does not see all of the tile
+          const int left = vis - j * kTileRows - part * kCols;
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (e >= left) x[e] = 0u;
+        }
         if (!(ok = bounded_warp_wait(&S.dp_full, it & 1u, &S.failed))) break;
         tc::fence_after();
+        tc::ld32(t_dp + mine, y);
+        tc::wait_ld32(y);
 #pragma unroll
-        for (int k = 0; k < 64; k += 32) {
-          uint32_t y[32], pk[16];
-          tc::ld32(t_dp + lanes + half * 64 + k, y);
-          tc::wait_ld32(y);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            y[e] = __float_as_uint(__uint_as_float(x[k + e]) * (__uint_as_float(y[e]) - delta));
-          if (__any_sync(0xffffffffu, left < 64)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k + e >= left) y[e] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = Bf16::pack(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-          tc::st16(buf + half * 64 + k / 2, pk);
-        }
+        for (int e = 0; e < kCols / 2; ++e)
+          pk[e] = Bf16::pack(__uint_as_float(x[2 * e]) * (__uint_as_float(y[2 * e]) - delta),
+                             __uint_as_float(x[2 * e + 1]) * (__uint_as_float(y[2 * e + 1]) - delta));
+        tc::st16(buf, pk);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -608,18 +589,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       const int rows = u.rows - quarter * 32;
       const long long tok0 = u.row0 + quarter * 32;
-      unsigned char* dq = p.dq.p + 2 * (tok0 * p.dq.ts + (long long)head * p.dq.hs) + half * D;
+      constexpr int kMine = D / kParts;
+      unsigned char* dq = p.dq.p + 2 * (tok0 * p.dq.ts + (long long)head * p.dq.hs + part * kMine);
       bool fine = true;
       if (n > 0) {
         if (!(ok = bounded_warp_wait(&S.acc_full, units & 1u, &S.failed))) break;
         ++units;
         tc::fence_after();
-        fine = store_half<D>(t_dq + lanes + half * (D / 2), p.scale, vis <= 0, dq, 2 * p.dq.ts, rows, lane);
+        fine = store_part<D>(t_dq + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kMine), p.scale, vis <= 0, dq,
+                             2 * p.dq.ts, rows, lane);
       } else {
-        clear_half<D>(dq, 2 * p.dq.ts, rows, lane);
+        clear_part<D>(dq, 2 * p.dq.ts, rows, lane);
       }
       const bool odd = __any_sync(0xffffffffu, there && !fine);
-      if (lane == 0) flags[(size_t)w * kGradFlags + 2 * quarter + half] = odd;
+      if (lane == 0) flags[(size_t)w * kGradFlags + kParts * quarter + part] = odd;
       tc::fence_before();
     }
   }

@@ -30,6 +30,14 @@ __device__ __forceinline__ bool bounded_warp_wait(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, failed));
 }
 
+// Two barriers in the time of one: every other lane looks at the second.
+__device__ __forceinline__ bool bounded_warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* failed) {
+  const bool second = threadIdx.x & 1;
+  const bool ok = __all_sync(0xffffffffu, bounded_wait(second ? b : a, second ? pb : pa, failed));
+  __syncwarp();
+  return ok;
+}
+
 // A CTA's units: every gridDim-th of the list, in turn from either end of a round,
 // since the list begins with the largest.
 __device__ __forceinline__ int unit_of(int round) {
