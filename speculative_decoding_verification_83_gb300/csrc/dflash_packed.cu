@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   });
 }
 
-// delta, the sum over d of dout out, and lse as the products' kernels read them; behind
+// delta, the sum over d of dout out, and lse as the products' kernels read them (their signs reversed); behind
 // the last row a tile's worth of zeros
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p) {
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p
     const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
     const float lse = p.lse[r];
     float* st = p.row_stats + (size_t)head * 2 * p.stat_pitch;
-    st[t] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
-    st[p.stat_pitch + t] = s;
+    st[t] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
+    st[p.stat_pitch + t] = -s;
   }
 }
 
@@ -221,7 +221,7 @@ __device__ void dq_row(const PackedParams& p, int t, int head, int i, int n, int
     g_row[lane + 32 * c] = value<T>(row_of(p.d_o, t, head), lane + 32 * c);
   }
   __syncwarp();
-  const float lse = p.lse[r], delta = p.row_stats[((size_t)head * 2 + 1) * p.stat_pitch + t];
+  const float lse = p.lse[r], delta = -p.row_stats[((size_t)head * 2 + 1) * p.stat_pitch + t];
   float acc[D / 32] = {};
   for (int j0 = 0; j0 < vis; j0 += 32) {
     const int j = j0 + lane, count = min(32, vis - j0);
@@ -268,7 +268,7 @@ __device__ void dkv_row(const PackedParams& p, int t, int kh, int j, int m, int 
         const long long at = (long long)(q0 + i) * p.q_heads + head;
         const float x = dot<T, D>(k_row, row_of(p.q, q0 + i, head)) * p.scale, lse = p.lse[at];
         w = lse == -INFINITY ? 0.0f : expf(x - lse);
-        ds = w * (dot<T, D>(v_row, row_of(p.d_o, q0 + i, head)) - p.row_stats[((size_t)head * 2 + 1) * p.stat_pitch + q0 + i]) * p.scale;
+        ds = w * (dot<T, D>(v_row, row_of(p.d_o, q0 + i, head)) + p.row_stats[((size_t)head * 2 + 1) * p.stat_pitch + q0 + i]) * p.scale;
       }
       for (int k = 0; k < count; ++k) {
         const float wk = __shfl_sync(kAll, w, k), dsk = __shfl_sync(kAll, ds, k);

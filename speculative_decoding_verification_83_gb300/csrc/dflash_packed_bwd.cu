@@ -55,7 +55,7 @@ template <int D>
 constexpr size_t kGradSmem = GradShape<D>::kBars + sizeof(GradShared);
 static_assert(kGradSmem<128> <= 232448, "one CTA's shared memory (227 KB)");
 
-// A head's statistics: lse, then (delta_at further on) delta
+// A head's statistics, their signs reversed: lse, then (stat_pitch further on) delta
 __device__ __forceinline__ const float* stats_of(const PackedParams& p, int head) {
   return p.row_stats + (size_t)head * 2 * p.stat_pitch;
 }
@@ -136,6 +136,10 @@ struct RingAt {
     }
   }
 };
+
+__device__ __forceinline__ float2 pair(const uint32_t* x, int e) {
+  return make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+}
 
 // A part of a warp's 32 rows of sums times `factor` to memory as bf16 (rows where `zero`
 // holds: 0, whatever the products left there); whether this lane's are finite
@@ -342,10 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kCols; e += 4) {
           const float4 s4 = lse4[e / 4];
-          x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -s4.x)));
-          x[e + 1] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e + 1]), c, -s4.y)));
-          x[e + 2] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e + 2]), c, -s4.z)));
-          x[e + 3] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e + 3]), c, -s4.w)));
+          const float2 a = fma2(pair(x, e), make_float2(c, c), make_float2(s4.x, s4.y));
+          const float2 b = fma2(pair(x, e + 2), make_float2(c, c), make_float2(s4.z, s4.w));
+          x[e] = __float_as_uint(ex2_approx(a.x));
+          x[e + 1] = __float_as_uint(ex2_approx(a.y));
+          x[e + 2] = __float_as_uint(ex2_approx(b.x));
+          x[e + 3] = __float_as_uint(ex2_approx(b.y));
         }
         if (from_front) {
 #pragma unroll
@@ -373,10 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kCols; e += 4) {
           const float4 s4 = delta4[e / 4];
-          pk[e / 2] = Bf16::pack(__uint_as_float(x[e]) * (__uint_as_float(y[e]) - s4.x),
-                                 __uint_as_float(x[e + 1]) * (__uint_as_float(y[e + 1]) - s4.y));
-          pk[e / 2 + 1] = Bf16::pack(__uint_as_float(x[e + 2]) * (__uint_as_float(y[e + 2]) - s4.z),
-                                     __uint_as_float(x[e + 3]) * (__uint_as_float(y[e + 3]) - s4.w));
+          const float2 a = mul2(pair(x, e), add2(pair(y, e), make_float2(s4.x, s4.y)));
+          const float2 b = mul2(pair(x, e + 2), add2(pair(y, e + 2), make_float2(s4.z, s4.w)));
+          pk[e / 2] = Bf16::pack(a.x, a.y);
+          pk[e / 2 + 1] = Bf16::pack(b.x, b.y);
         }
         tc::st16(t_dp + mine, pk);
         tc::wait_st();
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = w % p.q_heads, n = tiles_of(u);
       const bool there = row < u.rows;
       const int vis = there ? seen_keys(p.causal, u.n, u.m, u.i0 + row) : 0, vis0 = seen_keys(p.causal, u.n, u.m, u.i0);
-      const float lse = there ? stats_of(p, head)[u.row0 + row] : INFINITY;
+      const float lse = there ? stats_of(p, head)[u.row0 + row] : -INFINITY;
       const float delta = there ? stats_of(p, head)[p.stat_pitch + u.row0 + row] : 0.0f;
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t buf = t_s + (it & 1u) * 128u + mine;
@@ -564,7 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld32(buf, x);
         tc::wait_ld32(x);
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c, -lse)));
+        for (int e = 0; e < kCols; e += 2) {
+          const float2 a = fma2(pair(x, e), make_float2(c, c), make_float2(lse, lse));
+          x[e] = __float_as_uint(ex2_approx(a.x));
+          x[e + 1] = __float_as_uint(ex2_approx(a.y));
+        }
         if ((j + 1) * kTileRows > vis0) {  // some row does not see all of the tile
           const int left = vis - j * kTileRows - part * kCols;
 #pragma unroll
@@ -576,9 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::ld32(t_dp + mine, y);
         tc::wait_ld32(y);
 #pragma unroll
-        for (int e = 0; e < kCols / 2; ++e)
-          pk[e] = Bf16::pack(__uint_as_float(x[2 * e]) * (__uint_as_float(y[2 * e]) - delta),
-                             __uint_as_float(x[2 * e + 1]) * (__uint_as_float(y[2 * e + 1]) - delta));
+        for (int e = 0; e < kCols / 2; ++e) {
+          const float2 a = mul2(pair(x, 2 * e), add2(pair(y, 2 * e), make_float2(delta, delta)));
+          pk[e] = Bf16::pack(a.x, a.y);
+        }
         tc::st16(buf, pk);
         tc::wait_st();
         tc::fence_before();

@@ -65,7 +65,7 @@ struct PackedParams {
   int8_t* low;               // [q_tokens, q_heads, head_dim] or null: what the outputs' rounding left, see out_low
   float* lse;                // [q_tokens, q_heads]
   HeadRows d_o, dq, dk, dv;  // backward
-  // backward: by head, stat_pitch rows of lse log2 e (a row that sees nothing: +inf), then of delta = sum of d_o o
+  // backward: by head, stat_pitch rows of -lse log2 e (-inf for a row that sees nothing), then of -delta, delta = sum of d_o o
   float* row_stats;
   int stat_pitch;
   const int32_t *q_start, *kv_start;
