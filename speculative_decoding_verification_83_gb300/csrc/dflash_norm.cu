@@ -11,8 +11,8 @@
 // What bounds both is reading and writing each value once. A head lies in D / 16
 // lanes, two vectors of 8 values each, chosen so that both halves of a rotated
 // pair meet in one lane; the same lane place holds the same values of every head
-// that a thread goes through, so its weights stay in registers, and so do its
-// 32 sums of the weights' gradients. A block takes tokens in turn: their angles
+// that a thread goes through, so its sums of the weights' gradients stay in
+// registers. A block takes tokens in turn: their angles
 // go to shared memory while the first heads' values arrive. The weights'
 // gradients are summed per thread, per block, and over blocks by a second kernel,
 // always in the same order.
@@ -54,26 +54,37 @@ __device__ __forceinline__ void fill_turns(const NormParams& p, float2* turn, in
   }
 }
 
-// A row is one head of one token: queries, then keys.
+// Weights for a lane place: 16 of one head in pieces of 4, a piece of all lanes side
+// by side, so that reading them meets no bank twice.
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
+__device__ __forceinline__ void fill_weights(const NormParams& p, float4* w) {
+  constexpr int kLanes = D / 16;
+  for (int at = threadIdx.x; at < 2 * kLanes; at += kThreads) {
+    const int part = at / kLanes, i = at - part * kLanes;
+    const Place l = place_of(p, i);
+    const void* from = part ? p.k_weight : p.q_weight;
+    float a[8], b[8];
+    weight8<T>(from, p.weight_f32, l.va, a);
+    weight8<T>(from, p.weight_f32, l.vb, b);
+    float4* to = w + part * 4 * kLanes + i;
+    to[0] = make_float4(a[0], a[1], a[2], a[3]);
+    to[kLanes] = make_float4(a[4], a[5], a[6], a[7]);
+    to[2 * kLanes] = make_float4(b[0], b[1], b[2], b[3]);
+    to[3 * kLanes] = make_float4(b[4], b[5], b[6], b[7]);
+  }
+}
+
+// A row is one head of one token: queries, then keys. What bounds it: 302 MB of 8192
+// tokens, 64 + 8 heads of 128 in bf16 take XXX us; with the weights in registers, two
+// blocks an SM, they took 81.
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const NormParams p) {
   constexpr int kLanes = D / 16, kRows = kThreads / kLanes, kBatch = 2;
   __shared__ float2 turn[kGroup * D / 2];
+  __shared__ float4 weights[2 * 4 * kLanes];
   grid_dependency_sync();
   const int i = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
   const Place l = place_of(p, i);
-  float wq[16], wk[16];
-  {
-    float a[8], b[8];
-    weight8<T>(p.q_weight, p.weight_f32, l.va, a);
-    weight8<T>(p.q_weight, p.weight_f32, l.vb, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) wq[e] = a[e], wq[8 + e] = b[e];
-    weight8<T>(p.k_weight, p.weight_f32, l.va, a);
-    weight8<T>(p.k_weight, p.weight_f32, l.vb, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) wk[e] = a[e], wk[8 + e] = b[e];
-  }
   const int heads = p.q_heads + p.k_heads, t0 = blockIdx.x * kGroup, nt = min(kGroup, p.tokens - t0);
   const int rows = nt * heads, half = p.rot >> 1, rv = p.rot >> 4;
   bool ready = false;
@@ -91,6 +102,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
       y[k] = src[l.vb];
     }
     if (!ready) {
+      fill_weights<T, D>(p, weights);
       fill_turns(p, turn, t0, nt);
       __syncthreads();
       ready = true;
@@ -108,10 +120,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += a[e] * a[e] + b[e] * b[e];
       const float inv = rsqrtf(head_sum<kLanes>(sum) * (1.0f / D) + p.eps);
+      const float4* w = weights + (is_q ? 0 : 4 * kLanes) + i;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] *= inv * (is_q ? wq[e] : wk[e]);
-        b[e] *= inv * (is_q ? wq[8 + e] : wk[8 + e]);
+      for (int e = 0; e < 2; ++e) {
+        const float4 u = w[e * kLanes], v = w[(2 + e) * kLanes];
+        a[4 * e] *= inv * u.x, a[4 * e + 1] *= inv * u.y, a[4 * e + 2] *= inv * u.z, a[4 * e + 3] *= inv * u.w;
+        b[4 * e] *= inv * v.x, b[4 * e + 1] *= inv * v.y, b[4 * e + 2] *= inv * v.z, b[4 * e + 3] *= inv * v.w;
       }
       if (l.turned) turn_pairs(a, b, turn + ti * half + i, rv, l.split, false);
       const HeadRows& o = is_q ? p.qo : p.ko;
@@ -122,32 +136,35 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormParams p) {
   }
 }
 
+// Queries first, then keys: a thread's sums are those of one of them. The next row's
+// values are asked for before this one's are worked on.
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads) norm_grad_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const NormParams p) {
   constexpr int kLanes = D / 16, kRows = kThreads / kLanes;
   __shared__ float2 turn[kGroup * D / 2];
-  __shared__ float sums[2][kThreads / 32][D];
+  __shared__ float4 weights[2 * 4 * kLanes];
+  __shared__ float sums[kThreads / 32][D];
   grid_dependency_sync();
   const int tid = threadIdx.x, i = tid % kLanes, first = tid / kLanes;
   const Place l = place_of(p, i);
-  const int heads = p.q_heads + p.k_heads, half = p.rot >> 1, rv = p.rot >> 4;
-  float dw[2][16] = {};
-  // queries first, then keys: a thread's weights and sums are those of one of them
-#pragma unroll
+  const int half = p.rot >> 1, rv = p.rot >> 4;
+  fill_weights<T, D>(p, weights);
+  __syncthreads();
+#pragma unroll 1
   for (int part = 0; part < 2; ++part) {
-    const HeadRows &s = part ? p.k : p.q, &d = part ? p.dk : p.dq, &o = part ? p.ko : p.qo;
+    const HeadRows s = part ? p.k : p.q, d = part ? p.dk : p.dq, o = part ? p.ko : p.qo;
     const int hn = part ? p.k_heads : p.q_heads;
-    if (!hn) continue;
-    float w[16];
-    {
-      float a[8], b[8];
-      weight8<T>(part ? p.k_weight : p.q_weight, p.weight_f32, l.va, a);
-      weight8<T>(part ? p.k_weight : p.q_weight, p.weight_f32, l.vb, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = a[e], w[8 + e] = b[e];
-    }
-    for (int t0 = blockIdx.x * kGroup; t0 < p.tokens; t0 += gridDim.x * kGroup) {
+    float dw[16] = {};
+    for (int t0 = blockIdx.x * kGroup; hn && t0 < p.tokens; t0 += gridDim.x * kGroup) {
       const int nt = min(kGroup, p.tokens - t0), rows = nt * hn;
+      uint4 x0, x1, g0, g1;
+      auto load = [&](int r) {
+        const int ti = r / hn, h = r - ti * hn;
+        const uint4* xs = reinterpret_cast<const uint4*>(s.p + 2 * ((t0 + ti) * s.ts + (long long)h * s.hs));
+        const uint4* gs = reinterpret_cast<const uint4*>(d.p + 2 * ((t0 + ti) * d.ts + (long long)h * d.hs));
+        x0 = xs[l.va], x1 = xs[l.vb], g0 = gs[l.va], g1 = gs[l.vb];
+      };
+      if (first < rows) load(first);
       if (half) {
         __syncthreads();
         fill_turns(p, turn, t0, nt);
@@ -155,53 +172,59 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const NormParams p)
       }
       for (int r = first; r < rows; r += kRows) {
         const int ti = r / hn, h = r - ti * hn;
-        const uint4* xs = reinterpret_cast<const uint4*>(s.p + 2 * ((t0 + ti) * s.ts + (long long)h * s.hs));
-        const uint4* gs = reinterpret_cast<const uint4*>(d.p + 2 * ((t0 + ti) * d.ts + (long long)h * d.hs));
-        const uint4 x0 = xs[l.va], x1 = xs[l.vb], g0 = gs[l.va], g1 = gs[l.vb];
         float a[8], b[8], ga[8], gb[8];
         unpack8<T>(x0, a);
         unpack8<T>(x1, b);
         unpack8<T>(g0, ga);
         unpack8<T>(g1, gb);
+        if (r + kRows < rows) load(r + kRows);
         if (l.turned) turn_pairs(ga, gb, turn + ti * half + i, rv, l.split, true);
-        float sum = 0.0f, dot = 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += a[e] * a[e] + b[e] * b[e];
+        const float inv = rsqrtf(head_sum<kLanes>(sum) * (1.0f / D) + p.eps);
+        const float4* w = weights + part * 4 * kLanes + i;
+        float dot = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          sum += a[e] * a[e] + b[e] * b[e];
-          dot += a[e] * (ga[e] * w[e]) + b[e] * (gb[e] * w[8 + e]);
+          dw[e] += ga[e] * (a[e] * inv);
+          dw[8 + e] += gb[e] * (b[e] * inv);
         }
-        const float inv = rsqrtf(head_sum<kLanes>(sum) * (1.0f / D) + p.eps);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 u = w[e * kLanes], v = w[(2 + e) * kLanes];
+          ga[4 * e] *= u.x, ga[4 * e + 1] *= u.y, ga[4 * e + 2] *= u.z, ga[4 * e + 3] *= u.w;
+          gb[4 * e] *= v.x, gb[4 * e + 1] *= v.y, gb[4 * e + 2] *= v.z, gb[4 * e + 3] *= v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += a[e] * ga[e] + b[e] * gb[e];
         const float mean = head_sum<kLanes>(dot) * (1.0f / D) * inv * inv;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dw[part][e] += ga[e] * (a[e] * inv);
-          dw[part][8 + e] += gb[e] * (b[e] * inv);
-          a[e] = inv * (ga[e] * w[e] - a[e] * mean);
-          b[e] = inv * (gb[e] * w[8 + e] - b[e] * mean);
+          a[e] = inv * (ga[e] - a[e] * mean);
+          b[e] = inv * (gb[e] - b[e] * mean);
         }
         uint4* dst = reinterpret_cast<uint4*>(o.p + 2 * ((t0 + ti) * o.ts + (long long)h * o.hs));
         dst[l.va] = pack8<T>(a);
         dst[l.vb] = pack8<T>(b);
       }
     }
-  }
-  // the block's sums: over the heads inside a warp, then over the warps
-#pragma unroll
-  for (int part = 0; part < 2; ++part)
+    // the block's sums: over the heads inside a warp, then over the warps
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float v = dw[part][e];
+      float v = dw[e];
 #pragma unroll
-      for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if ((tid & 31) < kLanes) sums[part][tid >> 5][8 * (e < 8 ? l.va : l.vb) + (e & 7)] = v;
+      for (int m = 16; m >= kLanes; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+      if ((tid & 31) < kLanes) sums[tid >> 5][8 * (e < 8 ? l.va : l.vb) + (e & 7)] = v;
     }
-  __syncthreads();
-  for (int at = tid; at < 2 * D; at += kThreads) {
-    const int part = at / D, j = at - part * D;
-    float v = 0.0f;
+    __syncthreads();
+    for (int j = tid; j < D; j += kThreads) {
+      float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += sums[part][w][j];
-    p.partial[((size_t)blockIdx.x * 2 + part) * D + j] = v;
+      for (int k = 0; k < kThreads / 32; ++k) v += sums[k][j];
+      p.partial[((size_t)blockIdx.x * 2 + part) * D + j] = v;
+    }
   }
 }
 
