@@ -23,7 +23,7 @@ import struct
 from . import DFLASH_BF16, DFLASH_F32, DFlashError, ERR_INVALID_ARG
 from . import operators as _ops
 
-_pack8, _pack12, _pack16 = (struct.Struct(f"{n}q").pack for n in (8, 12, 16))
+_pack8, _pack12, _pack16 = (struct.Struct(f"{n}q").pack for n in (8, 12, 16))  # strides, as the library reads them
 _FLOATS = {}  # torch's types by code, filled with the first call
 
 
@@ -42,7 +42,8 @@ def _code(t, name) -> int:
 
 
 def _heads(t, name, dim, like):
-    """Data pointer and strides of a [tokens, heads, dim] view of `like`'s type and device."""
+    """A [tokens, heads, dim] view of `like`'s type and device as (itself, data pointer, token stride, head
+    stride, tokens, heads). Rows that share memory are copied out: the kernels take rows at places of their own."""
     if t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
     shape = t.shape
@@ -50,28 +51,28 @@ def _heads(t, name, dim, like):
         raise ValueError(f"{name} must have shape [tokens, heads, {dim}], got {tuple(shape)}")
     if t.device != like.device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {like.device}, got {t.device}")
+    n, heads, _ = shape
     ts, hs, one = t.stride()
+    if (ts < dim and n > 1) or (hs < dim and heads > 1):
+        t = t.contiguous()
+        ts, hs, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), ts, hs
+    return t, t.data_ptr(), ts, hs, n, heads
 
 
 def _usable(g, like):
-    """An upstream gradient as the kernels read it: autograd may hand over any strides."""
+    """An upstream gradient as the kernels read it, (itself, data pointer, token stride, head stride): autograd may
+    hand over any strides."""
     ts, hs, one = g.stride()
     dim = g.shape[2]
     if g.dtype != like.dtype:
-        g = g.to(like.dtype)
-    elif one == 1 and ts >= dim and hs >= dim and not (ts % 8 or hs % 8 or g.data_ptr() % 16):
-        return g
-    return g.contiguous()
-
-
-def _unbroadcast(t):
-    """A view whose rows share memory, copied out: the kernels take rows at places of their own."""
-    if t.dim() == 3 and any(s < t.shape[-1] and n > 1 for s, n in zip(t.stride()[:-1], t.shape[:-1])):
-        return t.contiguous()
-    return t
+        g = g.to(like.dtype).contiguous()
+    elif one != 1 or ts < dim or hs < dim or ts % 8 or hs % 8 or g.data_ptr() % 16:
+        g = g.contiguous()
+    else:
+        return g, g.data_ptr(), ts, hs
+    return (g, g.data_ptr(), *g.stride()[:2])
 
 
 def _once(backward):
@@ -86,52 +87,55 @@ def _once(backward):
 
 
 def _needs_graph(*tensors):
-    return _ops._modules[0].is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if _ops._modules[0].is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 # ---- norms with rotation -----------------------------------------------------------------
-def _norm_args(q, k, q_weight, k_weight, positions, phases):
-    x = q if q is not None else k
-    code, dev, D, n = _code(x, "q" if q is not None else "k"), x.device, x.shape[-1], x.shape[0]
-    wq, wk, wcode = _ops._norm_weights(q_weight, k_weight, D, x.dtype, code, dev)
-    rot = 0
-    if phases is not None:
-        if positions is None:
-            raise ValueError("phases need positions")
-        if phases.dim() != 1:
-            raise ValueError("phases must be one-dimensional")
-        rot = 2 * phases.shape[0]
-        torch = _ops._modules[0]
-        positions = _ops._vector(positions, n, "positions", torch.int32, dev)
-        phases = _ops._vector(phases, phases.shape[0], "phases", torch.int64, dev)
-    else:
-        positions = None
-    return code, dev, D, n, wq, wk, wcode, positions, phases, rot
+class _Norm:
+    """What a call and its backward pass hand to the library: pointers into tensors that the caller (and autograd)
+    keep."""
+    __slots__ = ("q", "k", "tokens", "code", "dim", "weights", "eps", "turn", "device")
 
-
-def _norm_forward(q, k, q_weight, k_weight, positions, phases, interleaved, eps):
-    torch = _ops._modules[0]
-    x = q if q is not None else k
-    if x.dim() != 3:
-        raise ValueError(f"{'q' if q is not None else 'k'} must have shape [tokens, heads, head_dim], got {tuple(x.shape)}")
-    code, dev, D, n, wq, wk, wcode, pos, ph, rot = _norm_args(q, k, q_weight, k_weight, positions, phases)
-    if q is not None and k is not None and q.shape[0] != k.shape[0]:
-        raise ValueError(f"q has {q.shape[0]} tokens, k {k.shape[0]}")
-    ins, outs = [], []
-    for t, name in ((q, "q"), (k, "k")):
-        if t is None:
-            ins.append((None, 0, 0, 0))
-            outs.append((None, None))
+    def __init__(self, q, k, q_weight, k_weight, positions, phases, interleaved, eps):
+        x, name = (q, "q") if q is not None else (k, "k")
+        if x.dim() != 3:
+            raise ValueError(f"{name} must have shape [tokens, heads, head_dim], got {tuple(x.shape)}")
+        self.code, self.device, self.dim = _code(x, name), x.device, x.shape[2]
+        none = None, None, 0, 0, x.shape[0], 0
+        self.q = none if q is None else _heads(q, "q", self.dim, x)
+        self.k = none if k is None else _heads(k, "k", self.dim, x)
+        n = self.tokens = self.q[4]
+        if self.k[4] != n:
+            raise ValueError(f"q has {n} tokens, k {self.k[4]}")
+        self.weights = _ops._norm_weights(q_weight, k_weight, self.dim, x.dtype, self.code, self.device)
+        self.eps = eps
+        if phases is None:
+            self.turn = None, None, 0, 0
         else:
-            ins.append((*_heads(t, name, D, x), t.shape[1]))
-            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-            outs.append((o, o.data_ptr()))
-    (pq, qt, qh, hq), (pk, kt, kh, hk) = ins
-    if n and hq + hk:
-        _ops._call(dev, _ops._library().dflash_norm_rotate, pq, pk, outs[0][1], outs[1][1], code, n, hq, hk, D,
-                   _pack8(qt, qh, kt, kh, hq * D, D, hk * D, D), wq, wk, wcode, eps, pos, ph, rot, 1 if interleaved else 0,
-                   _ops._raw_stream(None, dev))
-    return outs[0][0], outs[1][0]
+            if positions is None:
+                raise ValueError("phases need positions")
+            if phases.dim() != 1:
+                raise ValueError("phases must be one-dimensional")
+            torch, half = _ops._modules[0], phases.shape[0]
+            self.turn = (_ops._vector(positions, n, "positions", torch.int32, self.device),
+                         _ops._vector(phases, half, "phases", torch.int64, self.device), 2 * half, 1 if interleaved else 0)
+
+    def forward(self):
+        D = self.dim
+        q, pq, qt, qh, n, hq = self.q
+        k, pk, kt, kh, _, hk = self.k
+        qo = None if q is None else q.new_empty((n, hq, D))
+        ko = None if k is None else k.new_empty((n, hk, D))
+        if n and hq + hk:
+            _ops._call(self.device, _ops._library().dflash_norm_rotate, pq, pk, None if qo is None else qo.data_ptr(),
+                       None if ko is None else ko.data_ptr(), self.code, n, hq, hk, D,
+                       _pack8(qt, qh, kt, kh, hq * D, D, hk * D, D), *self.weights, self.eps, *self.turn,
+                       _ops._raw_stream(None, self.device))
+        return qo, ko
 
 
 _functions = {}
@@ -144,48 +148,46 @@ def _norm_function():
     torch = _ops._torch()
 
     def backward(ctx, dq_out, dk_out):
-        q, k, q_weight, k_weight, positions, phases = ctx.saved_tensors
-        code, dev, D, n, wq, wk, wcode, pos, ph, rot = _norm_args(q, k, q_weight, k_weight, positions, phases)
-        ptr, strides, grads, heads, held = [], [[], [], []], [], [], []
-        for x, g in ((q, dq_out), (k, dk_out)):
-            if x is None:
-                ptr.append((None, None, None))
-                for s in strides:
-                    s += [0, 0]
-                grads.append(None)
-                heads.append(0)
-                continue
-            g = _usable(g, x)
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            ptr.append((x.data_ptr(), g.data_ptr(), out.data_ptr()))
-            for s, t in zip(strides, (x, g, out)):
-                s += t.stride()[:2]
-            grads.append(out)
-            heads.append(x.shape[1])
-            held.append(g)  # until the launch
-        gw = [None if w is None or not need else torch.empty_like(w)
-              for w, need in ((q_weight, ctx.needs_input_grad[2]), (k_weight, ctx.needs_input_grad[3]))]
-        lib = _ops._library()
-        size = lib.dflash_norm_workspace_bytes(D)
-        if n and sum(heads):
+        a = ctx.call
+        _, _, q_weight, k_weight, _, _ = ctx.saved_tensors  # (and nothing has been written over since)
+        D, dev = a.dim, a.device
+        q, pq, qt, qh, n, hq = a.q
+        k, pk, kt, kh, _, hk = a.k
+        dq = dk = gq = gk = None
+        pdq = pdk = pgq = pgk = None
+        gqt = gqh = gkt = gkh = 0
+        if q is not None:
+            gq, pgq, gqt, gqh = _usable(dq_out, q)
+            dq = q.new_empty((n, hq, D))
+            pdq = dq.data_ptr()
+        if k is not None:
+            gk, pgk, gkt, gkh = _usable(dk_out, k)
+            dk = k.new_empty((n, hk, D))
+            pdk = dk.data_ptr()
+        need = ctx.needs_input_grad
+        dwq = torch.empty_like(q_weight) if q_weight is not None and need[2] else None
+        dwk = torch.empty_like(k_weight) if k_weight is not None and need[3] else None
+        if n and hq + hk:
+            lib = _ops._library()
+            size = lib.dflash_norm_workspace_bytes(D)
             ws = torch.empty(size, dtype=torch.uint8, device=dev)
-            _ops._call(dev, lib.dflash_norm_rotate_grad, ptr[0][0], ptr[1][0], ptr[0][1], ptr[1][1], ptr[0][2], ptr[1][2],
-                       code, n, heads[0], heads[1], D, _pack12(*strides[0], *strides[1], *strides[2]), wq, wk,
-                       *(None if w is None else w.data_ptr() for w in gw), wcode, ctx.eps, pos, ph, rot,
-                       1 if ctx.interleaved else 0, ws.data_ptr(), size, _ops._raw_stream(None, dev))
+            wq, wk, code = a.weights
+            _ops._call(dev, lib.dflash_norm_rotate_grad, pq, pk, pgq, pgk, pdq, pdk, a.code, n, hq, hk, D,
+                       _pack12(qt, qh, kt, kh, gqt, gqh, gkt, gkh, hq * D, D, hk * D, D), wq, wk,
+                       None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), code, a.eps,
+                       *a.turn, ws.data_ptr(), size, _ops._raw_stream(None, dev))
         else:
-            for w in gw:
+            for w in (dwq, dwk):
                 if w is not None:
                     w.zero_()
-        return grads[0], grads[1], gw[0], gw[1], None, None, None, None
+        return dq, dk, dwq, dwk, None, None, None, None
 
     class NormRotate(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, q_weight, k_weight, positions, phases, interleaved, eps):
-            out = _norm_forward(q, k, q_weight, k_weight, positions, phases, interleaved, eps)
+            ctx.call = a = _Norm(q, k, q_weight, k_weight, positions, phases, interleaved, eps)
             ctx.save_for_backward(q, k, q_weight, k_weight, positions, phases)
-            ctx.interleaved, ctx.eps = interleaved, eps
-            return out
+            return a.forward()
 
     NormRotate.backward = _once(backward)
     _functions["norm"] = NormRotate
@@ -199,14 +201,14 @@ def norm_rotate(q, k=None, q_weight=None, k_weight=None, positions=None, phases=
     int32 by ``phases`` (``rope_phases``; None: no rotation). Weights [head_dim]
     in the tokens' type or fp32, None: 1. Returns new tensors (q, k),
     differentiable in q, k and the weights."""
-    _setup()
+    if not _FLOATS:
+        _setup()
     if q is None and k is None:
         raise ValueError("neither q nor k is given")
-    q, k = (None if t is None else _unbroadcast(t) for t in (q, k))
-    args = q, k, q_weight, k_weight, positions, phases, interleaved, float(eps)
-    if not _needs_graph(q, k, q_weight, k_weight):
-        return _norm_forward(*args)
-    return _norm_function().apply(*args)
+    eps = float(eps)
+    if _needs_graph(q, k, q_weight, k_weight):
+        return (_functions.get("norm") or _norm_function()).apply(q, k, q_weight, k_weight, positions, phases, interleaved, eps)
+    return _Norm(q, k, q_weight, k_weight, positions, phases, interleaved, eps).forward()
 
 
 # ---- attention over packed sequences --------------------------------------------------------
@@ -217,31 +219,6 @@ class _Batch(ctypes.Structure):
                                               "causal")] + [("scale", ctypes.c_float)]
 
 
-def _batch(q, k, v, q_start, kv_start, scale, causal):
-    torch = _ops._modules[0]
-    code, dev = _code(q, "q"), q.device
-    if q.dim() != 3:
-        raise ValueError(f"q must have shape [tokens, heads, head_dim], got {tuple(q.shape)}")
-    D = q.shape[2]
-    pq, pk, pv = _heads(q, "q", D, q), _heads(k, "k", D, q), _heads(v, "v", D, q)
-    if k.shape != v.shape:
-        raise ValueError(f"k has shape {tuple(k.shape)}, v {tuple(v.shape)}")
-    if q_start.dim() != 1 or q_start.shape[0] < 2:
-        raise ValueError(f"q_start must have shape [batch + 1], got {tuple(q_start.shape)}")
-    n = q_start.shape[0]
-    if kv_start is None and k.shape[0] != q.shape[0]:
-        raise ValueError(f"q has {q.shape[0]} tokens, k and v {k.shape[0]}: kv_start is needed")
-    s = _ops._vector(q_start, n, "q_start", torch.int32, dev)
-    t = s if kv_start is None else _ops._vector(kv_start, n, "kv_start", torch.int32, dev)
-    return _Batch(s, t, n - 1, q.shape[0], k.shape[0], q.shape[1], k.shape[1], D, code, 1 if causal else 0,
-                  D ** -0.5 if scale is None else scale), pq, pk, pv
-
-
-def _workspace(size, device):
-    torch = _ops._modules[0]
-    return torch.empty(size, dtype=torch.uint8, device=device)
-
-
 def _size(function, *args):
     n = function(*args)
     if n == 0:
@@ -249,21 +226,46 @@ def _size(function, *args):
     return n
 
 
-def _attend(q, k, v, q_start, kv_start, scale, causal, keep, status, train=False):
-    torch, lib = _ops._modules
-    batch, pq, pk, pv = _batch(q, k, v, q_start, kv_start, scale, causal)
-    dev = q.device
-    word = _ops._status_word(status, dev)
-    n, hq, D = q.shape
-    out = torch.empty((n, hq, D), dtype=q.dtype, device=dev)
-    lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if keep else None
-    low = torch.empty((n, hq, D), dtype=torch.int8, device=dev) if train else None
-    size = _size(lib.dflash_packed_workspace_bytes, ctypes.byref(batch), 0)
-    ws = _workspace(size, dev)
-    _ops._call(dev, lib.dflash_packed_attention, ctypes.byref(batch), pq[0], pk[0], pv[0], out.data_ptr(),
-               _pack8(*pq[1:], *pk[1:], *pv[1:], hq * D, D), lse.data_ptr() if keep else None,
-               low.data_ptr() if train else None, 1, ws.data_ptr(), size, word, _ops._raw_stream(None, dev))
-    return out, lse, low
+class _Packed:
+    """What a call and its backward pass hand to the library (see _Norm)."""
+    __slots__ = ("batch", "ref", "q", "k", "v", "device", "word", "dim")
+
+    def __init__(self, q, k, v, q_start, kv_start, scale, causal, status):
+        torch = _ops._modules[0]
+        code, dev = _code(q, "q"), q.device
+        if q.dim() != 3:
+            raise ValueError(f"q must have shape [tokens, heads, head_dim], got {tuple(q.shape)}")
+        D = self.dim = q.shape[2]
+        self.q, self.k, self.v = _heads(q, "q", D, q), _heads(k, "k", D, q), _heads(v, "v", D, q)
+        _, _, _, _, nq, hq = self.q
+        _, _, _, _, nk, hk = self.k
+        if self.v[4:] != (nk, hk):
+            raise ValueError(f"k has shape {tuple(k.shape)}, v {tuple(v.shape)}")
+        if q_start.dim() != 1 or q_start.shape[0] < 2:
+            raise ValueError(f"q_start must have shape [batch + 1], got {tuple(q_start.shape)}")
+        n = q_start.shape[0]
+        if kv_start is None and nk != nq:
+            raise ValueError(f"q has {nq} tokens, k and v {nk}: kv_start is needed")
+        s = _ops._vector(q_start, n, "q_start", torch.int32, dev)
+        t = s if kv_start is None else _ops._vector(kv_start, n, "kv_start", torch.int32, dev)
+        self.batch = _Batch(s, t, n - 1, nq, nk, hq, hk, D, code, 1 if causal else 0, D ** -0.5 if scale is None else scale)
+        self.ref, self.device, self.word = ctypes.byref(self.batch), dev, _ops._status_word(status, dev)
+
+    def forward(self, keep, train):
+        torch, lib = _ops._modules
+        dev, D = self.device, self.dim
+        q, pq, qt, qh, n, hq = self.q
+        _, pk, kt, kh, _, _ = self.k
+        _, pv, vt, vh, _, _ = self.v
+        size = _size(lib.dflash_packed_workspace_bytes, self.ref, 0)
+        out = q.new_empty((n, hq, D))
+        lse = torch.empty((n, hq), dtype=torch.float32, device=dev) if keep else None
+        low = torch.empty((n, hq, D), dtype=torch.int8, device=dev) if train else None
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _ops._call(dev, lib.dflash_packed_attention, self.ref, pq, pk, pv, out.data_ptr(),
+                   _pack8(qt, qh, kt, kh, vt, vh, hq * D, D), lse.data_ptr() if keep else None,
+                   low.data_ptr() if train else None, 1, ws.data_ptr(), size, self.word, _ops._raw_stream(None, dev))
+        return out, lse, low
 
 
 def _attention_function():
@@ -273,26 +275,28 @@ def _attention_function():
     torch = _ops._torch()
 
     def backward(ctx, dout, _):
-        q, k, v, q_start, kv_start, out, lse, low, status = ctx.saved_tensors
-        lib, dev = _ops._library(), q.device
-        batch, pq, pk, pv = _batch(q, k, v, q_start, kv_start, ctx.scale, ctx.causal)
-        dout = _usable(dout, q)
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
-        size = _size(lib.dflash_packed_workspace_bytes, ctypes.byref(batch), 1)
-        ws = _workspace(size, dev)
-        _ops._call(dev, lib.dflash_packed_attention_grad, ctypes.byref(batch), pq[0], pk[0], pv[0], out.data_ptr(),
-                   lse.data_ptr(), low.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                   _pack16(*pq[1:], *pk[1:], *pv[1:], *out.stride()[:2], *dout.stride()[:2], *dq.stride()[:2],
-                           *dk.stride()[:2], *dv.stride()[:2]), 1, ws.data_ptr(), size,
-                   _ops._status_word(status, dev), _ops._raw_stream(None, dev))
+        a = ctx.call
+        _, _, _, _, _, out, lse, low, _ = ctx.saved_tensors
+        lib, dev, D = _ops._library(), a.device, a.dim
+        q, pq, qt, qh, n, hq = a.q
+        _, pk, kt, kh, m, hk = a.k
+        _, pv, vt, vh, _, _ = a.v
+        dout, pd, dt, dh = _usable(dout, q)
+        dq, dk, dv = q.new_empty((n, hq, D)), q.new_empty((m, hk, D)), q.new_empty((m, hk, D))
+        size = _size(lib.dflash_packed_workspace_bytes, a.ref, 1)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _ops._call(dev, lib.dflash_packed_attention_grad, a.ref, pq, pk, pv, out.data_ptr(), lse.data_ptr(), low.data_ptr(),
+                   pd, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                   _pack16(qt, qh, kt, kh, vt, vh, hq * D, D, dt, dh, hq * D, D, hk * D, D, hk * D, D), 1, ws.data_ptr(),
+                   size, a.word, _ops._raw_stream(None, dev))
         return dq, dk, dv, None, None, None, None, None
 
     class PackedAttention(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, v, q_start, kv_start, scale, causal, status):
-            out, lse, low = _attend(q, k, v, q_start, kv_start, scale, causal, True, status, True)
+            ctx.call = a = _Packed(q, k, v, q_start, kv_start, scale, causal, status)
+            out, lse, low = a.forward(True, True)
             ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, low, status)
-            ctx.scale, ctx.causal = scale, causal
             ctx.mark_non_differentiable(lse)
             return out, lse
 
@@ -311,16 +315,17 @@ def packed_attention(q, k, v, q_start, kv_start=None, scale=None, causal=True, r
     Returns ``out`` like q, with ``return_lse`` (out, lse [q_tokens, q_heads] fp32, which
     carries no gradient); rows of no sequence are 0 (lse: -inf). Differentiable
     in q, k and v for bf16. Single tokens over a cache: ``paged_attention``."""
-    _setup()
-    q, k, v = _unbroadcast(q), _unbroadcast(k), _unbroadcast(v)
-    args = q, k, v, q_start, kv_start, None if scale is None else float(scale), bool(causal)
+    if not _FLOATS:
+        _setup()
+    scale = None if scale is None else float(scale)
     if _needs_graph(q, k, v):
         if q.dtype != _ops._modules[0].bfloat16:
             raise TypeError(f"the packed attention has a gradient for bfloat16 only, got {q.dtype}: detach the inputs, "
                             "or call under torch.no_grad()")
-        out, lse = _attention_function().apply(*args, status)
+        out, lse = (_functions.get("attention") or _attention_function()).apply(q, k, v, q_start, kv_start, scale,
+                                                                                bool(causal), status)
     else:
-        out, lse, _ = _attend(*args, return_lse, status)
+        out, lse, _ = _Packed(q, k, v, q_start, kv_start, scale, causal, status).forward(return_lse, False)
     return (out, lse) if return_lse else out
 
 
@@ -346,19 +351,18 @@ def _entropy_args(h, weight, labels, row_weight):
             _ops._vector(row_weight, N, "row_weight", torch.float32, dev))
 
 
-def _entropy(h, weight, labels, row_weight, status, keep):
+def _entropy(h, head, status, keep):
     torch, lib = _ops._modules
-    head = _entropy_args(h, weight, labels, row_weight)
     dev, N = h.device, head[4]
     word = _ops._status_word(status, dev)
     loss = torch.empty((N,), dtype=torch.float32, device=dev)
     stats = torch.empty((N, 2), dtype=torch.float32, device=dev) if keep else None
     if N:
         size = lib.dflash_linear_entropy_workspace_bytes(*head[4:7], 0)
-        ws = _workspace(size, dev)  # (sizes that have none are refused by the call)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)  # (sizes that have none are refused by the call)
         _ops._call(dev, lib.dflash_linear_entropy, *head, loss.data_ptr(), stats.data_ptr() if keep else None,
                    ws.data_ptr(), size, word, _ops._raw_stream(None, dev))
-    return loss, stats
+    return loss, stats, word
 
 
 def _entropy_function():
@@ -368,17 +372,18 @@ def _entropy_function():
     torch = _ops._torch()
 
     def backward(ctx, upstream):
-        h, weight, labels, row_weight, stats, status = ctx.saved_tensors
-        head = _entropy_args(h, weight, labels, row_weight)
+        head, word = ctx.call
+        h, weight, _, _, stats, _ = ctx.saved_tensors
         lib, dev, N = _ops._library(), h.device, head[4]
-        dh = torch.empty(h.shape, dtype=h.dtype, device=dev) if ctx.needs_input_grad[0] else None
-        dw = torch.empty(weight.shape, dtype=weight.dtype, device=dev) if ctx.needs_input_grad[1] else None
+        need = ctx.needs_input_grad
+        dh = h.new_empty(h.shape) if need[0] else None
+        dw = weight.new_empty(weight.shape) if need[1] else None
         if N:
             size = lib.dflash_linear_entropy_workspace_bytes(*head[4:7], 1)
-            ws = _workspace(size, dev)
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
             _ops._call(dev, lib.dflash_linear_entropy_grad, *head, stats.data_ptr(), upstream.data_ptr(),
                        upstream.stride(0), None if dh is None else dh.data_ptr(), None if dw is None else dw.data_ptr(),
-                       ws.data_ptr(), size, _ops._status_word(status, dev), _ops._raw_stream(None, dev))
+                       ws.data_ptr(), size, word, _ops._raw_stream(None, dev))
         elif dw is not None:
             dw.zero_()
         return dh, dw, None, None, None
@@ -386,7 +391,9 @@ def _entropy_function():
     class LinearCrossEntropy(torch.autograd.Function):
         @staticmethod
         def forward(ctx, h, weight, labels, row_weight, status):
-            loss, stats = _entropy(h, weight, labels, row_weight, status, True)
+            head = _entropy_args(h, weight, labels, row_weight)
+            loss, stats, word = _entropy(h, head, status, True)
+            ctx.call = head, word
             ctx.save_for_backward(h, weight, labels, row_weight, stats, status)
             return loss
 
@@ -402,12 +409,13 @@ def linear_cross_entropy(hidden, weight, labels, row_weight=None, status=None):
     [rows] int32, -1 for a row that takes no part (its loss and gradient are 0,
     whatever its hidden state holds). Returns the losses [rows] fp32,
     differentiable in ``hidden`` and ``weight``."""
-    _setup()
+    if not _FLOATS:
+        _setup()
     if row_weight is not None and row_weight.requires_grad:
         raise ValueError("row_weight has no gradient here: detach it")
-    if not _needs_graph(hidden, weight):
-        return _entropy(hidden, weight, labels, row_weight, status, False)[0]
-    return _entropy_function().apply(hidden, weight, labels, row_weight, status)
+    if _needs_graph(hidden, weight):
+        return (_functions.get("entropy") or _entropy_function()).apply(hidden, weight, labels, row_weight, status)
+    return _entropy(hidden, _entropy_args(hidden, weight, labels, row_weight), status, False)[0]
 
 
 __all__ = ["norm_rotate", "packed_attention", "linear_cross_entropy"]
