@@ -167,48 +167,6 @@ __global__ void __launch_bounds__(32 * kWarps)
   });
 }
 
-// delta, the sum over d of dout out, and lse as the products' kernels read them (their signs reversed); behind
-// the last row a tile's worth of zeros
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps) delta_kernel(const PackedParams p) {
-  constexpr int kLanes = D / 8;  // 8 values each
-  grid_dependency_sync();
-  const int lane = threadIdx.x % kLanes;
-  const long long rows = (long long)p.q_tokens * p.q_heads;
-  const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
-  float s = 0.0f;
-  for (long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x; at < (p.stat_pitch - p.q_tokens) * 2ll * p.q_heads;
-       at += (long long)gridDim.x * blockDim.x) {
-    const int spare = p.stat_pitch - p.q_tokens;
-    p.row_stats[at / spare * p.stat_pitch + p.q_tokens + at % spare] = 0.0f;
-  }
-  if (r < rows) {
-    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
-    const uint4 a = reinterpret_cast<const uint4*>(row_of(p.o, t, head))[lane];
-    const uint4 g = reinterpret_cast<const uint4*>(row_of(p.d_o, t, head))[lane];
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {g.x, g.y, g.z, g.w};
-    uint2 l = make_uint2(0u, 0u);
-    if (p.low) l = reinterpret_cast<const uint2*>(p.low + r * D)[lane];
-    const uint32_t low[2] = {l.x, l.y};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t b = low[e >> 1] >> (16 * (e & 1));
-      const float2 v = T::unpack(y[e]);
-      s = fmaf(with_low(x[e] & 0xffffu, (int8_t)(b & 0xffu)), v.x,
-               fmaf(with_low(x[e] >> 16, (int8_t)((b >> 8) & 0xffu)), v.y, s));
-    }
-  }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  if (r < rows && lane == 0) {
-    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
-    const float lse = p.lse[r];
-    float* st = p.row_stats + (size_t)head * 2 * p.stat_pitch;
-    st[t] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
-    st[p.stat_pitch + t] = -s;
-  }
-}
-
 // Row t of the queries' gradients.
 template <class T, int D>
 __device__ void dq_row(const PackedParams& p, int t, int head, int i, int n, int kv0, int m, float* q_row, float* g_row) {
@@ -294,42 +252,33 @@ __device__ void dkv_row(const PackedParams& p, int t, int kh, int j, int m, int 
 
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kWarps)
-    redo_dq_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
+    redo_grad_kernel(const PackedParams p, const PackedList queries, const uint8_t* q_flags, const PackedList keys,
+                     const uint8_t* kv_flags) {
   __shared__ float rows[kWarps][2][D];
   grid_dependency_sync();
   const int warp = threadIdx.x >> 5;
-  each_flagged<kGradFlags, 4>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+  each_flagged<kGradFlags, 4>(queries, q_flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
     if (!row_not_finite<T, D>(row_of(p.dq, t, head))) return;
     dq_row<T, D>(p, t, head, i, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
   });
-  if (p.fill)
-    each_spare<D>(p.q_start, p.B, p.q_tokens, p.q_heads, [&](int t, int head, int c) { clear8(p.dq, t, head, c); });
-}
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps)
-    redo_dkv_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
-  __shared__ float rows[kWarps][2][D];
-  grid_dependency_sync();
-  const int warp = threadIdx.x >> 5;
-  each_flagged<kGradFlags, 4>(list, flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
+  each_flagged<kGradFlags, 4>(keys, kv_flags, p.kv_heads, [&](int t, int head, int j, const PackedUnit& u) {
     if (!row_not_finite<T, D>(row_of(p.dk, t, head)) && !row_not_finite<T, D>(row_of(p.dv, t, head))) return;
     dkv_row<T, D>(p, t, head, j, u.n, u.other0, u.m, rows[warp][0], rows[warp][1]);
   });
-  if (p.fill)
-    each_spare<D>(p.kv_start, p.B, p.kv_tokens, p.kv_heads, [&](int t, int head, int c) {
-      clear8(p.dk, t, head, c);
-      clear8(p.dv, t, head, c);
-    });
+  if (!p.fill) return;
+  each_spare<D>(p.q_start, p.B, p.q_tokens, p.q_heads, [&](int t, int head, int c) { clear8(p.dq, t, head, c); });
+  each_spare<D>(p.kv_start, p.B, p.kv_tokens, p.kv_heads, [&](int t, int head, int c) {
+    clear8(p.dk, t, head, c);
+    clear8(p.dv, t, head, c);
+  });
 }
 
 // The list of units: counted and sorted by one block. Work goes by how many of the
 // other array's rows the unit's last (queries) or first (keys) row meets; units of equal work keep
 // no order among themselves, which no result depends on.
 constexpr int kListThreads = 1024, kBuckets = 1024;
-__global__ void __launch_bounds__(kListThreads)
-    list_kernel(const PackedParams p, const int keys, const int rows, const PackedList list) {
+__device__ __noinline__ void build_list(const PackedParams& p, bool keys, int rows, const PackedList& list) {
   __shared__ int before[kMaxBatch + 1], warp_sum_[32], bucket[kBuckets];
-  grid_dependency_sync();
   const int32_t *sa = keys ? p.kv_start : p.q_start, *sb = keys ? p.q_start : p.kv_start;
   const int ta = keys ? p.kv_tokens : p.q_tokens, tb = keys ? p.q_tokens : p.kv_tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -420,6 +369,57 @@ __global__ void __launch_bounds__(kListThreads)
   if (bad) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
 }
 
+__global__ void __launch_bounds__(kListThreads) list_kernel(const PackedParams p, const PackedList list) {
+  grid_dependency_sync();
+  build_list(p, false, kForwardRows, list);
+}
+
+// What the gradients' kernels read: both lists (the first two blocks), and the rows'
+// statistics: delta, the sum over d of dout out, and lse, their signs reversed; behind
+// the last row a tile's worth of zeros.
+template <class T, int D>
+__global__ void __launch_bounds__(kListThreads, 2)
+    grad_prepare_kernel(const PackedParams p, const PackedList queries, const PackedList keys) {
+  constexpr int kLanes = D / 8;  // 8 values each
+  grid_dependency_sync();
+  if (blockIdx.x < 2) {
+    build_list(p, blockIdx.x == 1, kGradRows, blockIdx.x ? keys : queries);
+    return;
+  }
+  const long long id = (long long)(blockIdx.x - 2) * kListThreads + threadIdx.x;
+  const int lane = threadIdx.x % kLanes;
+  const long long rows = (long long)p.q_tokens * p.q_heads, r = id / kLanes;
+  const int spare = p.stat_pitch - p.q_tokens;
+  for (long long at = id; at < spare * 2ll * p.q_heads; at += (long long)(gridDim.x - 2) * kListThreads)
+    p.row_stats[at / spare * p.stat_pitch + p.q_tokens + at % spare] = 0.0f;
+  float s = 0.0f;
+  if (r < rows) {
+    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
+    const uint4 a = reinterpret_cast<const uint4*>(row_of(p.o, t, head))[lane];
+    const uint4 g = reinterpret_cast<const uint4*>(row_of(p.d_o, t, head))[lane];
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {g.x, g.y, g.z, g.w};
+    uint2 l = make_uint2(0u, 0u);
+    if (p.low) l = reinterpret_cast<const uint2*>(p.low + r * D)[lane];
+    const uint32_t low[2] = {l.x, l.y};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t b = low[e >> 1] >> (16 * (e & 1));
+      const float2 v = T::unpack(y[e]);
+      s = fmaf(with_low(x[e] & 0xffffu, (int8_t)(b & 0xffu)), v.x,
+               fmaf(with_low(x[e] >> 16, (int8_t)((b >> 8) & 0xffu)), v.y, s));
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  if (r < rows && lane == 0) {
+    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
+    const float lse = p.lse[r];
+    float* st = p.row_stats + (size_t)head * 2 * p.stat_pitch;
+    st[t] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
+    st[p.stat_pitch + t] = -s;
+  }
+}
+
 template <class... A>
 int launch(void (*kernel)(A...), unsigned grid, unsigned threads, void* stream, A... args) {
   cudaLaunchConfig_t cfg = {};
@@ -441,9 +441,6 @@ unsigned redo_blocks(long long flags) {
 
 }  // namespace
 
-int launch_list(const PackedParams& p, bool keys, int rows, const PackedList& list, void* stream) {
-  return launch(list_kernel, 1u, (unsigned)kListThreads, stream, p, (int)keys, rows, list);
-}
 int launch_redo_forward(const PackedParams& p, int dtype, int d, const PackedList& list, const uint8_t* flags,
                         void* stream) {
   const unsigned grid = redo_blocks((long long)most_units(p.q_tokens, p.B, kForwardRows) * p.q_heads * kForwardFlags);
@@ -453,24 +450,6 @@ int launch_redo_forward(const PackedParams& p, int dtype, int d, const PackedLis
   return d == 64 ? launch(redo_forward_kernel<F16, 64>, grid, 32u * kWarps, stream, p, list, flags)
                  : launch(redo_forward_kernel<F16, 128>, grid, 32u * kWarps, stream, p, list, flags);
 }
-int launch_redo_dq(const PackedParams& p, int d, const PackedList& list, const uint8_t* flags, void* stream) {
-  const unsigned grid = redo_blocks((long long)most_units(p.q_tokens, p.B, kGradRows) * p.q_heads * kGradFlags);
-  return d == 64 ? launch(redo_dq_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p, list, flags)
-                 : launch(redo_dq_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p, list, flags);
-}
-int launch_redo_dkv(const PackedParams& p, int d, const PackedList& list, const uint8_t* flags, void* stream) {
-  const unsigned grid = redo_blocks((long long)most_units(p.kv_tokens, p.B, kGradRows) * p.kv_heads * kGradFlags);
-  return d == 64 ? launch(redo_dkv_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p, list, flags)
-                 : launch(redo_dkv_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p, list, flags);
-}
-int launch_delta(const PackedParams& p, int head_dim, void* stream) {
-  const long long threads = (long long)p.q_tokens * p.q_heads * (head_dim / 8);
-  const unsigned grid = (unsigned)((threads + 32 * kWarps - 1) / (32 * kWarps));
-  if (!grid) return 0;
-  return head_dim == 64 ? launch(delta_kernel<Bf16, 64>, grid, 32u * kWarps, stream, p)
-                        : launch(delta_kernel<Bf16, 128>, grid, 32u * kWarps, stream, p);
-}
-
 // ---- workspaces
 // Forward: the list of queries, their flags. Backward: delta, both lists, both sets of flags.
 namespace {
@@ -492,7 +471,7 @@ size_t packed_workspace(int B, int q_tokens, int kv_tokens, int q_heads, int kv_
 int launch_packed(const PackedParams& p, int dtype, int head_dim, int sms, void* stream) {
   const PackedList list = list_at(p.ws);
   uint8_t* flags = p.ws + list_bytes(p.q_tokens, p.B, kForwardRows);
-  int e = launch_list(p, false, kForwardRows, list, stream);
+  int e = launch(list_kernel, 1u, (unsigned)kListThreads, stream, p, list);
   if (!e) e = launch_forward_tc(p, dtype, head_dim, list, flags, sms, stream);
   return e ? e : launch_redo_forward(p, dtype, head_dim, list, flags, stream);
 }
@@ -510,17 +489,18 @@ int launch_packed_grad(const PackedParams& p0, int head_dim, int sms, void* stre
   const PackedList keys = list_at(ws);
   ws += list_bytes(p.kv_tokens, p.B, kGradRows);
   uint8_t* kv_flags = ws;
-  int e = launch_delta(p, head_dim, stream);
-  if (!e && p.q_tokens) {
-    e = launch_list(p, false, kGradRows, queries, stream);
-    if (!e) e = launch_dq_tc(p, head_dim, queries, q_flags, sms, stream);
-    if (!e) e = launch_redo_dq(p, head_dim, queries, q_flags, stream);
-  }
-  if (!e && p.kv_tokens) {
-    e = launch_list(p, true, kGradRows, keys, stream);
-    if (!e) e = launch_dkv_tc(p, head_dim, keys, kv_flags, sms, stream);
-    if (!e) e = launch_redo_dkv(p, head_dim, keys, kv_flags, stream);
-  }
+  const unsigned blocks = 2u + (unsigned)(((long long)p.q_tokens * p.q_heads * (head_dim / 8) + kListThreads - 1) / kListThreads);
+  int e = head_dim == 64 ? launch(grad_prepare_kernel<Bf16, 64>, blocks, (unsigned)kListThreads, stream, p, queries, keys)
+                         : launch(grad_prepare_kernel<Bf16, 128>, blocks, (unsigned)kListThreads, stream, p, queries, keys);
+  if (!e && p.q_tokens) e = launch_dq_tc(p, head_dim, queries, q_flags, sms, stream);
+  if (!e && p.kv_tokens) e = launch_dkv_tc(p, head_dim, keys, kv_flags, p.q_tokens > 0, sms, stream);
+  if (e) return e;
+  const unsigned redo = redo_blocks((long long)most_units(p.q_tokens, p.B, kGradRows) * p.q_heads * kGradFlags +
+                                    (long long)most_units(p.kv_tokens, p.B, kGradRows) * p.kv_heads * kGradFlags);
+  e = head_dim == 64 ? launch(redo_grad_kernel<Bf16, 64>, redo, 32u * kWarps, stream, p, queries,
+                              (const uint8_t*)q_flags, keys, (const uint8_t*)kv_flags)
+                     : launch(redo_grad_kernel<Bf16, 128>, redo, 32u * kWarps, stream, p, queries,
+                              (const uint8_t*)q_flags, keys, (const uint8_t*)kv_flags);
   return e;
 }
 

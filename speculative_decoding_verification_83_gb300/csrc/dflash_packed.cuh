@@ -69,7 +69,6 @@ inline size_t list_bytes(int tokens, int B, int rows) {
   return 256 + ((size_t)most_units(tokens, B, rows) * sizeof(PackedUnit) + 255) / 256 * 256;
 }
 inline PackedList list_at(unsigned char* p) { return {reinterpret_cast<int*>(p), reinterpret_cast<PackedUnit*>(p + 256)}; }
-int launch_list(const PackedParams& p, bool keys, int rows, const PackedList& list, void* stream);
 
 // The tensor cores' kernels leave rows whose masked keys or queries hold values that
 // are not finite as NaN (0 times such a value), and a flag for 32 rows with a result that is
@@ -77,15 +76,14 @@ int launch_list(const PackedParams& p, bool keys, int rows, const PackedList& li
 // one by one, with exact masks, and set the rows of no sequence to 0.
 int launch_redo_forward(const PackedParams& p, int dtype, int head_dim, const PackedList& list, const uint8_t* flags,
                         void* stream);
-int launch_redo_dq(const PackedParams& p, int head_dim, const PackedList& list, const uint8_t* flags, void* stream);
-int launch_redo_dkv(const PackedParams& p, int head_dim, const PackedList& list, const uint8_t* flags, void* stream);
-int launch_delta(const PackedParams& p, int head_dim, void* stream);
 
 // The products (dflash_packed_fwd.cu, dflash_packed_bwd.cu).
 int launch_forward_tc(const PackedParams& p, int dtype, int head_dim, const PackedList& list, uint8_t* flags, int sms,
                       void* stream);
 int launch_dq_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, int sms, void* stream);
-int launch_dkv_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, int sms, void* stream);
+// (behind_dq: the kernel before it in the stream is the queries', whose results it does not read)
+int launch_dkv_tc(const PackedParams& p, int head_dim, const PackedList& list, uint8_t* flags, bool behind_dq, int sms,
+                  void* stream);
 constexpr int kForwardRows = 256, kGradRows = 128;  // of a unit
 constexpr int kForwardFlags = kForwardRows / 16, kGradFlags = kGradRows / 8;  // of a unit and head
 constexpr int kMaxBatch = 2048;

@@ -63,7 +63,7 @@ __device__ __forceinline__ const float* stats_of(const PackedParams& p, int head
 // What all roles of both kernels begin with: barriers, tensor memory (all of it, so it
 // begins at 0).
 template <int D>
-__device__ __forceinline__ void begin(GradShared& S, int warp, uint32_t second_readers) {
+__device__ __forceinline__ void begin(GradShared& S, int warp, uint32_t second_readers, bool wait) {
   using W = GradShape<D>;
   if (threadIdx.x == 0) {
     mbar_init(&S.own_full, 1);
@@ -89,7 +89,10 @@ __device__ __forceinline__ void begin(GradShared& S, int warp, uint32_t second_r
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  grid_dependency_sync();
+  if (wait)
+    grid_dependency_sync();
+  else
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void end(const PackedParams& p, GradShared& S, int warp) {
   tc::fence_before();
@@ -187,11 +190,14 @@ __device__ __forceinline__ QuerySpan query_span(const PackedUnit& u, int causal)
   return {at, (u.m - at + kTileRows - 1) / kTileRows};
 }
 
+// behind_dq: the kernel ahead in the stream is the queries', whose CTAs have waited for
+// what this one reads. So its CTAs begin as SMs become free, and wait only at their ends,
+// for the kernels behind.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do, const PackedParams p,
-               const PackedList list, uint8_t* flags) {
+               const PackedList list, uint8_t* flags, const bool behind_dq) {
   using W = GradShape<D>;
   extern __shared__ __align__(1024) unsigned char raw[];
   const uint32_t base = smem_addr(raw);
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   GradShared& S = *reinterpret_cast<GradShared*>(raw + W::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  begin<D>(S, warp, 1 + kWorkWarps);
+  begin<D>(S, warp, 1 + kWorkWarps, !behind_dq);
   constexpr uint32_t t_s = 0, t_dp = 128, t_dv = 256, t_dk = 256 + D;
   const uint32_t k_mem = base, v_mem = base + W::kTile;
   const int work = *list.count * p.kv_heads;  // (below 2^28)
@@ -421,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   end(p, S, warp);
+  if (behind_dq) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- queries
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   GradShared& S = *reinterpret_cast<GradShared*>(raw + W::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  begin<D>(S, warp, 1);
+  begin<D>(S, warp, 1, true);
   constexpr uint32_t t_s = 0, t_dp = 256, t_dq = 384;
   const uint32_t q_mem = base, do_mem = base + W::kTile;
   const int work = *list.count * p.q_heads;  // (below 2^27)
@@ -620,9 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   end(p, S, warp);
 }
 
-template <class K>
+template <class K, class... A>
 int launch(K kernel, const PackedParams& p, int D, size_t smem, long long most, const PackedList& list, uint8_t* flags, int sms,
-           bool* ready, void* stream) {
+           bool* ready, void* stream, A... more) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
@@ -652,7 +659,7 @@ int launch(K kernel, const PackedParams& p, int D, size_t smem, long long most, 
   cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  return (int)cudaLaunchKernelEx(&cfg, kernel, q, k, v, d_o, p, list, flags);
+  return (int)cudaLaunchKernelEx(&cfg, kernel, q, k, v, d_o, p, list, flags, more...);
 }
 template <int D>
 int launch_dq(const PackedParams& p, const PackedList& list, uint8_t* flags, int sms, void* stream) {
@@ -661,10 +668,10 @@ int launch_dq(const PackedParams& p, const PackedList& list, uint8_t* flags, int
                 sms, ready, stream);
 }
 template <int D>
-int launch_dkv(const PackedParams& p, const PackedList& list, uint8_t* flags, int sms, void* stream) {
+int launch_dkv(const PackedParams& p, const PackedList& list, uint8_t* flags, bool behind_dq, int sms, void* stream) {
   static bool ready[64] = {};
   return launch(dkv_kernel<D>, p, D, kGradSmem<D>, (long long)most_units(p.kv_tokens, p.B, kGradRows) * p.kv_heads, list,
-                flags, sms, ready, stream);
+                flags, sms, ready, stream, behind_dq);
 }
 
 }  // namespace
@@ -672,8 +679,10 @@ int launch_dkv(const PackedParams& p, const PackedList& list, uint8_t* flags, in
 int launch_dq_tc(const PackedParams& p, int d, const PackedList& list, uint8_t* flags, int sms, void* stream) {
   return d == 64 ? launch_dq<64>(p, list, flags, sms, stream) : launch_dq<128>(p, list, flags, sms, stream);
 }
-int launch_dkv_tc(const PackedParams& p, int d, const PackedList& list, uint8_t* flags, int sms, void* stream) {
-  return d == 64 ? launch_dkv<64>(p, list, flags, sms, stream) : launch_dkv<128>(p, list, flags, sms, stream);
+int launch_dkv_tc(const PackedParams& p, int d, const PackedList& list, uint8_t* flags, bool behind_dq, int sms,
+                  void* stream) {
+  return d == 64 ? launch_dkv<64>(p, list, flags, behind_dq, sms, stream)
+                 : launch_dkv<128>(p, list, flags, behind_dq, sms, stream);
 }
 
 }  // namespace dflash
