@@ -14,7 +14,10 @@
 // them. The gradients go through the vocabulary in pieces: the epilogue writes a
 // piece of g in bf16 (at most kPieceBytes, a rounding of half a step of the type
 // in which the products want it), from which dW's rows of the piece and the
-// piece's part of dh follow. dh is summed in fp32 over pieces, in up to kMaxSplits
+// piece's part of dh follow. A row's g is often ruled by its label's entry, and one
+// rounding then decides the error of the whole row: what it leaves of that entry
+// is kept in fp32 and added to dh, and to dW where there are few rows (over many
+// rows such errors average out). dh is summed in fp32 over pieces, in up to kMaxSplits
 // buffers where its tiles are too few to fill the SMs; every sum has a fixed
 // order.
 //
@@ -29,6 +32,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "dflash_norm.cuh"
 #include "dflash_tcgen05.cuh"
 #include "dflash_train.h"
 
@@ -66,6 +70,11 @@ struct GemmParams {
   // kLogitGrad
   const RowGrad* rows;
   int label0;                // the piece's first vocabulary entry
+  float* rest;               // per row: what rounding left of the label's entry
+  // kStoreBf16, with rest: rest_rows rows whose rest times their hidden state goes to their label's row
+  int rest_rows;
+  const unsigned char* h;
+  long long h_stride;
   // kSumF32
   int add;                   // to what is there
   int split_rows;            // rows between the splits' buffers
@@ -202,8 +211,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       uint32_t phase = 0;
       bool ok = true;
       const int chunk = kEpi == kStats ? p.chunk : 1 << 30;
-      for (int t = first; t < tiles && ok; t += pairs)
-      for (int left = tile_at(p, t).steps, more = 1; more && ok; left -= chunk, more = left > 0) {
+      for (int t = first, left = 0; t < tiles && ok; t += left > 0 ? 0 : pairs) {
+        if (left <= 0) left = tile_at(p, t).steps;
         const int steps = min(left, chunk);
         if (use > 0 && !__all_sync(0xffffffffu, wait_bar_cluster(&S.acc_empty[slot], (uint32_t)((use - 1) & 1), S))) {
           ok = false;
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           }
         }
         if (ok) tc::commit_pair(&S.acc_full[slot], lead);
+        left -= chunk;
         use += slot;
         slot ^= 1;
       }
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       if constexpr (kEpi == kStats) {
         // All but the last chunk of the inner index are added up in registers: every addition in
         // tensor memory cuts bits off, and over 5120 inner values that came to 2.4e-6 of a loss
-        // (2e-7 in chunks of 1024).
+        // (4.5e-7 in chunks of 1024).
         float total[128];
         for (int left = at.steps - p.chunk, k = 0;; left -= p.chunk, ++k) {
           const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((lt & 1) * kTile + half * 128);
@@ -358,9 +368,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
             x[e] = __float_as_uint(ex2_approx((__uint_as_float(x[e]) - rg.m) * kLog2e) * rg.scale);
           const int at_label = rg.label - (p.label0 + col0 + c);
           if (at_label >= 0 && at_label < 64) {
+            float z = 0.0f;
 #pragma unroll
             for (int e = 0; e < 64; ++e)
-              if (e == at_label) x[e] = __float_as_uint(__uint_as_float(x[e]) - rg.g);
+              if (e == at_label) {
+                z = __uint_as_float(x[e]) - rg.g;
+                x[e] = __float_as_uint(z);
+              }
+            p.rest[row] = z - __uint_as_float(Bf16::pack(z, 0.0f) << 16);
           }
           if (col0 + c < p.n && row0 < p.m)
             staged(
@@ -384,6 +399,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           tc::ld32(acc + c + 32, x + 32);
           tc::wait_ld32(x);
           tc::wait_ld32(x + 32);
+          for (int r = 0; r < p.rest_rows; ++r)
+            if (p.rows[r].label == p.label0 + row && col0 + c < p.n) {
+              const float f = p.rest[r];
+              const uint32_t* src = reinterpret_cast<const uint32_t*>(p.h + 2 * (r * p.h_stride + col0 + c));
+#pragma unroll
+              for (int e = 0; e < 64; e += 2)
+                if (col0 + c + e < p.n) {
+                  const float2 v = Bf16::unpack(src[e / 2]);
+                  x[e] = __float_as_uint(fmaf(f, v.x, __uint_as_float(x[e])));
+                  x[e + 1] = __float_as_uint(fmaf(f, v.y, __uint_as_float(x[e + 1])));
+                }
+            }
           if (col0 + c < p.n && row0 < p.m)
             staged(
                 [&] {
@@ -466,7 +493,7 @@ __global__ void __launch_bounds__(1024)
 // What each row's gradient is computed from, and the hidden states with the rows
 // that take no part set to 0 (their values may be anything, and 0 times anything
 // may not be 0 in dW). One block a row.
-__global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGrad* rows, uint16_t* h_used) {
+__global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGrad* rows, float* rest, uint16_t* h_used) {
   const int r = blockIdx.x, label = p.labels[r];
   const float u = (p.upstream ? p.upstream[(long long)r * p.upstream_stride] : 1.0f);
   const float weight = p.weight ? p.weight[r] : 1.0f;
@@ -477,6 +504,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGra
     RowGrad x = {s.x, g / s.y, g, label};
     if (dead) x = {0.0f, 0.0f, 0.0f, kDead};
     rows[r] = x;
+    rest[r] = 0.0f;
   }
   if (!h_used) return;
   const uint4* src = reinterpret_cast<const uint4*>(p.h + 2 * (long long)r * p.h_stride);
@@ -484,29 +512,35 @@ __global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGra
   for (int i = threadIdx.x; i < p.K / 8; i += 128) dst[i] = dead ? make_uint4(0u, 0u, 0u, 0u) : src[i];
 }
 
-// dh from its fp32 sums, the splits in order; 0 for rows that take no part.
-__global__ void __launch_bounds__(256)
-    hidden_kernel(const float* sums, int splits, size_t split_stride, const RowGrad* rows, int K, size_t n, uint16_t* dh) {
+// dh from its fp32 sums, the splits in order, and the rests of the labels' entries; 0 for
+// rows that take no part.
+__global__ void __launch_bounds__(256) hidden_kernel(const EntropyParams p, const float* sums, int splits,
+                                                     size_t split_stride, const RowGrad* rows, const float* rest) {
   const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (at >= n) return;
-  float x[8];
-  {
-    const float4 a = *reinterpret_cast<const float4*>(sums + at), b = *reinterpret_cast<const float4*>(sums + at + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  if (at >= (size_t)p.rows * p.K) return;
+  const int r = (int)(at / p.K), k = (int)(at - (size_t)r * p.K), label = rows[r].label;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (label != kDead) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p.w + 2 * (label * p.w_stride + k));
+    const float f = rest[r];
+    float x[8];
+    unpack8<Bf16>(w, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= f;
+    for (int s = 0; s < splits; ++s) {
+      const float* src = sums + s * split_stride + at;
+      const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+      x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += b.x, x[5] += b.y, x[6] += b.z, x[7] += b.w;
+    }
+    v = pack8<Bf16>(x);
   }
-  for (int s = 1; s < splits; ++s) {
-    const float* src = sums + s * split_stride + at;
-    const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-    x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w, x[4] += b.x, x[5] += b.y, x[6] += b.z, x[7] += b.w;
-  }
-  uint4 v = make_uint4(Bf16::pack(x[0], x[1]), Bf16::pack(x[2], x[3]), Bf16::pack(x[4], x[5]), Bf16::pack(x[6], x[7]));
-  if (rows[at / K].label == kDead) v = make_uint4(0u, 0u, 0u, 0u);
-  *reinterpret_cast<uint4*>(dh + at) = v;
+  *reinterpret_cast<uint4*>(p.dh + 2 * at) = v;
 }
 
 // ---- workspaces
 constexpr long long kPieceBytes = 512ll << 20;  // of g at a time
 constexpr int kMaxSplits = 8;
+constexpr int kFewRows = 64;  // whose labels' rests also go to dW
 constexpr int kPairs = 76;  // the splits' rule goes by a whole GPU's pairs of SMs
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -530,7 +564,7 @@ ForwardPlan forward_plan(int rows, int V) {
 struct BackwardPlan {
   int piece, pitch, splits;  // vocabulary entries of a piece, of a row of g
   int split_rows;            // rows of a split's sums: whole stores
-  size_t rows, h, g, sums, bytes;
+  size_t rows, rest, h, g, sums, bytes;
 };
 BackwardPlan backward_plan(int rows, int V, int K) {
   BackwardPlan b;
@@ -553,7 +587,8 @@ BackwardPlan backward_plan(int rows, int V, int K) {
   }
   b.split_rows = (rows + 31) / 32 * 32;
   b.rows = 0;
-  b.h = up((size_t)rows * sizeof(RowGrad));
+  b.rest = up((size_t)rows * sizeof(RowGrad));
+  b.h = b.rest + up((size_t)rows * sizeof(float));
   b.g = b.h + up((size_t)rows * K * 2);
   b.sums = b.g + up((size_t)rows * b.pitch * 2);
   b.bytes = b.sums + up((size_t)b.splits * b.split_rows * K * sizeof(float));
@@ -630,8 +665,9 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream) {
   const BackwardPlan b = backward_plan(p.rows, p.V, p.K);
   const cudaStream_t st = (cudaStream_t)stream;
   RowGrad* rows = reinterpret_cast<RowGrad*>(p.ws + b.rows);
+  float* rest = reinterpret_cast<float*>(p.ws + b.rest);
   unsigned char *h_used = p.ws + b.h, *g_mem = p.ws + b.g, *sums = p.ws + b.sums;
-  rows_kernel<<<(unsigned)p.rows, 128, 0, st>>>(p, rows, p.dw ? reinterpret_cast<uint16_t*>(h_used) : nullptr);
+  rows_kernel<<<(unsigned)p.rows, 128, 0, st>>>(p, rows, rest, p.dw ? reinterpret_cast<uint16_t*>(h_used) : nullptr);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return (int)e;
   CUtensorMap h, w, w_mn, hu, sum;
@@ -657,6 +693,7 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream) {
     q.b_y = v0;
     q.rows = rows;
     q.label0 = v0;
+    q.rest = rest;
     e = launch_gemm<false, false, kLogitGrad>(h, w, g_out, q, sms, st);
     if (e != cudaSuccess) return (int)e;
     if (p.dw) {
@@ -669,6 +706,12 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream) {
       d.n = p.K;
       d.k = p.rows;
       d.n_fast = 1;
+      d.rows = rows;
+      d.label0 = v0;
+      d.rest = rest;
+      d.rest_rows = p.rows <= kFewRows ? p.rows : 0;
+      d.h = p.h;
+      d.h_stride = p.h_stride;
       e = launch_gemm<true, true, kStoreBf16>(g_mn, hu, dw, d, sms, st);
       if (e != cudaSuccess) return (int)e;
     }
@@ -688,8 +731,8 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream) {
   }
   if (p.dh) {
     const size_t n = (size_t)p.rows * p.K;
-    hidden_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, st>>>(reinterpret_cast<const float*>(sums), b.splits,
-                                                                  (size_t)b.split_rows * p.K, rows, p.K, n, reinterpret_cast<uint16_t*>(p.dh));
+    hidden_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, st>>>(p, reinterpret_cast<const float*>(sums), b.splits,
+                                                                  (size_t)b.split_rows * p.K, rows, rest);
     e = cudaGetLastError();
   }
   return (int)e;

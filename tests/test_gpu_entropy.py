@@ -128,6 +128,37 @@ def test_strides(dv):
     assert torch.equal(c[0], a[1]) and torch.equal(c[1], a[2])
 
 
+@pytest.mark.parametrize("N", [1, 5, 64])
+def test_the_label_s_entry_is_not_rounded(dv, N):
+    """A label's entry of the logits' gradients rules its row of both gradients: there the bound is that of the
+    definition without the half step of bf16 of this entry."""
+    V, K = 600, 64
+    h, w, _, weight, up = inputs(9, N, V, K)
+    labels = torch.arange(N, device=DEV, dtype=torch.int32) * 9
+    w *= 2.0 ** -6
+    w[labels.long()] *= 2.0 ** 6
+    h *= 2.0 ** -4
+    x, y = (t.detach().requires_grad_(True) for t in (h, w))
+    loss = dv.linear_cross_entropy(x, y, labels, row_weight=weight)
+    dh, dw = torch.autograd.grad(loss, (x, y), up)
+    u, ids = refs.U[BF], labels.long()
+    r = refs.entropy64(h.double(), w.double(), labels, weight.double(), up.double(), u)
+    entry = (torch.softmax(h.double() @ w.double().t(), 1)[torch.arange(N), ids] - 1.0) * weight * up
+    edh = r[3] - u * entry.abs()[:, None] * w[ids].double().abs()
+    edw = r[5].clone()
+    edw[ids] -= u * entry.abs()[:, None] * h.double().abs()
+    assert ((dh.double() - r[2]).abs() <= refs.rounded(r[2], edh, BF)).all()
+    assert ((dw.double() - r[4]).abs() <= refs.rounded(r[4], edw, BF)).all()
+
+
+@pytest.mark.parametrize("N,V,K", [(1, 40000, 72), (31, 4095, 2056), (32, 40001, 1024), (32, 1, 8), (33, 40001, 1032)])
+def test_few_rows(dv, N, V, K):
+    """Few rows, vocabularies of more tiles than there are pairs of processors, several chunks of the inner index."""
+    h, w, labels, weight, up = inputs(N + V + K, N, V, K)
+    labels[0], labels[-1] = 0, V - 1
+    check(dv, h, w, labels, weight, up)
+
+
 def test_one_gradient_alone(dv):
     h, w, labels, weight, up = inputs(6, 300, 3000, 256)
     _, dh, dw = check(dv, h, w, labels, weight, up)
