@@ -458,6 +458,183 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
   if (tid == 0 && S.failed) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
 }
 
+// ---- few rows
+// Up to kFew rows are bound by reading W once, so its rows become the products' M: a
+// stage is 16 KB of W and 2 KB of hidden states, and kFewStages of them are in flight
+// where the other kernel has 6 with as many bytes of padded rows (7 rows of 5120 over
+// 248320 entries: 382 against 499 us, 6.66 TB/s). A lane of the epilogue owns a vocabulary
+// entry of the tile and keeps each row's largest logit and sum over all tiles of its CTA;
+// lanes are joined once, at the CTA's end.
+constexpr int kFew = 32, kFewStages = 12;
+constexpr uint32_t kFewBytes = kFew / 2 * kStep * 2u;  // hidden states of a stage and CTA
+constexpr int kFewThreads = 32 * 6;
+struct FewShared {
+  uint64_t full[kFewStages], empty[kFewStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  volatile int failed;
+  int labels[kFew];
+};
+constexpr size_t kFewSmem = 1024 + (size_t)kFewStages * (kOperandBytes + kFewBytes);
+static_assert(kFewSmem + sizeof(FewShared) <= 232448, "one CTA's shared memory (227 KB)");
+
+__global__ void __launch_bounds__(kFewThreads, 1) __cluster_dims__(2, 1, 1)
+    few_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, const GemmParams p) {
+  extern __shared__ unsigned char raw[];
+  __shared__ FewShared S;
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)tc::cluster_rank();
+  const int first = blockIdx.x / 2, pairs = gridDim.x / 2, stages = (p.k + kStep - 1) / kStep;
+  auto w_mem = [&](int s) { return base + (uint32_t)s * kOperandBytes; };
+  auto h_mem = [&](int s) { return base + kFewStages * kOperandBytes + (uint32_t)s * kFewBytes; };
+
+  if (tid == 0) {
+    for (int s = 0; s < kFewStages; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&S.acc_full[a], 1);
+      mbar_init(&S.acc_empty[a], 2 * 4);
+    }
+    S.failed = 0;
+    fence_barrier_init();
+  }
+  if (tid < kFew) S.labels[tid] = tid < p.m ? p.labels[tid] : -1;
+  if (warp == 1) tc::alloc_pair(&S.tmem, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      long long it = 0;
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < p.tiles_n && ok; t += pairs)
+        for (int ks = 0; ks < stages; ++ks, ++it) {
+          if (it >= kFewStages) {
+            const unsigned long long t0 = global_timer_ns();
+            if (!wait_from(&S.empty[s], phase ^ 1u, t0)) {
+              S.failed = 1;
+              ok = false;
+              break;
+            }
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2u * (kOperandBytes + kFewBytes));
+          const uint32_t bar = tc::in_first_cta(&S.full[s]);
+          tc::load_2d_pair(w_mem(s), &map_w, ks * kStep, t * kTile + rank * 128, bar);
+          tc::load_2d_pair(h_mem(s), &map_h, ks * kStep, rank * (kFew / 2), bar);
+          if (++s == kFewStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      const unsigned long long t1 = global_timer_ns();
+      for (long long q = it > kFewStages ? it - kFewStages : 0; q < it; ++q)
+        (void)wait_from(&S.empty[q % kFewStages], (uint32_t)((q / kFewStages) & 1), t1);
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      constexpr uint32_t id = tc::idesc<Bf16>(kTile, kFew, false, false);
+      const uint32_t lead = tc::elect();
+      int slot = 0, s = 0, use = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < p.tiles_n && ok; t += pairs)
+        for (int k0 = 0; k0 < stages && ok; k0 += p.chunk) {
+          if (use > 0) {
+            const unsigned long long t0 = global_timer_ns();
+            bool done = tc::try_wait_cluster(&S.acc_empty[slot], (uint32_t)((use - 1) & 1));
+            while (!done && global_timer_ns() - t0 <= kWaitLimitNs)
+              done = tc::try_wait_cluster(&S.acc_empty[slot], (uint32_t)((use - 1) & 1));
+            if (!(ok = __all_sync(0xffffffffu, done))) break;
+          }
+          tc::fence_after();
+          const int steps = min(p.chunk, stages - k0);
+          for (int ks = 0; ks < steps; ++ks) {
+            if (!(ok = __all_sync(0xffffffffu, wait_from(&S.full[s], phase, global_timer_ns())))) break;
+            tc::fence_after();
+            const uint64_t wd = tc::operand(w_mem(s)), hd = tc::operand(h_mem(s));
+#pragma unroll
+            for (int kk = 0; kk < kStep / 16; ++kk)
+              tc::mma_pair((uint32_t)(slot * kFew), wd + (uint64_t)(2 * kk), hd + (uint64_t)(2 * kk), id, (ks | kk) != 0, lead);
+            tc::commit_pair(&S.empty[s], lead);
+            if (++s == kFewStages) {
+              s = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) tc::commit_pair(&S.acc_full[slot], lead);
+          use += slot;
+          slot ^= 1;
+        }
+      if (!ok) S.failed = 1;
+    }
+  } else {
+    const int q = warp & 3;
+    float m[kFew], sum[kFew];
+#pragma unroll
+    for (int c = 0; c < kFew; ++c) m[c] = -INFINITY, sum[c] = 0.0f;
+    int lt = 0;
+    bool ok = true;
+    for (int t = first; t < p.tiles_n && ok; t += pairs) {
+      float total[kFew];
+      for (int k0 = 0; k0 < stages; k0 += p.chunk, ++lt) {
+        if (!(ok = __all_sync(0xffffffffu, wait_from(&S.acc_full[lt & 1], (uint32_t)((lt >> 1) & 1), global_timer_ns())))) break;
+        tc::fence_after();
+        uint32_t x[kFew];
+        tc::ld32(((uint32_t)(q * 32) << 16) + (uint32_t)((lt & 1) * kFew), x);
+        tc::wait_ld32(x);
+#pragma unroll
+        for (int c = 0; c < kFew; ++c) total[c] = k0 ? total[c] + __uint_as_float(x[c]) : __uint_as_float(x[c]);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0)
+            mbar_arrive(&S.acc_empty[lt & 1]);
+          else
+            tc::arrive_cluster(tc::in_first_cta(&S.acc_empty[lt & 1]));
+        }
+      }
+      if (!ok) break;
+      const int v = t * kTile + rank * 128 + q * 32 + lane;
+      if (v < p.n) {
+#pragma unroll
+        for (int c = 0; c < kFew; ++c) {
+          const float z = total[c], top = fmaxf(m[c], z), ref = top == -INFINITY ? 0.0f : top;
+          sum[c] = sum[c] * ex2_approx((m[c] - ref) * kLog2e) + ex2_approx((z - ref) * kLog2e);
+          m[c] = top;
+          if (S.labels[c] == v) p.label_logit[c] = z;
+        }
+      }
+    }
+    if (!ok) S.failed = 1;
+    // the CTA's lanes together
+#pragma unroll
+    for (int c = 0; c < kFew; ++c) {
+      const float top = warp_max_f32(m[c]), ref = top == -INFINITY ? 0.0f : top;
+      // (a sum over nothing is 0, or NaN)
+      float part = sum[c] * (m[c] == -INFINITY ? 1.0f : ex2_approx((m[c] - ref) * kLog2e));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      if (lane == 0 && c < p.m) p.parts[((size_t)blockIdx.x * 4 + q) * p.rows_pitch + c] = make_float2(top, part);
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::dealloc_pair(0, 512);
+  }
+  if (tid == 0 && S.failed) raise_status(p.status, DFLASH_STATUS_TIMEOUT);
+}
+
 // Joins the statistics of a row's tiles: 32 rows a block, 32 runs of parts.
 __global__ void __launch_bounds__(1024)
     join_kernel(const float2* parts, int n_parts, int pitch, const float* label_logit, const EntropyParams p) {
@@ -546,6 +723,7 @@ constexpr int kPairs = 76;  // the splits' rule goes by a whole GPU's pairs of S
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 int tiles_of(long long n) { return (int)((n + kTile - 1) / kTile); }
 
+constexpr int kMaxPairs = 128;  // of SMs, where the workspace counts them
 constexpr int kForwardRows = 16384;  // whose statistics are held at a time
 struct ForwardPlan {
   int n_parts, pitch;
@@ -555,6 +733,7 @@ ForwardPlan forward_plan(int rows, int V) {
   ForwardPlan f;
   rows = rows < kForwardRows ? rows : kForwardRows;
   f.n_parts = 2 * tiles_of(V);
+  if (rows <= kFew) f.n_parts = 8 * (tiles_of(V) < kMaxPairs ? tiles_of(V) : kMaxPairs);
   f.pitch = (rows + 31) / 32 * 32;
   f.parts = 0;
   f.labels = up((size_t)f.n_parts * f.pitch * sizeof(float2));
@@ -619,6 +798,26 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
       <<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kGemmThreads, kGemmSmem, stream>>>(a, b, out, p);
   return cudaGetLastError();
 }
+cudaError_t launch_few(const CUtensorMap& w, const CUtensorMap& h, GemmParams p, int sms, int* n_parts, cudaStream_t stream) {
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(few_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  p.tiles_n = tiles_of(p.n);
+  p.chunk = 1024 / kStep;
+  int pairs = sms / 2 < 1 ? 1 : sms / 2;
+  if (pairs > kMaxPairs) pairs = kMaxPairs;
+  if (pairs > p.tiles_n) pairs = p.tiles_n;
+  *n_parts = 8 * pairs;
+  few_rows_kernel<<<(unsigned)(2 * pairs), kFewThreads, kFewSmem, stream>>>(w, h, p);
+  return cudaGetLastError();
+}
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 
 }  // namespace
@@ -652,9 +851,17 @@ int launch_entropy(const EntropyParams& p, int sms, void* stream) {
     g.labels = q.labels;
     g.label_logit = reinterpret_cast<float*>(p.ws + f.labels);
     g.status = p.status;
-    cudaError_t e = launch_gemm<false, false, kStats>(h, w, w, g, sms, st);
+    int n_parts = f.n_parts;
+    cudaError_t e;
+    if (q.rows <= kFew && p.rows <= kFew) {
+      CUtensorMap few;
+      if (!tc::map_2d(&few, kBf16, 2, q.h, q.rows, p.K, 2 * p.h_stride, kFew / 2)) return (int)cudaErrorInvalidValue;
+      e = launch_few(w, few, g, sms, &n_parts, st);
+    } else {
+      e = launch_gemm<false, false, kStats>(h, w, w, g, sms, st);
+    }
     if (e != cudaSuccess) return (int)e;
-    join_kernel<<<(unsigned)((q.rows + 31) / 32), 1024, 0, st>>>(g.parts, f.n_parts, f.pitch, g.label_logit, q);
+    join_kernel<<<(unsigned)((q.rows + 31) / 32), 1024, 0, st>>>(g.parts, n_parts, f.pitch, g.label_logit, q);
     e = cudaGetLastError();
     if (e != cudaSuccess) return (int)e;
   }
