@@ -27,6 +27,7 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kSms = 152;
 constexpr int kGroup = 4;  // tokens whose angles a block holds at a time
 
 struct Place {
@@ -44,15 +45,62 @@ __device__ __forceinline__ Place place_of(const NormParams& p, int i) {
   return l;
 }
 
-// The angles of nt tokens from t0 on: pair 8 i + e at [token][e][i].
-__device__ __forceinline__ void fill_turns(const NormParams& p, float2* turn, int t0, int nt) {
-  const int half = p.rot >> 1, rv = p.rot >> 4;
-  if (!half) return;
-  for (int at = threadIdx.x; at < nt * half; at += kThreads) {
-    const int ti = at / half, j = at - ti * half;
-    turn[ti * half + (j & 7) * rv + (j >> 3)] = turn_at(p.phases[j], p.positions[t0 + ti]);
-  }
+__device__ __forceinline__ void ask16(uint4* to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
+__device__ __forceinline__ void ask_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void ask_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// The angles of kGroup tokens: pair 8 i + e at [token][e][i]. Positions are read while
+// the group before is worked on.
+template <int D>
+struct Turns {
+  static constexpr int kPer = (kGroup * D / 2 + kThreads - 1) / kThreads;
+  int pos[kPer];
+  __device__ __forceinline__ void ask(const NormParams& p, int t0) {
+    const int half = p.rot >> 1;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int at = threadIdx.x + k * kThreads, ti = half ? at / half : kGroup;
+      pos[k] = ti < kGroup && t0 + ti < p.tokens ? p.positions[t0 + ti] : 0;
+    }
+  }
+  __device__ __forceinline__ void put(const NormParams& p, float2* turn) const {
+    const int half = p.rot >> 1, rv = p.rot >> 4;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int at = threadIdx.x + k * kThreads;
+      if (at >= kGroup * half) continue;
+      const int ti = at / half, j = at - ti * half;
+      turn[ti * half + (j & 7) * rv + (j >> 3)] = turn_at(p.phases[j], pos[k]);
+    }
+  }
+};
+
+// A block's way through the rows (heads of tokens) of its groups of tokens, kRows at a time.
+template <int kRows>
+struct Walk {
+  int t0, r;  // the group's first token, the first row of the step
+  int heads;
+  unsigned long long per;  // r / heads = r per / 2^48 while r heads < 2^48 (r < 2^23, heads < 2^21)
+  __device__ __forceinline__ Walk(const NormParams& p, int heads_)
+      : t0(heads_ ? blockIdx.x * kGroup : p.tokens), r(0), heads(heads_),
+        per(heads_ ? (1ull << 48) / heads_ + 1 : 0) {}
+  __device__ __forceinline__ int rows(int tokens) const { return min(kGroup, tokens - t0) * heads; }
+  __device__ __forceinline__ int token(int row) const { return (int)((unsigned)row * per >> 48); }
+  __device__ __forceinline__ int after() const { return t0 + gridDim.x * kGroup; }
+  // true: on to the next group
+  __device__ __forceinline__ bool next(int tokens) {
+    r += kRows;
+    if (r < rows(tokens)) return false;
+    r = 0;
+    t0 = after();
+    return true;
+  }
+};
 
 // Weights for a lane place: 16 of one head in pieces of 4, a piece of all lanes side
 // by side, so that reading them meets no bank twice.
@@ -75,47 +123,58 @@ __device__ __forceinline__ void fill_weights(const NormParams& p, float4* w) {
 }
 
 // A row is one head of one token: queries, then keys. What bounds it: 302 MB of 8192
-// tokens, 64 + 8 heads of 128 in bf16 take XXX us; with the weights in registers, two
-// blocks an SM, they took 81.
+// tokens, 64 + 8 heads of 128 in bf16 take 56 us (5.4 TB/s). A thread's vectors are asked
+// for three steps ahead and wait in shared memory: with loads into registers and a
+// block for each group of tokens they took 61.
+constexpr int kForwardSlots = 4, kForwardBlocks = 4;
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const NormParams p) {
-  constexpr int kLanes = D / 16, kRows = kThreads / kLanes, kBatch = 2;
-  __shared__ float2 turn[kGroup * D / 2];
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) norm_kernel(const NormParams p) {
+  constexpr int kLanes = D / 16, kRows = kThreads / kLanes;
+  extern __shared__ uint4 ring[];  // [slot][2][thread]
+  __shared__ float2 turns[2][kGroup * D / 2];
   __shared__ float4 weights[2 * 4 * kLanes];
   grid_dependency_sync();
   const int i = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
   const Place l = place_of(p, i);
-  const int heads = p.q_heads + p.k_heads, t0 = blockIdx.x * kGroup, nt = min(kGroup, p.tokens - t0);
-  const int rows = nt * heads, half = p.rot >> 1, rv = p.rot >> 4;
-  bool ready = false;
-  for (int r0 = first; r0 < rows || !ready; r0 += kBatch * kRows) {
-    uint4 x[kBatch], y[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = r0 + k * kRows;
-      if (r >= rows) continue;
-      const int ti = r / heads, h = r - ti * heads;
-      const HeadRows& s = h < p.q_heads ? p.q : p.k;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          s.p + 2 * ((t0 + ti) * s.ts + (long long)(h < p.q_heads ? h : h - p.q_heads) * s.hs));
-      x[k] = src[l.va];
-      y[k] = src[l.vb];
+  const int half = p.rot >> 1, rv = p.rot >> 4;
+  Walk<kRows> at(p, p.q_heads + p.k_heads), to = at;  // where the work is, and the loads
+  auto ask = [&](int slot) {
+    if (to.t0 < p.tokens) {
+      const int r = to.r + first;
+      if (r < to.rows(p.tokens)) {
+        const int ti = to.token(r), h = r - ti * to.heads;
+        const HeadRows& s = h < p.q_heads ? p.q : p.k;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            s.p + 2 * ((to.t0 + ti) * s.ts + (long long)(h < p.q_heads ? h : h - p.q_heads) * s.hs));
+        ask16(ring + (2 * slot) * kThreads + threadIdx.x, src + l.va);
+        ask16(ring + (2 * slot + 1) * kThreads + threadIdx.x, src + l.vb);
+      }
+      to.next(p.tokens);
     }
-    if (!ready) {
-      fill_weights<T, D>(p, weights);
-      fill_turns(p, turn, t0, nt);
-      __syncthreads();
-      ready = true;
-    }
+    ask_end();
+  };
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = r0 + k * kRows;
-      if (r >= rows) continue;
-      const int ti = r / heads, h = r - ti * heads;
+  for (int s = 0; s < kForwardSlots - 1; ++s) ask(s);
+  Turns<D> ahead;
+  ahead.ask(p, at.t0);
+  fill_weights<T, D>(p, weights);
+  ahead.put(p, turns[0]);
+  ahead.ask(p, at.after());
+  __syncthreads();
+  int buf = 0;
+  for (int slot = 0; at.t0 < p.tokens; slot = slot + 1 == kForwardSlots ? 0 : slot + 1) {
+    ask_wait<kForwardSlots - 2>();
+    const int t0 = at.t0, r = at.r + first;
+    const bool mine = r < at.rows(p.tokens);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (mine) x = ring[(2 * slot) * kThreads + threadIdx.x], y = ring[(2 * slot + 1) * kThreads + threadIdx.x];
+    ask(slot ? slot - 1 : kForwardSlots - 1);  // the slot of the step before
+    if (mine) {
+      const int ti = at.token(r), h = r - ti * at.heads;
       const bool is_q = h < p.q_heads;
       float a[8], b[8];
-      unpack8<T>(x[k], a);
-      unpack8<T>(y[k], b);
+      unpack8<T>(x, a);
+      unpack8<T>(y, b);
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += a[e] * a[e] + b[e] * b[e];
@@ -127,21 +186,30 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const NormParams p) {
         a[4 * e] *= inv * u.x, a[4 * e + 1] *= inv * u.y, a[4 * e + 2] *= inv * u.z, a[4 * e + 3] *= inv * u.w;
         b[4 * e] *= inv * v.x, b[4 * e + 1] *= inv * v.y, b[4 * e + 2] *= inv * v.z, b[4 * e + 3] *= inv * v.w;
       }
-      if (l.turned) turn_pairs(a, b, turn + ti * half + i, rv, l.split, false);
+      if (l.turned) turn_pairs(a, b, turns[buf] + ti * half + i, rv, l.split, false);
       const HeadRows& o = is_q ? p.qo : p.ko;
       uint4* dst = reinterpret_cast<uint4*>(o.p + 2 * ((t0 + ti) * o.ts + (long long)(is_q ? h : h - p.q_heads) * o.hs));
       dst[l.va] = pack8<T>(a);
       dst[l.vb] = pack8<T>(b);
     }
+    if (at.next(p.tokens) && half) {
+      buf ^= 1;
+      ahead.put(p, turns[buf]);
+      ahead.ask(p, at.after());
+      __syncthreads();
+    }
   }
 }
 
-// Queries first, then keys: a thread's sums are those of one of them. The next row's
-// values are asked for before this one's are worked on.
+// Queries first, then keys: a thread's sums are those of one of them. What bounds it:
+// 503 MB of 16384 tokens, 32 + 8 heads of 128 in bf16 take 97 us (5.2 TB/s); with the next
+// row in registers they took 111, and three slots of the ring take 104.
+constexpr int kGradSlots = 4, kGradBlocks = 2;
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kThreads, kGradBlocks) norm_grad_kernel(const NormParams p) {
   constexpr int kLanes = D / 16, kRows = kThreads / kLanes;
-  __shared__ float2 turn[kGroup * D / 2];
+  extern __shared__ uint4 ring[];  // [slot][4][thread]
+  __shared__ float2 turns[2][kGroup * D / 2];
   __shared__ float4 weights[2 * 4 * kLanes];
   __shared__ float sums[kThreads / 32][D];
   grid_dependency_sync();
@@ -149,36 +217,50 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const NormParams
   const Place l = place_of(p, i);
   const int half = p.rot >> 1, rv = p.rot >> 4;
   fill_weights<T, D>(p, weights);
-  __syncthreads();
+  Turns<D> ahead;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
     const HeadRows s = part ? p.k : p.q, d = part ? p.dk : p.dq, o = part ? p.ko : p.qo;
-    const int hn = part ? p.k_heads : p.q_heads;
-    float dw[16] = {};
-    for (int t0 = blockIdx.x * kGroup; hn && t0 < p.tokens; t0 += gridDim.x * kGroup) {
-      const int nt = min(kGroup, p.tokens - t0), rows = nt * hn;
-      uint4 x0, x1, g0, g1;
-      auto load = [&](int r) {
-        const int ti = r / hn, h = r - ti * hn;
-        const uint4* xs = reinterpret_cast<const uint4*>(s.p + 2 * ((t0 + ti) * s.ts + (long long)h * s.hs));
-        const uint4* gs = reinterpret_cast<const uint4*>(d.p + 2 * ((t0 + ti) * d.ts + (long long)h * d.hs));
-        x0 = xs[l.va], x1 = xs[l.vb], g0 = gs[l.va], g1 = gs[l.vb];
-      };
-      if (first < rows) load(first);
-      if (half) {
-        __syncthreads();
-        fill_turns(p, turn, t0, nt);
-        __syncthreads();
+    Walk<kRows> at(p, part ? p.k_heads : p.q_heads), to = at;
+    auto ask = [&](int slot) {
+      if (to.t0 < p.tokens) {
+        const int r = to.r + first;
+        if (r < to.rows(p.tokens)) {
+          const int ti = to.token(r), h = r - ti * to.heads;
+          const uint4* xs = reinterpret_cast<const uint4*>(s.p + 2 * ((to.t0 + ti) * s.ts + (long long)h * s.hs));
+          const uint4* gs = reinterpret_cast<const uint4*>(d.p + 2 * ((to.t0 + ti) * d.ts + (long long)h * d.hs));
+          uint4* r4 = ring + 4 * slot * kThreads + tid;
+          ask16(r4, xs + l.va);
+          ask16(r4 + kThreads, xs + l.vb);
+          ask16(r4 + 2 * kThreads, gs + l.va);
+          ask16(r4 + 3 * kThreads, gs + l.vb);
+        }
+        to.next(p.tokens);
       }
-      for (int r = first; r < rows; r += kRows) {
-        const int ti = r / hn, h = r - ti * hn;
+      ask_end();
+    };
+#pragma unroll
+    for (int k = 0; k < kGradSlots - 1; ++k) ask(k);
+    ahead.ask(p, at.t0);
+    ahead.put(p, turns[0]);
+    ahead.ask(p, at.after());
+    __syncthreads();
+    int buf = 0;
+    float dw[16] = {};
+    for (int slot = 0; at.t0 < p.tokens; slot = slot + 1 == kGradSlots ? 0 : slot + 1) {
+      ask_wait<kGradSlots - 2>();
+      const int t0 = at.t0, r = at.r + first;
+      const bool mine = r < at.rows(p.tokens);
+      ask(slot ? slot - 1 : kGradSlots - 1);  // the slot of the step before
+      if (mine) {
+        const uint4* r4 = ring + 4 * slot * kThreads + tid;
+        const int ti = at.token(r), h = r - ti * at.heads;
         float a[8], b[8], ga[8], gb[8];
-        unpack8<T>(x0, a);
-        unpack8<T>(x1, b);
-        unpack8<T>(g0, ga);
-        unpack8<T>(g1, gb);
-        if (r + kRows < rows) load(r + kRows);
-        if (l.turned) turn_pairs(ga, gb, turn + ti * half + i, rv, l.split, true);
+        unpack8<T>(r4[0], a);
+        unpack8<T>(r4[kThreads], b);
+        unpack8<T>(r4[2 * kThreads], ga);
+        unpack8<T>(r4[3 * kThreads], gb);
+        if (l.turned) turn_pairs(ga, gb, turns[buf] + ti * half + i, rv, l.split, true);
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += a[e] * a[e] + b[e] * b[e];
@@ -207,6 +289,12 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_kernel(const NormParams
         uint4* dst = reinterpret_cast<uint4*>(o.p + 2 * ((t0 + ti) * o.ts + (long long)h * o.hs));
         dst[l.va] = pack8<T>(a);
         dst[l.vb] = pack8<T>(b);
+      }
+      if (at.next(p.tokens) && half) {
+        buf ^= 1;
+        ahead.put(p, turns[buf]);
+        ahead.ask(p, at.after());
+        __syncthreads();
       }
     }
     // the block's sums: over the heads inside a warp, then over the warps
@@ -252,10 +340,11 @@ __global__ void __launch_bounds__(1024) norm_weights_kernel(const NormParams p, 
 }
 
 template <class K, class... A>
-int launch(K kernel, int grid, int threads, void* stream, A... args) {
+int launch(K kernel, int grid, int threads, int smem, void* stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -264,17 +353,38 @@ int launch(K kernel, int grid, int threads, void* stream, A... args) {
   cfg.numAttrs = 1;
   return (int)cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+// Shared memory above 48 KB, once for each device.
+template <class K>
+int allow(K kernel, int smem, bool (&ready)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
+  if (ready[dev]) return 0;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  ready[dev] = e == cudaSuccess;
+  return (int)e;
+}
 
 template <class T, int D>
 int forward(const NormParams& p, void* stream) {
-  return launch(norm_kernel<T, D>, (p.tokens + kGroup - 1) / kGroup, kThreads, stream, p);
+  static bool ready[64] = {};
+  constexpr int kSmem = kForwardSlots * 2 * kThreads * 16, kBlocks = kForwardBlocks * kSms;
+  const int e = allow(norm_kernel<T, D>, kSmem, ready);
+  if (e) return e;
+  const int groups = (p.tokens + kGroup - 1) / kGroup;
+  return launch(norm_kernel<T, D>, groups < kBlocks ? groups : kBlocks, kThreads, kSmem, stream, p);
 }
 template <class T, int D>
 int backward(const NormParams& p, void* stream) {
+  static bool ready[64] = {};
+  constexpr int kSmem = kGradSlots * 4 * kThreads * 16;
+  int e = allow(norm_grad_kernel<T, D>, kSmem, ready);
+  if (e) return e;
   const int groups = (p.tokens + kGroup - 1) / kGroup, blocks = groups < kNormBlocks ? groups : kNormBlocks;
-  const int e = launch(norm_grad_kernel<T, D>, blocks, kThreads, stream, p);
+  e = launch(norm_grad_kernel<T, D>, blocks, kThreads, kSmem, stream, p);
   if (e || !(p.gq_weight || p.gk_weight)) return e;
-  return launch(norm_weights_kernel<T, D>, 2 * D / 32, 1024, stream, p, blocks);
+  return launch(norm_weights_kernel<T, D>, 2 * D / 32, 1024, 0, stream, p, blocks);
 }
 
 }  // namespace

@@ -32,7 +32,7 @@ struct NormParams {
   int rot, interleaved;
   float* partial;                // backward: [kNormBlocks][2][head_dim]
 };
-constexpr int kNormBlocks = 608;  // of the backward pass, at most
+constexpr int kNormBlocks = 304;  // of the backward pass, at most: two for each of 152 SMs
 inline size_t norm_workspace(int head_dim) { return (size_t)kNormBlocks * 2 * head_dim * sizeof(float); }
 int launch_norm(const NormParams& p, int dtype, int head_dim, void* stream);
 int launch_norm_grad(const NormParams& p, int dtype, int head_dim, void* stream);
