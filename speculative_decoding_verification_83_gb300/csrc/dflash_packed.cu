@@ -376,47 +376,63 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const PackedParams p
 
 // What the gradients' kernels read: both lists (the first two blocks), and the rows'
 // statistics: delta, the sum over d of dout out, and lse, their signs reversed; behind
-// the last row a tile's worth of zeros.
+// the last row a tile's worth of zeros. D / 8 lanes take four tokens of a head at a time,
+// whose loads are in flight together and whose statistics lie side by side (8192 tokens,
+// 32 heads of 128, 168 MB: 40 us, one token at a time 47).
 template <class T, int D>
-__global__ void __launch_bounds__(kListThreads, 2)
+__global__ void __launch_bounds__(kListThreads, 1)
     grad_prepare_kernel(const PackedParams p, const PackedList queries, const PackedList keys) {
-  constexpr int kLanes = D / 8;  // 8 values each
+  constexpr unsigned kLanes = D / 8;  // 8 values each
   grid_dependency_sync();
   if (blockIdx.x < 2) {
     build_list(p, blockIdx.x == 1, kGradRows, blockIdx.x ? keys : queries);
     return;
   }
   const long long id = (long long)(blockIdx.x - 2) * kListThreads + threadIdx.x;
-  const int lane = threadIdx.x % kLanes;
-  const long long rows = (long long)p.q_tokens * p.q_heads, r = id / kLanes;
-  const int spare = p.stat_pitch - p.q_tokens;
+  const unsigned lane = threadIdx.x % kLanes;
+  const unsigned unit = (unsigned)(id / kLanes), head = unit % (unsigned)p.q_heads;  // (as many as rows / 4: below 2^32)
+  const long long t0 = unit / (unsigned)p.q_heads * 4ll;
+  const int spare = p.stat_pitch - p.q_tokens, left = (int)(p.q_tokens - t0 < 4 ? p.q_tokens - t0 : 4);
   for (long long at = id; at < spare * 2ll * p.q_heads; at += (long long)(gridDim.x - 2) * kListThreads)
     p.row_stats[at / spare * p.stat_pitch + p.q_tokens + at % spare] = 0.0f;
-  float s = 0.0f;
-  if (r < rows) {
-    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
-    const uint4 a = reinterpret_cast<const uint4*>(row_of(p.o, t, head))[lane];
-    const uint4 g = reinterpret_cast<const uint4*>(row_of(p.d_o, t, head))[lane];
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {g.x, g.y, g.z, g.w};
-    uint2 l = make_uint2(0u, 0u);
-    if (p.low) l = reinterpret_cast<const uint2*>(p.low + r * D)[lane];
-    const uint32_t low[2] = {l.x, l.y};
+  uint4 a[4], g[4];
+  uint2 l[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    a[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
+    l[k] = make_uint2(0u, 0u);
+    if (k >= left) continue;
+    a[k] = reinterpret_cast<const uint4*>(row_of(p.o, (int)t0 + k, (int)head))[lane];
+    g[k] = reinterpret_cast<const uint4*>(row_of(p.d_o, (int)t0 + k, (int)head))[lane];
+    if (p.low) l[k] = reinterpret_cast<const uint2*>(p.low + ((t0 + k) * p.q_heads + head) * D)[lane];
+  }
+  float s[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+    const uint32_t low[2] = {l[k].x, l[k].y};
+    s[k] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t b = low[e >> 1] >> (16 * (e & 1));
       const float2 v = T::unpack(y[e]);
-      s = fmaf(with_low(x[e] & 0xffffu, (int8_t)(b & 0xffu)), v.x,
-               fmaf(with_low(x[e] >> 16, (int8_t)((b >> 8) & 0xffu)), v.y, s));
+      s[k] = fmaf(with_low(x[e] & 0xffffu, (int8_t)(b & 0xffu)), v.x,
+                  fmaf(with_low(x[e] >> 16, (int8_t)((b >> 8) & 0xffu)), v.y, s[k]));
     }
   }
+  // lane k of each four ends with token k's sum
+  const bool odd = lane & 1u, high = lane & 2u;
+  const float s01 = (odd ? s[1] : s[0]) + __shfl_xor_sync(kAll, odd ? s[0] : s[1], 1);
+  const float s23 = (odd ? s[3] : s[2]) + __shfl_xor_sync(kAll, odd ? s[2] : s[3], 1);
+  float sum = (high ? s23 : s01) + __shfl_xor_sync(kAll, high ? s01 : s23, 2);
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  if (r < rows && lane == 0) {
-    const int t = (int)(r / p.q_heads), head = (int)(r - (long long)t * p.q_heads);
-    const float lse = p.lse[r];
+  for (unsigned o = 4; o < kLanes; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if ((int)lane < left) {  // (no more than 4)
+    const long long t = t0 + lane;
+    const float lse = p.lse[t * p.q_heads + head];
     float* st = p.row_stats + (size_t)head * 2 * p.stat_pitch;
     st[t] = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
-    st[p.stat_pitch + t] = -s;
+    st[p.stat_pitch + t] = -sum;
   }
 }
 
@@ -489,7 +505,8 @@ int launch_packed_grad(const PackedParams& p0, int head_dim, int sms, void* stre
   const PackedList keys = list_at(ws);
   ws += list_bytes(p.kv_tokens, p.B, kGradRows);
   uint8_t* kv_flags = ws;
-  const unsigned blocks = 2u + (unsigned)(((long long)p.q_tokens * p.q_heads * (head_dim / 8) + kListThreads - 1) / kListThreads);
+  const long long lanes = (p.q_tokens + 3ll) / 4 * p.q_heads * (head_dim / 8);
+  const unsigned blocks = 2u + (unsigned)((lanes + kListThreads - 1) / kListThreads);
   int e = head_dim == 64 ? launch(grad_prepare_kernel<Bf16, 64>, blocks, (unsigned)kListThreads, stream, p, queries, keys)
                          : launch(grad_prepare_kernel<Bf16, 128>, blocks, (unsigned)kListThreads, stream, p, queries, keys);
   if (!e && p.q_tokens) e = launch_dq_tc(p, head_dim, queries, q_flags, sms, stream);
