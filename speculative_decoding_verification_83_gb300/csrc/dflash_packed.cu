@@ -17,6 +17,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "dflash_packed.cuh"
 
@@ -69,51 +70,102 @@ __device__ __forceinline__ bool row_not_finite(const unsigned char* row) {
   return __any_sync(kAll, found);
 }
 
-// Row t of the outputs: query i of n over m keys from kv0 on. One warp; q_row: its
-// D values of shared memory.
+// Row t of the outputs: query i of n over m keys from kv0 on. One warp; D / 8 lanes read a
+// key, 32 of which are scored at a time, and a lane ends with the score of its own.
 template <class T, int D>
-__device__ void attend_row(const PackedParams& p, int t, int head, int i, int n, int kv0, int m, float* q_row) {
-  const int lane = threadIdx.x & 31, kh = head / p.G, vis = seen_keys(p.causal, n, m, i);
+__device__ void attend_row(const PackedParams& p, int t, int head, int i, int n, int kv0, int m) {
+  constexpr int kLanes = D / 8, kWords = D / 64, kAtOnce = 8;  // of a key; a lane's columns of V, in pairs; keys in flight
+  constexpr uint32_t kExponents = std::is_same<T, F16>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t kCarry = std::is_same<T, F16>::value ? 0x04000400u : 0x00800080u;
+  const int lane = threadIdx.x & 31, part = lane % kLanes, kh = head / p.G, vis = seen_keys(p.causal, n, m, i);
   const long long r = (long long)t * p.q_heads + head;
-  const unsigned char* q = row_of(p.q, t, head);
   unsigned char* out = row_of(p.o, t, head);
-  __syncwarp();
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) q_row[lane + 32 * c] = value<T>(q, lane + 32 * c);
-  __syncwarp();
+  float2 q[4];
+  {
+    const uint4 u = reinterpret_cast<const uint4*>(row_of(p.q, t, head))[part];
+    q[0] = T::unpack(u.x), q[1] = T::unpack(u.y), q[2] = T::unpack(u.z), q[3] = T::unpack(u.w);
+  }
   float top = -INFINITY, sum = 0.0f, acc[D / 32] = {};
   uint32_t odd[D / 32] = {};  // values seen that are not finite: +inf (1), -inf (2), NaN (4)
   for (int j0 = 0; j0 < vis; j0 += 32) {
-    const int j = j0 + lane, count = min(32, vis - j0);
-    float x = -INFINITY;
-    if (j < vis) x = dot<T, D>(q_row, row_of(p.k, kv0 + j, kh)) * p.scale;
+    const int count = min(32, vis - j0);
+    float s[kLanes];
+#pragma unroll
+    for (int k0 = 0; k0 < kLanes; k0 += kAtOnce) {
+      uint4 u[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        u[k] = reinterpret_cast<const uint4*>(row_of(p.k, kv0 + j0 + min(k0 + k + lane - part, count - 1), kh))[part];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float2 a = T::unpack(u[k].x), b = T::unpack(u[k].y), c = T::unpack(u[k].z), d = T::unpack(u[k].w);
+        s[k0 + k] = fmaf(q[0].x, a.x, fmaf(q[0].y, a.y, fmaf(q[1].x, b.x, q[1].y * b.y))) +
+                    fmaf(q[2].x, c.x, fmaf(q[2].y, c.y, fmaf(q[3].x, d.x, q[3].y * d.y)));
+      }
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < o; ++k) {
+        const bool hi = lane & o;
+        s[k] = (hi ? s[k + o] : s[k]) + __shfl_xor_sync(kAll, hi ? s[k] : s[k + o], o);
+      }
+    const float x = lane < count ? s[0] * p.scale : -INFINITY;
     const float m1 = warp_max_f32(fmaxf(x, top)), ref = m1 == -INFINITY ? 0.0f : m1;
     const float f = expf(top - ref), w = expf(x - ref);  // (a score that is NaN leaves NaN)
     sum = sum * f + warp_sum(w);
     top = m1;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) acc[c] *= f;
-    for (int k = 0; k < count; ++k) {
-      const float wk = __shfl_sync(kAll, w, k);
-      const unsigned char* v = row_of(p.v, kv0 + j0 + k, kh);
+    for (int k0 = 0; k0 < count; k0 += kAtOnce) {
+      uint32_t v[kAtOnce][kWords];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const float y = value<T>(v, lane + 32 * c);
-        if (fabsf(y) < INFINITY)
-          acc[c] = fmaf(wk, y, acc[c]);
-        else
-          odd[c] |= y > 0.0f ? 1u : y < 0.0f ? 2u : 4u;
+      for (int k = 0; k < kAtOnce; ++k) {
+        const unsigned char* from = row_of(p.v, kv0 + j0 + min(k0 + k, count - 1), kh) + 4 * kWords * lane;
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) v[k][e] = reinterpret_cast<const uint32_t*>(from)[e];
+      }
+      uint32_t special = 0;  // a pair's exponent of all ones carries into its top bits
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) special |= (v[k][e] & kExponents) + kCarry;
+      if (!__any_sync(kAll, special & 0x80008000u)) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const float wk = __shfl_sync(kAll, w, (k0 + k) & 31);  // (0 from `count` on: no lane sees those keys)
+#pragma unroll
+          for (int e = 0; e < kWords; ++e) {
+            const float2 y = T::unpack(v[k][e]);
+            acc[2 * e] = fmaf(wk, y.x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(wk, y.y, acc[2 * e + 1]);
+          }
+        }
+        continue;
+      }
+      for (int k = k0; k < min(count, k0 + kAtOnce); ++k) {
+        const float wk = __shfl_sync(kAll, w, k);
+        const unsigned char* row = row_of(p.v, kv0 + j0 + k, kh);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const float y = value<T>(row, lane * (D / 32) + c);
+          if (fabsf(y) < INFINITY)
+            acc[c] = fmaf(wk, y, acc[c]);
+          else
+            odd[c] |= y > 0.0f ? 1u : y < 0.0f ? 2u : 4u;
+        }
       }
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
+    const int d = lane * (D / 32) + c;
     float y = acc[c] * inv;
     if (odd[c] && y == y) y = odd[c] == 1u ? INFINITY : odd[c] == 2u ? -INFINITY : NAN;
     const uint32_t hi = T::pack(y, 0.0f) & 0xffffu;
-    reinterpret_cast<uint16_t*>(out)[lane + 32 * c] = (uint16_t)hi;
-    if (p.low) p.low[r * D + lane + 32 * c] = low_bits(y, hi);
+    reinterpret_cast<uint16_t*>(out)[d] = (uint16_t)hi;
+    if (p.low) p.low[r * D + d] = low_bits(y, hi);
   }
   if (p.lse && lane == 0) p.lse[r] = sum == 0.0f ? -INFINITY : top + logf(sum);
 }
@@ -149,22 +201,57 @@ __device__ __forceinline__ void clear8(const HeadRows& h, int t, int head, int c
   reinterpret_cast<uint4*>(row_of(h, t, head))[c] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps)
-    redo_forward_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
-  __shared__ float q_row[kWarps][D];
-  grid_dependency_sync();
-  each_flagged<kForwardFlags, 2>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
-    if (row_not_finite<T, D>(row_of(p.o, t, head)))
-      attend_row<T, D>(p, t, head, i, u.n, u.other0, u.m, q_row[threadIdx.x >> 5]);
-  });
-  if (!p.fill) return;
+template <int D>
+__device__ __forceinline__ void clear_spare(const PackedParams& p) {
   each_spare<D>(p.q_start, p.B, p.q_tokens, p.q_heads, [&](int t, int head, int c) {
     clear8(p.o, t, head, c);
     const long long r = (long long)t * p.q_heads + head;
     if (p.low) reinterpret_cast<uint2*>(p.low + r * D)[c] = make_uint2(0u, 0u);
     if (p.lse && c == 0) p.lse[r] = -INFINITY;
   });
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kWarps)
+    redo_forward_kernel(const PackedParams p, const PackedList list, const uint8_t* flags) {
+  grid_dependency_sync();
+  each_flagged<kForwardFlags, 2>(list, flags, p.q_heads, [&](int t, int head, int i, const PackedUnit& u) {
+    if (row_not_finite<T, D>(row_of(p.o, t, head))) attend_row<T, D>(p, t, head, i, u.n, u.other0, u.m);
+  });
+  if (p.fill) clear_spare<D>(p);
+}
+
+// Prompts of few words: a warp a row, in one launch where the tensor cores' way takes
+// three. Latency bounds both. Replayed, 32 + 8 heads of 128: one prompt of 7 tokens 6.2
+// against 14.3 us, of 32 tokens 12.3 against 14.4, of 64 tokens 18.4 against 14.5 (but 23
+// against 27 called directly); 16 prompts of 4 tokens 10.2 against 28.6. A batch's offsets
+// are on the GPU, so the rule goes by what all its keys, in one sequence, would take.
+constexpr int kFewKeys = 64, kFewRows = 4096, kFewWarps = 2;
+constexpr int kFewBatch = 32 * kFewWarps - 1;  // (a thread an offset)
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const PackedParams p) {
+  __shared__ int starts[2][kFewBatch + 1];
+  grid_dependency_sync();
+  if (threadIdx.x <= p.B) {
+    starts[0][threadIdx.x] = p.q_start[threadIdx.x];
+    starts[1][threadIdx.x] = p.kv_start[threadIdx.x];
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, warps = gridDim.x * kFewWarps;
+  int next = blockIdx.x * kFewWarps + warp;  // this warp's next row, counted from the sequence's first
+  bool bad = false;
+  for (int b = 0; b < p.B; ++b) {
+    int q0, n, k0, m;
+    extent(starts[0], p.q_tokens, b, q0, n, bad);
+    extent(starts[1], p.kv_tokens, b, k0, m, bad);
+    for (; next < n * p.q_heads; next += warps) {
+      const int i = next / p.q_heads;
+      attend_row<T, D>(p, q0 + i, next - i * p.q_heads, i, n, k0, m);
+    }
+    next -= n * p.q_heads;
+  }
+  if (bad && blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, DFLASH_STATUS_BAD_LENGTH);
+  if (p.fill) clear_spare<D>(p);
 }
 
 // Row t of the queries' gradients.
@@ -278,43 +365,43 @@ __global__ void __launch_bounds__(32 * kWarps)
 // no order among themselves, which no result depends on.
 constexpr int kListThreads = 1024, kBuckets = 1024;
 __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int rows, const PackedList& list) {
-  __shared__ int before[kMaxBatch + 1], warp_sum_[32], bucket[kBuckets];
+  __shared__ int before[kMaxBatch + 1], bucket[kBuckets];
+  __shared__ long long warp_sum_[32];  // (offsets that do not ascend may name every row in every sequence)
   const int32_t *sa = keys ? p.kv_start : p.q_start, *sb = keys ? p.q_start : p.kv_start;
   const int ta = keys ? p.kv_tokens : p.q_tokens, tb = keys ? p.q_tokens : p.kv_tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   // units before each sequence
-  int done = 0;
+  long long done = 0;
   for (int b0 = 0; b0 < p.B; b0 += kListThreads) {
     const int b = b0 + tid;
-    int mine = 0;
+    long long mine = 0;
     if (b < p.B) {
       int first, n;
       extent(sb, tb, b, first, n, bad);
       extent(sa, ta, b, first, n, bad);
       mine = (n + rows - 1) / rows;
     }
-    int incl = mine;
+    long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kAll, incl, o);
+      const long long v = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += v;
     }
     if (lane == 31) warp_sum_[warp] = incl;
     __syncthreads();
-    int pre = 0, all = 0;
+    long long pre = 0, all = 0;
     for (int w = 0; w < 32; ++w) {
       if (w < warp) pre += warp_sum_[w];
       all += warp_sum_[w];
     }
-    if (b < p.B) before[b] = done + pre + incl - mine;
+    if (b < p.B) before[b] = (int)min(done + pre + incl - mine, 0x7fffffffll);
     done += all;
     __syncthreads();
   }
   // offsets that do not ascend may name more units than the list holds
-  const int total = min(done, most_units(ta, p.B, rows));
+  const int total = (int)min(done, (long long)most_units(ta, p.B, rows));
   if (tid == 0) {
-    before[p.B] = done;
     *list.count = total;
   }
   for (int i = tid; i < kBuckets; i += kListThreads) bucket[i] = 0;
@@ -357,7 +444,7 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
     if (lane == 31) warp_sum_[warp] = incl;
     __syncthreads();
     int pre = 0;
-    for (int w = 0; w < warp; ++w) pre += warp_sum_[w];
+    for (int w = 0; w < warp; ++w) pre += (int)warp_sum_[w];
     bucket[tid] = pre + incl - mine;
   }
   __syncthreads();
@@ -485,6 +572,15 @@ size_t packed_workspace(int B, int q_tokens, int kv_tokens, int q_heads, int kv_
 }
 
 int launch_packed(const PackedParams& p, int dtype, int head_dim, int sms, void* stream) {
+  if (!p.low && p.kv_tokens <= kFewKeys && p.B <= kFewBatch && (long long)p.q_tokens * p.q_heads <= kFewRows) {
+    const int rows = p.q_tokens * p.q_heads;
+    const unsigned grid = (unsigned)(rows < kFewWarps ? 1 : (rows + kFewWarps - 1) / kFewWarps);
+    if (dtype == DFLASH_BF16)
+      return head_dim == 64 ? launch(few_rows_kernel<Bf16, 64>, grid, 32u * kFewWarps, stream, p)
+                            : launch(few_rows_kernel<Bf16, 128>, grid, 32u * kFewWarps, stream, p);
+    return head_dim == 64 ? launch(few_rows_kernel<F16, 64>, grid, 32u * kFewWarps, stream, p)
+                          : launch(few_rows_kernel<F16, 128>, grid, 32u * kFewWarps, stream, p);
+  }
   const PackedList list = list_at(p.ws);
   uint8_t* flags = p.ws + list_bytes(p.q_tokens, p.B, kForwardRows);
   int e = launch(list_kernel, 1u, (unsigned)kListThreads, stream, p, list);

@@ -119,6 +119,53 @@ def test_rising_scores(dv, dtype):
     check(out, lse, None, q, k, v, do, [n], [n], 1.0, False)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("cq,ck,Hq,Hk,D,causal", [
+    ([1], None, 8, 1, 64, True), ([33], None, 10, 2, 128, True), ([64], None, 64, 8, 64, True), ([65], None, 5, 1, 128, True),
+    ([64], None, 65, 5, 128, False), ([1] * 63, None, 4, 2, 64, True), ([1] * 64, None, 4, 2, 128, True),
+    ([3, 0, 17, 9], [20, 5, 1, 38], 6, 3, 128, True), ([2, 40, 0], [0, 31, 33], 4, 4, 64, False)])
+def test_few_words(dv, cq, ck, Hq, Hk, D, causal, dtype):
+    """Short prompts, at the sizes at which another kernel takes over, between rows of no sequence."""
+    nq, nk = sum(cq) + 3, sum(ck or cq) + 3
+    q, k, v, do = inputs(nq + Hq, nq, nk, Hq, Hk, D, dtype)
+    for t in (q, k, v):
+        t[:1], t[-2:] = math.nan, math.inf
+    qs, ks = starts(cq, 1), starts(ck or cq, 1)
+    status = torch.zeros(1, device=DEV, dtype=torch.int32)
+
+    def run():
+        return dv.packed_attention(q, k, v, qs, kv_start=ks, causal=causal, return_lse=True, status=status)
+
+    out, lse = run()
+    check(out, lse, None, q, k, v, do, cq, ck or cq, D ** -0.5, causal, 1, 1)
+    for rows in (slice(0, 1), slice(-2, None)):
+        assert not out[rows].any() and (lse[rows] == -math.inf).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse) and int(status) == 0
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_few_words_beside_values_that_are_not_seen(dv, bad):
+    q, k, v, do = inputs(4, 50, 50, 4, 2, 64, BF)
+    clean, lse = dv.packed_attention(q, k, v, starts([20, 10, 20]), return_lse=True)
+    k[20:30], v[20:30], q[20:30], v[45, 1, 5] = bad, bad, bad, bad
+    out, lse2 = dv.packed_attention(q, k, v, starts([20, 10, 20]), return_lse=True)
+    same = torch.ones((50, 4, 64), device=DEV, dtype=torch.bool)
+    same[20:30], same[45:, 2:, 5] = False, False
+    assert torch.equal(out[same], clean[same]) and torch.equal(lse2[:20], lse[:20]) and torch.equal(lse2[30:], lse[30:])
+    hit = out[45:, 2:, 5].float()
+    assert hit.isnan().all() if math.isnan(bad) else (hit == bad).all()
+
+
 def test_strides_and_fused_projections(dv):
     g = torch.Generator(device=DEV)
     g.manual_seed(6)
