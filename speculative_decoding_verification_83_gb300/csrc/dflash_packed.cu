@@ -365,45 +365,42 @@ __global__ void __launch_bounds__(32 * kWarps)
 // no order among themselves, which no result depends on.
 constexpr int kListThreads = 1024, kBuckets = 1024;
 __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int rows, const PackedList& list) {
-  __shared__ int before[kMaxBatch + 1], bucket[kBuckets];
-  __shared__ long long warp_sum_[32];  // (offsets that do not ascend may name every row in every sequence)
+  __shared__ int before[kMaxBatch], warp_sum_[32], bucket[kBuckets];
   const int32_t *sa = keys ? p.kv_start : p.q_start, *sb = keys ? p.q_start : p.kv_start;
   const int ta = keys ? p.kv_tokens : p.q_tokens, tb = keys ? p.q_tokens : p.kv_tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
-  // units before each sequence
-  long long done = 0;
+  // units before each sequence (2^28 at most, where offsets name every row in every sequence)
+  int done = 0;
   for (int b0 = 0; b0 < p.B; b0 += kListThreads) {
     const int b = b0 + tid;
-    long long mine = 0;
+    int mine = 0;
     if (b < p.B) {
       int first, n;
       extent(sb, tb, b, first, n, bad);
       extent(sa, ta, b, first, n, bad);
       mine = (n + rows - 1) / rows;
     }
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(kAll, incl, o);
+      const int v = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += v;
     }
     if (lane == 31) warp_sum_[warp] = incl;
     __syncthreads();
-    long long pre = 0, all = 0;
+    int pre = 0, all = 0;
     for (int w = 0; w < 32; ++w) {
       if (w < warp) pre += warp_sum_[w];
       all += warp_sum_[w];
     }
-    if (b < p.B) before[b] = (int)min(done + pre + incl - mine, 0x7fffffffll);
+    if (b < p.B) before[b] = done + pre + incl - mine;
     done += all;
     __syncthreads();
   }
   // offsets that do not ascend may name more units than the list holds
-  const int total = (int)min(done, (long long)most_units(ta, p.B, rows));
-  if (tid == 0) {
-    *list.count = total;
-  }
+  const int total = min(done, most_units(ta, p.B, rows));
+  if (tid == 0) *list.count = total;
   for (int i = tid; i < kBuckets; i += kListThreads) bucket[i] = 0;
   __syncthreads();
   auto unit_at = [&](int k, int& work) {
@@ -444,7 +441,7 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
     if (lane == 31) warp_sum_[warp] = incl;
     __syncthreads();
     int pre = 0;
-    for (int w = 0; w < warp; ++w) pre += (int)warp_sum_[w];
+    for (int w = 0; w < warp; ++w) pre += warp_sum_[w];
     bucket[tid] = pre + incl - mine;
   }
   __syncthreads();
