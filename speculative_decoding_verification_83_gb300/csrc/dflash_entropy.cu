@@ -16,8 +16,7 @@
 // in which the products want it), from which dW's rows of the piece and the
 // piece's part of dh follow. A row's g is often ruled by its label's entry, and one
 // rounding then decides the error of the whole row: what it leaves of that entry
-// is kept in fp32 and added to dh, and to dW where there are few rows (over many
-// rows such errors average out). dh is summed in fp32 over pieces, in up to kMaxSplits
+// is kept in fp32 and added to dh and dW. dh is summed in fp32 over pieces, in up to kMaxSplits
 // buffers where its tiles are too few to fill the SMs; every sum has a fixed
 // order.
 //
@@ -71,8 +70,8 @@ struct GemmParams {
   const RowGrad* rows;
   int label0;                // the piece's first vocabulary entry
   float* rest;               // per row: what rounding left of the label's entry
-  // kStoreBf16, with rest: rest_rows rows whose rest times their hidden state goes to their label's row
-  int rest_rows;
+  // kStoreBf16: every row's rest times its hidden state goes to its label's row
+  const int32_t* used;       // the labels of k rows, kDead: takes no part
   const unsigned char* h;
   long long h_stride;
   // kSumF32
@@ -81,11 +80,13 @@ struct GemmParams {
   uint32_t* status;
 };
 
+constexpr int kHits = 32;
 struct GemmShared {
   uint64_t full[kStages], empty[kStages];
   uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
   volatile int failed;
+  int hits[kEpiWarps][kHits];  // kStoreBf16: rows with their label in a warp's part of the tile, and which entry it is
 };
 constexpr size_t kGemmSmem = 1024 + (size_t)kStages * 2 * kOperandBytes + kEpiWarps * kStageOut;
 static_assert(kGemmSmem + sizeof(GemmShared) <= 232448, "one CTA's shared memory (227 KB)");
@@ -292,6 +293,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       [[maybe_unused]] RowGrad rg = {0.0f, 0.0f, 0.0f, kDead};
       if (kEpi == kStats && row < p.m) label = p.labels[row];
       if (kEpi == kLogitGrad && row < p.m) rg = p.rows[row];
+      // rows whose label is one of this warp's 32 entries, in order; 256 rows are looked at at a time
+      [[maybe_unused]] auto each_hit = [&](auto&& hit) {
+        for (int r0 = 0; r0 < p.k; r0 += 256) {
+          int at[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = r0 + 32 * e + lane;
+            at[e] = r < p.k ? p.used[r] - p.label0 - row0 : -1;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            for (uint32_t found = __ballot_sync(0xffffffffu, at[e] >= 0 && at[e] < 32); found; found &= found - 1) {
+              const int k = __ffs(found) - 1;
+              hit(r0 + 32 * e + k, __shfl_sync(0xffffffffu, at[e], k));
+            }
+        }
+      };
+      [[maybe_unused]] int hits = 0;
+      if constexpr (kEpi == kStoreBf16) {  // (while the products run)
+        each_hit([&](int r, int at) {
+          if (hits < kHits && lane == 0) S.hits[warp - 2][hits] = r << 5 | at;
+          ++hits;
+        });
+        __syncwarp();
+      }
       if (!__all_sync(0xffffffffu, wait_bar(&S.acc_full[lt & 1], (uint32_t)((lt >> 1) & 1), S))) {
         S.failed = 1;
         break;
@@ -399,18 +425,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           tc::ld32(acc + c + 32, x + 32);
           tc::wait_ld32(x);
           tc::wait_ld32(x + 32);
-          for (int r = 0; r < p.rest_rows; ++r)
-            if (p.rows[r].label == p.label0 + row && col0 + c < p.n) {
-              const float f = p.rest[r];
-              const uint32_t* src = reinterpret_cast<const uint32_t*>(p.h + 2 * (r * p.h_stride + col0 + c));
+          auto add_rest = [&](int r, int at) {
+            if (lane != at) return;
+            const float f = p.rest[r];
+            const uint4* src = reinterpret_cast<const uint4*>(p.h + 2 * (r * p.h_stride + col0 + c));
+            uint4 u[8];
 #pragma unroll
-              for (int e = 0; e < 64; e += 2)
-                if (col0 + c + e < p.n) {
-                  const float2 v = Bf16::unpack(src[e / 2]);
-                  x[e] = __float_as_uint(fmaf(f, v.x, __uint_as_float(x[e])));
-                  x[e + 1] = __float_as_uint(fmaf(f, v.y, __uint_as_float(x[e + 1])));
-                }
+            for (int i = 0; i < 8; ++i) u[i] = col0 + c + 8 * i < p.n ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float v[8];
+              unpack8<Bf16>(u[i], v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[8 * i + e] = __float_as_uint(fmaf(f, v[e], __uint_as_float(x[8 * i + e])));
             }
+          };
+          if (hits <= kHits)
+            for (int i = 0; i < hits; ++i) add_rest(S.hits[warp - 2][i] >> 5, S.hits[warp - 2][i] & 31);
+          else
+            each_hit(add_rest);
           if (col0 + c < p.n && row0 < p.m)
             staged(
                 [&] {
@@ -670,7 +703,8 @@ __global__ void __launch_bounds__(1024)
 // What each row's gradient is computed from, and the hidden states with the rows
 // that take no part set to 0 (their values may be anything, and 0 times anything
 // may not be 0 in dW). One block a row.
-__global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGrad* rows, float* rest, uint16_t* h_used) {
+__global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGrad* rows, float* rest, int32_t* used,
+                                                   uint16_t* h_used) {
   const int r = blockIdx.x, label = p.labels[r];
   const float u = (p.upstream ? p.upstream[(long long)r * p.upstream_stride] : 1.0f);
   const float weight = p.weight ? p.weight[r] : 1.0f;
@@ -682,6 +716,7 @@ __global__ void __launch_bounds__(128) rows_kernel(const EntropyParams p, RowGra
     if (dead) x = {0.0f, 0.0f, 0.0f, kDead};
     rows[r] = x;
     rest[r] = 0.0f;
+    used[r] = x.label;
   }
   if (!h_used) return;
   const uint4* src = reinterpret_cast<const uint4*>(p.h + 2 * (long long)r * p.h_stride);
@@ -717,7 +752,6 @@ __global__ void __launch_bounds__(256) hidden_kernel(const EntropyParams p, cons
 // ---- workspaces
 constexpr long long kPieceBytes = 512ll << 20;  // of g at a time
 constexpr int kMaxSplits = 8;
-constexpr int kFewRows = 64;  // whose labels' rests also go to dW
 constexpr int kPairs = 76;  // the splits' rule goes by a whole GPU's pairs of SMs
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -743,7 +777,7 @@ ForwardPlan forward_plan(int rows, int V) {
 struct BackwardPlan {
   int piece, pitch, splits;  // vocabulary entries of a piece, of a row of g
   int split_rows;            // rows of a split's sums: whole stores
-  size_t rows, rest, h, g, sums, bytes;
+  size_t rows, rest, used, h, g, sums, bytes;
 };
 BackwardPlan backward_plan(int rows, int V, int K) {
   BackwardPlan b;
@@ -767,7 +801,8 @@ BackwardPlan backward_plan(int rows, int V, int K) {
   b.split_rows = (rows + 31) / 32 * 32;
   b.rows = 0;
   b.rest = up((size_t)rows * sizeof(RowGrad));
-  b.h = b.rest + up((size_t)rows * sizeof(float));
+  b.used = b.rest + up((size_t)rows * sizeof(float));
+  b.h = b.used + up((size_t)rows * sizeof(int32_t));
   b.g = b.h + up((size_t)rows * K * 2);
   b.sums = b.g + up((size_t)rows * b.pitch * 2);
   b.bytes = b.sums + up((size_t)b.splits * b.split_rows * K * sizeof(float));
@@ -873,8 +908,9 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream) {
   const cudaStream_t st = (cudaStream_t)stream;
   RowGrad* rows = reinterpret_cast<RowGrad*>(p.ws + b.rows);
   float* rest = reinterpret_cast<float*>(p.ws + b.rest);
+  int32_t* used = reinterpret_cast<int32_t*>(p.ws + b.used);
   unsigned char *h_used = p.ws + b.h, *g_mem = p.ws + b.g, *sums = p.ws + b.sums;
-  rows_kernel<<<(unsigned)p.rows, 128, 0, st>>>(p, rows, rest, p.dw ? reinterpret_cast<uint16_t*>(h_used) : nullptr);
+  rows_kernel<<<(unsigned)p.rows, 128, 0, st>>>(p, rows, rest, used, p.dw ? reinterpret_cast<uint16_t*>(h_used) : nullptr);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return (int)e;
   CUtensorMap h, w, w_mn, hu, sum;
@@ -913,10 +949,9 @@ int launch_entropy_grad(const EntropyParams& p, int sms, void* stream) {
       d.n = p.K;
       d.k = p.rows;
       d.n_fast = 1;
-      d.rows = rows;
       d.label0 = v0;
       d.rest = rest;
-      d.rest_rows = p.rows <= kFewRows ? p.rows : 0;
+      d.used = used;
       d.h = p.h;
       d.h_stride = p.h_stride;
       e = launch_gemm<true, true, kStoreBf16>(g_mn, hu, dw, d, sms, st);

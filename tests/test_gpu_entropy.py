@@ -128,13 +128,13 @@ def test_strides(dv):
     assert torch.equal(c[0], a[1]) and torch.equal(c[1], a[2])
 
 
-@pytest.mark.parametrize("N", [1, 5, 64])
+@pytest.mark.parametrize("N", [1, 5, 64, 65, 600])
 def test_the_label_s_entry_is_not_rounded(dv, N):
     """A label's entry of the logits' gradients rules its row of both gradients: there the bound is that of the
     definition without the half step of bf16 of this entry."""
     V, K = 600, 64
     h, w, _, weight, up = inputs(9, N, V, K)
-    labels = torch.arange(N, device=DEV, dtype=torch.int32) * 9
+    labels = torch.arange(N, device=DEV, dtype=torch.int32) * 389 % V  # (no label twice)
     w *= 2.0 ** -6
     w[labels.long()] *= 2.0 ** 6
     h *= 2.0 ** -4
@@ -149,6 +149,13 @@ def test_the_label_s_entry_is_not_rounded(dv, N):
     edw[ids] -= u * entry.abs()[:, None] * h.double().abs()
     assert ((dh.double() - r[2]).abs() <= refs.rounded(r[2], edh, BF)).all()
     assert ((dw.double() - r[4]).abs() <= refs.rounded(r[4], edw, BF)).all()
+
+
+def test_many_rows_of_few_labels(dv):
+    """One label, and two beside each other, for hundreds of rows."""
+    h, w, labels, weight, up = inputs(10, 700, 300, 72)
+    for ids in (torch.full((700,), 299, device=DEV, dtype=torch.int32), 31 + labels % 2):
+        check(dv, h, w, ids.to(torch.int32), weight, up)
 
 
 @pytest.mark.parametrize("N,V,K", [(1, 40000, 72), (31, 4095, 2056), (32, 40001, 1024), (32, 1, 8), (33, 40001, 1032)])
