@@ -276,7 +276,7 @@ def _attention_function():
 
     def backward(ctx, dout, _):
         a = ctx.call
-        _, _, _, _, _, out, lse, low, _ = ctx.saved_tensors
+        _, _, _, _, _, out, lse, low = ctx.saved_tensors
         lib, dev, D = _ops._library(), a.device, a.dim
         q, pq, qt, qh, n, hq = a.q
         _, pk, kt, kh, m, hk = a.k
@@ -296,7 +296,8 @@ def _attention_function():
         def forward(ctx, q, k, v, q_start, kv_start, scale, causal, status):
             ctx.call = a = _Packed(q, k, v, q_start, kv_start, scale, causal, status)
             out, lse, low = a.forward(True, True)
-            ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, low, status)
+            ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, low)
+            ctx.status = status  # (kept alive; its owner may reset it between the passes)
             ctx.mark_non_differentiable(lse)
             return out, lse
 
@@ -373,7 +374,7 @@ def _entropy_function():
 
     def backward(ctx, upstream):
         head, word = ctx.call
-        h, weight, _, _, stats, _ = ctx.saved_tensors
+        h, weight, _, _, stats = ctx.saved_tensors
         lib, dev, N = _ops._library(), h.device, head[4]
         need = ctx.needs_input_grad
         dh = h.new_empty(h.shape) if need[0] else None
@@ -394,7 +395,8 @@ def _entropy_function():
             head = _entropy_args(h, weight, labels, row_weight)
             loss, stats, word = _entropy(h, head, status, True)
             ctx.call = head, word
-            ctx.save_for_backward(h, weight, labels, row_weight, stats, status)
+            ctx.save_for_backward(h, weight, labels, row_weight, stats)
+            ctx.status = status  # (see PackedAttention)
             return loss
 
     LinearCrossEntropy.backward = _once(backward)

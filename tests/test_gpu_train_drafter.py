@@ -107,3 +107,21 @@ def test_serving_agrees_with_packed_sequences(ex):
 def test_example_runs(ex):
     report = ex.run(counts=(40, 9), steps=2)
     assert len(report) == 2 and all(0 < x < 100 for x in report)
+
+
+def test_a_status_word_may_be_reset_between_the_passes(ex):
+    """The word is its owner's: read and reset after the forward passes, it still takes the backward passes' reports."""
+    dv, g = ex.dv, torch.Generator(device="cuda")
+    g.manual_seed(4)
+    q, k, v = (torch.randn((40, 2, 64), generator=g, device="cuda").bfloat16().requires_grad_(True) for _ in range(3))
+    w = torch.randn((50, 128), generator=g, device="cuda").bfloat16().requires_grad_(True)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 30, 45], dtype=torch.int32, device="cuda")  # past the end: reported by either pass
+    out = dv.packed_attention(q, k, v, starts, status=status)
+    assert int(status) == dv.STATUS_BAD_LENGTH
+    status.zero_()
+    loss = dv.linear_cross_entropy(out.flatten(1), w, torch.arange(40, dtype=torch.int32, device="cuda"), status=status)
+    assert int(status) == 0
+    status.zero_()
+    loss.sum().backward()
+    assert int(status) == dv.STATUS_BAD_LENGTH and all(t.grad.isfinite().all() for t in (q, k, v, w))
