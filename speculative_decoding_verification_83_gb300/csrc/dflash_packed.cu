@@ -363,16 +363,17 @@ __global__ void __launch_bounds__(32 * kWarps)
 // The list of units: counted and sorted by one block. Work goes by how many of the
 // other array's rows the unit's last (queries) or first (keys) row meets; units of equal work keep
 // no order among themselves, which no result depends on.
-constexpr int kListThreads = 1024, kBuckets = 1024;
+constexpr int kListThreads = 1024, kPrepareThreads = 512, kBuckets = 1024;
+template <int kN>  // threads
 __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int rows, const PackedList& list) {
-  __shared__ int before[kMaxBatch], warp_sum_[32], bucket[kBuckets];
+  __shared__ int before[kMaxBatch], warp_sum_[kN / 32], bucket[kBuckets];
   const int32_t *sa = keys ? p.kv_start : p.q_start, *sb = keys ? p.q_start : p.kv_start;
   const int ta = keys ? p.kv_tokens : p.q_tokens, tb = keys ? p.q_tokens : p.kv_tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
   // units before each sequence (2^28 at most, where offsets name every row in every sequence)
   int done = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kListThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += kN) {
     const int b = b0 + tid;
     int mine = 0;
     if (b < p.B) {
@@ -390,7 +391,7 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
     if (lane == 31) warp_sum_[warp] = incl;
     __syncthreads();
     int pre = 0, all = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < kN / 32; ++w) {
       if (w < warp) pre += warp_sum_[w];
       all += warp_sum_[w];
     }
@@ -401,7 +402,7 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
   // offsets that do not ascend may name more units than the list holds
   const int total = min(done, most_units(ta, p.B, rows));
   if (tid == 0) *list.count = total;
-  for (int i = tid; i < kBuckets; i += kListThreads) bucket[i] = 0;
+  for (int i = tid; i < kBuckets; i += kN) bucket[i] = 0;
   __syncthreads();
   auto unit_at = [&](int k, int& work) {
     int lo = 0, hi = p.B;  // the last b with before[b] <= k
@@ -424,14 +425,17 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
     work = kBuckets - 1 - min(kBuckets - 1, (max(0, meets) + 127) / 128);  // most work: bucket 0
     return u;
   };
-  for (int k = tid; k < total; k += kListThreads) {
+  for (int k = tid; k < total; k += kN) {
     int work;
     unit_at(k, work);
     atomicAdd(&bucket[work], 1);
   }
   __syncthreads();
   {
-    const int mine = bucket[tid];
+    constexpr int kPer = kBuckets / kN;  // buckets of a thread, side by side
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) mine += bucket[tid * kPer + k];
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -440,12 +444,17 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
     }
     if (lane == 31) warp_sum_[warp] = incl;
     __syncthreads();
-    int pre = 0;
+    int pre = incl - mine;
     for (int w = 0; w < warp; ++w) pre += warp_sum_[w];
-    bucket[tid] = pre + incl - mine;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int n = bucket[tid * kPer + k];
+      bucket[tid * kPer + k] = pre;
+      pre += n;
+    }
   }
   __syncthreads();
-  for (int k = tid; k < total; k += kListThreads) {
+  for (int k = tid; k < total; k += kN) {
     int work;
     const PackedUnit u = unit_at(k, work);
     list.units[atomicAdd(&bucket[work], 1)] = u;
@@ -455,29 +464,29 @@ __device__ __noinline__ void build_list(const PackedParams& p, bool keys, int ro
 
 __global__ void __launch_bounds__(kListThreads) list_kernel(const PackedParams p, const PackedList list) {
   grid_dependency_sync();
-  build_list(p, false, kForwardRows, list);
+  build_list<kListThreads>(p, false, kForwardRows, list);
 }
 
 // What the gradients' kernels read: both lists (the first two blocks), and the rows'
 // statistics: delta, the sum over d of dout out, and lse, their signs reversed; behind
 // the last row a tile's worth of zeros. D / 8 lanes take four tokens of a head at a time,
 // whose loads are in flight together and whose statistics lie side by side (8192 tokens,
-// 32 heads of 128, 168 MB: 40 us, one token at a time 47).
+// 32 heads of 128, 168 MB: 38 us, one token at a time 47, 1024 threads a block 40).
 template <class T, int D>
-__global__ void __launch_bounds__(kListThreads, 1)
+__global__ void __launch_bounds__(kPrepareThreads, 2)
     grad_prepare_kernel(const PackedParams p, const PackedList queries, const PackedList keys) {
   constexpr unsigned kLanes = D / 8;  // 8 values each
   grid_dependency_sync();
   if (blockIdx.x < 2) {
-    build_list(p, blockIdx.x == 1, kGradRows, blockIdx.x ? keys : queries);
+    build_list<kPrepareThreads>(p, blockIdx.x == 1, kGradRows, blockIdx.x ? keys : queries);
     return;
   }
-  const long long id = (long long)(blockIdx.x - 2) * kListThreads + threadIdx.x;
+  const long long id = (long long)(blockIdx.x - 2) * kPrepareThreads + threadIdx.x;
   const unsigned lane = threadIdx.x % kLanes;
   const unsigned unit = (unsigned)(id / kLanes), head = unit % (unsigned)p.q_heads;  // (as many as rows / 4: below 2^32)
   const long long t0 = unit / (unsigned)p.q_heads * 4ll;
   const int spare = p.stat_pitch - p.q_tokens, left = (int)(p.q_tokens - t0 < 4 ? p.q_tokens - t0 : 4);
-  for (long long at = id; at < spare * 2ll * p.q_heads; at += (long long)(gridDim.x - 2) * kListThreads)
+  for (long long at = id; at < spare * 2ll * p.q_heads; at += (long long)(gridDim.x - 2) * kPrepareThreads)
     p.row_stats[at / spare * p.stat_pitch + p.q_tokens + at % spare] = 0.0f;
   uint4 a[4], g[4];
   uint2 l[4];
@@ -599,9 +608,9 @@ int launch_packed_grad(const PackedParams& p0, int head_dim, int sms, void* stre
   ws += list_bytes(p.kv_tokens, p.B, kGradRows);
   uint8_t* kv_flags = ws;
   const long long lanes = (p.q_tokens + 3ll) / 4 * p.q_heads * (head_dim / 8);
-  const unsigned blocks = 2u + (unsigned)((lanes + kListThreads - 1) / kListThreads);
-  int e = head_dim == 64 ? launch(grad_prepare_kernel<Bf16, 64>, blocks, (unsigned)kListThreads, stream, p, queries, keys)
-                         : launch(grad_prepare_kernel<Bf16, 128>, blocks, (unsigned)kListThreads, stream, p, queries, keys);
+  const unsigned blocks = 2u + (unsigned)((lanes + kPrepareThreads - 1) / kPrepareThreads);
+  int e = head_dim == 64 ? launch(grad_prepare_kernel<Bf16, 64>, blocks, (unsigned)kPrepareThreads, stream, p, queries, keys)
+                         : launch(grad_prepare_kernel<Bf16, 128>, blocks, (unsigned)kPrepareThreads, stream, p, queries, keys);
   if (!e && p.q_tokens) e = launch_dq_tc(p, head_dim, queries, q_flags, sms, stream);
   if (!e && p.kv_tokens) e = launch_dkv_tc(p, head_dim, keys, kv_flags, p.q_tokens > 0, sms, stream);
   if (e) return e;
