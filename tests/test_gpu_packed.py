@@ -289,6 +289,21 @@ def test_no_tokens(dv):
     assert not dk.any() and not dvv.any()
 
 
+def test_lse_beside_the_gradients(dv):
+    """With and without lse the gradients are the same; lse itself carries none."""
+    q, k, v, do = inputs(15, 70, 70, 4, 2, 64, BF)
+    for t in (q, k, v):
+        t.requires_grad_(True)
+    alone = dv.packed_attention(q, k, v, starts([70]))
+    out, lse = dv.packed_attention(q, k, v, starts([70]), return_lse=True)
+    assert torch.equal(out, alone) and not lse.requires_grad and lse.shape == (70, 4)
+    a, b = (torch.autograd.grad(o, (q, k, v), do) for o in (alone, out))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    out, lse = dv.packed_attention(q, k, v, starts([70]), return_lse=True)
+    (out.float().sum() + lse.sum()).backward()
+    assert q.grad.isfinite().all()
+
+
 def test_repeats_bit_for_bit_on_any_stream(dv):
     cq = [400, 33, 250]
     q, k, v, do = inputs(13, 683, 683, 8, 2, 128, BF)
