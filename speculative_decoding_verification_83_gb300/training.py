@@ -274,7 +274,9 @@ def _attention_function():
         return f
     torch = _ops._torch()
 
-    def backward(ctx, dout, _):
+    def backward(ctx, dout, _=None):
+        if dout is None:
+            return (None,) * 9
         a = ctx.call
         _, _, _, _, _, out, lse, low = ctx.saved_tensors
         lib, dev, D = _ops._library(), a.device, a.dim
@@ -289,15 +291,18 @@ def _attention_function():
                    pd, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                    _pack16(qt, qh, kt, kh, vt, vh, hq * D, D, dt, dh, hq * D, D, hk * D, D, hk * D, D), 1, ws.data_ptr(),
                    size, a.word, _ops._raw_stream(None, dev))
-        return dq, dk, dv, None, None, None, None, None
+        return dq, dk, dv, None, None, None, None, None, None
 
     class PackedAttention(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, v, q_start, kv_start, scale, causal, status):
+        def forward(ctx, q, k, v, q_start, kv_start, scale, causal, status, return_lse):
+            ctx.set_materialize_grads(False)  # (zeros for lse would be a launch)
             ctx.call = a = _Packed(q, k, v, q_start, kv_start, scale, causal, status)
             out, lse, low = a.forward(True, True)
             ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, low)
             ctx.status = status  # (kept alive; its owner may reset it between the passes)
+            if not return_lse:
+                return out
             ctx.mark_non_differentiable(lse)
             return out, lse
 
@@ -323,10 +328,9 @@ def packed_attention(q, k, v, q_start, kv_start=None, scale=None, causal=True, r
         if q.dtype != _ops._modules[0].bfloat16:
             raise TypeError(f"the packed attention has a gradient for bfloat16 only, got {q.dtype}: detach the inputs, "
                             "or call under torch.no_grad()")
-        out, lse = (_functions.get("attention") or _attention_function()).apply(q, k, v, q_start, kv_start, scale,
-                                                                                bool(causal), status)
-    else:
-        out, lse, _ = _Packed(q, k, v, q_start, kv_start, scale, causal, status).forward(return_lse, False)
+        return (_functions.get("attention") or _attention_function()).apply(q, k, v, q_start, kv_start, scale, bool(causal),
+                                                                            status, return_lse)
+    out, lse, _ = _Packed(q, k, v, q_start, kv_start, scale, causal, status).forward(return_lse, False)
     return (out, lse) if return_lse else out
 
 
