@@ -509,8 +509,8 @@ int dflash_distill_loss_grad(const void* student, int64_t row_stride, int rows, 
  * head_dim] (bf16 or f16): y = R(n) (x w / sqrt(mean x^2 + eps)), R the rotation of
  * dflash_kv_append by the token's position n = positions[token] ([device] int32,
  * any sign), all in fp32, rounded once. 0 heads: that array is left out.
- * head_dim 64, 128 or 256; weights as for dflash_kv_append_norm; rot_dim a
- * multiple of 16, 0 for no rotation. strides [host]: token and head stride of q,
+ * head_dim 64, 128 or 256; tokens <= 2^30; weights as for dflash_kv_append_norm;
+ * rot_dim a multiple of 16, 0 for no rotation. strides [host]: token and head stride of q,
  * k, q_out, k_out, in elements, multiples of 16 bytes. q_out may be q, k_out k. */
 int dflash_norm_rotate(const void* q, const void* k, void* q_out, void* k_out, int dtype, int tokens, int q_heads,
                        int k_heads, int head_dim, const int64_t* strides, const void* q_weight, const void* k_weight,

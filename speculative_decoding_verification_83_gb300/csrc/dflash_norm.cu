@@ -381,7 +381,8 @@ int backward(const NormParams& p, void* stream) {
   constexpr int kSmem = kGradSlots * 4 * kThreads * 16;
   int e = allow(norm_grad_kernel<T, D>, kSmem, ready);
   if (e) return e;
-  const int groups = (p.tokens + kGroup - 1) / kGroup, blocks = groups < kNormBlocks ? groups : kNormBlocks;
+  const int groups = p.tokens ? (p.tokens + kGroup - 1) / kGroup : 1;  // (without tokens the weights' gradients are 0)
+  const int blocks = groups < kNormBlocks ? groups : kNormBlocks;
   e = launch(norm_grad_kernel<T, D>, blocks, kThreads, kSmem, stream, p);
   if (e || !(p.gq_weight || p.gk_weight)) return e;
   return launch(norm_weights_kernel<T, D>, 2 * D / 32, 1024, 0, stream, p, blocks);

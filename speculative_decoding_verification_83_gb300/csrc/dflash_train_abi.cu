@@ -88,7 +88,8 @@ int bind_norm(int dtype, int tokens, int q_heads, int k_heads, int head_dim, con
   if (tokens < 0) return fail(DFLASH_ERR_INVALID_ARG, "tokens=%d must not be negative", tokens);
   if (q_heads < 0 || k_heads < 0 || q_heads + (long long)k_heads < 1)
     return fail(DFLASH_ERR_INVALID_ARG, "q_heads=%d and k_heads=%d must not be negative, and not both 0", q_heads, k_heads);
-  // a block's rows (4 tokens) and all rows are counted in 32 bits
+  if (tokens > 1 << 30) return fail(DFLASH_ERR_UNSUPPORTED, "tokens=%d is more than 2^30", tokens);
+  // a block's rows (4 tokens) are counted in 32 bits
   if (q_heads + (long long)k_heads > 1 << 20)
     return fail(DFLASH_ERR_UNSUPPORTED, "%lld heads are more than a token may have", q_heads + (long long)k_heads);
   if (weight_dtype != dtype && weight_dtype != DFLASH_F32)
@@ -217,6 +218,7 @@ int dflash_norm_rotate_grad(const void* q, const void* k, const void* dq_out, co
        (rc = bind_rows(dk_out, strides + 6, tokens, k_heads, head_dim, "dk_out", &p.dk)) ||
        (rc = bind_rows(dk, strides + 10, tokens, k_heads, head_dim, "dk", &p.ko))))
     return rc;
+  if (tokens == 0) p.rot = 0;  // (the weights' gradients are 0, without positions and phases)
   p.gq_weight = dq_weight;
   p.gk_weight = dk_weight;
   p.partial = static_cast<float*>(workspace);

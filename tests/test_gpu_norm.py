@@ -104,6 +104,28 @@ def test_no_tokens(dv):
     assert out.shape == (0, 4, 64) and dq.shape == (0, 4, 64) and not dw.any()
 
 
+def test_gradients_of_no_tokens_by_the_library(dv):
+    """No tokens, positions or phases: the weights' gradients are 0."""
+    lib = dv.load()
+    gw = [torch.full((128,), 7.0, device=DEV) for _ in range(2)]
+    w = torch.ones(128, device=DEV)
+    size = lib.dflash_norm_workspace_bytes(128)
+    ws = torch.empty(size, device=DEV, dtype=torch.uint8)
+    code = lib.dflash_norm_rotate_grad(None, None, None, None, None, None, dv.DFLASH_BF16, 0, 4, 2, 128, None, w.data_ptr(),
+                                       w.data_ptr(), gw[0].data_ptr(), gw[1].data_ptr(), dv.DFLASH_F32, 1e-6, None, None, 64,
+                                       0, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    assert code == dv.OK and not gw[0].any() and not gw[1].any()
+
+
+def test_many_heads(dv):
+    """A token's heads are found by a multiplication: at counts where 32 bits would not do for it."""
+    q = torch.randn((3, 40001, 64), device=DEV).to(BF)
+    w = torch.ones(64, device=DEV)
+    out, _ = dv.norm_rotate(q, None, w)
+    want = q.double() * torch.rsqrt(q.double().square().mean(-1, keepdim=True) + 1e-6)
+    assert ((out.double() - want).abs() <= refs.rounded(want, 32 * refs.F32 * want.abs(), BF)).all()
+
+
 def test_strides_broadcast_inputs_and_upstream(dv):
     g = torch.Generator(device=DEV)
     g.manual_seed(4)

@@ -39,7 +39,7 @@ def norm_grad(lib, q=P, k=P, qo=P, ko=P, dtype=0, tokens=2, hq=4, hk=2, dim=128,
 @pytest.mark.parametrize("kw,code,word", [
     (dict(dtype=dv.DFLASH_F32), 1, "dtype"), (dict(dtype=7), 1, "dtype"), (dict(dim=96), 2, "head_dim"),
     (dict(dim=512), 2, "head_dim"), (dict(tokens=-1), 1, "tokens"), (dict(hq=0, hk=0), 1, "heads"), (dict(hk=-1), 1, "heads"),
-    (dict(hq=1 << 20), 2, "heads"), (dict(wtype=dv.DFLASH_F16), 1, "weight_dtype"), (dict(wq=ODD), 1, "weights"),
+    (dict(hq=1 << 20), 2, "heads"), (dict(tokens=(1 << 30) + 1), 2, "tokens"), (dict(wtype=dv.DFLASH_F16), 1, "weight_dtype"), (dict(wq=ODD), 1, "weights"),
     (dict(eps=-1.0), 1, "eps"), (dict(eps=float("nan")), 1, "eps"), (dict(eps=float("inf")), 1, "eps"),
     (dict(rot=24), 2, "rot_dim"), (dict(rot=144), 2, "rot_dim"), (dict(phases=None), 1, "phases"), (dict(pos=None), 1, "positions"),
     (dict(q=None), 1, "null q"), (dict(k=ODD), 1, "k must"), (dict(strides=(768, 128, 768, 100) + (512, 128) * 2), 1, "k: strides"),
