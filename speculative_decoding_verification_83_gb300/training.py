@@ -94,10 +94,20 @@ def _needs_graph(*tensors):
     return False
 
 
+def _lies(t, bound):
+    """Whether a [tokens, heads, dim] tensor lies where _heads found it."""
+    return t is None or (t.data_ptr(), *t.stride()[:2]) == bound[1:4]
+
+
+def _at(t, pointer):
+    return t is None or t.data_ptr() == pointer
+
+
 # ---- norms with rotation -----------------------------------------------------------------
 class _Norm:
-    """What a call and its backward pass hand to the library: pointers into tensors that the caller (and autograd)
-    keep."""
+    """What a call and its backward pass hand to the library. The forward call's tensors are handed over to autograd,
+    which frees them after the backward pass, and may hand back others in their place (checkpointing, offloading):
+    the pointers hold while the tensors lie where they lay."""
     __slots__ = ("q", "k", "tokens", "code", "dim", "weights", "eps", "turn", "device")
 
     def __init__(self, q, k, q_weight, k_weight, positions, phases, interleaved, eps):
@@ -124,6 +134,15 @@ class _Norm:
             self.turn = (_ops._vector(positions, n, "positions", torch.int32, self.device),
                          _ops._vector(phases, half, "phases", torch.int64, self.device), 2 * half, 1 if interleaved else 0)
 
+    def holds(self, q, k, q_weight, k_weight, positions, phases):
+        return (_lies(q, self.q) and _lies(k, self.k) and _at(q_weight, self.weights[0]) and _at(k_weight, self.weights[1])
+                and (phases is None or _at(phases, self.turn[1]) and _at(positions, self.turn[0])))
+
+    def hand_over(self):
+        tensors = self.q[0], self.k[0]
+        self.q, self.k = (None, *self.q[1:]), (None, *self.k[1:])
+        return tensors
+
     def forward(self):
         D = self.dim
         q, pq, qt, qh, n, hq = self.q
@@ -149,10 +168,13 @@ def _norm_function():
 
     def backward(ctx, dq_out, dk_out):
         a = ctx.call
-        _, _, q_weight, k_weight, _, _ = ctx.saved_tensors  # (and nothing has been written over since)
+        q, k, q_weight, k_weight, positions, phases = ctx.saved_tensors  # (and nothing has been written over since)
+        if not a.holds(q, k, q_weight, k_weight, positions, phases):
+            a = _Norm(q, k, q_weight, k_weight, positions, phases, a.turn[3], a.eps)
+            q, k = a.q[0], a.k[0]
         D, dev = a.dim, a.device
-        q, pq, qt, qh, n, hq = a.q
-        k, pk, kt, kh, _, hk = a.k
+        _, pq, qt, qh, n, hq = a.q
+        _, pk, kt, kh, _, hk = a.k
         dq = dk = gq = gk = None
         pdq = pdk = pgq = pgk = None
         gqt = gqh = gkt = gkh = 0
@@ -186,8 +208,9 @@ def _norm_function():
         @staticmethod
         def forward(ctx, q, k, q_weight, k_weight, positions, phases, interleaved, eps):
             ctx.call = a = _Norm(q, k, q_weight, k_weight, positions, phases, interleaved, eps)
-            ctx.save_for_backward(q, k, q_weight, k_weight, positions, phases)
-            return a.forward()
+            outs = a.forward()
+            ctx.save_for_backward(*a.hand_over(), q_weight, k_weight, positions, phases)
+            return outs
 
     NormRotate.backward = _once(backward)
     _functions["norm"] = NormRotate
@@ -251,6 +274,15 @@ class _Packed:
         self.batch = _Batch(s, t, n - 1, nq, nk, hq, hk, D, code, 1 if causal else 0, D ** -0.5 if scale is None else scale)
         self.ref, self.device, self.word = ctypes.byref(self.batch), dev, _ops._status_word(status, dev)
 
+    def holds(self, q, k, v, q_start, kv_start):
+        return (_lies(q, self.q) and _lies(k, self.k) and _lies(v, self.v) and _at(q_start, self.batch.q_start)
+                and _at(kv_start, self.batch.kv_start))
+
+    def hand_over(self):
+        tensors = self.q[0], self.k[0], self.v[0]
+        self.q, self.k, self.v = (None, *self.q[1:]), (None, *self.k[1:]), (None, *self.v[1:])
+        return tensors
+
     def forward(self, keep, train):
         torch, lib = _ops._modules
         dev, D = self.device, self.dim
@@ -278,9 +310,12 @@ def _attention_function():
         if dout is None:
             return (None,) * 9
         a = ctx.call
-        _, _, _, _, _, out, lse, low = ctx.saved_tensors
+        q, k, v, q_start, kv_start, out, lse, low = ctx.saved_tensors
+        if not a.holds(q, k, v, q_start, kv_start):
+            a = _Packed(q, k, v, q_start, kv_start, a.batch.scale, a.batch.causal, ctx.status)
+            q = a.q[0]
         lib, dev, D = _ops._library(), a.device, a.dim
-        q, pq, qt, qh, n, hq = a.q
+        _, pq, qt, qh, n, hq = a.q
         _, pk, kt, kh, m, hk = a.k
         _, pv, vt, vh, _, _ = a.v
         dout, pd, dt, dh = _usable(dout, q)
@@ -299,7 +334,7 @@ def _attention_function():
             ctx.set_materialize_grads(False)  # (zeros for lse would be a launch)
             ctx.call = a = _Packed(q, k, v, q_start, kv_start, scale, causal, status)
             out, lse, low = a.forward(True, True)
-            ctx.save_for_backward(q, k, v, q_start, kv_start, out, lse, low)
+            ctx.save_for_backward(*a.hand_over(), q_start, kv_start, out, lse, low)
             ctx.status = status  # (kept alive; its owner may reset it between the passes)
             if not return_lse:
                 return out
@@ -378,7 +413,10 @@ def _entropy_function():
 
     def backward(ctx, upstream):
         head, word = ctx.call
-        h, weight, _, _, stats = ctx.saved_tensors
+        h, weight, labels, row_weight, stats = ctx.saved_tensors
+        if not ((h.data_ptr(), h.stride(0), weight.data_ptr(), weight.stride(0)) == head[:4] and _at(labels, head[7])
+                and _at(row_weight, head[8])):
+            head = _entropy_args(h, weight, labels, row_weight)
         lib, dev, N = _ops._library(), h.device, head[4]
         need = ctx.needs_input_grad
         dh = h.new_empty(h.shape) if need[0] else None

@@ -2,6 +2,7 @@
 against the same network in 64 bits, and the same layer serving from a paged cache."""
 import os
 import sys
+import weakref
 
 import pytest
 
@@ -125,3 +126,53 @@ def test_a_status_word_may_be_reset_between_the_passes(ex):
     status.zero_()
     loss.sum().backward()
     assert int(status) == dv.STATUS_BAD_LENGTH and all(t.grad.isfinite().all() for t in (q, k, v, w))
+
+
+def test_inputs_are_freed_after_the_backward_pass(ex):
+    """A result that is kept keeps no inputs, once the backward pass is done; retained graphs go back twice."""
+    dv, g = ex.dv, torch.Generator(device="cuda")
+    g.manual_seed(5)
+    leaf = torch.randn((40, 4, 64), generator=g, device="cuda").bfloat16().requires_grad_(True)
+    starts = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    calls = {"norm": lambda x: dv.norm_rotate(x)[0], "attention": lambda x: dv.packed_attention(x, x, x, starts),
+             "attention of strided heads": lambda x: dv.packed_attention(x[:, :2], x[:, 2:].expand(40, 2, 64), x[:, 2:], starts),
+             "entropy": lambda x: dv.linear_cross_entropy(x.flatten(1), x.flatten(1), starts[:1].expand(40).contiguous())}
+    for name, call in calls.items():
+        x = leaf * 2
+        out = call(x)
+        gone = weakref.ref(x)
+        a, = torch.autograd.grad(out.float().sum(), leaf, retain_graph=True)
+        b, = torch.autograd.grad(out.float().sum(), leaf)
+        del x
+        assert gone() is None and torch.equal(a, b) and a.any(), name
+
+
+@pytest.mark.parametrize("way", ["checkpoint", "offload"])
+def test_tensors_that_autograd_keeps_elsewhere(ex, way):
+    """Checkpointing computes the saved tensors again, offloading brings copies back: the gradients follow them, not the
+    places of the forward pass."""
+    from torch.utils.checkpoint import checkpoint
+
+    dv, g = ex.dv, torch.Generator(device="cuda")
+    g.manual_seed(6)
+    leaf = torch.randn((40, 6, 64), generator=g, device="cuda").bfloat16().requires_grad_(True)
+    base = torch.rand(64, generator=g, device="cuda") + 0.5
+    phases = dv.rope_phases(1e4 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64), "cuda")
+
+    def net(x):
+        x = x * 2  # what follows is the checkpoint's own
+        pos = torch.arange(40, dtype=torch.int32, device="cuda") * 3
+        q, k = dv.norm_rotate(x[:, :2], x[:, 2:4], base * 1.5, base * 0.5, pos, phases=phases)
+        out = dv.packed_attention(q, k, x[:, 4:] * 1, torch.tensor([0, 25, 40], device="cuda", dtype=torch.int32))
+        labels = torch.arange(40, device="cuda", dtype=torch.int32) % 30
+        return dv.linear_cross_entropy(out.flatten(1), x.flatten(1)[:30, :128], labels, row_weight=base[:40] * 2)
+
+    want, = torch.autograd.grad(net(leaf).sum(), leaf)
+    if way == "checkpoint":
+        loss = checkpoint(net, leaf, use_reentrant=False)
+    else:
+        with torch.autograd.graph.save_on_cpu():
+            loss = net(leaf)
+    junk = [torch.full((40, 6, 64), 1e4, device="cuda", dtype=torch.bfloat16) for _ in range(20)]  # where they lay
+    got, = torch.autograd.grad(loss.sum(), leaf)
+    assert torch.equal(got, want) and want.any() and len(junk) == 20
