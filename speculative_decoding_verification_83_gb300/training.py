@@ -63,13 +63,13 @@ def _heads(t, name, dim, like):
 
 def _usable(g, like):
     """An upstream gradient as the kernels read it, (itself, data pointer, token stride, head stride): autograd may
-    hand over any strides."""
+    hand over any strides, and a contiguous part of another gradient that begins anywhere."""
     ts, hs, one = g.stride()
     dim = g.shape[2]
     if g.dtype != like.dtype:
         g = g.to(like.dtype).contiguous()
     elif one != 1 or ts < dim or hs < dim or ts % 8 or hs % 8 or g.data_ptr() % 16:
-        g = g.contiguous()
+        g = g.clone(memory_format=_ops._modules[0].contiguous_format)
     else:
         return g, g.data_ptr(), ts, hs
     return (g, g.data_ptr(), *g.stride()[:2])
