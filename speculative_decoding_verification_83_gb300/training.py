@@ -455,8 +455,8 @@ def linear_cross_entropy(hidden, weight, labels, row_weight=None, status=None):
     differentiable in ``hidden`` and ``weight``."""
     if not _FLOATS:
         _setup()
-    if row_weight is not None and row_weight.requires_grad:
-        raise ValueError("row_weight has no gradient here: detach it")
+    if _needs_graph(row_weight):
+        raise ValueError("row_weight has no gradient here: detach it, or call under torch.no_grad()")
     if _needs_graph(hidden, weight):
         return (_functions.get("entropy") or _entropy_function()).apply(hidden, weight, labels, row_weight, status)
     return _entropy(hidden, _entropy_args(hidden, weight, labels, row_weight), status, False)[0]

@@ -46,3 +46,12 @@ def test_attention(dv, lead):
     whole, up = joined(lead, [dv.packed_attention(*leaves, start)], [do])
     got = torch.autograd.grad(whole, leaves, up)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_row_weights_that_are_learned(dv):
+    h, w = torch.randn((40, 64), device=DEV).to(BF), torch.randn((300, 64), device=DEV).to(BF)
+    labels = torch.arange(40, device=DEV, dtype=torch.int32)
+    weight = torch.rand(40, device=DEV)
+    want = dv.linear_cross_entropy(h, w, labels, row_weight=weight)
+    with torch.no_grad():
+        assert torch.equal(dv.linear_cross_entropy(h, w, labels, row_weight=weight.clone().requires_grad_(True)), want)

@@ -26,3 +26,14 @@ def test_upstream_gradients_anywhere_in_memory(shape, first):
     assert (ts, hs) == got.stride()[:2] and got.stride(2) == 1
     if g.data_ptr() % 16 == 0:
         assert pointer == g.data_ptr()  # no copy
+
+
+def test_row_weights_that_are_learned():
+    """A gradient that would be dropped is refused; under no_grad none is, and the call goes on to its other checks."""
+    args = (torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros((10, 64), dtype=torch.bfloat16),
+            torch.zeros(2, dtype=torch.int32))
+    weight = torch.ones(2, requires_grad=True)
+    with pytest.raises(ValueError, match="row_weight"):
+        dv.linear_cross_entropy(*args, row_weight=weight)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        dv.linear_cross_entropy(*args, row_weight=weight)
