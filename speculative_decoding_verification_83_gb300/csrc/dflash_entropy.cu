@@ -82,9 +82,10 @@ struct GemmParams {
   uint32_t* status;
 };
 
-// Rows of a label whose rests join dW: what is left out of n rows is at most sqrt(n - 4) / n, a
-// quarter, of a rounding of their sum's size, and all of them would take as long as the products where
-// rows share few labels.
+// Rows of a label whose rests join dW. Each of n rows beyond them adds its own rounding of the label's
+// entry, half a step of bf16 at most: where rows differ, about sqrt(n - 4) / n of a half step of their sum's
+// size is left out; rows that repeat have equal rests, and (n - 4) / n of one is, almost what rounding every
+// entry leaves. All of them would take as long as the products where rows share few labels.
 constexpr int kHits = 4;
 struct GemmShared {
   uint64_t full[kStages], empty[kStages];
