@@ -589,8 +589,10 @@ int dflash_linear_entropy(const void* h, int64_t h_stride, const void* w, int64_
 /* Its gradients for an upstream gradient of the losses ([device] float [rows],
  * upstream_stride elements apart, 0 for one that all rows share; NULL: 1): dh
  * [rows, K] and dw [V, K] (bf16, contiguous; NULL: not computed). The logits'
- * gradients go to the products as bf16, in pieces of the vocabulary. A row whose
- * upstream gradient is 0 takes no part. */
+ * gradients go to the products as bf16, in pieces of the vocabulary: of 512 MiB at
+ * most up to 2^16 rows, of 8 KiB a row beyond (8 GiB at 2^20 rows). The workspace
+ * holds one piece, a copy of h, and dh in fp32 up to 8 times. A row whose upstream
+ * gradient is 0 takes no part. */
 int dflash_linear_entropy_grad(const void* h, int64_t h_stride, const void* w, int64_t w_stride, int rows, int V, int K,
                                const int32_t* labels, const float* row_weight, const float* row_stats,
                                const float* upstream, int64_t upstream_stride, void* dh, void* dw, void* workspace,

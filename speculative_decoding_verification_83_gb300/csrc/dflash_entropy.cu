@@ -12,8 +12,8 @@
 // memory, into each row's largest logit and sum of exponentials over 128 columns
 // (8 bytes for 128 logits), and picks out the labels' logits; a small kernel joins
 // them. The gradients go through the vocabulary in pieces: the epilogue writes a
-// piece of g in bf16 (at most kPieceBytes, a rounding of half a step of the type
-// in which the products want it), from which dW's rows of the piece and the
+// piece of g in bf16 (kPieceBytes at most, or 4096 entries' worth of more than 2^16 rows; a
+// rounding of half a step of the type in which the products want it), from which dW's rows of the piece and the
 // piece's part of dh follow. A row's g is often ruled by its label's entry, and one
 // rounding then decides the error of the whole row: what it leaves of that entry
 // is kept in fp32 and added to dh, and to dW for a label's first kHits rows. dh is summed in fp32 over pieces, in up to kMaxSplits
@@ -755,7 +755,10 @@ __global__ void __launch_bounds__(256) hidden_kernel(const EntropyParams p, cons
 }
 
 // ---- workspaces
-constexpr long long kPieceBytes = 512ll << 20;  // of g at a time
+// Of g at a time. Beyond 2^16 rows a piece keeps kLeastPiece entries, 8 KB a row: each piece's part
+// of dh is added to fp32 sums, 8 bytes moved for 2 products an entry of the piece.
+constexpr long long kPieceBytes = 512ll << 20;
+constexpr int kLeastPiece = 16 * kTile;
 constexpr int kMaxSplits = 8;
 constexpr int kPairs = 76;  // the splits' rule goes by a whole GPU's pairs of SMs
 
@@ -787,7 +790,7 @@ struct BackwardPlan {
 BackwardPlan backward_plan(int rows, int V, int K) {
   BackwardPlan b;
   long long piece = kPieceBytes / 2 / rows / kTile * kTile;
-  if (piece < 16 * kTile) piece = 16 * kTile;
+  if (piece < kLeastPiece) piece = kLeastPiece;
   if (piece > V) piece = V;
   b.piece = (int)piece;
   b.pitch = (b.piece + 63) / 64 * 64;
