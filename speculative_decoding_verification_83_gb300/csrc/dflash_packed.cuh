@@ -17,20 +17,6 @@ __device__ __forceinline__ void extent(const int32_t* start, int tokens, int b, 
   n = last - first;
   bad |= first != s || last != e;
 }
-// The sequence that holds row t, or -1. (Offsets that do not ascend name any
-// sequence; the caller checks the row against its extent.)
-__device__ __forceinline__ int sequence_of(const int32_t* start, int B, int t) {
-  int lo = 0, hi = B;  // the last b with start[b] <= t
-  if (t < start[0] || t >= start[B]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
 // Keys that query i of n sees of m.
 __device__ __forceinline__ int seen_keys(int causal, int n, int m, int i) {
   return causal ? min(m, max(0, m - n + i + 1)) : m;
