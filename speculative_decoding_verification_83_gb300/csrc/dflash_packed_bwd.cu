@@ -12,14 +12,16 @@
 //    two buffers of scores.
 // What bounds both: the products. They are issued in an order that leaves each
 // exchange with the threads in the shadow of two products: dV(j), S(j + 1) run while
-// dS(j) is made, dK(j), dP(j + 1) while P(j + 1) is. 8 warps make P and dS, two for each quarter
-// of the lanes, half of the columns each; since the results take the scores' place, the
-// two meet once they have read (`met`). The rows' lse and delta lie as pairs by head,
-// made with delta ahead of the kernels; for the keys' kernel 128 of them come with each
-// tile of dO. Masks select P = 0 in tiles at a border only (dS is then 0 times
-// something, which is 0 or mended with the rest). 8 x 1024 queries over 8 x 4096 keys, 32
-// heads of 128 over 8: keys 645 us (1.70 PFLOP/s), queries 463 us (1.78 PFLOP/s); over
-// 1024 keys, 185 and 140 us, the units' beginnings and ends weigh more. Rows with a result that is not
+// dS(j) is made, dK(j), dP(j + 1) while P(j + 1) is. 16 warps make P and dS, four for each
+// quarter of the lanes, 32 of the columns each. Their results take the place of scores:
+// a warp's 32 columns, packed, lie in the first 16 of the 32 that it has read itself, so no
+// warp writes over what another still reads (mma_rows steps over the parts so). A row's
+// lse and delta, made ahead of the kernels, lie by head, all of lse and then all of delta; for the
+// keys' kernel 128 of lse come with each tile of Q and 128 of delta with each tile of dO.
+// Masks select P = 0 in tiles at a border only (dS is then 0 times something, which is 0 or
+// mended with the rest). 8 x 1024 queries over 8 x 4096 keys, 32 heads of 128 over 8: keys
+// 654 us (1.68 PFLOP/s), queries 465 us (1.77 PFLOP/s); over 1024 keys, 187 and 139 us, the
+// units' beginnings and ends weigh more. Rows with a result that is not
 // finite are flagged (see dflash_packed.cuh). Every wait is bounded; a CTA that gives up
 // raises DFLASH_STATUS_TIMEOUT.
 #include <cuda_runtime.h>
@@ -120,8 +122,8 @@ __device__ __forceinline__ void mma_inner(uint32_t d, uint32_t a, uint32_t b, ui
     tc::mma_ss(d, ad + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), bd + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), id, k > 0,
                lead);
 }
-// D (+)= A B over 128 rows of B; A in tensor memory
-// (each part of A's columns lies over that part of the scores)
+// D (+)= A B over 128 rows of B; A in tensor memory, each part of its columns in the first
+// half of that part of the scores, which the warp that wrote it had read
 template <int D>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool add, uint32_t lead) {
   constexpr uint32_t id = tc::idesc<Bf16>(128, D, false, true);
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   begin<D>(S, warp, 1, true);
   constexpr uint32_t t_s = 0, t_dp = 256, t_dq = 384;
   const uint32_t q_mem = base, do_mem = base + W::kTile;
-  const int work = *list.count * p.q_heads;  // (below 2^27)
+  const int work = *list.count * p.q_heads;  // (below 2^28)
   auto tiles_of = [&](const PackedUnit& u) {
     return (seen_keys(p.causal, u.n, u.m, u.i0 + u.rows - 1) + kTileRows - 1) / kTileRows;
   };
