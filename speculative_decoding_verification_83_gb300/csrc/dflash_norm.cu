@@ -123,9 +123,9 @@ __device__ __forceinline__ void fill_weights(const NormParams& p, float4* w) {
 }
 
 // A row is one head of one token: queries, then keys. What bounds it: 302 MB of 8192
-// tokens, 64 + 8 heads of 128 in bf16 take 56 us (5.4 TB/s). A thread's vectors are asked
-// for three steps ahead and wait in shared memory: with loads into registers and a
-// block for each group of tokens they took 61.
+// tokens, 64 + 8 heads of 128 in bf16 take 52 us (5.8 TB/s), replayed from graphs 55. A
+// thread's vectors are asked for three steps ahead and wait in shared memory: with loads
+// into registers and a block for each group of tokens they took 61 replayed.
 constexpr int kForwardSlots = 4, kForwardBlocks = 4;
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads, kForwardBlocks) norm_kernel(const NormParams p) {
